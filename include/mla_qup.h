@@ -329,6 +329,225 @@ typedef struct {
  * MLA_EUNSUPPORTED when T*H*(D_k + D_v)/8 exceeds 2^31 - 1. */
 MLA_API mla_status mla_kv_rope(const mla_kv_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Decoding: a few new (drafted) tokens per sequence, their keys and values in
+ * a paged cache. One step of a server that drafts tokens calls
+ *   mla_qup_fwd_w4       the query up-projection with 4-bit weights,
+ *   mla_pages_reserve    room for the drafts (copy on write),
+ *   mla_kv_rope_paged    their key and value rows into the pages,
+ *   mla_tree_attention   drafts over the committed tokens and their ancestors,
+ *   mla_draft_accept     the accepted path becomes part of the sequence,
+ * and mla_pages_fork / _free / _copy / _compact as sequences branch and end.
+ * Sequence lengths, tables and counts live on the device and nothing is read
+ * back, so the whole step can be recorded in a HIP graph and replayed.
+ * ------------------------------------------------------------------------ */
+
+/* MXFP4-quantize a row-major matrix along its rows (blocks of 32 consecutive
+ * elements of a row; OCP Microscaling Formats v1.0, E2M1 elements). Per block:
+ * amax = max|x|; E = clamp(floor(log2 amax) - 2, -127, 127) (E = -127 when
+ * amax = 0); scale byte E + 127; element = E2M1 round-to-nearest-even of
+ * x*2^-E, saturated to +-6, sign of zero kept. A block holding NaN or Inf gets
+ * scale 0xFF (a NaN block) and codes 7.
+ *   x      : as mxfp8_quantize (bf16 or fp32, 16-byte aligned rows).
+ *   rows >= 0; cols > 0, a multiple of 32; rows * cols <= 2^36; ld >= cols.
+ *   codes  : device uint8[rows*cols/2], element (r, c) in byte r*cols/2 + c/2,
+ *            the even column in its low four bits; 4-byte aligned.
+ *   scales : device uint8[rows*cols/32].
+ * Errors: MLA_EINVAL, MLA_EALIAS. */
+MLA_API mla_status mxfp4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
+                                  int64_t ld, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The forward for few tokens, with MXFP4 weights and bf16 activations:
+ * Q = X deq(W)^T (+ bias), RoPE, BHSD store as mla_qup_fwd. E2M1 times E8M0 is
+ * exact in bf16, products accumulate in fp32 on the bf16 MFMA. Bound by reading
+ * W once (K N / 2 + K N / 32 bytes); any T is valid, beyond 64 tokens W is read
+ * once per 64.
+ *   positions: device int32[T], the position of each token row, in place of
+ *     the token format's (drafted tokens sit behind their sequence's committed
+ *     ones), or NULL. A position outside the table gives NaN in the rotated
+ *     elements, as everywhere. With positions the table needs one row at least. */
+typedef struct {
+  const void* x;            /* bf16 [T, K]; 16-B aligned */
+  const uint8_t* w;         /* MXFP4 codes [N, K/2] (mxfp4_quantize); 16-B aligned */
+  const uint8_t* w_scales;  /* [N, K/32] */
+  const void* bias;         /* bf16 [N] or NULL; 2-B aligned */
+  int32_t K;                /* > 0, multiple of 32 */
+  int32_t H, d_nope, d_rope; /* as the forward's */
+  mla_tokens tokens;
+  const int32_t* positions;
+  mla_rope rope;
+  int32_t out_dtype;        /* MLA_DTYPE_BF16 or MLA_DTYPE_MXFP8 */
+  void* out;                /* BHSD; 16-B aligned */
+  uint8_t* out_scales;      /* MXFP8: BHSD [.., D/32]; else NULL */
+} mla_qup_w4_args;
+
+/* Errors: as mla_qup_fwd (W may span any size). */
+MLA_API mla_status mla_qup_fwd_w4(const mla_qup_w4_args* args, void* stream);
+
+/* A cache of num_pages pages of page_size token rows. Sequence i holds the
+ * pages table[i*max_pages + k], k < held[i], row r of the sequence being row
+ * r % page_size of page r / page_size; lens[i] rows are committed, the rows
+ * behind them (within the held pages) take drafted tokens. refs[p] counts the
+ * table entries that name page p; 0 means free. A new pool has zeros in refs,
+ * lens and held and -1 in table. All arrays are device memory. lens may only
+ * be lowered through mla_pages_free.
+ * Buffers: up to four, buffer b's page p at buf[b] + p*page_bytes[b], its
+ * page_size rows one after the other:
+ *   bf16 : key [H, D_k], then value [H, D_v] unless D_v = 0
+ *   MXFP8: key codes [H, D_k], key scales [H, D_k/32], then value codes and
+ *          value scales unless D_v = 0
+ * Entries of `seqs` arguments are rows of the table, at most MLA_MAX_SEQS of
+ * them in one call. An entry outside [0, max_seqs) is ignored, and so is one
+ * listed before in the same call: a sequence listed twice counts once. */
+enum { MLA_MAX_SEQS = 1024, MLA_MAX_PAGES = 1 << 20, MLA_MAX_PAGE_SIZE = 4096 };
+
+typedef struct {
+  int32_t num_pages;   /* 1 .. MLA_MAX_PAGES */
+  int32_t page_size;   /* 1 .. MLA_MAX_PAGE_SIZE */
+  int32_t max_seqs;    /* rows of the table, >= 1 */
+  int32_t max_pages;   /* columns of the table, >= 1; max_pages*page_size < 2^31 */
+  int32_t* refs;       /* int32[num_pages] */
+  int32_t* table;      /* int32[max_seqs*max_pages] */
+  int32_t* lens;       /* int32[max_seqs] */
+  int32_t* held;       /* int32[max_seqs] */
+  int32_t nbuf;        /* 1 .. 4 */
+  void* buf[4];        /* 16-byte aligned */
+  int64_t page_bytes[4]; /* a multiple of page_size */
+} mla_pool;
+
+/* Workspace bytes that mla_pages_reserve and mla_pages_compact need (16-byte
+ * aligned); 0 for an invalid pool. Its contents need not survive between calls
+ * and need not start at zero. */
+MLA_API size_t mla_pages_workspace_size(const mla_pool* pool);
+
+/* Copy whole pages: page src_ids[i] of src to page dst_ids[i] of dst, every
+ * buffer (src and dst may be one pool; both need the same page_size, nbuf and
+ * page_bytes; refs and tables are neither read nor written). An entry is
+ * skipped if an id lies outside its pool, if its dst id stands earlier in
+ * dst_ids, or, within one pool, if its dst id is among src_ids: the result does
+ * not depend on any order. 0 <= n <= 65536.
+ * Errors: MLA_EINVAL, MLA_EALIAS (two different pools that overlap). */
+MLA_API mla_status mla_pages_copy(const mla_pool* src, const mla_pool* dst, const int32_t* src_ids,
+                                  const int32_t* dst_ids, int32_t n, void* stream);
+
+/* Make room for new_tokens[i] rows behind the committed rows of seqs[i]: pages
+ * are added until held*page_size >= lens + new_tokens, and where the first new
+ * row falls into a page that other sequences name too, its lens % page_size
+ * committed rows move to a page of the sequence's own (copy on write; if all
+ * who name it are in this call, the last listed keeps it). Pages are taken in
+ * ascending order of their ids, in the order of seqs, a copied page before the
+ * added ones.
+ *   status: device int32[1], 0 when done. Otherwise nothing has changed: the
+ *   number of pages missing, or -1 if a new_tokens is negative or a sequence
+ *   would exceed max_pages.
+ * Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EDEVICE. */
+MLA_API mla_status mla_pages_reserve(const mla_pool* pool, const int32_t* seqs, const int32_t* new_tokens,
+                                     int32_t n, int32_t* status, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Branch: sequence dst[i] takes the committed rows of src[i] by naming the same
+ * pages. An entry is skipped if dst holds pages, if its dst stands earlier in
+ * dst, or if its src is a dst of this call.
+ * Errors: MLA_EINVAL, MLA_EDEVICE. */
+MLA_API mla_status mla_pages_fork(const mla_pool* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                                  void* stream);
+
+/* Cut sequence seqs[i] to its first keep[i] committed rows (at most lens; keep
+ * NULL: none) and drop every page behind them, reserved ones too; a page that
+ * no sequence names any more is free.
+ * Errors: MLA_EINVAL, MLA_EDEVICE. */
+MLA_API mla_status mla_pages_free(const mla_pool* pool, const int32_t* seqs, const int32_t* keep, int32_t n,
+                                  void* stream);
+
+/* Pack the pages in use to the front: with U pages in use, those with ids >= U
+ * move, in ascending order, to the free ids < U, and tables follow.
+ *   used: device int32[1], U.
+ * Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EDEVICE. */
+MLA_API mla_status mla_pages_compact(const mla_pool* pool, int32_t* used, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* Accept drafted rows: rows lens + path[i*max_path + a], a < n_acc[i], of
+ * sequence seqs[i] become rows lens + a, and lens grows by n_acc[i]. An entry
+ * whose path does not strictly increase from >= 0, reaches behind the held
+ * pages, or whose n_acc lies outside [0, max_path], is left unchanged. The rows
+ * are written in place: reserve them first, which unshares them.
+ * Errors: MLA_EINVAL, MLA_EDEVICE. */
+MLA_API mla_status mla_draft_accept(const mla_pool* pool, const int32_t* seqs, const int32_t* path,
+                                    const int32_t* n_acc, int32_t n, int32_t max_path, void* stream);
+
+/* Key and value rows of new tokens into the pages: as mla_kv_rope, token
+ * cu_q[j] + i going to row lens[seqs[j]] + i of sequence seqs[j]. The latent
+ * form has H = 1, d_nope = the latent's width and d_v = 0. A token without a
+ * held page is not written (nor one behind cu_q[nseq]); a sequence listed a
+ * second time is ignored with its tokens. lens stays: mla_draft_accept moves it.
+ *   positions: device int32[T] for the rotation, or NULL for lens + i. */
+typedef struct {
+  const void* kv;           /* bf16 [T, H, d_nope + d_v]; 16-B aligned */
+  const void* k_pe;         /* bf16 [T, d_rope]; 16-B aligned */
+  int32_t H, d_nope, d_rope, d_v;   /* as mla_kv_rope's */
+  int64_t T;                /* token rows of kv, < 2^31 */
+  const int32_t* seqs;      /* device int32[nseq] */
+  const int32_t* cu_q;      /* device int32[nseq + 1], nondecreasing */
+  int32_t nseq;             /* 0 .. MLA_MAX_SEQS */
+  int32_t max_q;            /* positions NULL: bound on the new tokens of a sequence
+                               (documentation of the plan; the table is checked
+                               row by row) */
+  const int32_t* positions;
+  mla_rope rope;
+  int32_t cache_dtype;      /* MLA_DTYPE_BF16 or MLA_DTYPE_MXFP8 */
+  const mla_pool* pool;
+} mla_kv_paged_args;
+
+/* Errors: MLA_EINVAL, MLA_EROPE_TABLE, MLA_EALIAS, MLA_EDEVICE. */
+MLA_API mla_status mla_kv_rope_paged(const mla_kv_paged_args* args, void* stream);
+
+/* Attention of drafted tokens over the cache. Query token cu_q[j] + i belongs
+ * to sequence seqs[j]; it sees the sequence's committed rows r < lens and, of
+ * its drafted rows lens + k, k < cu_q[j+1] - cu_q[j], those with bit k % 32 of
+ * mask[t*mask_words + k/32] set (NULL: k <= i, a chain). Per head h, with its
+ * key head h / (H / H_kv), s_r = scale q.key_r over the rows seen:
+ *   out = sum_r e^(s_r) value_r / sum_r e^(s_r),   lse = ln sum_r e^(s_r).
+ * A token that sees no row gets out = 0 and lse = -inf. What lies in rows that
+ * a token does not see, NaN and infinities included, has no influence on it.
+ * Statistics and sums are fp32; the weights e^(s - max) are rounded to bf16
+ * for the product with the values. Results do not depend on timing.
+ * Widths (D_k, D_v): latent cache (no value buffer, value = the key's first
+ * D_v elements): (576, 512), (96, 64); with values: (192, 128), (128, 128),
+ * (64, 64). Others: MLA_EUNSUPPORTED. bf16 or MXFP8 cache; queries are bf16.
+ * A sequence that outgrows max_q or max_len, and a page id outside the pool,
+ * give NaN in the rows concerned, never a read out of bounds. Query rows
+ * behind cu_q[nseq] are left as they are. */
+typedef struct {
+  const void* q;            /* bf16; element (t, h, d) at q[t*q_stride_t + h*q_stride_h + d];
+                               16-B aligned, strides multiples of 8 */
+  int64_t q_stride_t, q_stride_h;
+  void* out;                /* bf16, likewise with its own strides; 16-B aligned */
+  int64_t out_stride_t, out_stride_h;   /* multiples of 8 */
+  float* lse;               /* fp32 [T, H] or NULL */
+  int64_t T;                /* query rows */
+  int32_t H, H_kv, d_k, d_v; /* H a multiple of H_kv */
+  float scale;              /* finite */
+  const int32_t* seqs;      /* device int32[nseq] */
+  const int32_t* cu_q;      /* device int32[nseq + 1], nondecreasing from 0 */
+  int32_t nseq;             /* 0 .. 65535 */
+  int32_t max_q;            /* host-side bound on cu_q[j+1] - cu_q[j], >= 1 */
+  int32_t max_len;          /* host-side bound on lens + drafted rows, >= 1 */
+  const uint32_t* mask;     /* device uint32[T*mask_words] or NULL */
+  int32_t mask_words;       /* >= ceil(max_q / 32) when mask is given */
+  int32_t cache_dtype;      /* MLA_DTYPE_BF16 or MLA_DTYPE_MXFP8 */
+  const mla_pool* pool;
+  void* workspace;          /* >= mla_tree_attention_workspace_size() bytes, 256-B aligned;
+                               NULL allowed if that is 0 */
+  size_t workspace_bytes;
+} mla_tree_attn_args;
+
+/* Workspace bytes for these arguments: the partial results of the cache's
+ * chunks. Never dereferences device pointers; 0 for invalid shapes. */
+MLA_API size_t mla_tree_attention_workspace_size(const mla_tree_attn_args* args);
+
+/* Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED, MLA_EDEVICE. */
+MLA_API mla_status mla_tree_attention(const mla_tree_attn_args* args, void* stream);
+
 /* Static string naming a status code. */
 MLA_API const char* mla_status_str(mla_status status);
 

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_double, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch  # imported before the library so both share torch's HIP runtime
 
@@ -25,7 +25,11 @@ FMT_BSHD, FMT_SBHD, FMT_THD = 0, 1, 2
 
 FUNCTIONS = ("rope_cache_build", "mxfp8_quantize", "mxfp8_quantize_t", "mla_qup_fwd", "mla_qup_bwd",
              "mla_qup_bwd_workspace_size", "mla_qup_bwd_noalloc", "mla_qup_bwd_mxfp8",
-             "mla_qup_bwd_mxfp8_workspace_size", "mla_kv_rope", "mla_status_str")
+             "mla_qup_bwd_mxfp8_workspace_size", "mla_kv_rope", "mla_status_str",
+             "mxfp4_quantize", "mla_qup_fwd_w4", "mla_pages_workspace_size", "mla_pages_copy",
+             "mla_pages_reserve", "mla_pages_fork", "mla_pages_free", "mla_pages_compact",
+             "mla_draft_accept", "mla_kv_rope_paged", "mla_tree_attention",
+             "mla_tree_attention_workspace_size")
 
 
 class mla_tokens(Structure):
@@ -67,6 +71,35 @@ class mla_qup_bwd_args(Structure):
                 ("workspace_bytes", c_size_t)]
 
 
+class mla_pool(Structure):
+    _fields_ = [("num_pages", c_int32), ("page_size", c_int32), ("max_seqs", c_int32), ("max_pages", c_int32),
+                ("refs", c_void_p), ("table", c_void_p), ("lens", c_void_p), ("held", c_void_p),
+                ("nbuf", c_int32), ("buf", c_void_p * 4), ("page_bytes", c_int64 * 4)]
+
+
+class mla_qup_w4_args(Structure):
+    _fields_ = [("x", c_void_p), ("w", c_void_p), ("w_scales", c_void_p), ("bias", c_void_p), ("K", c_int32),
+                ("H", c_int32), ("d_nope", c_int32), ("d_rope", c_int32), ("tokens", mla_tokens),
+                ("positions", c_void_p), ("rope", mla_rope), ("out_dtype", c_int32), ("out", c_void_p),
+                ("out_scales", c_void_p)]
+
+
+class mla_kv_paged_args(Structure):
+    _fields_ = [("kv", c_void_p), ("k_pe", c_void_p), ("H", c_int32), ("d_nope", c_int32), ("d_rope", c_int32),
+                ("d_v", c_int32), ("T", c_int64), ("seqs", c_void_p), ("cu_q", c_void_p), ("nseq", c_int32),
+                ("max_q", c_int32), ("positions", c_void_p), ("rope", mla_rope), ("cache_dtype", c_int32),
+                ("pool", POINTER(mla_pool))]
+
+
+class mla_tree_attn_args(Structure):
+    _fields_ = [("q", c_void_p), ("q_stride_t", c_int64), ("q_stride_h", c_int64), ("out", c_void_p),
+                ("out_stride_t", c_int64), ("out_stride_h", c_int64), ("lse", c_void_p), ("T", c_int64),
+                ("H", c_int32), ("H_kv", c_int32), ("d_k", c_int32), ("d_v", c_int32), ("scale", c_float),
+                ("seqs", c_void_p), ("cu_q", c_void_p), ("nseq", c_int32), ("max_q", c_int32),
+                ("max_len", c_int32), ("mask", c_void_p), ("mask_words", c_int32), ("cache_dtype", c_int32),
+                ("pool", POINTER(mla_pool)), ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
 _lib = None
 
 
@@ -95,6 +128,25 @@ def lib() -> ctypes.CDLL:
         L.mla_kv_rope.argtypes = [POINTER(mla_kv_args), c_void_p]
         L.mla_status_str.argtypes = [c_int32]
         L.mla_status_str.restype = c_char_p
+        pool = POINTER(mla_pool)
+        L.mxfp4_quantize.argtypes = L.mxfp8_quantize.argtypes
+        L.mla_qup_fwd_w4.argtypes = [POINTER(mla_qup_w4_args), c_void_p]
+        L.mla_pages_workspace_size.argtypes = [pool]
+        L.mla_pages_workspace_size.restype = c_size_t
+        L.mla_pages_copy.argtypes = [pool, pool, c_void_p, c_void_p, c_int32, c_void_p]
+        L.mla_pages_reserve.argtypes = [pool, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p]
+        L.mla_pages_fork.argtypes = [pool, c_void_p, c_void_p, c_int32, c_void_p]
+        L.mla_pages_free.argtypes = [pool, c_void_p, c_void_p, c_int32, c_void_p]
+        L.mla_pages_compact.argtypes = [pool, c_void_p, c_void_p, c_size_t, c_void_p]
+        L.mla_draft_accept.argtypes = [pool, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p]
+        L.mla_kv_rope_paged.argtypes = [POINTER(mla_kv_paged_args), c_void_p]
+        L.mla_tree_attention.argtypes = [POINTER(mla_tree_attn_args), c_void_p]
+        L.mla_tree_attention_workspace_size.argtypes = [POINTER(mla_tree_attn_args)]
+        L.mla_tree_attention_workspace_size.restype = c_size_t
+        for f in ("mxfp4_quantize", "mla_qup_fwd_w4", "mla_pages_copy", "mla_pages_reserve", "mla_pages_fork",
+                  "mla_pages_free", "mla_pages_compact", "mla_draft_accept", "mla_kv_rope_paged",
+                  "mla_tree_attention"):
+            getattr(L, f).restype = c_int32
         for f in ("rope_cache_build", "mxfp8_quantize", "mxfp8_quantize_t", "mla_qup_fwd", "mla_qup_bwd",
                   "mla_qup_bwd_noalloc", "mla_qup_bwd_mxfp8", "mla_kv_rope"):
             getattr(L, f).restype = c_int32
@@ -371,3 +423,260 @@ def mla_kv_rope(kv, k_pe, key, value, *, H, d_nope, d_rope, d_v, cos=None, sin=N
     a.key_scales = chk(key_scales, "key_scales", (_U8,), numel=T * H * Dk // 32)
     a.value_scales = chk(value_scales, "value_scales", (_U8,), numel=T * H * Dv // 32)
     _check(lib().mla_kv_rope(ctypes.byref(a), _stream(stream)), "mla_kv_rope")
+
+
+# ------------------------------------------------------------------ decoding --
+class _On:
+    """The stream of a call and, while it lasts, its device as the current one
+    (a launch on the default stream goes to the current device)."""
+
+    def __init__(self, device, stream):
+        self.guard = None
+        if device is not None and device.type == "cuda" and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.arg = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.arg)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def mxfp4_quantize(x, codes, scales, stream=None):
+    """x [rows, cols] bf16/fp32 (row stride may exceed cols) -> codes uint8
+    [rows, cols/2] (even column in the low four bits), scales uint8 [rows, cols/32]."""
+    chk = _Dev("mxfp4_quantize")
+    if x.dim() != 2 or x.stride(-1) != 1:
+        raise ValueError("mxfp4_quantize: x must be 2-D with contiguous rows")
+    rows, cols = x.shape
+    if rows > 1 and x.stride(0) < cols:
+        raise ValueError("mxfp4_quantize: the rows of x overlap")
+    ld = max(x.stride(0), cols) if rows > 1 else cols
+    span = x.as_strided(((rows - 1) * ld + cols,) if rows else (0,), (1,))
+    px = chk(span, "x", (_BF16, _FP32))
+    dt = DTYPE_FP32 if x.dtype == torch.float32 else DTYPE_BF16
+    pc = chk(codes, "codes", (_U8,), numel=rows * cols // 2)
+    psc = chk(scales, "scales", (_U8,), numel=rows * cols // 32)
+    with _On(chk.device, stream) as s:
+        _check(lib().mxfp4_quantize(px, dt, rows, cols, ld, pc, psc, s), "mxfp4_quantize")
+
+
+def mla_qup_fwd_w4(x, w, w_scales, out, *, H, d_nope, d_rope, cos=None, sin=None, positions=None, bias=None,
+                   out_scales=None, fmt=FMT_BSHD, B=1, S=None, cu_seqlens=None, max_seqlen=None, stream=None):
+    """Forward of few tokens with MXFP4 weights: x bf16 [T,K], w uint8 [N,K/2] and w_scales uint8 [N,K/32] from
+    mxfp4_quantize; out and out_scales as mla_qup_fwd's. positions int32 [T]: each token's position, in place of
+    the format's."""
+    chk = _Dev("mla_qup_fwd_w4")
+    a = mla_qup_w4_args()
+    if x.dim() != 2:
+        raise ValueError("mla_qup_fwd_w4: x must be [T, K]")
+    T, K = x.shape
+    N = H * (d_nope + d_rope)
+    a.x = chk(x, "x", (_BF16,))
+    a.w = chk(w, "w", (_U8,), numel=N * K // 2)
+    a.w_scales = chk(w_scales, "w_scales", (_U8,), numel=N * K // 32)
+    a.bias = chk(bias, "bias", (_BF16,), numel=N)
+    a.K, a.H, a.d_nope, a.d_rope = K, H, d_nope, d_rope
+    a.tokens = _tokens(chk, T, fmt, B, S, cu_seqlens, max_seqlen)
+    a.positions = chk(positions, "positions", (_I32,), numel=T)
+    a.rope = _rope(chk, cos, sin, d_rope)
+    a.out_dtype = DTYPE_MXFP8 if out.dtype == torch.uint8 else DTYPE_BF16
+    a.out = chk(out, "out", (_BF16, _U8), numel=T * N)
+    a.out_scales = chk(out_scales, "out_scales", (_U8,), numel=T * N // 32)
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_qup_fwd_w4(ctypes.byref(a), s), "mla_qup_fwd_w4")
+
+
+class PagePool:
+    """A paged cache (mla_pool): buffers [num_pages, page_size, heads, width] (bf16: key, then value unless the
+    cache is latent; MXFP8, uint8: key codes, key scales [.., width/32], then value codes and scales), and
+    int32 refs [num_pages], table [max_seqs, max_pages], lens [max_seqs], held [max_seqs]. The tensors are
+    checked once, here; the pool keeps them alive and they must stay as they are (their values are the state)."""
+
+    def __init__(self, bufs, refs, table, lens, held):
+        chk = _Dev("PagePool")
+        bufs = list(bufs)
+        if not 1 <= len(bufs) <= 4 or any(b.dim() != 4 for b in bufs):
+            raise ValueError("PagePool: one to four buffers [num_pages, page_size, heads, width]")
+        if any(b.shape[:2] != bufs[0].shape[:2] or b.shape[2] != bufs[0].shape[2] or b.dtype != bufs[0].dtype
+               for b in bufs):
+            raise ValueError("PagePool: buffers must agree in pages, page size, heads and dtype")
+        if table.dim() != 2:
+            raise ValueError("PagePool: table must be [max_seqs, max_pages]")
+        self.mx = bufs[0].dtype == torch.uint8
+        if self.mx:
+            if len(bufs) % 2 or any(bufs[k].shape[3] != 32 * bufs[k + 1].shape[3] for k in range(0, len(bufs), 2)):
+                raise ValueError("PagePool: an MXFP8 cache has codes and scales [.., width/32] in pairs")
+        elif len(bufs) > 2:
+            raise ValueError("PagePool: a bf16 cache has a key and at most a value buffer")
+        n, page = bufs[0].shape[:2]
+        c = mla_pool()
+        c.num_pages, c.page_size, c.max_seqs, c.max_pages = n, page, table.shape[0], table.shape[1]
+        c.refs = chk(refs, "refs", (_I32,), numel=n)
+        c.table = chk(table, "table", (_I32,))
+        c.lens = chk(lens, "lens", (_I32,), numel=table.shape[0])
+        c.held = chk(held, "held", (_I32,), numel=table.shape[0])
+        c.nbuf = len(bufs)
+        for k, b in enumerate(bufs):
+            c.buf[k] = chk(b, f"bufs[{k}]", (_BF16, _U8))
+            c.page_bytes[k] = b.stride(0) * b.element_size() if n > 1 else b.numel() * b.element_size()
+        self.c, self.device = c, chk.device
+        self.ref = ctypes.byref(c)
+        self.bufs, self.refs, self.table, self.lens, self.held = bufs, refs, table, lens, held
+        self.heads, self.d_k = bufs[0].shape[2:]
+        self.latent = len(bufs) == (2 if self.mx else 1)
+        self.d_v = None if self.latent else bufs[2 if self.mx else 1].shape[3]
+
+
+def _pool_chk(where, pool) -> _Dev:
+    if not isinstance(pool, PagePool):
+        raise ValueError(f"{where}: pool must be a PagePool")
+    chk = _Dev(where)
+    chk.device = pool.device
+    return chk
+
+
+def _workspace(chk, workspace):
+    return chk(workspace, "workspace", (_U8,)), (workspace.numel() if workspace is not None else 0)
+
+
+def mla_pages_workspace_size(pool) -> int:
+    _pool_chk("mla_pages_workspace_size", pool)
+    return int(lib().mla_pages_workspace_size(pool.ref))
+
+
+def mla_pages_copy(src, dst, src_ids, dst_ids, stream=None):
+    """Page src_ids[i] of pool src to page dst_ids[i] of pool dst (int32 tensors), every buffer."""
+    chk = _pool_chk("mla_pages_copy", src)
+    if not isinstance(dst, PagePool) or dst.device != src.device:
+        raise ValueError("mla_pages_copy: dst must be a PagePool on src's device")
+    n = src_ids.numel()
+    a, b = chk(src_ids, "src_ids", (_I32,)), chk(dst_ids, "dst_ids", (_I32,), numel=n)
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_pages_copy(src.ref, dst.ref, a, b, n, s), "mla_pages_copy")
+
+
+def mla_pages_reserve(pool, seqs, new_tokens, status, *, workspace, stream=None):
+    """Room for new_tokens[i] rows behind sequence seqs[i] (int32 [n] each), copying shared pages on write.
+    status int32 [1]: 0 when done, else nothing changed. workspace: mla_pages_workspace_size() bytes."""
+    chk = _pool_chk("mla_pages_reserve", pool)
+    n = seqs.numel()
+    a, b = chk(seqs, "seqs", (_I32,)), chk(new_tokens, "new_tokens", (_I32,), numel=n)
+    st = chk(status, "status", (_I32,), numel=1)
+    w, size = _workspace(chk, workspace)
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_pages_reserve(pool.ref, a, b, n, st, w, size, s), "mla_pages_reserve")
+
+
+def mla_pages_fork(pool, src, dst, stream=None):
+    """Sequence dst[i] (empty) takes the committed rows of src[i] by sharing its pages."""
+    chk = _pool_chk("mla_pages_fork", pool)
+    a, b = chk(src, "src", (_I32,)), chk(dst, "dst", (_I32,), numel=src.numel())
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_pages_fork(pool.ref, a, b, src.numel(), s), "mla_pages_fork")
+
+
+def mla_pages_free(pool, seqs, keep=None, stream=None):
+    """Cut sequences to keep[i] committed rows (None: none) and drop the pages behind them."""
+    chk = _pool_chk("mla_pages_free", pool)
+    a, b = chk(seqs, "seqs", (_I32,)), chk(keep, "keep", (_I32,), numel=seqs.numel())
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_pages_free(pool.ref, a, b, seqs.numel(), s), "mla_pages_free")
+
+
+def mla_pages_compact(pool, used, *, workspace, stream=None):
+    """Move the pages in use to the front of the pool; used int32 [1] receives their number."""
+    chk = _pool_chk("mla_pages_compact", pool)
+    u = chk(used, "used", (_I32,), numel=1)
+    w, size = _workspace(chk, workspace)
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_pages_compact(pool.ref, u, w, size, s), "mla_pages_compact")
+
+
+def mla_draft_accept(pool, seqs, path, n_acc, stream=None):
+    """Drafted rows path[i, :n_acc[i]] (counted behind the committed ones) of sequence seqs[i] become its next rows."""
+    chk = _pool_chk("mla_draft_accept", pool)
+    n = seqs.numel()
+    if path.dim() != 2 or path.shape[0] != n:
+        raise ValueError("mla_draft_accept: path must be [n, max_path]")
+    a, b = chk(seqs, "seqs", (_I32,)), chk(path, "path", (_I32,))
+    c = chk(n_acc, "n_acc", (_I32,), numel=n)
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_draft_accept(pool.ref, a, b, c, n, path.shape[1], s), "mla_draft_accept")
+
+
+def mla_kv_rope_paged(kv, k_pe, pool, seqs, cu_q, *, H, d_nope, d_rope, d_v, cos=None, sin=None, positions=None,
+                      max_q=None, stream=None):
+    """Key and value rows of new tokens into the cache: kv bf16 [T,H,d_nope+d_v], k_pe bf16 [T,d_rope]; token
+    cu_q[j] + i becomes row lens[seqs[j]] + i. positions int32 [T] or None for the rows themselves."""
+    chk = _pool_chk("mla_kv_rope_paged", pool)
+    a = mla_kv_paged_args()
+    T = kv.shape[0]
+    a.kv = chk(kv, "kv", (_BF16,), numel=T * H * (d_nope + d_v))
+    a.k_pe = chk(k_pe, "k_pe", (_BF16,), numel=T * d_rope)
+    a.H, a.d_nope, a.d_rope, a.d_v, a.T = H, d_nope, d_rope, d_v, T
+    a.nseq = seqs.numel()
+    a.seqs = chk(seqs, "seqs", (_I32,))
+    a.cu_q = chk(cu_q, "cu_q", (_I32,), numel=a.nseq + 1)
+    a.max_q = max(1, T) if max_q is None else max_q
+    a.positions = chk(positions, "positions", (_I32,), numel=T)
+    a.rope = _rope(chk, cos, sin, d_rope)
+    a.cache_dtype = DTYPE_MXFP8 if pool.mx else DTYPE_BF16
+    a.pool = ctypes.pointer(pool.c)
+    with _On(chk.device, stream) as s:
+        _check(lib().mla_kv_rope_paged(ctypes.byref(a), s), "mla_kv_rope_paged")
+
+
+def make_tree_attn_args(q, pool, out, seqs, cu_q, *, max_q, max_len, scale, lse=None, mask=None,
+                        workspace=None) -> mla_tree_attn_args:
+    where = "mla_tree_attention"
+    chk = _pool_chk(where, pool)
+    a = mla_tree_attn_args()
+    if q.dim() != 3 or out.dim() != 3 or q.shape[:2] != out.shape[:2]:
+        raise ValueError(f"{where}: q must be [T, H, d_k] and out [T, H, d_v]")
+    for t, name in ((q, "q"), (out, "out")):  # token and head strides are free, elements are dense
+        if not isinstance(t, torch.Tensor) or t.device != pool.device or t.dtype != _BF16:
+            raise ValueError(f"{where}: {name} must be a bf16 tensor on {pool.device}")
+        if t.numel() and t.stride(2) != 1:
+            raise ValueError(f"{where}: the elements of a row of {name} must be dense")
+    T, H, d_k = q.shape
+    a.q, a.q_stride_t, a.q_stride_h = q.data_ptr(), q.stride(0), q.stride(1)
+    a.out, a.out_stride_t, a.out_stride_h = out.data_ptr(), out.stride(0), out.stride(1)
+    a.T, a.H, a.H_kv, a.d_k, a.d_v = T, H, pool.heads, d_k, out.shape[2]
+    if d_k != pool.d_k or (not pool.latent and a.d_v != pool.d_v):
+        raise ValueError(f"{where}: widths of q and out do not fit the cache")
+    a.lse = chk(lse, "lse", (_FP32,), numel=T * H)
+    a.scale = scale
+    a.nseq = seqs.numel()
+    a.seqs = chk(seqs, "seqs", (_I32,))
+    a.cu_q = chk(cu_q, "cu_q", (_I32,), numel=a.nseq + 1)
+    a.max_q, a.max_len = max_q, max_len
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[0] != T:
+            raise ValueError(f"{where}: mask must be [T, words]")
+        a.mask, a.mask_words = chk(mask, "mask", (_I32, torch.uint32)), mask.shape[1]
+    a.cache_dtype = DTYPE_MXFP8 if pool.mx else DTYPE_BF16
+    a.pool = ctypes.pointer(pool.c)
+    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
+    return a
+
+
+def mla_tree_attention_workspace_size(q, pool, out, seqs, cu_q, **kw) -> int:
+    kw.pop("stream", None)
+    a = make_tree_attn_args(q, pool, out, seqs, cu_q, **kw)
+    return int(lib().mla_tree_attention_workspace_size(ctypes.byref(a)))
+
+
+def mla_tree_attention(q, pool, out, seqs, cu_q, *, stream=None, **kw):
+    """Attention of drafted tokens over the cache: q bf16 [T,H,d_k] and out bf16 [T,H,d_v] (rows dense, token and
+    head strides free), tokens cu_q[j] .. cu_q[j+1] belonging to sequence seqs[j] (int32). mask int32 [T, words]:
+    the drafts of its sequence that a token sees, one bit each (None: a chain). max_q and max_len bound the drafts
+    and the rows, drafts included, of any sequence. lse fp32 [T,H] or None; workspace:
+    mla_tree_attention_workspace_size() bytes (None if that is 0)."""
+    a = make_tree_attn_args(q, pool, out, seqs, cu_q, **kw)
+    with _On(pool.device, stream) as s:
+        _check(lib().mla_tree_attention(ctypes.byref(a), s), "mla_tree_attention")
