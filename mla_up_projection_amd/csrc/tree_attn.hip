@@ -20,6 +20,7 @@
 
 #include "device_common.h"
 #include "internal_decode.h"
+#include "tree_attn_wide.h"
 
 namespace mla {
 namespace {
@@ -27,7 +28,7 @@ namespace {
 constexpr int TILE = 32;         // cache rows per step
 constexpr int BLK = TILE * 128;  // LDS bytes of a 64-column block of a tile
 constexpr int MAX_CHUNK_PAGES = 1024;
-constexpr float LAZY = 8.0f;     // the maximum may lag by this many powers of two
+constexpr float LAZY = 64.0f;    // how many powers of two a score may lie above its row's reference
 constexpr float NEG_INF = -__builtin_huge_valf();
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -59,12 +60,13 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int64_t item, Ite
   it.j = (int)(item / p.H_kv);
   if (it.j >= p.nseq) return false;
   const int T = (int)p.T;
-  it.t0 = min(max(p.cu[it.j], 0), T);
-  it.n = min(max(p.cu[it.j + 1], it.t0), T) - it.t0;
+  // the same for every lane: kept in scalar registers
+  it.t0 = min(max(__builtin_amdgcn_readfirstlane(p.cu[it.j]), 0), T);
+  it.n = min(max(__builtin_amdgcn_readfirstlane(p.cu[it.j + 1]), it.t0), T) - it.t0;
   it.rows = it.n * p.group;
-  it.seq = p.seqs[it.j];
+  it.seq = __builtin_amdgcn_readfirstlane(p.seqs[it.j]);
   it.broken = it.seq < 0 || it.seq >= p.pool.max_seqs || it.n > p.max_q;
-  it.len = it.broken ? 0 : p.pool.lens[it.seq];
+  it.len = it.broken ? 0 : __builtin_amdgcn_readfirstlane(p.pool.lens[it.seq]);
   it.broken |= it.len < 0 || it.len > p.max_len - it.n;
   it.total = it.len + it.n;
   it.chunks = it.broken ? 1 : max(1, (it.total + p.plan.chunk - 1) / p.plan.chunk);
@@ -100,56 +102,419 @@ __device__ __forceinline__ uint32_t visible(const AttnParams& p, const Item& it,
   return left >= 32 ? bits : left <= 0 ? 0 : bits & ((1u << left) - 1);
 }
 
-// bf16 pair with non-finite elements replaced by zero / by a code (+inf 1,
-// -inf 64, NaN 4096, finite 0).
-__device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
-  if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
-  if ((v & 0x7F800000u) == 0x7F800000u) v &= 0xFFFFu;
-  return v;
+// Whether one of two bf16 is infinite or NaN.
+__device__ __forceinline__ bool not_finite_pair(uint32_t v) {
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
 }
-__device__ __forceinline__ uint32_t code16(uint32_t v) {
-  if ((v & 0x7F80u) != 0x7F80u) return 0;
-  return (v & 0x7Fu) ? 0x4580u : (v & 0x8000u) ? 0x4280u : 0x3F80u;  // bf16 of 4096, 64, 1
-}
-__device__ __forceinline__ uint32_t code_pair(uint32_t v) { return code16(v & 0xFFFFu) | code16(v >> 16) << 16; }
 
+// Sizes of a kernel variant. A workgroup has WAVES waves of 32 query rows each
+// and a ring of STAGES tiles in LDS: four waves keep as many tiles as fit 160
+// KB; one and two waves keep one and two, so that four waves' worth of
+// workgroups share a CU and hide each other's loads.
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 struct Shape {
+  static constexpr int THREADS = 64 * WAVES;
   static constexpr int NBK = (DK + 63) / 64, NBV = SHARED ? 0 : (DV + 63) / 64;
+  static constexpr int NB = NBK + NBV;       // 64-column blocks of a tile: keys, then values
   static constexpr int KK = DK / 16, NT = DV / 32;
-  static constexpr int LDS = (NBK + NBV) * BLK;
+  static constexpr int TILE_LDS = NB * BLK;
+  static constexpr bool WIDE = DK == 576 && DV == 512;  // the products are written out (tree_attn_wide.h)
+  static constexpr int STAGES = MX ? (WAVES == 1 ? 1 : 2) : WAVES == 4 ? (NB > 5 ? 4 : 3) : WAVES;
+  static constexpr int RPT = TILE / (8 * WAVES);  // rows of a tile that a thread stages (16 bytes of each block)
+  static constexpr int LOADS = RPT * NB;          // its loads per tile
 };
+
+__device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// 16 bytes per lane from any address to LDS bytes [lds_addr + 16 lane, + 16).
+__device__ __forceinline__ void dma16_far(const void* p, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :
+               : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(p)
+               : "memory", "m0");
+}
+
+// Barrier after this wave's LDS reads have returned (a loading instruction may
+// overwrite what they read once all waves have passed).
+__device__ __forceinline__ void barrier_reads_done() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int DK, int DV, bool SHARED, bool MX, int WAVES>
+struct Worker {
+  using S = Shape<DK, DV, SHARED, MX, WAVES>;
+  const AttnParams& p;
+  const Item& it;
+  uint8_t* lds;
+  const int* s_page;
+  int page0, tk_begin, tk_end;
+  bool odd;  // a value that is not finite lies in a tile that some rows do not see whole
+  // the lane's query row
+  int64_t qt;
+  int qi;
+  bf16x8_t q[S::KK];
+  f32x16_t o[S::NT];
+  float m, top, l;  // reference, largest score, sum of weights
+  // LDS offsets of fragments, see init()
+  int koff[4], voff[2][2];
+  int lane, half, tid, wave;
+  // MXFP8: the next tile's codes and scales, on their way to LDS as bf16
+  static constexpr int HELD = MX && S::RPT == 1 ? S::NB : 1;
+  uint2 code[HELD];
+  uint32_t sc[HELD];
+
+  __device__ __forceinline__ Worker(const AttnParams& p_, const Item& it_) : p(p_), it(it_) {}
+
+  // Row (of width d) of cache row tok; rows behind the chunk read its last one.
+  __device__ __forceinline__ int64_t cache_row(int tok) const {
+    const uint32_t rel = (uint32_t)(min(tok, tk_end - 1) - page0 * p.pool.page_size);
+    const uint32_t pk = p.page_magic ? __umulhi(rel, p.page_magic) : rel;
+    const int64_t page = max(s_page[pk], 0);
+    return (page * p.pool.page_size + (rel - pk * p.pool.page_size)) * p.H_kv + it.kvh;
+  }
+
+  // The 16-byte chunk of block b that this thread stages of row r goes to LDS
+  // place tid % 8 of the row, so it is the chunk that belongs there.
+  __device__ __forceinline__ int chunk_of(int r, int b) const {
+    int c = (tid & 7) ^ swz(r);
+    if (DK % 64 && b == S::NBK - 1) c &= (DK % 64) / 8 - 1;  // half a block: its other places are not read
+    return c;
+  }
+
+  __device__ __forceinline__ void load_bf16(int tk, int slot) const {
+#pragma unroll
+    for (int g = 0; g < S::RPT; ++g) {
+      const int r = g * (8 * WAVES) + (tid >> 3);
+      const int64_t row = cache_row(tk + r);
+      const uint32_t to = lds_u32(lds) + slot * S::TILE_LDS + g * (8 * WAVES) * 128 + wave * 1024;
+#pragma unroll
+      for (int b = 0; b < S::NB; ++b) {
+        const bool k = b < S::NBK;
+        const uint8_t* src = p.pool.buf[k ? 0 : 1] + (row * (k ? DK : DV) + (k ? b : b - S::NBK) * 64 + 8 * chunk_of(r, b)) * 2;
+        dma16_far(src, to + b * BLK);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void load_mx(int64_t row, int r, uint2* cd, uint32_t* sb) const {
+#pragma unroll
+    for (int b = 0; b < S::NB; ++b) {
+      const bool k = b < S::NBK;
+      const int d = k ? DK : DV, at = (k ? b : b - S::NBK) * 64 + 8 * chunk_of(r, b);
+      cd[b] = *reinterpret_cast<const uint2*>(p.pool.buf[k ? 0 : 2] + row * d + at);
+      sb[b] = p.pool.buf[k ? 1 : 3][row * (d / 32) + at / 32];
+    }
+  }
+  __device__ __forceinline__ void store_mx(int r, int slot, const uint2* cd, const uint32_t* sb) const {
+#pragma unroll
+    for (int b = 0; b < S::NB; ++b) {
+      // E4M3 times 2^(byte - 127) is exact in bf16 down to its subnormals
+      const float f = __uint_as_float(sb[b] ? sb[b] << 23 : 0x00400000u);
+      u32x4_t v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].x, f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].x, f, true)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].y, f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].y, f, true))};
+      if (sb[b] == 0xFF) v = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+      *reinterpret_cast<u32x4_t*>(lds + slot * S::TILE_LDS + b * BLK + r * 128 + ((tid & 7) << 4)) = v;
+    }
+  }
+
+  typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+  // V^T fragment of value columns 32 n .. + 31 and the tile's 16-row step c
+  __device__ __forceinline__ u32x4_t v_frag(const uint8_t* tile, int n, int c) const {
+    const uint8_t* base = tile + (SHARED ? 0 : S::NBK * BLK) + (n >> 1) * BLK + c * 16 * 128;
+    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[0][n & 1])));
+    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[1][n & 1])));
+    return u32x4_t{a.x, a.y, b.x, b.y};
+  }
+
+  // S^T: element i is cache row 8 (i / 4) + 4 half + i % 4, column the lane's query
+  __device__ __forceinline__ f32x16_t scores(const uint8_t* tile) const {
+    f32x16_t s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0;
+#pragma unroll
+    for (int kk = 0; kk < S::KK; ++kk)
+      s = mfma(*reinterpret_cast<const bf16x8_t*>(tile + (kk >> 2) * BLK + koff[kk & 3]), q[kk], s);
+    return s;
+  }
+
+  // Scores (in powers of two) to weights 2^(s - m). m is the largest score of the
+  // row's first tile with a row it sees. Weights above 1 cost nothing: fp32 and
+  // bf16 both reach 2^127, and a row's weights keep their precision relative to
+  // each other. So O is never rescaled on the way; a row whose scores rise more
+  // than 2^LAZY above m (top says so at the end) is done again with m = top.
+  __device__ __forceinline__ void weights(f32x16_t& s) {
+    float t = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t = fmaxf(t, s[i]);
+    const u32x2_t x = swap_halves(__float_as_uint(t), __float_as_uint(t));
+    t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    top = fmaxf(top, t);
+    m = m == NEG_INF ? t : m;
+    const float mu = m == NEG_INF ? 0.0f : m;
+    float sum = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = exp2_hw(s[i] - mu);
+      sum += s[i];
+    }
+    l += sum;  // of this half's rows; the halves are added at the end
+  }
+
+  // P^T operands of the two 16-row steps: weights rounded to bf16 (each by half
+  // a unit of 2^-8 at most, independently, so the error of their sum averages out)
+  __device__ __forceinline__ static bf16x8_t p_frag(const f32x16_t& s, int c) {
+    const u32x4_t v = {pack_bf16x2(s[8 * c], s[8 * c + 1]), pack_bf16x2(s[8 * c + 2], s[8 * c + 3]),
+                       pack_bf16x2(s[8 * c + 4], s[8 * c + 5]), pack_bf16x2(s[8 * c + 6], s[8 * c + 7])};
+    return __builtin_bit_cast(bf16x8_t, v);
+  }
+
+  // The scores of a tile that ends the sequence or the chunk or holds drafts:
+  // rows not seen get -infinity. Their values may still be anything, and the
+  // product would make NaN of 0 times infinity, so this thread's share of the
+  // tile's values is looked over: if one is not finite, slow_rows() takes over.
+  __device__ __forceinline__ void mask(f32x16_t& s, const uint8_t* tile, int tk) {
+    uint32_t vis = visible(p, it, qt, qi, tk);
+    if (tk_end - tk < TILE) vis &= (1u << (tk_end - tk)) - 1;
+    vis >>= 4 * half;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = vis & (1u << (8 * (i / 4) + i % 4)) ? s[i] : NEG_INF;
+    const uint8_t* vals = tile + (SHARED ? 0 : S::NBK * BLK);
+#pragma unroll 1
+    for (int i = tid; i < DV * TILE / 8; i += S::THREADS) {  // 16 bytes each, in any order
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(vals + 16 * i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) odd |= not_finite_pair(v[k]);
+    }
+  }
+
+  // Tile i at `tile`: scores, weights, O^T += V^T P^T.
+  __device__ __forceinline__ void step(uint8_t* tile, int i, int full) {
+    if constexpr (S::WIDE) {
+      step_wide(tile, i, full);
+    } else {
+      f32x16_t s = scores(tile);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
+      if (__builtin_expect(i >= full, 0)) mask(s, tile, tk_begin + i * TILE);
+      weights(s);
+      const bf16x8_t p0 = p_frag(s, 0), p1 = p_frag(s, 1);
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n) {
+        o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 0)), p0, o[n]);
+        o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 1)), p1, o[n]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void step_wide(uint8_t* tile, int i, int full) {
+    const uint32_t at = lds_u32(tile);
+    f32x16_t s;
+    u32x4_t t[7];  // V's first fragments, in the quads where the blocks keep them
+    asm volatile(WIDE_SCORES_ASM
+                 : [s] "=&v"(s), "=&{v[240:243]}"(t[0]), "=&{v[244:247]}"(t[1]), "=&{v[248:251]}"(t[2]), "=&{v[252:255]}"(t[3]), "=&{v[224:227]}"(t[4]), "=&{v[228:231]}"(t[5]), "=&{v[232:235]}"(t[6])
+                 : [k0] "v"(at + koff[0]), [k1] "v"(at + koff[1]), [k2] "v"(at + koff[2]), [k3] "v"(at + koff[3]),
+                   [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]), [v10] "v"(at + voff[1][0]),
+                   [v11] "v"(at + voff[1][1]), [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]), [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]), [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]), [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]), [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]), [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]), [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
+                 : "memory", "v236", "v237", "v238", "v239");
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
+    if (__builtin_expect(i >= full, 0)) mask(s, tile, tk_begin + i * TILE);
+    weights(s);
+    const bf16x8_t p0 = p_frag(s, 0), p1 = p_frag(s, 1);
+    asm volatile(WIDE_VALUES_ASM
+                 : [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]), [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]), [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]), [o15] "+a"(o[15]),
+                   "+{v[240:243]}"(t[0]), "+{v[244:247]}"(t[1]), "+{v[248:251]}"(t[2]), "+{v[252:255]}"(t[3]), "+{v[224:227]}"(t[4]), "+{v[228:231]}"(t[5]), "+{v[232:235]}"(t[6])
+                 : [p0] "v"(p0), [p1] "v"(p1), [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]),
+                   [v10] "v"(at + voff[1][0]), [v11] "v"(at + voff[1][1])
+                 : "memory", "v236", "v237", "v238", "v239");
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < S::NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[n][i] = 0;
+    top = NEG_INF;
+    l = 0;
+    odd = false;
+  }
+
+  // All tiles of the chunk.
+  __device__ __forceinline__ void pass(int tiles, int full) {
+    clear();
+    if constexpr (!MX) {
+      constexpr int AHEAD = S::STAGES - 1;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (i < tiles) load_bf16(tk_begin + i * TILE, i);
+      int slot = 0, next = AHEAD;  // ring places of tile i and of tile i + AHEAD
+      for (int i = 0; i < tiles; ++i) {
+        if constexpr (AHEAD == 0) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the previous tile is read
+          load_bf16(tk_begin + i * TILE, 0);
+          vm_wait<0>();
+        } else {
+          // tile i has landed when only the AHEAD - 1 younger ones are under way;
+          // near the end there are fewer, so wait for all
+          if (i + AHEAD <= tiles) vm_wait<(AHEAD - 1) * S::LOADS>();
+          else vm_wait<0>();
+          barrier_reads_done();
+          if (i + AHEAD < tiles) load_bf16(tk_begin + (i + AHEAD) * TILE, next);
+        }
+        step(lds + slot * S::TILE_LDS, i, full);
+        slot = slot + 1 == S::STAGES ? 0 : slot + 1;
+        next = next + 1 == S::STAGES ? 0 : next + 1;
+      }
+    } else {
+      int slot = 0;
+      const int r = tid >> 3;
+      if constexpr (S::RPT == 1) load_mx(cache_row(tk_begin + r), r, code, sc);
+      for (int i = 0; i < tiles; ++i) {
+        if constexpr (S::RPT == 1) {
+          store_mx(r, slot, code, sc);
+          barrier_reads_done();  // (two slots: the one written next was read before this barrier)
+          if (i + 1 < tiles) load_mx(cache_row(tk_begin + (i + 1) * TILE + r), r, code, sc);
+        } else {
+          if constexpr (S::STAGES == 1) __syncthreads();
+#pragma unroll
+          for (int g = 0; g < S::RPT; ++g) {
+            const int rr = g * (8 * WAVES) + r;
+            uint2 cd[S::NB];
+            uint32_t sb[S::NB];
+            load_mx(cache_row(tk_begin + i * TILE + rr), rr, cd, sb);
+            store_mx(rr, slot, cd, sb);
+          }
+          __syncthreads();
+        }
+        step(lds + slot * S::TILE_LDS, i, full);
+        slot = slot + 1 == S::STAGES ? 0 : slot + 1;
+      }
+    }
+    if constexpr (S::WIDE)
+#pragma unroll
+      for (int n = 0; n < S::NT; ++n) asm volatile("" : "+a"(o[n]));  // O stays where it is up to here
+  }
+};
+
+// One element of a cache row (bf16, or E4M3 times its scale) in fp32.
+template <bool MX>
+__device__ __forceinline__ float cache_value(const PoolParams& pool, int b, int64_t row, int d, int c) {
+  if constexpr (!MX) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(pool.buf[b])[row * d + c]);
+  const uint32_t code = pool.buf[2 * b][row * d + c], sc = pool.buf[2 * b + 1][row * (d / 32) + c / 32];
+  if (sc == 0xFF) return __builtin_nanf("");
+  const uint32_t v = __builtin_bit_cast(
+      uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, __uint_as_float(sc ? sc << 23 : 0x00400000u), false));
+  return bf16_bits_to_f32(v & 0xFFFFu);
+}
+
+// The workgroup's rows without the matrix units, for chunks where a page id
+// lies outside the pool or a row must not see what another sees (an infinite
+// or NaN value: no weight keeps it out of a product). A wave takes its rows one
+// by one, a lane every 64th column; a row that is not seen is not looked at.
+// Writes what the fast path writes.
+template <int DK, int DV, bool SHARED, bool MX, int WAVES>
+__device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, const int* s_page, int page0, int tk_begin,
+                                       int tk_end) {
+  constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ps = p.pool.page_size;
+  const int64_t slot = ((((int64_t)it.j * p.H_kv + it.kvh) * p.plan.row_tiles + it.rt) * p.plan.chunks + it.chunk) * WAVES + wave;
+  for (int r32 = 0; r32 < 32; ++r32) {
+    const int row = (it.rt * WAVES + wave) * 32 + r32;
+    if (row >= it.rows) return;
+    const int qi = row / p.group, h = it.kvh * p.group + row - qi * p.group;
+    const int64_t qt = it.t0 + qi;
+    float q[NQ], o[NO], m = NEG_INF, l = 0;
+#pragma unroll
+    for (int k = 0; k < NQ; ++k)
+      q[k] = lane + 64 * k < DK ? bf16_bits_to_f32(p.q[qt * p.q_t + h * p.q_h + lane + 64 * k]) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < NO; ++k) o[k] = 0;
+    uint32_t vis = 0;
+    for (int tk = tk_begin; tk < tk_end; ++tk) {
+      if (((tk - tk_begin) & 31) == 0) vis = visible(p, it, qt, qi, tk);
+      if (!((vis >> ((tk - tk_begin) & 31)) & 1)) continue;
+      const int rel = tk - page0 * ps, pk = rel / ps;
+      const int64_t page = s_page[pk];
+      const int64_t crow = (max(page, (int64_t)0) * ps + rel - pk * ps) * p.H_kv + it.kvh;
+      float s = 0;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k)
+        if (lane + 64 * k < DK) s += q[k] * cache_value<MX>(p.pool, 0, crow, DK, lane + 64 * k);
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+      s = page < 0 ? __builtin_nanf("") : s * p.scale_log2;
+      const float mn = s > m || __builtin_isnan(s) ? s : m;  // NaN stays
+      const float f = m == NEG_INF ? 0.0f : exp2_hw(m - mn), w = s == NEG_INF ? 0.0f : exp2_hw(s - mn);
+      m = mn;
+      l = (f == 1.0f ? l : l * f) + w;
+#pragma unroll
+      for (int k = 0; k < NO; ++k)
+        if (lane + 64 * k < DV) {
+          const float v = cache_value<MX>(p.pool, SHARED ? 0 : 1, crow, SHARED ? DK : DV, lane + 64 * k);
+          o[k] = (f == 1.0f ? o[k] : m == NEG_INF ? 0.0f : o[k] * f) + w * v;
+        }
+    }
+    const float inv = l == 0 ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int k = 0; k < NO; ++k) {
+      const int c = lane + 64 * k;
+      if (c >= DV) continue;
+      if (it.chunks == 1)
+        p.out[qt * p.o_t + h * p.o_h + c] = (uint16_t)f32_to_bf16_bits(o[k] * inv);
+      else  // column 32 n + 8 g + 4 half + e
+        p.part_o[(slot * (DV * 8) + (c >> 3) * 64 + ((c >> 2) & 1) * 32 + r32) * 4 + (c & 3)] = o[k];
+    }
+    if (lane == 0) {
+      if (it.chunks > 1)
+        reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r32] = make_float2(m, l);
+      else if (p.lse)
+        p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    }
+  }
+}
 
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(1, DV > 256 ? 1 : 4)))
 void tree_attn_kernel(AttnParams p) {
   using S = Shape<DK, DV, SHARED, MX, WAVES>;
-  constexpr int THREADS = 64 * WAVES;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::STAGES * S::TILE_LDS];
   __shared__ int s_page[MAX_CHUNK_PAGES];
   __shared__ int s_bad;
   // consecutive items (row tiles that read the same chunk) go to one XCD's L2
   const int64_t per = gridDim.x / 8;
   Item it;
   if (!find_item(p, (blockIdx.x % 8) * per + blockIdx.x / 8, it)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l32 = lane & 31, half = lane >> 5;
   if (it.broken) {
     if (it.chunk == 0 && it.rt == 0) write_nan(p, it);
     return;
   }
+  Worker<DK, DV, SHARED, MX, WAVES> w(p, it);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l32 = lane & 31, half = lane >> 5;
+  w.tid = tid;
+  w.lane = lane;
+  w.wave = __builtin_amdgcn_readfirstlane(wave);
+  w.half = half;
   const int row0 = it.rt * 32 * WAVES;
   const int tk_begin = it.chunk * p.plan.chunk;
   const int tk_end = min(tk_begin + p.plan.chunk, it.total);
   if (row0 >= it.rows || tk_begin >= tk_end) return;
+  w.tk_begin = tk_begin;
+  w.tk_end = tk_end;
 
   // the chunk's pages
   const int ps = p.pool.page_size;
   const int page0 = tk_begin / ps, pages = (tk_end - 1) / ps - page0 + 1;
-  const int held = min(p.pool.held[it.seq], p.pool.max_pages);
+  w.page0 = page0;
+  const int held = min(__builtin_amdgcn_readfirstlane(p.pool.held[it.seq]), p.pool.max_pages);
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  for (int k = tid; k < pages; k += THREADS) {
+  for (int k = tid; k < pages; k += S::THREADS) {
     int id = page0 + k < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + page0 + k] : -1;
     if (id < 0 || id >= p.pool.num_pages) {
       id = -1;
@@ -164,187 +529,46 @@ void tree_attn_kernel(AttnParams p) {
   const int qi = live ? row / p.group : 0;
   const int64_t qt = it.t0 + qi;
   const int h = it.kvh * p.group + (live ? row - qi * p.group : 0);
-  bf16x8_t q[S::KK];
+  w.qt = qt;
+  w.qi = qi;
 #pragma unroll
   for (int kk = 0; kk < S::KK; ++kk)
-    q[kk] = *reinterpret_cast<const bf16x8_t*>(p.q + qt * p.q_t + h * p.q_h + 16 * kk + 8 * half);
-  f32x16_t o[S::NT];
-#pragma unroll
-  for (int n = 0; n < S::NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[n][i] = 0;
-  float m = NEG_INF, l = 0;
+    w.q[kk] = *reinterpret_cast<const bf16x8_t*>(p.q + qt * p.q_t + h * p.q_h + 16 * kk + 8 * half);
+  w.m = NEG_INF;
   __syncthreads();
-  const bool bad = s_bad;
-
+  const bool bad = __builtin_amdgcn_readfirstlane(s_bad);
+  w.lds = lds;
+  w.s_page = s_page;
   // LDS offsets: K fragment (row l32, chunk 2 (kk % 4) + half), V fragment
   // (rows 4 half + 0..3 of an 8-row group, 16 columns per 16 lanes)
-  int koff[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) koff[c] = l32 * 128 + (((2 * c + half) ^ swz(l32)) << 4);
+  for (int c = 0; c < 4; ++c) w.koff[c] = l32 * 128 + (((2 * c + half) ^ swz(l32)) << 4);
   const int q4 = lane & 15;
-  int voff[2][2];  // [row 8 group][column half of the block]
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int t = 8 * e + 4 * half + (q4 >> 2);
-      voff[e][c] = t * 128 + (((4 * c + 2 * ((lane >> 4) & 1) + ((q4 & 3) >> 1)) ^ swz(t)) << 4) + (q4 & 1) * 8;
+      w.voff[e][c] = t * 128 + (((4 * c + 2 * ((lane >> 4) & 1) + ((q4 & 3) >> 1)) ^ swz(t)) << 4) + (q4 & 1) * 8;
     }
-  const uint8_t* vlds = lds + (SHARED ? 0 : S::NBK * BLK);
 
-  for (int tk = tk_begin; tk < tk_end; tk += TILE) {
-    __syncthreads();  // the previous tile is read
-    // stage: 16-byte chunk c of row r of block b; rows behind the chunk's end are zeros
-    constexpr int CPR = DK / 8, VPR = SHARED ? 0 : DV / 8;  // 16-byte chunks per row
-    for (int i = tid; i < TILE * (CPR + VPR); i += THREADS) {
-      const bool isk = i < TILE * CPR;
-      const int ii = isk ? i : i - TILE * CPR;
-      const int cpr = isk ? CPR : VPR;
-      const int r = ii / cpr, c = ii - r * cpr;
-      const int tok = tk + r;
-      u32x4_t v = {0, 0, 0, 0};
-      if (tok < tk_end) {
-        const int rel = tok - page0 * ps;
-        const int pk = rel / ps;
-        const int64_t page = max(s_page[pk], 0);
-        const int in = rel - pk * ps;
-        const int d = isk ? DK : DV;
-        const int64_t crow = (page * ps + in) * p.H_kv + it.kvh;  // row of width d
-        if (!MX) {
-          v = *reinterpret_cast<const u32x4_t*>(p.pool.buf[isk ? 0 : 1] + (crow * d + 8 * c) * 2);
-        } else {
-          const uint2 code = *reinterpret_cast<const uint2*>(p.pool.buf[isk ? 0 : 2] + crow * d + 8 * c);
-          const uint32_t sb = p.pool.buf[isk ? 1 : 3][crow * (d / 32) + c / 4];
-          const float sc = __uint_as_float(sb ? sb << 23 : 0x00400000u);
-          v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, sc, false));
-          v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, sc, true));
-          v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, sc, false));
-          v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, sc, true));
-          if (sb == 0xFF) v = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
-        }
-      }
-      *reinterpret_cast<u32x4_t*>(lds + ((isk ? 0 : S::NBK) + c / 8) * BLK + r * 128 + (((c & 7) ^ swz(r)) << 4)) = v;
-    }
-    __syncthreads();
-    // S^T: element i is cache row 8 (i / 4) + 4 half + i % 4, column the lane's query
-    f32x16_t s;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0;
-#pragma unroll
-    for (int kk = 0; kk < S::KK; ++kk) {
-      const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(lds + (kk >> 2) * BLK + koff[kk & 3]);
-      s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[kk], s, 0, 0, 0);
-    }
-    const bool masked = bad || tk + TILE > it.len;  // else every row sees the whole tile
-    uint32_t vis = 0xFFFFFFFFu, nan_rows = 0;
-    if (masked) {
-      vis = visible(p, it, qt, qi, tk);
-      if (tk_end - tk < TILE) vis &= (1u << (tk_end - tk)) - 1;
-      if (bad)
-        for (int r = 0; r < TILE && tk + r < tk_end; ++r)
-          if (s_page[(tk + r - page0 * ps) / ps] < 0) nan_rows |= 1u << r;
-    }
-    float top = NEG_INF;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int b = 8 * (i / 4) + (i % 4);
-      s[i] *= p.scale_log2;
-      if (masked) {
-        const uint32_t bit = 1u << (b + 4 * half);
-        if (nan_rows & bit) s[i] = __builtin_nanf("");
-        if (!(vis & bit)) s[i] = NEG_INF;
-      }
-      top = fmaxf(top, s[i]);
-    }
-    {
-      const u32x2_t x = swap_halves(__float_as_uint(top), __float_as_uint(top));
-      top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-    }
-    // The maximum is raised only when a row's grew by more than 2^LAZY: weights
-    // stay below 2^LAZY, and O, 32 DV bits a row, is rarely rescaled.
-    if (__any(top > m + LAZY || (m == NEG_INF && top > NEG_INF))) {
-      const float mn = fmaxf(m, top);
-      const float f = mn == NEG_INF ? 1.0f : exp2_hw(m - mn);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int n = 0; n < S::NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[n][i] *= f;
-    }
-    const float mu = m == NEG_INF ? 0.0f : m;
-    float sum = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[i] = exp2_hw(s[i] - mu);
-      sum += s[i];
-    }
-    l += sum;  // of this half's rows; the halves are added at the end
-    // P^T for the two 16-row steps: weights rounded to bf16 (half a unit in
-    // 2^-8 each, independent of each other, so the sum's error averages out)
-    bf16x8_t pt[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const u32x4_t v = {pack_bf16x2(s[8 * c], s[8 * c + 1]), pack_bf16x2(s[8 * c + 2], s[8 * c + 3]),
-                         pack_bf16x2(s[8 * c + 4], s[8 * c + 5]), pack_bf16x2(s[8 * c + 6], s[8 * c + 7])};
-      pt[c] = __builtin_bit_cast(bf16x8_t, v);
-    }
-    uint32_t odd = 0;  // non-finite values in a tile that some rows do not see
-#pragma unroll
-    for (int n = 0; n < S::NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-        const uint8_t* base = vlds + (n >> 1) * BLK + c * 16 * 128;
-        const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[0][n & 1]));
-        const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[1][n & 1]));
-        const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
-        u32x4_t v = {ua.x, ua.y, ub.x, ub.y};
-        if (masked)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t f = finite_pair(v[k]);
-            odd |= f ^ v[k];
-            v[k] = f;
-          }
-        o[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), pt[c], o[n], 0, 0, 0);
-      }
-    if (__any(odd)) {
-      // the non-finite values by themselves: counts of +inf, -inf and NaN among
-      // the rows seen, in one sum (at most 32 of each), then added as such
-      u32x4_t one[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int b0 = 8 * ((8 * c + 2 * k) / 4) + (2 * k) % 4 + 4 * half;
-          one[c][k] = ((vis >> b0) & 1 ? 0x3F80u : 0) | ((vis >> (b0 + 1)) & 1 ? 0x3F800000u : 0);
-        }
-#pragma unroll
-      for (int n = 0; n < S::NT; ++n) {
-        f32x16_t cnt;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) cnt[i] = 0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-          const uint8_t* base = vlds + (n >> 1) * BLK + c * 16 * 128;
-          const uint2 ua = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[0][n & 1])));
-          const uint2 ub = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[1][n & 1])));
-          const u32x4_t v = {code_pair(ua.x), code_pair(ua.y), code_pair(ub.x), code_pair(ub.y)};
-          cnt = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, one[c]), cnt, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t k = (uint32_t)cnt[i];
-          if (k >= 4096 || ((k & 63) && (k & 4032))) o[n][i] = __builtin_nanf("");
-          else if (k & 63) o[n][i] += __builtin_huge_valf();
-          else if (k) o[n][i] -= __builtin_huge_valf();
-        }
-      }
-    }
+  const int tiles = (tk_end - tk_begin + TILE - 1) / TILE;
+  // tiles before the first draft and wholly inside the chunk need no mask
+  const int full = max(0, (min(tk_end, it.len) - tk_begin) / TILE);
+  bool slow = bad;
+  while (!slow) {
+    w.pass(tiles, full);
+    slow = __syncthreads_or(w.odd);
+    // (the barriers also end all reads of LDS before a second pass loads)
+    if (__builtin_expect(!__syncthreads_or(w.top > w.m + LAZY), 1)) break;
+    w.m = w.top;  // the largest score of all: the next pass is the last
   }
+  if (__builtin_expect(slow, 0)) {
+    slow_rows<DK, DV, SHARED, MX, WAVES>(p, it, s_page, page0, tk_begin, tk_end);
+    return;
+  }
+  const float m = w.m;
+  float l = w.l;
   {
     const u32x2_t x = swap_halves(__float_as_uint(l), __float_as_uint(l));
     l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
@@ -358,8 +582,8 @@ void tree_attn_kernel(AttnParams p) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * half) =
-              make_uint2(pack_bf16x2(o[n][4 * g] * inv, o[n][4 * g + 1] * inv),
-                         pack_bf16x2(o[n][4 * g + 2] * inv, o[n][4 * g + 3] * inv));
+              make_uint2(pack_bf16x2(w.o[n][4 * g] * inv, w.o[n][4 * g + 1] * inv),
+                         pack_bf16x2(w.o[n][4 * g + 2] * inv, w.o[n][4 * g + 3] * inv));
       if (p.lse && half == 0)
         p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
     }
@@ -372,7 +596,7 @@ void tree_attn_kernel(AttnParams p) {
   for (int n = 0; n < S::NT; ++n)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      po[(n * 4 + g) * 64 + lane] = f32x4_t{o[n][4 * g], o[n][4 * g + 1], o[n][4 * g + 2], o[n][4 * g + 3]};
+      po[(n * 4 + g) * 64 + lane] = f32x4_t{w.o[n][4 * g], w.o[n][4 * g + 1], w.o[n][4 * g + 2], w.o[n][4 * g + 3]};
   if (half == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + l32] = make_float2(m, l);
 }
 
