@@ -197,6 +197,21 @@ struct Worker {
     }
   }
 
+  // The loads of a later tile that step_wide issues between its MFMAs: in a
+  // burst in front of them they kept the matrix units waiting.
+  struct Next {
+    const uint8_t* src = nullptr;
+    uint32_t to = 0;
+    bool live = false;
+  };
+  static constexpr bool SPREAD = S::WIDE && !MX && S::RPT == 1;
+
+  __device__ __forceinline__ Next next_loads(int tk, int slot) const {
+    const int r = tid >> 3;
+    return Next{p.pool.buf[0] + (cache_row(tk + r) * DK + 8 * chunk_of(r, 0)) * 2,
+                (uint32_t)__builtin_amdgcn_readfirstlane(lds_u32(lds) + slot * S::TILE_LDS + wave * 1024), true};
+  }
+
   __device__ __forceinline__ void load_mx(int64_t row, int r, uint2* cd, uint32_t* sb) const {
 #pragma unroll
     for (int b = 0; b < S::NB; ++b) {
@@ -292,9 +307,9 @@ struct Worker {
   }
 
   // Tile i at `tile`: scores, weights, O^T += V^T P^T.
-  __device__ __forceinline__ void step(uint8_t* tile, int i, int full) {
+  __device__ __forceinline__ void step(uint8_t* tile, int i, int full, const Next& next) {
     if constexpr (S::WIDE) {
-      step_wide(tile, i, full);
+      step_wide(tile, i, full, next);
     } else {
       f32x16_t s = scores(tile);
 #pragma unroll
@@ -310,16 +325,25 @@ struct Worker {
     }
   }
 
-  __device__ __forceinline__ void step_wide(uint8_t* tile, int i, int full) {
+  __device__ __forceinline__ void step_wide(uint8_t* tile, int i, int full, const Next& next) {
     const uint32_t at = lds_u32(tile);
     f32x16_t s;
     u32x4_t t[7];  // V's first fragments, in the quads where the blocks keep them
-    asm volatile(WIDE_SCORES_ASM
-                 : [s] "=&v"(s), "=&{v[240:243]}"(t[0]), "=&{v[244:247]}"(t[1]), "=&{v[248:251]}"(t[2]), "=&{v[252:255]}"(t[3]), "=&{v[224:227]}"(t[4]), "=&{v[228:231]}"(t[5]), "=&{v[232:235]}"(t[6])
-                 : [k0] "v"(at + koff[0]), [k1] "v"(at + koff[1]), [k2] "v"(at + koff[2]), [k3] "v"(at + koff[3]),
-                   [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]), [v10] "v"(at + voff[1][0]),
-                   [v11] "v"(at + voff[1][1]), [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]), [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]), [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]), [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]), [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]), [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]), [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
-                 : "memory", "v236", "v237", "v238", "v239");
+    if (next.live) {
+      asm volatile(WIDE_SCORES_LOAD_ASM
+                   : [s] "=&v"(s), "=&{v[240:243]}"(t[0]), "=&{v[244:247]}"(t[1]), "=&{v[248:251]}"(t[2]), "=&{v[252:255]}"(t[3]), "=&{v[224:227]}"(t[4]), "=&{v[228:231]}"(t[5]), "=&{v[232:235]}"(t[6])
+                   : [k0] "v"(at + koff[0]), [k1] "v"(at + koff[1]), [k2] "v"(at + koff[2]), [k3] "v"(at + koff[3]),
+                     [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]), [v10] "v"(at + voff[1][0]),
+                     [v11] "v"(at + voff[1][1]), [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]), [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]), [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]), [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]), [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]), [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]), [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35]), [src] "v"(next.src), [to] "s"(next.to)
+                   : "memory", "v236", "v237", "v238", "v239", "m0", "scc");
+    } else {
+      asm volatile(WIDE_SCORES_ASM
+                   : [s] "=&v"(s), "=&{v[240:243]}"(t[0]), "=&{v[244:247]}"(t[1]), "=&{v[248:251]}"(t[2]), "=&{v[252:255]}"(t[3]), "=&{v[224:227]}"(t[4]), "=&{v[228:231]}"(t[5]), "=&{v[232:235]}"(t[6])
+                   : [k0] "v"(at + koff[0]), [k1] "v"(at + koff[1]), [k2] "v"(at + koff[2]), [k3] "v"(at + koff[3]),
+                     [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]), [v10] "v"(at + voff[1][0]),
+                     [v11] "v"(at + voff[1][1]), [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]), [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]), [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]), [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]), [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]), [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]), [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
+                   : "memory", "v236", "v237", "v238", "v239");
+    }
 #pragma unroll
     for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
     if (__builtin_expect(i >= full, 0)) mask(s, tile, tk_begin + i * TILE);
@@ -353,6 +377,7 @@ struct Worker {
         if (i < tiles) load_bf16(tk_begin + i * TILE, i);
       int slot = 0, next = AHEAD;  // ring places of tile i and of tile i + AHEAD
       for (int i = 0; i < tiles; ++i) {
+        Next loads;
         if constexpr (AHEAD == 0) {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the previous tile is read
           load_bf16(tk_begin + i * TILE, 0);
@@ -363,9 +388,12 @@ struct Worker {
           if (i + AHEAD <= tiles) vm_wait<(AHEAD - 1) * S::LOADS>();
           else vm_wait<0>();
           barrier_reads_done();
-          if (i + AHEAD < tiles) load_bf16(tk_begin + (i + AHEAD) * TILE, next);
+          if (i + AHEAD < tiles) {
+            if constexpr (SPREAD) loads = next_loads(tk_begin + (i + AHEAD) * TILE, next);
+            else load_bf16(tk_begin + (i + AHEAD) * TILE, next);
+          }
         }
-        step(lds + slot * S::TILE_LDS, i, full);
+        step(lds + slot * S::TILE_LDS, i, full, loads);
         slot = slot + 1 == S::STAGES ? 0 : slot + 1;
         next = next + 1 == S::STAGES ? 0 : next + 1;
       }
@@ -390,7 +418,7 @@ struct Worker {
           }
           __syncthreads();
         }
-        step(lds + slot * S::TILE_LDS, i, full);
+        step(lds + slot * S::TILE_LDS, i, full, Next{});
         slot = slot + 1 == S::STAGES ? 0 : slot + 1;
       }
     }

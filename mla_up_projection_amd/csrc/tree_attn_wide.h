@@ -145,6 +145,154 @@ namespace mla {
   "s_nop 15\n\t" \
   "s_nop 1\n\t"
 
+// The same with the loads of a later tile's 16 bytes a lane of each 64-column
+// block spread over the MFMAs (src: the lane's bytes of block 0, to: the LDS
+// address of its wave's part; an instruction's offset counts for both).
+#define WIDE_SCORES_LOAD_ASM \
+  "ds_read_b128 v[224:227], %[k0] offset:0\n\t" \
+  "ds_read_b128 v[228:231], %[k1] offset:0\n\t" \
+  "ds_read_b128 v[232:235], %[k2] offset:0\n\t" \
+  "ds_read_b128 v[236:239], %[k3] offset:0\n\t" \
+  "ds_read_b128 v[240:243], %[k0] offset:4096\n\t" \
+  "ds_read_b128 v[244:247], %[k1] offset:4096\n\t" \
+  "ds_read_b128 v[248:251], %[k2] offset:4096\n\t" \
+  "ds_read_b128 v[252:255], %[k3] offset:4096\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[224:227], %[q0], 0\n\t" \
+  "ds_read_b128 v[224:227], %[k0] offset:8192\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[228:231], %[q1], %[s]\n\t" \
+  "ds_read_b128 v[228:231], %[k1] offset:8192\n\t" \
+  "s_add_u32 m0, %[to], 0\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:0\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[232:235], %[q2], %[s]\n\t" \
+  "ds_read_b128 v[232:235], %[k2] offset:8192\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[236:239], %[q3], %[s]\n\t" \
+  "ds_read_b128 v[236:239], %[k3] offset:8192\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[240:243], %[q4], %[s]\n\t" \
+  "ds_read_b128 v[240:243], %[k0] offset:12288\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[244:247], %[q5], %[s]\n\t" \
+  "ds_read_b128 v[244:247], %[k1] offset:12288\n\t" \
+  "s_add_u32 m0, %[to], 3968\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:128\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[248:251], %[q6], %[s]\n\t" \
+  "ds_read_b128 v[248:251], %[k2] offset:12288\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[252:255], %[q7], %[s]\n\t" \
+  "ds_read_b128 v[252:255], %[k3] offset:12288\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[224:227], %[q8], %[s]\n\t" \
+  "ds_read_b128 v[224:227], %[k0] offset:16384\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[228:231], %[q9], %[s]\n\t" \
+  "ds_read_b128 v[228:231], %[k1] offset:16384\n\t" \
+  "s_add_u32 m0, %[to], 7936\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:256\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[232:235], %[q10], %[s]\n\t" \
+  "ds_read_b128 v[232:235], %[k2] offset:16384\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[236:239], %[q11], %[s]\n\t" \
+  "ds_read_b128 v[236:239], %[k3] offset:16384\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[240:243], %[q12], %[s]\n\t" \
+  "ds_read_b128 v[240:243], %[k0] offset:20480\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[244:247], %[q13], %[s]\n\t" \
+  "ds_read_b128 v[244:247], %[k1] offset:20480\n\t" \
+  "s_add_u32 m0, %[to], 11904\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:384\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[248:251], %[q14], %[s]\n\t" \
+  "ds_read_b128 v[248:251], %[k2] offset:20480\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[252:255], %[q15], %[s]\n\t" \
+  "ds_read_b128 v[252:255], %[k3] offset:20480\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[224:227], %[q16], %[s]\n\t" \
+  "ds_read_b128 v[224:227], %[k0] offset:24576\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[228:231], %[q17], %[s]\n\t" \
+  "ds_read_b128 v[228:231], %[k1] offset:24576\n\t" \
+  "s_add_u32 m0, %[to], 15872\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:512\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[232:235], %[q18], %[s]\n\t" \
+  "ds_read_b128 v[232:235], %[k2] offset:24576\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[236:239], %[q19], %[s]\n\t" \
+  "ds_read_b128 v[236:239], %[k3] offset:24576\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[240:243], %[q20], %[s]\n\t" \
+  "ds_read_b128 v[240:243], %[k0] offset:28672\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[244:247], %[q21], %[s]\n\t" \
+  "ds_read_b128 v[244:247], %[k1] offset:28672\n\t" \
+  "s_add_u32 m0, %[to], 19840\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:640\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[248:251], %[q22], %[s]\n\t" \
+  "ds_read_b128 v[248:251], %[k2] offset:28672\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[252:255], %[q23], %[s]\n\t" \
+  "ds_read_b128 v[252:255], %[k3] offset:28672\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[224:227], %[q24], %[s]\n\t" \
+  "ds_read_b128 v[224:227], %[k0] offset:32768\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[228:231], %[q25], %[s]\n\t" \
+  "ds_read_b128 v[228:231], %[k1] offset:32768\n\t" \
+  "s_add_u32 m0, %[to], 23808\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:768\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[232:235], %[q26], %[s]\n\t" \
+  "ds_read_b128 v[232:235], %[k2] offset:32768\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[236:239], %[q27], %[s]\n\t" \
+  "ds_read_b128 v[236:239], %[k3] offset:32768\n\t" \
+  "s_waitcnt lgkmcnt(7)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[240:243], %[q28], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[240:241], %[v00] offset:0\n\t" \
+  "ds_read_b64_tr_b16 v[242:243], %[v10] offset:0\n\t" \
+  "s_waitcnt lgkmcnt(8)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[244:247], %[q29], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[244:245], %[v00] offset:2048\n\t" \
+  "ds_read_b64_tr_b16 v[246:247], %[v10] offset:2048\n\t" \
+  "s_add_u32 m0, %[to], 27776\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:896\n\t" \
+  "s_waitcnt lgkmcnt(9)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[248:251], %[q30], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[248:249], %[v01] offset:0\n\t" \
+  "ds_read_b64_tr_b16 v[250:251], %[v11] offset:0\n\t" \
+  "s_waitcnt lgkmcnt(10)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[252:255], %[q31], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[252:253], %[v01] offset:2048\n\t" \
+  "ds_read_b64_tr_b16 v[254:255], %[v11] offset:2048\n\t" \
+  "s_waitcnt lgkmcnt(11)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[224:227], %[q32], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[224:225], %[v00] offset:4096\n\t" \
+  "ds_read_b64_tr_b16 v[226:227], %[v10] offset:4096\n\t" \
+  "s_waitcnt lgkmcnt(12)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[228:231], %[q33], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[228:229], %[v00] offset:6144\n\t" \
+  "ds_read_b64_tr_b16 v[230:231], %[v10] offset:6144\n\t" \
+  "s_add_u32 m0, %[to], 31744\n\t" \
+  "global_load_lds_dwordx4 %[src], off offset:1024\n\t" \
+  "s_waitcnt lgkmcnt(13)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[232:235], %[q34], %[s]\n\t" \
+  "ds_read_b64_tr_b16 v[232:233], %[v01] offset:4096\n\t" \
+  "ds_read_b64_tr_b16 v[234:235], %[v11] offset:4096\n\t" \
+  "s_waitcnt lgkmcnt(14)\n\t" \
+  "v_mfma_f32_32x32x16_bf16 %[s], v[236:239], %[q35], %[s]\n\t" \
+  "s_waitcnt lgkmcnt(0)\n\t" \
+  "s_nop 15\n\t" \
+  "s_nop 1\n\t"
+
 // O^T (o0..o15) += V^T P^T (p0, p1), V's first fragments being in their quads.
 #define WIDE_VALUES_ASM \
   "s_nop 1\n\t" \
