@@ -197,19 +197,19 @@ struct Worker {
     }
   }
 
-  // The loads of a later tile that step_wide issues between its MFMAs: in a
+  // The loads of a later tile that step_ahead issues between its MFMAs: in a
   // burst in front of them they kept the matrix units waiting.
   struct Next {
     const uint8_t* src = nullptr;
     uint32_t to = 0;
-    bool live = false;
+    uint64_t live = 0;  // lanes that load
   };
-  static constexpr bool SPREAD = S::WIDE && !MX && S::RPT == 1;
+  static constexpr bool SPREAD = S::WIDE && !MX && S::STAGES == 4;
 
   __device__ __forceinline__ Next next_loads(int tk, int slot) const {
     const int r = tid >> 3;
     return Next{p.pool.buf[0] + (cache_row(tk + r) * DK + 8 * chunk_of(r, 0)) * 2,
-                (uint32_t)__builtin_amdgcn_readfirstlane(lds_u32(lds) + slot * S::TILE_LDS + wave * 1024), true};
+                (uint32_t)__builtin_amdgcn_readfirstlane(lds_u32(lds) + slot * S::TILE_LDS + wave * 1024), ~(uint64_t)0};
   }
 
   __device__ __forceinline__ void load_mx(int64_t row, int r, uint2* cd, uint32_t* sb) const {
@@ -245,14 +245,32 @@ struct Worker {
     return u32x4_t{a.x, a.y, b.x, b.y};
   }
 
-  // S^T: element i is cache row 8 (i / 4) + 4 half + i % 4, column the lane's query
+  // S^T times the scale: element i is cache row 8 (i / 4) + 4 half + i % 4,
+  // column the lane's query
   __device__ __forceinline__ f32x16_t scores(const uint8_t* tile) const {
     f32x16_t s;
+    if constexpr (S::WIDE) {
+      const uint32_t k = lds_u32(tile);
+      asm volatile(WIDE_SCORES
+                   : [s] "=&v"(s)
+                   : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
+                     [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
+                     [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
+                     [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
+                     [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]),
+                     [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]),
+                     [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]),
+                     [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
+                   : "memory", WIDE_CLOBBERS);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0;
+      for (int i = 0; i < 16; ++i) s[i] = 0;
 #pragma unroll
-    for (int kk = 0; kk < S::KK; ++kk)
-      s = mfma(*reinterpret_cast<const bf16x8_t*>(tile + (kk >> 2) * BLK + koff[kk & 3]), q[kk], s);
+      for (int kk = 0; kk < S::KK; ++kk)
+        s = mfma(*reinterpret_cast<const bf16x8_t*>(tile + (kk >> 2) * BLK + koff[kk & 3]), q[kk], s);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
     return s;
   }
 
@@ -306,17 +324,21 @@ struct Worker {
     }
   }
 
-  // Tile i at `tile`: scores, weights, O^T += V^T P^T.
-  __device__ __forceinline__ void step(uint8_t* tile, int i, int full, const Next& next) {
+  // O^T += V^T P^T for a tile at `tile` with weights s
+  __device__ __forceinline__ void values(const uint8_t* tile, const f32x16_t& s) {
+    const bf16x8_t p0 = p_frag(s, 0), p1 = p_frag(s, 1);
     if constexpr (S::WIDE) {
-      step_wide(tile, i, full, next);
+      const uint32_t v = lds_u32(tile);
+      asm volatile(WIDE_VALUES
+                   :
+                     [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]),
+                     [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
+                     [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
+                     [o15] "+a"(o[15])
+                   : [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
+                     [v11] "v"(v + voff[1][1]), [p0] "v"(p0), [p1] "v"(p1)
+                   : "memory", WIDE_CLOBBERS);
     } else {
-      f32x16_t s = scores(tile);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
-      if (__builtin_expect(i >= full, 0)) mask(s, tile, tk_begin + i * TILE);
-      weights(s);
-      const bf16x8_t p0 = p_frag(s, 0), p1 = p_frag(s, 1);
 #pragma unroll
       for (int n = 0; n < S::NT; ++n) {
         o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 0)), p0, o[n]);
@@ -325,36 +347,36 @@ struct Worker {
     }
   }
 
-  __device__ __forceinline__ void step_wide(uint8_t* tile, int i, int full, const Next& next) {
-    const uint32_t at = lds_u32(tile);
-    f32x16_t s;
-    u32x4_t t[7];  // V's first fragments, in the quads where the blocks keep them
-    if (next.live) {
-      asm volatile(WIDE_SCORES_LOAD_ASM
-                   : [s] "=&v"(s), "=&{v[240:243]}"(t[0]), "=&{v[244:247]}"(t[1]), "=&{v[248:251]}"(t[2]), "=&{v[252:255]}"(t[3]), "=&{v[224:227]}"(t[4]), "=&{v[228:231]}"(t[5]), "=&{v[232:235]}"(t[6])
-                   : [k0] "v"(at + koff[0]), [k1] "v"(at + koff[1]), [k2] "v"(at + koff[2]), [k3] "v"(at + koff[3]),
-                     [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]), [v10] "v"(at + voff[1][0]),
-                     [v11] "v"(at + voff[1][1]), [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]), [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]), [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]), [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]), [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]), [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]), [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35]), [src] "v"(next.src), [to] "s"(next.to)
-                   : "memory", "v236", "v237", "v238", "v239", "m0", "scc");
-    } else {
-      asm volatile(WIDE_SCORES_ASM
-                   : [s] "=&v"(s), "=&{v[240:243]}"(t[0]), "=&{v[244:247]}"(t[1]), "=&{v[248:251]}"(t[2]), "=&{v[252:255]}"(t[3]), "=&{v[224:227]}"(t[4]), "=&{v[228:231]}"(t[5]), "=&{v[232:235]}"(t[6])
-                   : [k0] "v"(at + koff[0]), [k1] "v"(at + koff[1]), [k2] "v"(at + koff[2]), [k3] "v"(at + koff[3]),
-                     [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]), [v10] "v"(at + voff[1][0]),
-                     [v11] "v"(at + voff[1][1]), [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]), [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]), [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]), [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]), [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]), [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]), [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
-                   : "memory", "v236", "v237", "v238", "v239");
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
+  // Tile i at `tile` by itself: scores, weights, O^T += V^T P^T.
+  __device__ __forceinline__ void step(uint8_t* tile, int i, int full) {
+    f32x16_t s = scores(tile);
     if (__builtin_expect(i >= full, 0)) mask(s, tile, tk_begin + i * TILE);
     weights(s);
-    const bf16x8_t p0 = p_frag(s, 0), p1 = p_frag(s, 1);
-    asm volatile(WIDE_VALUES_ASM
-                 : [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]), [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]), [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]), [o15] "+a"(o[15]),
-                   "+{v[240:243]}"(t[0]), "+{v[244:247]}"(t[1]), "+{v[248:251]}"(t[2]), "+{v[252:255]}"(t[3]), "+{v[224:227]}"(t[4]), "+{v[228:231]}"(t[5]), "+{v[232:235]}"(t[6])
-                 : [p0] "v"(p0), [p1] "v"(p1), [v00] "v"(at + voff[0][0]), [v01] "v"(at + voff[0][1]),
-                   [v10] "v"(at + voff[1][0]), [v11] "v"(at + voff[1][1])
-                 : "memory", "v236", "v237", "v238", "v239");
+    values(tile, s);
+  }
+
+  // Softmax and value products of the tile at `tile` (scores s), scores of the
+  // one at `ahead` into s, and the loads of a later one.
+  __device__ __forceinline__ void step_ahead(const uint8_t* tile, const uint8_t* ahead, f32x16_t& s, const Next& next) {
+    const uint32_t k = lds_u32(ahead), v = lds_u32(tile);
+    float t0, t1;
+    asm volatile(WIDE_STEP
+                 : [s] "+{v[192:207]}"(s), [m] "+v"(m), [top] "+v"(top), [l] "+v"(l), [t0] "=&v"(t0), [t1] "=&v"(t1),
+                   [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]),
+                   [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
+                   [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
+                   [o15] "+a"(o[15])
+                 : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
+                   [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
+                   [v11] "v"(v + voff[1][1]), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
+                   [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
+                   [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
+                   [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
+                   [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]),
+                   [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]),
+                   [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]),
+                   [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
+                 : "memory", "vcc", "scc", "m0", "v184", "v185", "v186", "v187", "v188", "v189", "v190", "v191", WIDE_CLOBBERS);
   }
 
   __device__ __forceinline__ void clear() {
@@ -376,26 +398,44 @@ struct Worker {
       for (int i = 0; i < AHEAD; ++i)
         if (i < tiles) load_bf16(tk_begin + i * TILE, i);
       int slot = 0, next = AHEAD;  // ring places of tile i and of tile i + AHEAD
-      for (int i = 0; i < tiles; ++i) {
-        Next loads;
-        if constexpr (AHEAD == 0) {
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the previous tile is read
-          load_bf16(tk_begin + i * TILE, 0);
-          vm_wait<0>();
-        } else {
-          // tile i has landed when only the AHEAD - 1 younger ones are under way;
-          // near the end there are fewer, so wait for all
-          if (i + AHEAD <= tiles) vm_wait<(AHEAD - 1) * S::LOADS>();
-          else vm_wait<0>();
+      if constexpr (SPREAD) {
+        // Tiles i and i + 1 are in LDS, i + 2 under way and i + 3 asked for
+        // during step i, into the place of i - 1, which all have left when
+        // they meet at the barrier.
+        if (tiles > 2) vm_wait<2 * S::LOADS>();
+        else vm_wait<0>();
+        barrier_reads_done();
+        f32x16_t s = scores(lds);
+        for (int i = 0; i < tiles; ++i) {
+          Next loads;
+          const int after = slot + 1 == S::STAGES ? 0 : slot + 1;
+          vm_wait<S::LOADS>();
           barrier_reads_done();
-          if (i + AHEAD < tiles) {
-            if constexpr (SPREAD) loads = next_loads(tk_begin + (i + AHEAD) * TILE, next);
-            else load_bf16(tk_begin + (i + AHEAD) * TILE, next);
-          }
+          if (i + AHEAD < tiles) loads = next_loads(tk_begin + (i + AHEAD) * TILE, next);
+          if (__builtin_expect(i >= full, 0)) mask(s, lds + slot * S::TILE_LDS, tk_begin + i * TILE);
+          // (behind the last tile the scores of what lies there are not used)
+          step_ahead(lds + slot * S::TILE_LDS, lds + after * S::TILE_LDS, s, loads);
+          slot = after;
+          next = next + 1 == S::STAGES ? 0 : next + 1;
         }
-        step(lds + slot * S::TILE_LDS, i, full, loads);
-        slot = slot + 1 == S::STAGES ? 0 : slot + 1;
-        next = next + 1 == S::STAGES ? 0 : next + 1;
+      } else {
+        for (int i = 0; i < tiles; ++i) {
+          if constexpr (AHEAD == 0) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the previous tile is read
+            load_bf16(tk_begin + i * TILE, 0);
+            vm_wait<0>();
+          } else {
+            // tile i has landed when only the AHEAD - 1 younger ones are under way;
+            // near the end there are fewer, so wait for all
+            if (i + AHEAD <= tiles) vm_wait<(AHEAD - 1) * S::LOADS>();
+            else vm_wait<0>();
+            barrier_reads_done();
+            if (i + AHEAD < tiles) load_bf16(tk_begin + (i + AHEAD) * TILE, next);
+          }
+          step(lds + slot * S::TILE_LDS, i, full);
+          slot = slot + 1 == S::STAGES ? 0 : slot + 1;
+          next = next + 1 == S::STAGES ? 0 : next + 1;
+        }
       }
     } else {
       int slot = 0;
@@ -418,13 +458,14 @@ struct Worker {
           }
           __syncthreads();
         }
-        step(lds + slot * S::TILE_LDS, i, full, Next{});
+        step(lds + slot * S::TILE_LDS, i, full);
         slot = slot + 1 == S::STAGES ? 0 : slot + 1;
       }
     }
-    if constexpr (S::WIDE)
+    if constexpr (S::WIDE) {  // O stays where it is up to here
 #pragma unroll
-      for (int n = 0; n < S::NT; ++n) asm volatile("" : "+a"(o[n]));  // O stays where it is up to here
+      for (int n = 0; n < S::NT; ++n) asm volatile("" : "+a"(o[n]));
+    }
   }
 };
 
