@@ -514,6 +514,8 @@ MLA_API mla_status mla_kv_rope_paged(const mla_kv_paged_args* args, void* stream
  * Widths (D_k, D_v): latent cache (no value buffer, value = the key's first
  * D_v elements): (576, 512), (96, 64); with values: (192, 128), (128, 128),
  * (64, 64). Others: MLA_EUNSUPPORTED. bf16 or MXFP8 cache; queries are bf16.
+ * A 576-wide MXFP8 cache must hold an even number of rows (num_pages *
+ * page_size * H_kv): its scale buffer is read in words of 4 bytes.
  * A sequence that outgrows max_q or max_len, and a page id outside the pool,
  * give NaN in the rows concerned, never a read out of bounds. Query rows
  * behind cu_q[nseq] are left as they are. */

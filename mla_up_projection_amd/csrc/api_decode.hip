@@ -377,7 +377,7 @@ AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int m
   (void)d_k;
   AttnPlan pl{};
   const int64_t rows = (int64_t)max_q * (H / H_kv);
-  pl.waves = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+  pl.waves = rows <= 32 && d_v <= 256 ? 1 : rows <= 64 && d_v <= 256 ? 2 : 4;
   const int64_t tiles = (rows + 32 * pl.waves - 1) / (32 * pl.waves);
   pl.row_tiles = (int)std::min<int64_t>(tiles, INT32_MAX);
   const int64_t units = std::max<int64_t>(1, (int64_t)nseq * H_kv * tiles);
@@ -415,6 +415,9 @@ mla_status check_attn(const mla_tree_attn_args* a, mla::AttnPlan* plan) {
   const bool shared = a->pool->nbuf == (a->cache_dtype == MLA_DTYPE_MXFP8 ? 2 : 1);
   if (!mla::attn_shape_supported(a->d_k, a->d_v, shared)) return MLA_EUNSUPPORTED;
   if ((st = check_cache(a->pool, a->cache_dtype, a->H_kv, a->d_k, shared ? 0 : a->d_v))) return st;
+  // scale rows of 18 bytes are read in aligned words: none may reach behind the buffer
+  if (a->cache_dtype == MLA_DTYPE_MXFP8 && a->d_k == 576 && a->pool->num_pages * a->pool->page_bytes[1] % 4)
+    return MLA_EINVAL;
   if ((int64_t)a->max_q * (a->H / a->H_kv) > INT32_MAX / 2) return MLA_EINVAL;
   *plan = mla::plan_attn(a->T, a->nseq, a->H, a->H_kv, a->d_k, a->d_v, a->max_q, a->max_len, a->pool->page_size);
   // grids stay within 2^31 workgroups' work-items

@@ -108,8 +108,10 @@ __device__ __forceinline__ bool not_finite_pair(uint32_t v) {
 }
 
 // Sizes of a kernel variant. A workgroup has WAVES waves of 32 query rows each
-// and a ring of STAGES tiles in LDS: four waves keep as many tiles as fit 160
-// KB; one and two waves keep one and two, so that four waves' worth of
+// and a ring of STAGES tiles in LDS. The widest shape always has four waves, one
+// to a SIMD: waves without rows only help to load (with one wave of rows a CU
+// still takes a tile in less time than HBM delivers it). The others: four waves
+// keep three or four tiles, two waves two and one wave one, so that several
 // workgroups share a CU and hide each other's loads.
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 struct Shape {
@@ -119,7 +121,10 @@ struct Shape {
   static constexpr int KK = DK / 16, NT = DV / 32;
   static constexpr int TILE_LDS = NB * BLK;
   static constexpr bool WIDE = DK == 576 && DV == 512;  // the products are written out (tree_attn_wide.h)
-  static constexpr int STAGES = MX ? (WAVES == 1 ? 1 : 2) : WAVES == 4 ? (NB > 5 ? 4 : 3) : WAVES;
+  static constexpr int STAGES = WIDE ? (MX ? 3 : 4) : MX ? (WAVES == 1 ? 1 : 2) : WAVES == 4 ? (NB > 5 ? 4 : 3) : WAVES;
+  // WIDE MXFP8, two places each: codes of a tile, 4.5 blocks of 128 bytes a row, and scales, five words a row
+  static constexpr int RAW_LDS = 5 * BLK, SCALE_LDS = TILE * 20;
+  static constexpr int LDS = STAGES * TILE_LDS + (WIDE && MX ? 2 * (RAW_LDS + SCALE_LDS) : 0);
   static constexpr int RPT = TILE / (8 * WAVES);  // rows of a tile that a thread stages (16 bytes of each block)
   static constexpr int LOADS = RPT * NB;          // its loads per tile
 };
@@ -131,6 +136,14 @@ __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
 // 16 bytes per lane from any address to LDS bytes [lds_addr + 16 lane, + 16).
 __device__ __forceinline__ void dma16_far(const void* p, uint32_t lds_addr) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :
+               : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(p)
+               : "memory", "m0");
+}
+
+// The same with 4 bytes per lane.
+__device__ __forceinline__ void dma4_far(const void* p, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+               :
                : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(p)
                : "memory", "m0");
 }
@@ -160,7 +173,7 @@ struct Worker {
   int koff[4], voff[2][2];
   int lane, half, tid, wave;
   // MXFP8: the next tile's codes and scales, on their way to LDS as bf16
-  static constexpr int HELD = MX && S::RPT == 1 ? S::NB : 1;
+  static constexpr int HELD = MX && S::RPT == 1 && !S::WIDE ? S::NB : 1;
   uint2 code[HELD];
   uint32_t sc[HELD];
 
@@ -204,12 +217,65 @@ struct Worker {
     uint32_t to = 0;
     uint64_t live = 0;  // lanes that load
   };
-  static constexpr bool SPREAD = S::WIDE && !MX && S::STAGES == 4;
-
   __device__ __forceinline__ Next next_loads(int tk, int slot) const {
     const int r = tid >> 3;
-    return Next{p.pool.buf[0] + (cache_row(tk + r) * DK + 8 * chunk_of(r, 0)) * 2,
-                (uint32_t)__builtin_amdgcn_readfirstlane(lds_u32(lds) + slot * S::TILE_LDS + wave * 1024), ~(uint64_t)0};
+    const int64_t row = cache_row(tk + r);
+    const uint8_t* src;
+    uint32_t to = lds_u32(lds) + wave * 1024;
+    if constexpr (MX) {
+      src = p.pool.buf[0] + row * DK + 16 * (tid & 7);
+      to += S::STAGES * S::TILE_LDS + slot * S::RAW_LDS;
+    } else {
+      src = p.pool.buf[0] + (row * DK + 8 * chunk_of(r, 0)) * 2;
+      to += slot * S::TILE_LDS;
+    }
+    return Next{src, (uint32_t)__builtin_amdgcn_readfirstlane(to), ~(uint64_t)0};
+  }
+
+  // The same loads in a burst, outside the loop and for waves without rows.
+  __device__ __forceinline__ void load_now(const Next& n) const {
+    if (!n.live) {
+      vm_wait<0>();
+      return;
+    }
+#pragma unroll
+    for (int b = 0; b < (MX ? 4 : S::NB); ++b) dma16_far(n.src + 128 * b, n.to + b * BLK);
+    if (MX && (tid & 7) < 4) dma16_far(n.src + 512, n.to + 4 * BLK);
+  }
+
+  // WIDE MXFP8: a row's 18 scale bytes, in the five aligned words that hold
+  // them, to LDS: thread 5 r + k takes word k of row r.
+  __device__ __forceinline__ void load_scales(int tk, int slot) const {
+    if (tid >= 5 * TILE) return;
+    const int r = tid / 5;
+    const uint8_t* src = p.pool.buf[1] + (cache_row(tk + r) * 18 & ~(int64_t)3) + 4 * (tid - 5 * r);
+    dma4_far(src, lds_u32(lds) + S::STAGES * S::TILE_LDS + 2 * S::RAW_LDS + slot * S::SCALE_LDS + wave * 256);
+  }
+
+  // A tile's codes to bf16. E4M3 times 2^(byte - 127) is exact in bf16 down to
+  // its subnormals; the convert reads the scale's exponent field, 0 meaning
+  // 2^-127 and 255 NaN, as E8M0 does.
+  __device__ __forceinline__ void convert(int tk, int raw, int slot) const {
+    const int r = tid >> 3, c = (tid & 7) ^ swz(r);
+    const uint8_t* from = lds + S::STAGES * S::TILE_LDS + raw * S::RAW_LDS + r * 128 + c * 8;
+    const uint32_t* sw = reinterpret_cast<const uint32_t*>(lds + S::STAGES * S::TILE_LDS + 2 * S::RAW_LDS + raw * S::SCALE_LDS) + 5 * r;
+    // first byte wanted of the row's words: rows start at even bytes, odd rows
+    // in the middle of a word
+    const uint32_t sh = 2 * ((uint32_t)cache_row(tk + r) & 1) + (c >> 2);
+    uint32_t w[5];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __builtin_amdgcn_alignbyte(sw[k + 1], sw[k], sh);
+    w[4] = sw[4] >> (8 * sh);
+#pragma unroll
+    for (int b = 0; b < S::NBK; ++b) {
+      const uint2 cd = *reinterpret_cast<const uint2*>(from + (b >> 1) * BLK + (b & 1) * 64);
+      const float f = __uint_as_float((b & 1 ? w[b / 2] << 7 : w[b / 2] << 23) & 0x7F800000u);
+      const u32x4_t v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd.x, f, false)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd.x, f, true)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd.y, f, false)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd.y, f, true))};
+      *reinterpret_cast<u32x4_t*>(lds + slot * S::TILE_LDS + b * BLK + r * 128 + ((tid & 7) << 4)) = v;
+    }
   }
 
   __device__ __forceinline__ void load_mx(int64_t row, int r, uint2* cd, uint32_t* sb) const {
@@ -224,13 +290,11 @@ struct Worker {
   __device__ __forceinline__ void store_mx(int r, int slot, const uint2* cd, const uint32_t* sb) const {
 #pragma unroll
     for (int b = 0; b < S::NB; ++b) {
-      // E4M3 times 2^(byte - 127) is exact in bf16 down to its subnormals
-      const float f = __uint_as_float(sb[b] ? sb[b] << 23 : 0x00400000u);
-      u32x4_t v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].x, f, false)),
+      const float f = __uint_as_float(sb[b] << 23);  // (see convert)
+      const u32x4_t v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].x, f, false)),
                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].x, f, true)),
                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].y, f, false)),
                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(cd[b].y, f, true))};
-      if (sb[b] == 0xFF) v = u32x4_t{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
       *reinterpret_cast<u32x4_t*>(lds + slot * S::TILE_LDS + b * BLK + r * 128 + ((tid & 7) << 4)) = v;
     }
   }
@@ -305,16 +369,19 @@ struct Worker {
     return __builtin_bit_cast(bf16x8_t, v);
   }
 
-  // The scores of a tile that ends the sequence or the chunk or holds drafts:
-  // rows not seen get -infinity. Their values may still be anything, and the
-  // product would make NaN of 0 times infinity, so this thread's share of the
-  // tile's values is looked over: if one is not finite, slow_rows() takes over.
-  __device__ __forceinline__ void mask(f32x16_t& s, const uint8_t* tile, int tk) {
+  // A tile that ends the sequence or the chunk or holds drafts. Scores of rows
+  // that the lane's query does not see become -infinity.
+  __device__ __forceinline__ void mask(f32x16_t& s, int tk) const {
     uint32_t vis = visible(p, it, qt, qi, tk);
     if (tk_end - tk < TILE) vis &= (1u << (tk_end - tk)) - 1;
     vis >>= 4 * half;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = vis & (1u << (8 * (i / 4) + i % 4)) ? s[i] : NEG_INF;
+  }
+  // Values that some rows do not see may be anything, and the product would make
+  // NaN of 0 times infinity, so this thread's share of the tile's values is
+  // looked over: if one is not finite, slow_rows() takes over.
+  __device__ __forceinline__ void look_over(const uint8_t* tile) {
     const uint8_t* vals = tile + (SHARED ? 0 : S::NBK * BLK);
 #pragma unroll 1
     for (int i = tid; i < DV * TILE / 8; i += S::THREADS) {  // 16 bytes each, in any order
@@ -327,30 +394,20 @@ struct Worker {
   // O^T += V^T P^T for a tile at `tile` with weights s
   __device__ __forceinline__ void values(const uint8_t* tile, const f32x16_t& s) {
     const bf16x8_t p0 = p_frag(s, 0), p1 = p_frag(s, 1);
-    if constexpr (S::WIDE) {
-      const uint32_t v = lds_u32(tile);
-      asm volatile(WIDE_VALUES
-                   :
-                     [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]),
-                     [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
-                     [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
-                     [o15] "+a"(o[15])
-                   : [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
-                     [v11] "v"(v + voff[1][1]), [p0] "v"(p0), [p1] "v"(p1)
-                   : "memory", WIDE_CLOBBERS);
-    } else {
 #pragma unroll
-      for (int n = 0; n < S::NT; ++n) {
-        o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 0)), p0, o[n]);
-        o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 1)), p1, o[n]);
-      }
+    for (int n = 0; n < S::NT; ++n) {
+      o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 0)), p0, o[n]);
+      o[n] = mfma(__builtin_bit_cast(bf16x8_t, v_frag(tile, n, 1)), p1, o[n]);
     }
   }
 
   // Tile i at `tile` by itself: scores, weights, O^T += V^T P^T.
   __device__ __forceinline__ void step(uint8_t* tile, int i, int full) {
     f32x16_t s = scores(tile);
-    if (__builtin_expect(i >= full, 0)) mask(s, tile, tk_begin + i * TILE);
+    if (__builtin_expect(i >= full, 0)) {
+      mask(s, tk_begin + i * TILE);
+      look_over(tile);
+    }
     weights(s);
     values(tile, s);
   }
@@ -360,23 +417,44 @@ struct Worker {
   __device__ __forceinline__ void step_ahead(const uint8_t* tile, const uint8_t* ahead, f32x16_t& s, const Next& next) {
     const uint32_t k = lds_u32(ahead), v = lds_u32(tile);
     float t0, t1;
-    asm volatile(WIDE_STEP
-                 : [s] "+{v[192:207]}"(s), [m] "+v"(m), [top] "+v"(top), [l] "+v"(l), [t0] "=&v"(t0), [t1] "=&v"(t1),
-                   [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]),
-                   [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
-                   [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
-                   [o15] "+a"(o[15])
-                 : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
-                   [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
-                   [v11] "v"(v + voff[1][1]), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
-                   [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
-                   [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
-                   [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
-                   [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]),
-                   [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]),
-                   [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]),
-                   [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
-                 : "memory", "vcc", "scc", "m0", "v184", "v185", "v186", "v187", "v188", "v189", "v190", "v191", WIDE_CLOBBERS);
+    if constexpr (MX) {
+      asm volatile(WIDE_STEP_MX
+                   : [s] "+{v[192:207]}"(s), [m] "+v"(m), [top] "+v"(top), [l] "+v"(l), [t0] "=&v"(t0), [t1] "=&v"(t1),
+                     [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]),
+                     [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
+                     [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
+                     [o15] "+a"(o[15])
+                   : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
+                     [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
+                     [v11] "v"(v + voff[1][1]), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
+                     [half] "s"(next.live & 0x0F0F0F0F0F0F0F0Full),
+                     [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
+                     [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
+                     [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
+                     [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]),
+                     [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]),
+                     [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]),
+                     [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
+                   : "memory", "vcc", "scc", "m0", "v184", "v185", "v186", "v187", "v188", "v189", "v190", "v191", WIDE_CLOBBERS);
+    } else {
+      asm volatile(WIDE_STEP
+                   : [s] "+{v[192:207]}"(s), [m] "+v"(m), [top] "+v"(top), [l] "+v"(l), [t0] "=&v"(t0), [t1] "=&v"(t1),
+                     [o0] "+a"(o[0]), [o1] "+a"(o[1]), [o2] "+a"(o[2]), [o3] "+a"(o[3]), [o4] "+a"(o[4]),
+                     [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
+                     [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
+                     [o15] "+a"(o[15])
+                   : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
+                     [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
+                     [v11] "v"(v + voff[1][1]), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
+                     [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
+                     [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
+                     [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
+                     [q16] "v"(q[16]), [q17] "v"(q[17]), [q18] "v"(q[18]), [q19] "v"(q[19]), [q20] "v"(q[20]),
+                     [q21] "v"(q[21]), [q22] "v"(q[22]), [q23] "v"(q[23]), [q24] "v"(q[24]), [q25] "v"(q[25]),
+                     [q26] "v"(q[26]), [q27] "v"(q[27]), [q28] "v"(q[28]), [q29] "v"(q[29]), [q30] "v"(q[30]),
+                     [q31] "v"(q[31]), [q32] "v"(q[32]), [q33] "v"(q[33]), [q34] "v"(q[34]), [q35] "v"(q[35])
+                   : "memory", "vcc", "scc", "m0", "v184", "v185", "v186", "v187", "v188", "v189", "v190", "v191", WIDE_CLOBBERS);
+    }
   }
 
   __device__ __forceinline__ void clear() {
@@ -392,50 +470,91 @@ struct Worker {
   // All tiles of the chunk.
   __device__ __forceinline__ void pass(int tiles, int full) {
     clear();
+    if constexpr (S::WIDE) pass_wide(tiles, full);
+    else pass_any(tiles, full);
+  }
+
+  // Step i works on tiles i and i + 1, which are in LDS as bf16.
+  __device__ __forceinline__ void pass_wide(int tiles, int full) {
+    const bool active = it.rt * 32 * WAVES + wave * 32 < it.rows;
+    f32x16_t s;
+    if constexpr (!MX) {
+      // Tile i + 2 is under way and i + 3 asked for during step i, into the
+      // place of i - 1, which all have left when they meet at the barrier.
+      for (int i = 0; i < min(3, tiles); ++i) load_now(next_loads(tk_begin + i * TILE, i));
+      if (tiles > 2) vm_wait<2 * S::LOADS>();
+      else vm_wait<0>();
+      barrier_reads_done();
+    } else {
+      // During step i the codes of tile i + 2 are converted (before the
+      // products) and those of i + 3 asked for.
+      load_now(next_loads(tk_begin, 0));
+      load_now(next_loads(tk_begin + TILE, 1));
+      load_scales(tk_begin, 0);
+      load_scales(tk_begin + TILE, 1);
+      vm_wait<0>();
+      barrier_reads_done();
+      convert(tk_begin, 0, 0);
+      convert(tk_begin + TILE, 1, 1);
+      barrier_reads_done();
+      load_now(next_loads(tk_begin + 2 * TILE, 0));
+      load_scales(tk_begin + 2 * TILE, 0);
+    }
+    if (active) s = scores(lds);
+    int slot = 0, third = MX ? 2 : 3;  // ring places of tile i and of the one that comes in
+    for (int i = 0; i < tiles; ++i) {
+      const int after = slot + 1 == S::STAGES ? 0 : slot + 1;
+      Next loads;
+      if constexpr (!MX) {
+        vm_wait<S::LOADS>();
+        barrier_reads_done();
+        if (i + 3 < tiles) loads = next_loads(tk_begin + (i + 3) * TILE, third);
+      } else {
+        vm_wait<0>();
+        barrier_reads_done();
+        if (i + 2 < tiles) convert(tk_begin + (i + 2) * TILE, i & 1, third);
+        if (i + 3 < tiles) {
+          loads = next_loads(tk_begin + (i + 3) * TILE, (i + 1) & 1);
+          load_scales(tk_begin + (i + 3) * TILE, (i + 1) & 1);
+        }
+      }
+      if (__builtin_expect(i >= full, 0)) {
+        if (active) mask(s, tk_begin + i * TILE);
+        look_over(lds + slot * S::TILE_LDS);
+      }
+      // (behind the last tile the scores of what lies there are not used)
+      if (active) step_ahead(lds + slot * S::TILE_LDS, lds + after * S::TILE_LDS, s, loads);
+      else load_now(loads);
+      slot = after;
+      third = third + 1 == S::STAGES ? 0 : third + 1;
+    }
+#pragma unroll
+    for (int n = 0; n < S::NT; ++n) asm volatile("" : "+a"(o[n]));  // O stays where it is up to here
+  }
+
+  __device__ __forceinline__ void pass_any(int tiles, int full) {
     if constexpr (!MX) {
       constexpr int AHEAD = S::STAGES - 1;
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i)
         if (i < tiles) load_bf16(tk_begin + i * TILE, i);
       int slot = 0, next = AHEAD;  // ring places of tile i and of tile i + AHEAD
-      if constexpr (SPREAD) {
-        // Tiles i and i + 1 are in LDS, i + 2 under way and i + 3 asked for
-        // during step i, into the place of i - 1, which all have left when
-        // they meet at the barrier.
-        if (tiles > 2) vm_wait<2 * S::LOADS>();
-        else vm_wait<0>();
-        barrier_reads_done();
-        f32x16_t s = scores(lds);
-        for (int i = 0; i < tiles; ++i) {
-          Next loads;
-          const int after = slot + 1 == S::STAGES ? 0 : slot + 1;
-          vm_wait<S::LOADS>();
+      for (int i = 0; i < tiles; ++i) {
+        if constexpr (AHEAD == 0) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the previous tile is read
+          load_bf16(tk_begin + i * TILE, 0);
+          vm_wait<0>();
+        } else {
+          // tile i has landed when only the AHEAD - 1 younger ones are under way;
+          // near the end there are fewer, so wait for all
+          if (i + AHEAD <= tiles) vm_wait<(AHEAD - 1) * S::LOADS>();
+          else vm_wait<0>();
           barrier_reads_done();
-          if (i + AHEAD < tiles) loads = next_loads(tk_begin + (i + AHEAD) * TILE, next);
-          if (__builtin_expect(i >= full, 0)) mask(s, lds + slot * S::TILE_LDS, tk_begin + i * TILE);
-          // (behind the last tile the scores of what lies there are not used)
-          step_ahead(lds + slot * S::TILE_LDS, lds + after * S::TILE_LDS, s, loads);
-          slot = after;
-          next = next + 1 == S::STAGES ? 0 : next + 1;
+          if (i + AHEAD < tiles) load_bf16(tk_begin + (i + AHEAD) * TILE, next);
         }
-      } else {
-        for (int i = 0; i < tiles; ++i) {
-          if constexpr (AHEAD == 0) {
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the previous tile is read
-            load_bf16(tk_begin + i * TILE, 0);
-            vm_wait<0>();
-          } else {
-            // tile i has landed when only the AHEAD - 1 younger ones are under way;
-            // near the end there are fewer, so wait for all
-            if (i + AHEAD <= tiles) vm_wait<(AHEAD - 1) * S::LOADS>();
-            else vm_wait<0>();
-            barrier_reads_done();
-            if (i + AHEAD < tiles) load_bf16(tk_begin + (i + AHEAD) * TILE, next);
-          }
-          step(lds + slot * S::TILE_LDS, i, full);
-          slot = slot + 1 == S::STAGES ? 0 : slot + 1;
-          next = next + 1 == S::STAGES ? 0 : next + 1;
-        }
+        step(lds + slot * S::TILE_LDS, i, full);
+        slot = slot + 1 == S::STAGES ? 0 : slot + 1;
+        next = next + 1 == S::STAGES ? 0 : next + 1;
       }
     } else {
       int slot = 0;
@@ -462,10 +581,6 @@ struct Worker {
         slot = slot + 1 == S::STAGES ? 0 : slot + 1;
       }
     }
-    if constexpr (S::WIDE) {  // O stays where it is up to here
-#pragma unroll
-      for (int n = 0; n < S::NT; ++n) asm volatile("" : "+a"(o[n]));
-    }
   }
 };
 
@@ -474,9 +589,8 @@ template <bool MX>
 __device__ __forceinline__ float cache_value(const PoolParams& pool, int b, int64_t row, int d, int c) {
   if constexpr (!MX) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(pool.buf[b])[row * d + c]);
   const uint32_t code = pool.buf[2 * b][row * d + c], sc = pool.buf[2 * b + 1][row * (d / 32) + c / 32];
-  if (sc == 0xFF) return __builtin_nanf("");
   const uint32_t v = __builtin_bit_cast(
-      uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, __uint_as_float(sc ? sc << 23 : 0x00400000u), false));
+      uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, __uint_as_float(sc << 23), false));
   return bf16_bits_to_f32(v & 0xFFFFu);
 }
 
@@ -551,7 +665,7 @@ template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(1, DV > 256 ? 1 : 4)))
 void tree_attn_kernel(AttnParams p) {
   using S = Shape<DK, DV, SHARED, MX, WAVES>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::STAGES * S::TILE_LDS];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   __shared__ int s_page[MAX_CHUNK_PAGES];
   __shared__ int s_bad;
   // consecutive items (row tiles that read the same chunk) go to one XCD's L2
@@ -718,7 +832,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks)
 
 template <int DK, int DV, bool SHARED, bool MX>
 void launch_shape(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  if (p.plan.waves == 1)
+  if constexpr (DV > 256) {
+    hipLaunchKernelGGL((tree_attn_kernel<DK, DV, SHARED, MX, 4>), dim3(grid), dim3(256), 0, stream, p);
+    return;
+  }
+  else if (p.plan.waves == 1)
     hipLaunchKernelGGL((tree_attn_kernel<DK, DV, SHARED, MX, 1>), dim3(grid), dim3(64), 0, stream, p);
   else if (p.plan.waves == 2)
     hipLaunchKernelGGL((tree_attn_kernel<DK, DV, SHARED, MX, 2>), dim3(grid), dim3(128), 0, stream, p);

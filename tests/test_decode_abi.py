@@ -242,6 +242,8 @@ def test_cache_must_fit_the_widths(L):
     mx = dict(nbuf=2, buf__1=addr(6), page_bytes__0=64 * 576, page_bytes__1=64 * 18)
     assert L.mla_tree_attention_workspace_size(ctypes.byref(attn(pool=pool(**mx), cache_dtype=2))) > 0
     assert L.mla_tree_attention(ctypes.byref(attn(pool=pool(**(mx | dict(page_bytes__1=64 * 36))), cache_dtype=2)), None) == 1
+    odd = mx | dict(num_pages=99, page_size=7, page_bytes__0=7 * 576, page_bytes__1=7 * 18)  # an odd number of rows
+    assert L.mla_tree_attention(ctypes.byref(attn(pool=pool(**odd), cache_dtype=2)), None) == 1
 
 
 def test_bindings_refuse_host_tensors_and_wrong_sizes(monkeypatch):

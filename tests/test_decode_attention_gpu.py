@@ -38,6 +38,7 @@ class Case:
         for j, s in enumerate(order):
             held[s] = max(held[s], -(-(lens[s] + drafts[j]) // page))  # a sequence may be listed twice
         num = sum(held) + spare
+        num += num % 2 if mx else 0  # an even number of rows
         ids = torch.randperm(num, generator=g).tolist()
         self.table = torch.full((n, max(1, max(held)) + 1), -1, dtype=torch.int32)
         for i in range(n):
