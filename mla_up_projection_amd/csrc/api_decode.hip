@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "api_checks.h"
 #include "internal_decode.h"
@@ -377,17 +378,35 @@ AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int m
   (void)d_k;
   AttnPlan pl{};
   const int64_t rows = (int64_t)max_q * (H / H_kv);
-  pl.waves = rows <= 32 && d_v <= 256 ? 1 : rows <= 64 && d_v <= 256 ? 2 : 4;
+  // the pages of a chunk fit the kernel's list (with one more at each end)
+  const int64_t most = std::max<int64_t>(32, std::min<int64_t>(65536, (int64_t)1000 * page_size / 32 * 32));
+  if (d_v > 256) {
+    // the widest shape fills a CU with one workgroup; the kernel divides the
+    // steps that there are by the rule that bounds their number here
+    pl.waves = 4;
+    const int64_t tiles = (rows + 127) / 128;
+    pl.row_tiles = (int)std::min<int64_t>(tiles, INT32_MAX);
+    pl.chunk = (int)most;
+    pl.chunks = 1;
+    const double steps = std::max(1.0, (double)nseq * H_kv * (double)tiles * ((max_len + 31) / 32));
+    pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(28.0 * steps)) + 1});
+    if (pl.groups > 1) {
+      const size_t slots = (size_t)2 * pl.groups * pl.waves;
+      pl.part_o = 0;
+      pl.part_ml = slots * 32 * (size_t)d_v * 4;
+      pl.sums = pl.part_ml + slots * 32 * 8;
+      pl.total = pl.sums + ((size_t)nseq + 2) * 8;
+    }
+    return pl;
+  }
+  pl.waves = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
   const int64_t tiles = (rows + 32 * pl.waves - 1) / (32 * pl.waves);
   pl.row_tiles = (int)std::min<int64_t>(tiles, INT32_MAX);
   const int64_t units = std::max<int64_t>(1, (int64_t)nseq * H_kv * tiles);
   // workgroups to fill the chip twice over with the waves that fit
   const int64_t want = std::max<int64_t>(1, 2 * 256 * 4 / pl.waves / units);
-  const int64_t most = std::max(1, (max_len + 127) / 128);  // four tiles at least
-  const int64_t n = std::min(want, most);
-  int64_t chunk = ((max_len + n - 1) / n + 31) / 32 * 32;
-  // the pages of a chunk fit the kernel's list (with one more at each end)
-  chunk = std::min<int64_t>(chunk, std::min<int64_t>(65536, (int64_t)1000 * page_size / 32 * 32));
+  const int64_t n = std::min<int64_t>(want, std::max(1, (max_len + 127) / 128));  // four tiles at least
+  const int64_t chunk = std::min((((int64_t)max_len + n - 1) / n + 31) / 32 * 32, most);
   pl.chunk = (int)std::max<int64_t>(chunk, 32);
   pl.chunks = (max_len + pl.chunk - 1) / pl.chunk;
   if (pl.chunks > 1) {
@@ -495,6 +514,7 @@ mla_status mla_tree_attention(const mla_tree_attn_args* a, void* stream) {
   p.plan = plan;
   p.part_o = (float*)((uint8_t*)a->workspace + plan.part_o);
   p.part_ml = (float*)((uint8_t*)a->workspace + plan.part_ml);
+  p.sums = (int64_t*)((uint8_t*)a->workspace + plan.sums);
   return launched(mla::launch_tree_attn(p, (hipStream_t)stream));
 }
 

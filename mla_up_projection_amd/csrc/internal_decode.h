@@ -89,7 +89,10 @@ struct AttnPlan {
   int row_tiles;   // per (sequence, key head)
   int chunk;       // cache rows per workgroup, a multiple of the tile
   int chunks;      // per sequence, at most
-  size_t part_o, part_ml, total;  // workspace: offset of the partial outputs and of (max, sum), bytes in all
+  int groups;      // > 0: the even plan of the widest shape, with at most that many workgroups (chunk: rows whose
+                   // pages the kernel lists at a time)
+  size_t part_o, part_ml, sums, total;  // workspace: offsets of the partial outputs, of (max, sum) and of the even
+                                        // plan's sums; bytes in all
 };
 
 struct AttnParams {
@@ -111,6 +114,7 @@ struct AttnParams {
   uint32_t page_magic;  // ceil(2^32 / page_size): quotient of small rows by a high product
   float* part_o;
   float* part_ml;
+  int64_t* sums;  // even plan: all steps, workgroups, steps before each sequence
   AttnPlan plan;
 };
 bool attn_shape_supported(int d_k, int d_v, bool shared);

@@ -42,35 +42,71 @@ __device__ __forceinline__ int swz(int t) { return ((t >> 1) & 1) << 2 | ((t >> 
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// What a workgroup works on.
+// A row tile of a sequence and key head, or a part of its cache rows.
 struct Item {
-  int j, kvh, chunk, rt;
+  int j, kvh, rt;
   int t0, n, rows;      // first query token, drafts, query rows (n * group)
   int len, total, seq;  // committed rows, with drafts
-  int chunks;           // of this sequence
   bool broken;          // it outgrew the plan or its entry is invalid: NaN
+  bool whole;           // all of the sequence's cache rows are taken: the result is final
+  int64_t slot;         // else the place of its partial result
 };
 
-__device__ __forceinline__ bool find_item(const AttnParams& p, int64_t item, Item& it) {
-  it.rt = (int)(item % p.plan.row_tiles);
-  item /= p.plan.row_tiles;
-  it.chunk = (int)(item % p.plan.chunks);
-  item /= p.plan.chunks;
-  it.kvh = (int)(item % p.H_kv);
-  it.j = (int)(item / p.H_kv);
-  if (it.j >= p.nseq) return false;
+// Sequence j of the call. Any lane may ask for any j.
+__device__ __forceinline__ void load_seq(const AttnParams& p, int j, Item& it) {
   const int T = (int)p.T;
-  // the same for every lane: kept in scalar registers
-  it.t0 = min(max(__builtin_amdgcn_readfirstlane(p.cu[it.j]), 0), T);
-  it.n = min(max(__builtin_amdgcn_readfirstlane(p.cu[it.j + 1]), it.t0), T) - it.t0;
+  it.j = j;
+  it.t0 = min(max(p.cu[j], 0), T);
+  it.n = min(max(p.cu[j + 1], it.t0), T) - it.t0;
   it.rows = it.n * p.group;
-  it.seq = __builtin_amdgcn_readfirstlane(p.seqs[it.j]);
+  it.seq = p.seqs[j];
   it.broken = it.seq < 0 || it.seq >= p.pool.max_seqs || it.n > p.max_q;
-  it.len = it.broken ? 0 : __builtin_amdgcn_readfirstlane(p.pool.lens[it.seq]);
+  it.len = it.broken ? 0 : p.pool.lens[it.seq];
   it.broken |= it.len < 0 || it.len > p.max_len - it.n;
   it.total = it.len + it.n;
-  it.chunks = it.broken ? 1 : max(1, (it.total + p.plan.chunk - 1) / p.plan.chunk);
+}
+// The same in scalar registers, for a j that all lanes share.
+__device__ __forceinline__ void load_seq_uniform(const AttnParams& p, int j, Item& it) {
+  load_seq(p, j, it);
+  it.t0 = __builtin_amdgcn_readfirstlane(it.t0);
+  it.n = __builtin_amdgcn_readfirstlane(it.n);
+  it.rows = it.n * p.group;
+  it.seq = __builtin_amdgcn_readfirstlane(it.seq);
+  it.len = __builtin_amdgcn_readfirstlane(it.len);
+  it.broken = __builtin_amdgcn_readfirstlane(it.broken);
+  it.total = it.len + it.n;
+}
+
+// Chunked plan: item number -> item and its chunk; false if there is none.
+__device__ __forceinline__ bool find_item(const AttnParams& p, int64_t item, Item& it, int& chunk) {
+  it.slot = item;
+  it.rt = (int)(item % p.plan.row_tiles);
+  item /= p.plan.row_tiles;
+  chunk = (int)(item % p.plan.chunks);
+  item /= p.plan.chunks;
+  it.kvh = (int)(item % p.H_kv);
+  const int j = (int)(item / p.H_kv);
+  if (j >= p.nseq) return false;
+  load_seq_uniform(p, j, it);
+  it.whole = it.total <= p.plan.chunk;
   return it.n > 0;
+}
+
+// Even plan (the widest shape): the steps of all items, one cache tile of one
+// row tile each, are numbered through, and workgroup b of G takes the steps
+// [b W / G, (b + 1) W / G). Steps of sequence j:
+constexpr int WIDE_ROWS = 128;
+__device__ __forceinline__ int row_tiles_of(const Item& it) { return (it.rows + WIDE_ROWS - 1) / WIDE_ROWS; }
+__device__ __forceinline__ int tiles_of(const Item& it) { return (it.total + TILE - 1) / TILE; }
+__device__ __forceinline__ int64_t steps_of(const AttnParams& p, const Item& it) {
+  return it.broken || it.n == 0 ? 0 : (int64_t)p.H_kv * row_tiles_of(it) * tiles_of(it);
+}
+__device__ __forceinline__ int64_t first_step(int64_t W, int G, int b) { return W * b / G; }
+// More workgroups shorten the longest but write more partial results: a step
+// takes 2.2 us, a partial result (256 KB out and in again) 0.08 us of all
+// workgroups' time, and W 2.2 / G + 0.08 G is least at G = sqrt(28 W).
+__device__ __forceinline__ int workgroups_for(const AttnParams& p, int64_t W) {
+  return (int)min((int64_t)p.plan.groups, min(W, (int64_t)max(1.0f, sqrtf(28.0f * (float)W))));
 }
 
 // Every row of a broken sequence, by one workgroup.
@@ -169,9 +205,10 @@ struct Worker {
   bf16x8_t q[S::KK];
   f32x16_t o[S::NT];
   float m, top, l;  // reference, largest score, sum of weights
-  // LDS offsets of fragments, see init()
-  int koff[4], voff[2][2];
-  int lane, half, tid, wave;
+  // LDS offsets of the first fragments. A tile starts at a multiple of 128
+  // bytes, so the others differ in single bits.
+  uint32_t koff0, voff0;
+  int half, tid, wave;
   // MXFP8: the next tile's codes and scales, on their way to LDS as bf16
   static constexpr int HELD = MX && S::RPT == 1 && !S::WIDE ? S::NB : 1;
   uint2 code[HELD];
@@ -217,8 +254,16 @@ struct Worker {
     uint32_t to = 0;
     uint64_t live = 0;  // lanes that load
   };
+  // The thread's number, anew: what follows from it is then worked out where it
+  // is used instead of occupying registers all through the loop.
+  __device__ __forceinline__ int thread() const {
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    return t;
+  }
+
   __device__ __forceinline__ Next next_loads(int tk, int slot) const {
-    const int r = tid >> 3;
+    const int tid = thread(), r = tid >> 3;
     const int64_t row = cache_row(tk + r);
     const uint8_t* src;
     uint32_t to = lds_u32(lds) + wave * 1024;
@@ -226,7 +271,7 @@ struct Worker {
       src = p.pool.buf[0] + row * DK + 16 * (tid & 7);
       to += S::STAGES * S::TILE_LDS + slot * S::RAW_LDS;
     } else {
-      src = p.pool.buf[0] + (row * DK + 8 * chunk_of(r, 0)) * 2;
+      src = p.pool.buf[0] + (row * DK + 8 * ((tid & 7) ^ swz(r))) * 2;
       to += slot * S::TILE_LDS;
     }
     return Next{src, (uint32_t)__builtin_amdgcn_readfirstlane(to), ~(uint64_t)0};
@@ -246,6 +291,7 @@ struct Worker {
   // WIDE MXFP8: a row's 18 scale bytes, in the five aligned words that hold
   // them, to LDS: thread 5 r + k takes word k of row r.
   __device__ __forceinline__ void load_scales(int tk, int slot) const {
+    const int tid = thread();
     if (tid >= 5 * TILE) return;
     const int r = tid / 5;
     const uint8_t* src = p.pool.buf[1] + (cache_row(tk + r) * 18 & ~(int64_t)3) + 4 * (tid - 5 * r);
@@ -256,7 +302,7 @@ struct Worker {
   // its subnormals; the convert reads the scale's exponent field, 0 meaning
   // 2^-127 and 255 NaN, as E8M0 does.
   __device__ __forceinline__ void convert(int tk, int raw, int slot) const {
-    const int r = tid >> 3, c = (tid & 7) ^ swz(r);
+    const int tid = thread(), r = tid >> 3, c = (tid & 7) ^ swz(r);
     const uint8_t* from = lds + S::STAGES * S::TILE_LDS + raw * S::RAW_LDS + r * 128 + c * 8;
     const uint32_t* sw = reinterpret_cast<const uint32_t*>(lds + S::STAGES * S::TILE_LDS + 2 * S::RAW_LDS + raw * S::SCALE_LDS) + 5 * r;
     // first byte wanted of the row's words: rows start at even bytes, odd rows
@@ -299,13 +345,21 @@ struct Worker {
     }
   }
 
+  // K: chunk 2 c + half of a block's rows. V: rows 8 e + 4 half + .., columns
+  // 32 c + .. of a block.
+  __device__ __forceinline__ uint32_t k_at(uint32_t tile, int c) const { return (tile + koff0) ^ (32 * c); }
+  __device__ __forceinline__ uint32_t v_at(uint32_t tile, int e, int c) const {
+    return ((tile + voff0) ^ (16 * e + 64 * c)) + 1024 * e;
+  }
+
   typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+  typedef __attribute__((address_space(3))) const bf16x8_t lds_bf16x8;
 
   // V^T fragment of value columns 32 n .. + 31 and the tile's 16-row step c
   __device__ __forceinline__ u32x4_t v_frag(const uint8_t* tile, int n, int c) const {
-    const uint8_t* base = tile + (SHARED ? 0 : S::NBK * BLK) + (n >> 1) * BLK + c * 16 * 128;
-    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[0][n & 1])));
-    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + voff[1][n & 1])));
+    const uint32_t at = lds_u32(tile) + (SHARED ? 0 : S::NBK * BLK), off = (n >> 1) * BLK + c * 16 * 128;
+    const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(v_at(at, 0, n & 1) + off)));
+    const uint2 b = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(v_at(at, 1, n & 1) + off)));
     return u32x4_t{a.x, a.y, b.x, b.y};
   }
 
@@ -317,7 +371,7 @@ struct Worker {
       const uint32_t k = lds_u32(tile);
       asm volatile(WIDE_SCORES
                    : [s] "=&v"(s)
-                   : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
+                   : [k0] "v"(k_at(k, 0)), [k1] "v"(k_at(k, 1)), [k2] "v"(k_at(k, 2)), [k3] "v"(k_at(k, 3)),
                      [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
                      [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
                      [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
@@ -331,7 +385,7 @@ struct Worker {
       for (int i = 0; i < 16; ++i) s[i] = 0;
 #pragma unroll
       for (int kk = 0; kk < S::KK; ++kk)
-        s = mfma(*reinterpret_cast<const bf16x8_t*>(tile + (kk >> 2) * BLK + koff[kk & 3]), q[kk], s);
+        s = mfma(*(lds_bf16x8*)(uintptr_t)(k_at(lds_u32(tile), kk & 3) + (kk >> 2) * BLK), q[kk], s);
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) s[k] *= p.scale_log2;
@@ -382,6 +436,7 @@ struct Worker {
   // NaN of 0 times infinity, so this thread's share of the tile's values is
   // looked over: if one is not finite, slow_rows() takes over.
   __device__ __forceinline__ void look_over(const uint8_t* tile) {
+    const int tid = thread();
     const uint8_t* vals = tile + (SHARED ? 0 : S::NBK * BLK);
 #pragma unroll 1
     for (int i = tid; i < DV * TILE / 8; i += S::THREADS) {  // 16 bytes each, in any order
@@ -424,9 +479,9 @@ struct Worker {
                      [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
                      [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
                      [o15] "+a"(o[15])
-                   : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
-                     [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
-                     [v11] "v"(v + voff[1][1]), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
+                   : [k0] "v"(k_at(k, 0)), [k1] "v"(k_at(k, 1)), [k2] "v"(k_at(k, 2)), [k3] "v"(k_at(k, 3)),
+                     [v00] "v"(v_at(v, 0, 0)), [v01] "v"(v_at(v, 0, 1)), [v10] "v"(v_at(v, 1, 0)),
+                     [v11] "v"(v_at(v, 1, 1)), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
                      [half] "s"(next.live & 0x0F0F0F0F0F0F0F0Full),
                      [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
                      [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
@@ -443,9 +498,9 @@ struct Worker {
                      [o5] "+a"(o[5]), [o6] "+a"(o[6]), [o7] "+a"(o[7]), [o8] "+a"(o[8]), [o9] "+a"(o[9]),
                      [o10] "+a"(o[10]), [o11] "+a"(o[11]), [o12] "+a"(o[12]), [o13] "+a"(o[13]), [o14] "+a"(o[14]),
                      [o15] "+a"(o[15])
-                   : [k0] "v"(k + koff[0]), [k1] "v"(k + koff[1]), [k2] "v"(k + koff[2]), [k3] "v"(k + koff[3]),
-                     [v00] "v"(v + voff[0][0]), [v01] "v"(v + voff[0][1]), [v10] "v"(v + voff[1][0]),
-                     [v11] "v"(v + voff[1][1]), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
+                   : [k0] "v"(k_at(k, 0)), [k1] "v"(k_at(k, 1)), [k2] "v"(k_at(k, 2)), [k3] "v"(k_at(k, 3)),
+                     [v00] "v"(v_at(v, 0, 0)), [v01] "v"(v_at(v, 0, 1)), [v10] "v"(v_at(v, 1, 0)),
+                     [v11] "v"(v_at(v, 1, 1)), [c] "s"(p.scale_log2), [src] "v"(next.src), [to] "s"(next.to), [live] "s"(next.live),
                      [q0] "v"(q[0]), [q1] "v"(q[1]), [q2] "v"(q[2]), [q3] "v"(q[3]), [q4] "v"(q[4]), [q5] "v"(q[5]),
                      [q6] "v"(q[6]), [q7] "v"(q[7]), [q8] "v"(q[8]), [q9] "v"(q[9]), [q10] "v"(q[10]),
                      [q11] "v"(q[11]), [q12] "v"(q[12]), [q13] "v"(q[13]), [q14] "v"(q[14]), [q15] "v"(q[15]),
@@ -469,7 +524,6 @@ struct Worker {
 
   // All tiles of the chunk.
   __device__ __forceinline__ void pass(int tiles, int full) {
-    clear();
     if constexpr (S::WIDE) pass_wide(tiles, full);
     else pass_any(tiles, full);
   }
@@ -600,12 +654,12 @@ __device__ __forceinline__ float cache_value(const PoolParams& pool, int b, int6
 // by one, a lane every 64th column; a row that is not seen is not looked at.
 // Writes what the fast path writes.
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
-__device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, const int* s_page, int page0, int tk_begin,
-                                       int tk_end) {
+__device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, int tk_begin, int tk_end) {
   constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ps = p.pool.page_size;
-  const int64_t slot = ((((int64_t)it.j * p.H_kv + it.kvh) * p.plan.row_tiles + it.rt) * p.plan.chunks + it.chunk) * WAVES + wave;
+  const int held = min(p.pool.held[it.seq], p.pool.max_pages);
+  const int64_t slot = it.slot * WAVES + wave;
   for (int r32 = 0; r32 < 32; ++r32) {
     const int row = (it.rt * WAVES + wave) * 32 + r32;
     if (row >= it.rows) return;
@@ -621,9 +675,10 @@ __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, c
     for (int tk = tk_begin; tk < tk_end; ++tk) {
       if (((tk - tk_begin) & 31) == 0) vis = visible(p, it, qt, qi, tk);
       if (!((vis >> ((tk - tk_begin) & 31)) & 1)) continue;
-      const int rel = tk - page0 * ps, pk = rel / ps;
-      const int64_t page = s_page[pk];
-      const int64_t crow = (max(page, (int64_t)0) * ps + rel - pk * ps) * p.H_kv + it.kvh;
+      const int pk = tk / ps;
+      int64_t page = pk < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + pk] : -1;
+      if (page >= p.pool.num_pages) page = -1;
+      const int64_t crow = (max(page, (int64_t)0) * ps + tk - pk * ps) * p.H_kv + it.kvh;
       float s = 0;
 #pragma unroll
       for (int k = 0; k < NQ; ++k)
@@ -647,13 +702,13 @@ __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, c
     for (int k = 0; k < NO; ++k) {
       const int c = lane + 64 * k;
       if (c >= DV) continue;
-      if (it.chunks == 1)
+      if (it.whole)
         p.out[qt * p.o_t + h * p.o_h + c] = (uint16_t)f32_to_bf16_bits(o[k] * inv);
       else  // column 32 n + 8 g + 4 half + e
         p.part_o[(slot * (DV * 8) + (c >> 3) * 64 + ((c >> 2) & 1) * 32 + r32) * 4 + (c & 3)] = o[k];
     }
     if (lane == 0) {
-      if (it.chunks > 1)
+      if (!it.whole)
         reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r32] = make_float2(m, l);
       else if (p.lse)
         p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
@@ -661,53 +716,40 @@ __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, c
   }
 }
 
-template <int DK, int DV, bool SHARED, bool MX, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(1, DV > 256 ? 1 : 4)))
-void tree_attn_kernel(AttnParams p) {
-  using S = Shape<DK, DV, SHARED, MX, WAVES>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
-  __shared__ int s_page[MAX_CHUNK_PAGES];
-  __shared__ int s_bad;
-  // consecutive items (row tiles that read the same chunk) go to one XCD's L2
-  const int64_t per = gridDim.x / 8;
-  Item it;
-  if (!find_item(p, (blockIdx.x % 8) * per + blockIdx.x / 8, it)) return;
-  if (it.broken) {
-    if (it.chunk == 0 && it.rt == 0) write_nan(p, it);
-    return;
-  }
-  Worker<DK, DV, SHARED, MX, WAVES> w(p, it);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l32 = lane & 31, half = lane >> 5;
-  w.tid = tid;
-  w.lane = lane;
-  w.wave = __builtin_amdgcn_readfirstlane(wave);
-  w.half = half;
-  const int row0 = it.rt * 32 * WAVES;
-  const int tk_begin = it.chunk * p.plan.chunk;
-  const int tk_end = min(tk_begin + p.plan.chunk, it.total);
-  if (row0 >= it.rows || tk_begin >= tk_end) return;
-  w.tk_begin = tk_begin;
-  w.tk_end = tk_end;
-
-  // the chunk's pages
-  const int ps = p.pool.page_size;
-  const int page0 = tk_begin / ps, pages = (tk_end - 1) / ps - page0 + 1;
-  w.page0 = page0;
+// Page ids of cache rows [tk_begin, tk_end) to s_page, -1 for those outside the
+// pool; returns whether there are any. All threads; the list is complete after.
+template <int THREADS>
+__device__ __forceinline__ bool fill_pages(const AttnParams& p, const Item& it, int* s_page, int page0, int tk_end) {
+  const int pages = (tk_end - 1) / p.pool.page_size - page0 + 1;
   const int held = min(__builtin_amdgcn_readfirstlane(p.pool.held[it.seq]), p.pool.max_pages);
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  for (int k = tid; k < pages; k += S::THREADS) {
+  int bad = 0;
+  for (int k = threadIdx.x; k < pages; k += THREADS) {
     int id = page0 + k < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + page0 + k] : -1;
     if (id < 0 || id >= p.pool.num_pages) {
       id = -1;
-      s_bad = 1;
+      bad = 1;
     }
     s_page[k] = id;
   }
+  return __syncthreads_or(bad);
+}
 
+// Cache rows [tk_begin, tk_end) of an item, and its result or partial result.
+// `most`: cache rows whose pages fit the list.
+template <int DK, int DV, bool SHARED, bool MX, int WAVES>
+__device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, uint8_t* lds, int* s_page, int tk_begin,
+                                         int tk_end, int most) {
+  using S = Shape<DK, DV, SHARED, MX, WAVES>;
+  Worker<DK, DV, SHARED, MX, WAVES> w(p, it);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l32 = lane & 31, half = lane >> 5;
+  w.tid = tid;
+  w.wave = wave;
+  w.half = half;
+  w.lds = lds;
+  w.s_page = s_page;
   // this lane's query row
-  const int row = row0 + wave * 32 + l32;
+  const int row = it.rt * 32 * WAVES + wave * 32 + l32;
   const bool live = row < it.rows;
   const int qi = live ? row / p.group : 0;
   const int64_t qt = it.t0 + qi;
@@ -718,36 +760,35 @@ void tree_attn_kernel(AttnParams p) {
   for (int kk = 0; kk < S::KK; ++kk)
     w.q[kk] = *reinterpret_cast<const bf16x8_t*>(p.q + qt * p.q_t + h * p.q_h + 16 * kk + 8 * half);
   w.m = NEG_INF;
-  __syncthreads();
-  const bool bad = __builtin_amdgcn_readfirstlane(s_bad);
-  w.lds = lds;
-  w.s_page = s_page;
-  // LDS offsets: K fragment (row l32, chunk 2 (kk % 4) + half), V fragment
-  // (rows 4 half + 0..3 of an 8-row group, 16 columns per 16 lanes)
-#pragma unroll
-  for (int c = 0; c < 4; ++c) w.koff[c] = l32 * 128 + (((2 * c + half) ^ swz(l32)) << 4);
-  const int q4 = lane & 15;
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int t = 8 * e + 4 * half + (q4 >> 2);
-      w.voff[e][c] = t * 128 + (((4 * c + 2 * ((lane >> 4) & 1) + ((q4 & 3) >> 1)) ^ swz(t)) << 4) + (q4 & 1) * 8;
-    }
+  // K: row l32, chunk half. V: rows 4 half + 0..3, 16 columns per 16 lanes
+  w.koff0 = l32 * 128 + ((half ^ swz(l32)) << 4);
+  const int q4 = lane & 15, vt = 4 * half + (q4 >> 2);
+  w.voff0 = vt * 128 + (((2 * ((lane >> 4) & 1) + ((q4 & 3) >> 1)) ^ swz(vt)) << 4) + (q4 & 1) * 8;
 
-  const int tiles = (tk_end - tk_begin + TILE - 1) / TILE;
-  // tiles before the first draft and wholly inside the chunk need no mask
-  const int full = max(0, (min(tk_end, it.len) - tk_begin) / TILE);
-  bool slow = bad;
-  while (!slow) {
-    w.pass(tiles, full);
-    slow = __syncthreads_or(w.odd);
-    // (the barriers also end all reads of LDS before a second pass loads)
-    if (__builtin_expect(!__syncthreads_or(w.top > w.m + LAZY), 1)) break;
+  bool slow;
+  while (true) {
+    w.clear();
+    slow = false;
+    // (only the widest shape's parts can be longer than its list of pages)
+    for (int begin = tk_begin; begin < tk_end; begin += most) {
+      const int end = S::WIDE ? min(begin + most, tk_end) : tk_end;
+      w.tk_begin = begin;
+      w.tk_end = end;
+      w.page0 = begin / p.pool.page_size;
+      __syncthreads();  // LDS is read: the list may change and tiles come in
+      slow = fill_pages<S::THREADS>(p, it, s_page, w.page0, end);
+      if (slow) break;
+      // tiles before the first draft and wholly inside the part need no mask
+      const int full = max(0, (min(end, it.len) - begin) / TILE);
+      w.pass((end - begin + TILE - 1) / TILE, full);
+      if constexpr (!S::WIDE) break;
+    }
+    slow = __syncthreads_or(w.odd) || slow;
+    if (slow || __builtin_expect(!__syncthreads_or(w.top > w.m + LAZY), 1)) break;
     w.m = w.top;  // the largest score of all: the next pass is the last
   }
   if (__builtin_expect(slow, 0)) {
-    slow_rows<DK, DV, SHARED, MX, WAVES>(p, it, s_page, page0, tk_begin, tk_end);
+    slow_rows<DK, DV, SHARED, MX, WAVES>(p, it, tk_begin, tk_end);
     return;
   }
   const float m = w.m;
@@ -756,24 +797,23 @@ void tree_attn_kernel(AttnParams p) {
     const u32x2_t x = swap_halves(__float_as_uint(l), __float_as_uint(l));
     l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
   }
-  if (it.chunks == 1) {
+  if (!live) return;
+  if (it.whole) {
     const float inv = l == 0 ? 0.0f : 1.0f / l;
-    if (live) {
-      uint16_t* dst = p.out + qt * p.o_t + h * p.o_h;
+    uint16_t* dst = p.out + qt * p.o_t + h * p.o_h;
 #pragma unroll
-      for (int n = 0; n < S::NT; ++n)
+    for (int n = 0; n < S::NT; ++n)
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * half) =
-              make_uint2(pack_bf16x2(w.o[n][4 * g] * inv, w.o[n][4 * g + 1] * inv),
-                         pack_bf16x2(w.o[n][4 * g + 2] * inv, w.o[n][4 * g + 3] * inv));
-      if (p.lse && half == 0)
-        p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
-    }
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * half) =
+            make_uint2(pack_bf16x2(w.o[n][4 * g] * inv, w.o[n][4 * g + 1] * inv),
+                       pack_bf16x2(w.o[n][4 * g + 2] * inv, w.o[n][4 * g + 3] * inv));
+    if (p.lse && half == 0)
+      p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
     return;
   }
   // partial result, in register order: [slot][wave][32 DV floats as NT * 4 vectors of 64 lanes]
-  const int64_t slot = ((((int64_t)it.j * p.H_kv + it.kvh) * p.plan.row_tiles + it.rt) * p.plan.chunks + it.chunk) * WAVES + wave;
+  const int64_t slot = it.slot * WAVES + wave;
   f32x4_t* po = reinterpret_cast<f32x4_t*>(p.part_o) + slot * (DV * 8);
 #pragma unroll
   for (int n = 0; n < S::NT; ++n)
@@ -783,38 +823,184 @@ void tree_attn_kernel(AttnParams p) {
   if (half == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + l32] = make_float2(m, l);
 }
 
-// Joins the chunks of a row tile's wave: out = sum_c 2^(m_c - M) O_c / sum_c
-// 2^(m_c - M) l_c, chunk by chunk in order. A thread takes one 4-element vector
-// of one query row in every chunk.
+// Chunked plan: a workgroup an item.
+template <int DK, int DV, bool SHARED, bool MX, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(1, 4)))
+void tree_attn_kernel(AttnParams p) {
+  using S = Shape<DK, DV, SHARED, MX, WAVES>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  __shared__ int s_page[MAX_CHUNK_PAGES];
+  // consecutive items (row tiles that read the same chunk) go to one XCD's L2
+  const int64_t per = gridDim.x / 8;
+  Item it;
+  int chunk;
+  if (!find_item(p, (blockIdx.x % 8) * per + blockIdx.x / 8, it, chunk)) return;
+  if (it.broken) {
+    if (chunk == 0 && it.rt == 0) write_nan(p, it);
+    return;
+  }
+  const int tk_begin = chunk * p.plan.chunk;
+  const int tk_end = min(tk_begin + p.plan.chunk, it.total);
+  if (it.rt * 32 * WAVES >= it.rows || tk_begin >= tk_end) return;
+  run_item<DK, DV, SHARED, MX, WAVES>(p, it, lds, s_page, tk_begin, tk_end, p.plan.chunk);
+}
+
+// Even plan: a workgroup a run of steps. Every workgroup finds its first
+// sequence from a sum over all of them; the first one leaves the sums for the
+// join.
+template <bool MX>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void tree_attn_even_kernel(AttnParams p) {
+  using S = Shape<576, 512, true, MX, 4>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
+  __shared__ int s_page[MAX_CHUNK_PAGES];
+  __shared__ int64_t s_sum[4], s_base;
+  __shared__ int s_seq;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  Item it;
+  // a run of sequences per thread
+  const int per = (p.nseq + 255) / 256;
+  const int j0 = min(tid * per, p.nseq), j1 = min(j0 + per, p.nseq);
+  int64_t sum = 0;
+  int broken = 0;
+  for (int j = j0; j < j1; ++j) {
+    load_seq(p, j, it);
+    sum += steps_of(p, it);
+    broken |= it.broken && it.n > 0;
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) s_sum[wave] = inc;
+  if (__syncthreads_or(broken)) {
+    for (int j = blockIdx.x; j < p.nseq; j += gridDim.x) {
+      load_seq_uniform(p, j, it);
+      if (it.broken)
+        for (it.kvh = 0; it.kvh < p.H_kv; ++it.kvh) write_nan(p, it);
+    }
+  }
+  int64_t W = 0, before = inc - sum;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    before += w < wave ? s_sum[w] : 0;
+    W += s_sum[w];
+  }
+  if (W == 0) return;
+  const int G = workgroups_for(p, W);
+  // consecutive runs go to one XCD: row tiles of a sequence share its L2
+  const int runs = (G + 7) / 8;
+  const int b = (blockIdx.x % 8) * runs + blockIdx.x / 8;
+  if (blockIdx.x == 0 && G > 1) {
+    int64_t at = before;
+    for (int j = j0; j < j1; ++j) {
+      p.sums[2 + j] = at;
+      load_seq(p, j, it);
+      at += steps_of(p, it);
+    }
+    if (tid == 0) {
+      p.sums[0] = W;
+      p.sums[1] = G;
+    }
+  }
+  if ((int)(blockIdx.x / 8) >= runs || b >= G) return;
+  const int64_t begin = first_step(W, G, b), end = first_step(W, G, b + 1);
+  if (before <= begin && begin < before + sum) {
+    int64_t at = before;
+    for (int j = j0; j < j1; ++j) {
+      load_seq(p, j, it);
+      const int64_t n = steps_of(p, it);
+      if (begin < at + n) {
+        s_seq = j;
+        s_base = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int j = __builtin_amdgcn_readfirstlane(s_seq);
+  int64_t base = s_base;  // steps before sequence j
+  for (int64_t step = begin; step < end;) {
+    load_seq_uniform(p, j, it);
+    const int tiles = tiles_of(it);
+    const int64_t n = steps_of(p, it);
+    if (step >= base + n) {  // on to the next sequence that has steps
+      base += n;
+      ++j;
+      continue;
+    }
+    const int item = __builtin_amdgcn_readfirstlane((int)((step - base) / tiles));
+    const int first = __builtin_amdgcn_readfirstlane((int)(step - base - (int64_t)item * tiles));
+    const int last = (int)min((int64_t)tiles, first + (end - step));
+    it.kvh = item / row_tiles_of(it);
+    it.rt = item - it.kvh * row_tiles_of(it);
+    it.whole = first == 0 && last == tiles;
+    it.slot = 2 * b + (step == begin ? 0 : 1);
+    run_item<576, 512, true, MX, 4>(p, it, lds, s_page, first * TILE, min(last * TILE, it.total), p.plan.chunk);
+    step += last - first;
+  }
+}
+
+// Joins the partial results of a row tile's wave: out = sum_c 2^(m_c - M) O_c /
+// sum_c 2^(m_c - M) l_c, in the order of the cache rows. A thread takes one
+// 4-element vector of one query row of every part.
+template <bool EVEN>
 __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks) {
   const int waves = p.plan.waves;
   int64_t b = blockIdx.x;
   const int vb = (int)(b % vec_blocks);
   b /= vec_blocks;
   const int wave = (int)(b % waves);
-  b /= waves;
-  Item it;
-  // item numbering with the chunk left out
-  const int64_t tile = b;
+  const int64_t tile = b / waves;
   const int64_t head = tile / p.plan.row_tiles;
-  if (!find_item(p, head * p.plan.chunks * p.plan.row_tiles + tile % p.plan.row_tiles, it)) return;
-  if (it.broken || it.chunks == 1) return;
+  Item it;
+  int chunk = 0, parts, first = 0;  // parts in order: slots at(0) .. at(parts - 1)
+  int64_t slot0 = 0;
+  if constexpr (EVEN) {
+    it.kvh = (int)(head % p.H_kv);
+    it.rt = (int)(tile % p.plan.row_tiles);
+    const int j = (int)(head / p.H_kv);
+    load_seq_uniform(p, j, it);
+    if (it.broken || it.rt >= row_tiles_of(it)) return;
+    const int64_t W = p.sums[0], s0 = p.sums[2 + j] + (int64_t)(it.kvh * row_tiles_of(it) + it.rt) * tiles_of(it);
+    const int64_t s1 = s0 + tiles_of(it);
+    const int G = (int)p.sums[1];
+    first = (int)(s0 * G / W);  // the workgroup of step s0
+    while (first_step(W, G, first + 1) <= s0) ++first;
+    while (first > 0 && first_step(W, G, first) > s0) --first;
+    if (first_step(W, G, first + 1) >= s1) return;  // all of it: the result is there
+    parts = 1;
+    while (first_step(W, G, first + parts) < s1) ++parts;
+    slot0 = 2 * first + (first_step(W, G, first) < s0 ? 1 : 0);
+  } else {
+    if (!find_item(p, head * p.plan.chunks * p.plan.row_tiles + tile % p.plan.row_tiles, it, chunk)) return;
+    if (it.broken || it.whole) return;
+    parts = (it.total + p.plan.chunk - 1) / p.plan.chunk;
+    slot0 = it.slot;
+  }
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
   const int v = vb * 4 + (threadIdx.x >> 6);  // vector of the row: 8-column group n * 4 + g
   const int row = (it.rt * waves + wave) * 32 + l32;
   if (v * 8 >= p.d_v || row >= it.rows) return;
-  const int64_t slot0 = (tile * p.plan.chunks) * waves + wave;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot0 * 32 + l32;
-  const f32x4_t* po = reinterpret_cast<const f32x4_t*>(p.part_o) + slot0 * (p.d_v * 8) + v * 64 + lane;
+  // place of part c
+  auto at = [&](int c) {
+    const int64_t s = c == 0 ? slot0 : EVEN ? 2 * (int64_t)(first + c) : slot0 + (int64_t)c * p.plan.row_tiles;
+    return s * waves + wave;
+  };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + l32;
+  const f32x4_t* po = reinterpret_cast<const f32x4_t*>(p.part_o) + v * 64 + lane;
   float M = NEG_INF;
-  for (int c = 0; c < it.chunks; ++c) M = fmaxf(M, ml[(int64_t)c * waves * 32].x);
+  for (int c = 0; c < parts; ++c) M = fmaxf(M, ml[at(c) * 32].x);
   const float Mu = M == NEG_INF ? 0.0f : M;
   float l = 0;
   f32x4_t acc = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int c = 0; c < it.chunks; ++c) {
-    const float2 e = ml[(int64_t)c * waves * 32];
-    const f32x4_t x = po[(int64_t)c * waves * (p.d_v * 8)];
+  for (int c = 0; c < parts; ++c) {
+    const float2 e = ml[at(c) * 32];
+    const f32x4_t x = po[at(c) * (p.d_v * 8)];
     const float w = exp2_hw(e.x - Mu);
     l += w * e.y;
 #pragma unroll
@@ -832,11 +1018,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks)
 
 template <int DK, int DV, bool SHARED, bool MX>
 void launch_shape(const AttnParams& p, unsigned grid, hipStream_t stream) {
-  if constexpr (DV > 256) {
-    hipLaunchKernelGGL((tree_attn_kernel<DK, DV, SHARED, MX, 4>), dim3(grid), dim3(256), 0, stream, p);
-    return;
-  }
-  else if (p.plan.waves == 1)
+  if (p.plan.waves == 1)
     hipLaunchKernelGGL((tree_attn_kernel<DK, DV, SHARED, MX, 1>), dim3(grid), dim3(64), 0, stream, p);
   else if (p.plan.waves == 2)
     hipLaunchKernelGGL((tree_attn_kernel<DK, DV, SHARED, MX, 2>), dim3(grid), dim3(128), 0, stream, p);
@@ -857,15 +1039,20 @@ hipError_t launch_tree_attn(const AttnParams& p, hipStream_t stream) {
   const int64_t items = tiles * p.plan.chunks;
   if (items == 0 || p.T == 0) return hipSuccess;
   const unsigned grid = (unsigned)((items + 7) / 8 * 8);
-  if (p.d_k == 576) launch_dtype<576, 512, true>(p, grid, stream);
-  else if (p.d_k == 96) launch_dtype<96, 64, true>(p, grid, stream);
+  if (p.plan.groups > 0) {
+    const dim3 g((unsigned)((p.plan.groups + 7) / 8 * 8));
+    if (p.mx) hipLaunchKernelGGL(tree_attn_even_kernel<true>, g, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(tree_attn_even_kernel<false>, g, dim3(256), 0, stream, p);
+  } else if (p.d_k == 96) launch_dtype<96, 64, true>(p, grid, stream);
   else if (p.d_k == 192) launch_dtype<192, 128, false>(p, grid, stream);
   else if (p.d_k == 128) launch_dtype<128, 128, false>(p, grid, stream);
   else launch_dtype<64, 64, false>(p, grid, stream);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.plan.chunks == 1) return e;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (p.plan.groups > 0 ? p.plan.groups == 1 : p.plan.chunks == 1)) return e;
   const int vec_blocks = (p.d_v / 8 + 3) / 4;
-  hipLaunchKernelGGL(join_kernel, dim3((unsigned)(tiles * p.plan.waves * vec_blocks)), dim3(256), 0, stream, p, vec_blocks);
+  const dim3 join((unsigned)(tiles * p.plan.waves * vec_blocks));
+  if (p.plan.groups > 0) hipLaunchKernelGGL(join_kernel<true>, join, dim3(256), 0, stream, p, vec_blocks);
+  else hipLaunchKernelGGL(join_kernel<false>, join, dim3(256), 0, stream, p, vec_blocks);
   return hipGetLastError();
 }
 
