@@ -389,13 +389,13 @@ AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int m
     pl.chunk = (int)most;
     pl.chunks = 1;
     const double steps = std::max(1.0, (double)nseq * H_kv * (double)tiles * ((max_len + 31) / 32));
-    pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(28.0 * steps)) + 1});
+    pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(17.0 * steps)) + 1});
     if (pl.groups > 1) {
       const size_t slots = (size_t)2 * pl.groups * pl.waves;
       pl.part_o = 0;
       pl.part_ml = slots * 32 * (size_t)d_v * 4;
       pl.sums = pl.part_ml + slots * 32 * 8;
-      pl.total = pl.sums + ((size_t)nseq + 2) * 8;
+      pl.total = pl.sums + ((size_t)nseq + 3) * 8;
     }
     return pl;
   }
@@ -439,9 +439,10 @@ mla_status check_attn(const mla_tree_attn_args* a, mla::AttnPlan* plan) {
     return MLA_EINVAL;
   if ((int64_t)a->max_q * (a->H / a->H_kv) > INT32_MAX / 2) return MLA_EINVAL;
   *plan = mla::plan_attn(a->T, a->nseq, a->H, a->H_kv, a->d_k, a->d_v, a->max_q, a->max_len, a->pool->page_size);
-  // grids stay within 2^31 workgroups' work-items
+  // every grid stays within 2^31 work-items
   const double items = (double)a->nseq * a->H_kv * plan->row_tiles * plan->chunks;
-  if (items > (1 << 23) || items * plan->waves * (a->d_v / 32) > (double)(1 << 24)) return MLA_EINVAL;
+  const double joins = (double)a->nseq * a->H_kv * plan->row_tiles * plan->waves * (a->d_v / 8);
+  if (items > (1 << 23) || joins > (double)(1 << 23)) return MLA_EINVAL;
   return MLA_OK;
 }
 

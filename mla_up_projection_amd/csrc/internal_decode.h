@@ -114,7 +114,7 @@ struct AttnParams {
   uint32_t page_magic;  // ceil(2^32 / page_size): quotient of small rows by a high product
   float* part_o;
   float* part_ml;
-  int64_t* sums;  // even plan: all steps, workgroups, steps before each sequence
+  int64_t* sums;  // even plan: units, workgroups, quantum, units before each sequence
   AttnPlan plan;
 };
 bool attn_shape_supported(int d_k, int d_v, bool shared);

@@ -65,9 +65,9 @@ __device__ __forceinline__ void load_seq(const AttnParams& p, int j, Item& it) {
   it.broken |= it.len < 0 || it.len > p.max_len - it.n;
   it.total = it.len + it.n;
 }
-// The same in scalar registers, for a j that all lanes share.
-__device__ __forceinline__ void load_seq_uniform(const AttnParams& p, int j, Item& it) {
-  load_seq(p, j, it);
+// What all lanes agree on goes to scalar registers.
+__device__ __forceinline__ void uniform(const AttnParams& p, Item& it) {
+  it.j = __builtin_amdgcn_readfirstlane(it.j);
   it.t0 = __builtin_amdgcn_readfirstlane(it.t0);
   it.n = __builtin_amdgcn_readfirstlane(it.n);
   it.rows = it.n * p.group;
@@ -75,6 +75,10 @@ __device__ __forceinline__ void load_seq_uniform(const AttnParams& p, int j, Ite
   it.len = __builtin_amdgcn_readfirstlane(it.len);
   it.broken = __builtin_amdgcn_readfirstlane(it.broken);
   it.total = it.len + it.n;
+}
+__device__ __forceinline__ void load_seq_uniform(const AttnParams& p, int j, Item& it) {
+  load_seq(p, j, it);
+  uniform(p, it);
 }
 
 // Chunked plan: item number -> item and its chunk; false if there is none.
@@ -92,21 +96,34 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int64_t item, Ite
   return it.n > 0;
 }
 
-// Even plan (the widest shape): the steps of all items, one cache tile of one
-// row tile each, are numbered through, and workgroup b of G takes the steps
-// [b W / G, (b + 1) W / G). Steps of sequence j:
+// Even plan (the widest shape). A step is one cache tile of one row tile; the
+// call has W of them in `items` row tiles. Two ways to divide them over
+// workgroups, chosen by each from the lengths on the device:
+//  - many workgroups per item: an item is cut into parts of at most `quantum`
+//    steps, a workgroup takes one part (a second item would cost it another 10 us
+//    for queries, pages and the first tiles);
+//  - few: the steps are numbered through, and workgroup b of G takes the steps
+//    [b W / G, (b + 1) W / G), so that all end at the same time.
+// Units below are parts (quantum > 0, one per workgroup) or steps.
 constexpr int WIDE_ROWS = 128;
 __device__ __forceinline__ int row_tiles_of(const Item& it) { return (it.rows + WIDE_ROWS - 1) / WIDE_ROWS; }
 __device__ __forceinline__ int tiles_of(const Item& it) { return (it.total + TILE - 1) / TILE; }
-__device__ __forceinline__ int64_t steps_of(const AttnParams& p, const Item& it) {
-  return it.broken || it.n == 0 ? 0 : (int64_t)p.H_kv * row_tiles_of(it) * tiles_of(it);
+__device__ __forceinline__ int units_of_item(const Item& it, int quantum) {
+  return quantum ? (tiles_of(it) + quantum - 1) / quantum : tiles_of(it);
 }
-__device__ __forceinline__ int64_t first_step(int64_t W, int G, int b) { return W * b / G; }
+__device__ __forceinline__ int64_t units_of(const AttnParams& p, const Item& it, int quantum) {
+  return it.broken || it.n == 0 ? 0 : (int64_t)p.H_kv * row_tiles_of(it) * units_of_item(it, quantum);
+}
+__device__ __forceinline__ int64_t first_unit(int64_t units, int G, int b) { return units * b / G; }
 // More workgroups shorten the longest but write more partial results: a step
-// takes 2.2 us, a partial result (256 KB out and in again) 0.08 us of all
-// workgroups' time, and W 2.2 / G + 0.08 G is least at G = sqrt(28 W).
+// takes 2 us, a partial result (256 KB out and in again) 0.12 us of all
+// workgroups' time, and W 2 / G + 0.12 G is least at G = sqrt(17 W).
 __device__ __forceinline__ int workgroups_for(const AttnParams& p, int64_t W) {
-  return (int)min((int64_t)p.plan.groups, min(W, (int64_t)max(1.0f, sqrtf(28.0f * (float)W))));
+  return (int)min((int64_t)p.plan.groups, min(W, (int64_t)max(1.0f, sqrtf(17.0f * (float)W))));
+}
+// sum over items of ceil(steps / quantum) <= W / quantum + items <= G
+__device__ __forceinline__ int quantum_for(int64_t W, int64_t items, int G) {
+  return 4 * items <= G ? (int)((W + (G - items) - 1) / (G - items)) : 0;
 }
 
 // Every row of a broken sequence, by one workgroup.
@@ -200,21 +217,56 @@ struct Worker {
   int page0, tk_begin, tk_end;
   bool odd;  // a value that is not finite lies in a tile that some rows do not see whole
   // the lane's query row
-  int64_t qt;
-  int qi;
   bf16x8_t q[S::KK];
   f32x16_t o[S::NT];
   float m, top, l;  // reference, largest score, sum of weights
   // LDS offsets of the first fragments. A tile starts at a multiple of 128
   // bytes, so the others differ in single bits.
   uint32_t koff0, voff0;
-  int half, tid, wave;
+  int tid, wave;
   // MXFP8: the next tile's codes and scales, on their way to LDS as bf16
   static constexpr int HELD = MX && S::RPT == 1 && !S::WIDE ? S::NB : 1;
   uint2 code[HELD];
   uint32_t sc[HELD];
 
   __device__ __forceinline__ Worker(const AttnParams& p_, const Item& it_) : p(p_), it(it_) {}
+
+  // The thread's number, anew: what follows from it is then worked out where it
+  // is used instead of occupying registers all through the loop.
+  __device__ __forceinline__ int thread() const {
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    return t;
+  }
+
+  // The lane's query row: draft qi, token qt, head h.
+  struct Row {
+    int l32, half, qi, h;
+    int64_t qt;
+    bool live;
+  };
+  __device__ __forceinline__ Row row() const {
+    const int lane = thread() & 63;
+    Row r;
+    r.l32 = lane & 31;
+    r.half = lane >> 5;
+    const int at = (it.rt * WAVES + wave) * 32 + r.l32;
+    r.live = at < it.rows;
+    r.qi = r.live ? at / p.group : 0;
+    r.qt = it.t0 + r.qi;
+    r.h = it.kvh * p.group + (r.live ? at - r.qi * p.group : 0);
+    return r;
+  }
+
+  // K: chunk 2 c + half of a block's rows. V: rows 8 e + 4 half + .., columns
+  // 32 c + .. of a block.
+  __device__ __forceinline__ uint32_t k_at(uint32_t tile, int c) const { return (tile + koff0) ^ (32 * c); }
+  __device__ __forceinline__ uint32_t v_at(uint32_t tile, int e, int c) const {
+    return ((tile + voff0) ^ (16 * e + 64 * c)) + 1024 * e;
+  }
+
+  typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+  typedef __attribute__((address_space(3))) const bf16x8_t lds_bf16x8;
 
   // Row (of width d) of cache row tok; rows behind the chunk read its last one.
   __device__ __forceinline__ int64_t cache_row(int tok) const {
@@ -254,14 +306,6 @@ struct Worker {
     uint32_t to = 0;
     uint64_t live = 0;  // lanes that load
   };
-  // The thread's number, anew: what follows from it is then worked out where it
-  // is used instead of occupying registers all through the loop.
-  __device__ __forceinline__ int thread() const {
-    int t = tid;
-    asm volatile("" : "+v"(t));
-    return t;
-  }
-
   __device__ __forceinline__ Next next_loads(int tk, int slot) const {
     const int tid = thread(), r = tid >> 3;
     const int64_t row = cache_row(tk + r);
@@ -277,15 +321,41 @@ struct Worker {
     return Next{src, (uint32_t)__builtin_amdgcn_readfirstlane(to), ~(uint64_t)0};
   }
 
-  // The same loads in a burst, outside the loop and for waves without rows.
+  // Such loads in a burst: `blocks` of 128 bytes, and half a block more.
+  __device__ __forceinline__ static void load_now(const Next& n, int blocks, bool half_more) {
+    for (int b = 0; b < blocks; ++b) dma16_far(n.src + 128 * b, n.to + b * BLK);
+    if (half_more && (threadIdx.x & 7) < 4) dma16_far(n.src + 128 * blocks, n.to + blocks * BLK);
+  }
+  // next_loads() outside the loop and for waves without rows
   __device__ __forceinline__ void load_now(const Next& n) const {
-    if (!n.live) {
-      vm_wait<0>();
-      return;
-    }
+    if (n.live) load_now(n, MX ? 4 : S::NB, MX);
+    else vm_wait<0>();
+  }
+
+  // Query rows 32 g .. + 31 of the row tile, as a tile of the ring: 128 bytes of a
+  // row at a time instead of the 32 that a fragment's lanes would ask for
+  // (7 drafts x 8 sequences of 1000, 32 heads: 11 of 43 us less). Rows that there
+  // are not repeat the last.
+  __device__ __forceinline__ void load_queries(int g, int slot) const {
+    const int tid = thread(), r = tid >> 3;
+    const int row = min((it.rt * WAVES + g) * 32 + r, it.rows - 1), i = row / p.group;
+    const uint16_t* src = p.q + (it.t0 + i) * p.q_t + (it.kvh * p.group + row - i * p.group) * p.q_h + 8 * ((tid & 7) ^ swz(r));
+    load_now(Next{reinterpret_cast<const uint8_t*>(src), lds_u32(lds) + slot * S::TILE_LDS + wave * 1024, 1}, S::NBK, false);
+  }
+  // All queries. LDS must be free (four tiles of it; of an MXFP8 ring the fourth
+  // lies where codes come in); it is again for those who meet at the next barrier
+  // after take_queries().
+  __device__ __forceinline__ void ask_queries() const {
+    static_assert(S::LDS >= 4 * S::TILE_LDS, "room for four tiles");
+    for (int g = 0; g < 4; ++g)
+      if ((it.rt * WAVES + g) * 32 < it.rows) load_queries(g, g);
+  }
+  __device__ __forceinline__ void take_queries() {
+    vm_wait<0>();
+    barrier_reads_done();
 #pragma unroll
-    for (int b = 0; b < (MX ? 4 : S::NB); ++b) dma16_far(n.src + 128 * b, n.to + b * BLK);
-    if (MX && (tid & 7) < 4) dma16_far(n.src + 512, n.to + 4 * BLK);
+    for (int kk = 0; kk < S::KK; ++kk)
+      q[kk] = *(lds_bf16x8*)(uintptr_t)(k_at(lds_u32(lds) + wave * S::TILE_LDS, kk & 3) + (kk >> 2) * BLK);
   }
 
   // WIDE MXFP8: a row's 18 scale bytes, in the five aligned words that hold
@@ -344,16 +414,6 @@ struct Worker {
       *reinterpret_cast<u32x4_t*>(lds + slot * S::TILE_LDS + b * BLK + r * 128 + ((tid & 7) << 4)) = v;
     }
   }
-
-  // K: chunk 2 c + half of a block's rows. V: rows 8 e + 4 half + .., columns
-  // 32 c + .. of a block.
-  __device__ __forceinline__ uint32_t k_at(uint32_t tile, int c) const { return (tile + koff0) ^ (32 * c); }
-  __device__ __forceinline__ uint32_t v_at(uint32_t tile, int e, int c) const {
-    return ((tile + voff0) ^ (16 * e + 64 * c)) + 1024 * e;
-  }
-
-  typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-  typedef __attribute__((address_space(3))) const bf16x8_t lds_bf16x8;
 
   // V^T fragment of value columns 32 n .. + 31 and the tile's 16-row step c
   __device__ __forceinline__ u32x4_t v_frag(const uint8_t* tile, int n, int c) const {
@@ -426,9 +486,10 @@ struct Worker {
   // A tile that ends the sequence or the chunk or holds drafts. Scores of rows
   // that the lane's query does not see become -infinity.
   __device__ __forceinline__ void mask(f32x16_t& s, int tk) const {
-    uint32_t vis = visible(p, it, qt, qi, tk);
+    const Row r = row();
+    uint32_t vis = visible(p, it, r.qt, r.qi, tk);
     if (tk_end - tk < TILE) vis &= (1u << (tk_end - tk)) - 1;
-    vis >>= 4 * half;
+    vis >>= 4 * r.half;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = vis & (1u << (8 * (i / 4) + i % 4)) ? s[i] : NEG_INF;
   }
@@ -745,26 +806,27 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
   const int l32 = lane & 31, half = lane >> 5;
   w.tid = tid;
   w.wave = wave;
-  w.half = half;
   w.lds = lds;
   w.s_page = s_page;
-  // this lane's query row
-  const int row = it.rt * 32 * WAVES + wave * 32 + l32;
-  const bool live = row < it.rows;
-  const int qi = live ? row / p.group : 0;
-  const int64_t qt = it.t0 + qi;
-  const int h = it.kvh * p.group + (live ? row - qi * p.group : 0);
-  w.qt = qt;
-  w.qi = qi;
-#pragma unroll
-  for (int kk = 0; kk < S::KK; ++kk)
-    w.q[kk] = *reinterpret_cast<const bf16x8_t*>(p.q + qt * p.q_t + h * p.q_h + 16 * kk + 8 * half);
   w.m = NEG_INF;
   // K: row l32, chunk half. V: rows 4 half + 0..3, 16 columns per 16 lanes
   w.koff0 = l32 * 128 + ((half ^ swz(l32)) << 4);
   const int q4 = lane & 15, vt = 4 * half + (q4 >> 2);
   w.voff0 = vt * 128 + (((2 * ((lane >> 4) & 1) + ((q4 & 3) >> 1)) ^ swz(vt)) << 4) + (q4 & 1) * 8;
 
+  bool filled = S::WIDE, bad = false;  // the first part's pages are listed
+  if constexpr (S::WIDE) {
+    __syncthreads();  // LDS is read
+    w.ask_queries();
+    w.page0 = tk_begin / p.pool.page_size;
+    bad = fill_pages<S::THREADS>(p, it, s_page, w.page0, min(tk_begin + most, tk_end));  // while they come
+    w.take_queries();
+  } else {
+    const auto r = w.row();
+#pragma unroll
+    for (int kk = 0; kk < S::KK; ++kk)
+      w.q[kk] = *reinterpret_cast<const bf16x8_t*>(p.q + r.qt * p.q_t + r.h * p.q_h + 16 * kk + 8 * half);
+  }
   bool slow;
   while (true) {
     w.clear();
@@ -776,7 +838,9 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
       w.tk_end = end;
       w.page0 = begin / p.pool.page_size;
       __syncthreads();  // LDS is read: the list may change and tiles come in
-      slow = fill_pages<S::THREADS>(p, it, s_page, w.page0, end);
+      if (!filled || begin > tk_begin) bad = fill_pages<S::THREADS>(p, it, s_page, w.page0, end);
+      filled = begin == tk_begin && (!S::WIDE || end == tk_end);  // for a second pass
+      slow = bad;
       if (slow) break;
       // tiles before the first draft and wholly inside the part need no mask
       const int full = max(0, (min(end, it.len) - begin) / TILE);
@@ -797,19 +861,20 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     const u32x2_t x = swap_halves(__float_as_uint(l), __float_as_uint(l));
     l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
   }
-  if (!live) return;
+  const auto r = w.row();
+  if (!r.live) return;
   if (it.whole) {
     const float inv = l == 0 ? 0.0f : 1.0f / l;
-    uint16_t* dst = p.out + qt * p.o_t + h * p.o_h;
+    uint16_t* dst = p.out + r.qt * p.o_t + r.h * p.o_h;
 #pragma unroll
     for (int n = 0; n < S::NT; ++n)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * half) =
+        *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * r.half) =
             make_uint2(pack_bf16x2(w.o[n][4 * g] * inv, w.o[n][4 * g + 1] * inv),
                        pack_bf16x2(w.o[n][4 * g + 2] * inv, w.o[n][4 * g + 3] * inv));
-    if (p.lse && half == 0)
-      p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    if (p.lse && r.half == 0)
+      p.lse[r.qt * p.H + r.h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
     return;
   }
   // partial result, in register order: [slot][wave][32 DV floats as NT * 4 vectors of 64 lanes]
@@ -819,8 +884,8 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
   for (int n = 0; n < S::NT; ++n)
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      po[(n * 4 + g) * 64 + lane] = f32x4_t{w.o[n][4 * g], w.o[n][4 * g + 1], w.o[n][4 * g + 2], w.o[n][4 * g + 3]};
-  if (half == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + l32] = make_float2(m, l);
+      po[(n * 4 + g) * 64 + 32 * r.half + r.l32] = f32x4_t{w.o[n][4 * g], w.o[n][4 * g + 1], w.o[n][4 * g + 2], w.o[n][4 * g + 3]};
+  if (r.half == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r.l32] = make_float2(m, l);
 }
 
 // Chunked plan: a workgroup an item.
@@ -845,8 +910,29 @@ void tree_attn_kernel(AttnParams p) {
   run_item<DK, DV, SHARED, MX, WAVES>(p, it, lds, s_page, tk_begin, tk_end, p.plan.chunk);
 }
 
-// Even plan: a workgroup a run of steps. Every workgroup finds its first
-// sequence from a sum over all of them; the first one leaves the sums for the
+// Sum of v over the workgroup's earlier threads (256); all: over all of them.
+__device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* lds, int64_t& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t inc = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 63) lds[wave] = inc;
+  __syncthreads();
+  int64_t before = inc - v;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    before += w < wave ? lds[w] : 0;
+    all += lds[w];
+  }
+  return before;
+}
+
+// Even plan: a workgroup a run of units. Every workgroup finds its first
+// sequence from sums over all of them; the first one leaves the sums for the
 // join.
 template <bool MX>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
@@ -854,66 +940,67 @@ void tree_attn_even_kernel(AttnParams p) {
   using S = Shape<576, 512, true, MX, 4>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   __shared__ int s_page[MAX_CHUNK_PAGES];
-  __shared__ int64_t s_sum[4], s_base;
-  __shared__ int s_seq;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int64_t s_sum[3][4], s_base;
+  __shared__ Item s_item;
+  const int tid = threadIdx.x;
   Item it;
   // a run of sequences per thread
   const int per = (p.nseq + 255) / 256;
   const int j0 = min(tid * per, p.nseq), j1 = min(j0 + per, p.nseq);
-  int64_t sum = 0;
+  int64_t steps = 0, items = 0, W, all_items;
   int broken = 0;
   for (int j = j0; j < j1; ++j) {
     load_seq(p, j, it);
-    sum += steps_of(p, it);
+    const int64_t n = units_of(p, it, 0);
+    steps += n;
+    items += n ? (int64_t)p.H_kv * row_tiles_of(it) : 0;
     broken |= it.broken && it.n > 0;
   }
-  int64_t inc = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(inc, d);
-    if (lane >= d) inc += o;
-  }
-  if (lane == 63) s_sum[wave] = inc;
+  sum_before(items, s_sum[0], all_items);
+  sum_before(steps, s_sum[1], W);
   if (__syncthreads_or(broken)) {
+    Item bad;
     for (int j = blockIdx.x; j < p.nseq; j += gridDim.x) {
-      load_seq_uniform(p, j, it);
-      if (it.broken)
-        for (it.kvh = 0; it.kvh < p.H_kv; ++it.kvh) write_nan(p, it);
+      load_seq_uniform(p, j, bad);
+      if (bad.broken)
+        for (bad.kvh = 0; bad.kvh < p.H_kv; ++bad.kvh) write_nan(p, bad);
     }
   }
-  int64_t W = 0, before = inc - sum;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    before += w < wave ? s_sum[w] : 0;
-    W += s_sum[w];
-  }
   if (W == 0) return;
-  const int G = workgroups_for(p, W);
+  int G = workgroups_for(p, W);
+  const int quantum = quantum_for(W, all_items, G);
+  int64_t mine = 0, units;
+  for (int j = j0; j < j1; ++j) {
+    if (per > 1) load_seq(p, j, it);  // (else `it` is that sequence)
+    mine += units_of(p, it, quantum);
+  }
+  const int64_t before = sum_before(mine, s_sum[2], units);
+  if (quantum) G = (int)units;
   // consecutive runs go to one XCD: row tiles of a sequence share its L2
   const int runs = (G + 7) / 8;
   const int b = (blockIdx.x % 8) * runs + blockIdx.x / 8;
-  if (blockIdx.x == 0 && G > 1) {
+  if (blockIdx.x == 0 && p.plan.groups > 1) {
     int64_t at = before;
     for (int j = j0; j < j1; ++j) {
-      p.sums[2 + j] = at;
-      load_seq(p, j, it);
-      at += steps_of(p, it);
+      p.sums[3 + j] = at;
+      if (per > 1) load_seq(p, j, it);
+      at += units_of(p, it, quantum);
     }
     if (tid == 0) {
-      p.sums[0] = W;
+      p.sums[0] = units;
       p.sums[1] = G;
+      p.sums[2] = quantum;
     }
   }
   if ((int)(blockIdx.x / 8) >= runs || b >= G) return;
-  const int64_t begin = first_step(W, G, b), end = first_step(W, G, b + 1);
-  if (before <= begin && begin < before + sum) {
+  const int64_t begin = first_unit(units, G, b), end = first_unit(units, G, b + 1);
+  if (before <= begin && begin < before + mine) {
     int64_t at = before;
     for (int j = j0; j < j1; ++j) {
-      load_seq(p, j, it);
-      const int64_t n = steps_of(p, it);
+      if (per > 1) load_seq(p, j, it);
+      const int64_t n = units_of(p, it, quantum);
       if (begin < at + n) {
-        s_seq = j;
+        s_item = it;
         s_base = at;
         break;
       }
@@ -921,33 +1008,38 @@ void tree_attn_even_kernel(AttnParams p) {
     }
   }
   __syncthreads();
-  int j = __builtin_amdgcn_readfirstlane(s_seq);
-  int64_t base = s_base;  // steps before sequence j
-  for (int64_t step = begin; step < end;) {
-    load_seq_uniform(p, j, it);
-    const int tiles = tiles_of(it);
-    const int64_t n = steps_of(p, it);
-    if (step >= base + n) {  // on to the next sequence that has steps
+  it = s_item;
+  uniform(p, it);
+  int64_t base = s_base;  // units before the sequence
+  for (int64_t unit = begin; unit < end;) {
+    const int tiles = tiles_of(it), each = units_of_item(it, quantum);
+    const int64_t n = units_of(p, it, quantum);
+    if (unit >= base + n) {  // on to the next sequence that has units
       base += n;
-      ++j;
+      if (it.j + 1 >= p.nseq) break;
+      load_seq(p, it.j + 1, it);
+      uniform(p, it);
       continue;
     }
-    const int item = __builtin_amdgcn_readfirstlane((int)((step - base) / tiles));
-    const int first = __builtin_amdgcn_readfirstlane((int)(step - base - (int64_t)item * tiles));
-    const int last = (int)min((int64_t)tiles, first + (end - step));
+    const int item = __builtin_amdgcn_readfirstlane((int)((unit - base) / each));
+    const int at = __builtin_amdgcn_readfirstlane((int)(unit - base - (int64_t)item * each));
+    const int count = quantum ? 1 : (int)min((int64_t)(each - at), end - unit);
+    const int first = quantum ? (int)((int64_t)tiles * at / each) : at;
+    const int last = quantum ? (int)((int64_t)tiles * (at + 1) / each) : at + count;
     it.kvh = item / row_tiles_of(it);
     it.rt = item - it.kvh * row_tiles_of(it);
     it.whole = first == 0 && last == tiles;
-    it.slot = 2 * b + (step == begin ? 0 : 1);
+    it.slot = 2 * b + (unit == begin ? 0 : 1);
     run_item<576, 512, true, MX, 4>(p, it, lds, s_page, first * TILE, min(last * TILE, it.total), p.plan.chunk);
-    step += last - first;
+    unit += count;
   }
 }
 
 // Joins the partial results of a row tile's wave: out = sum_c 2^(m_c - M) O_c /
-// sum_c 2^(m_c - M) l_c, in the order of the cache rows. A thread takes one
-// 4-element vector of one query row of every part.
-template <bool EVEN>
+// sum_c 2^(m_c - M) l_c. A thread takes one 4-element vector of one query row of
+// every part, or, where few rows have many parts (SPLIT), of every fourth: four
+// waves then share a vector and add up in LDS. The order of the sum is fixed.
+template <bool EVEN, bool SPLIT>
 __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks) {
   const int waves = p.plan.waves;
   int64_t b = blockIdx.x;
@@ -965,26 +1057,27 @@ __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks)
     const int j = (int)(head / p.H_kv);
     load_seq_uniform(p, j, it);
     if (it.broken || it.rt >= row_tiles_of(it)) return;
-    const int64_t W = p.sums[0], s0 = p.sums[2 + j] + (int64_t)(it.kvh * row_tiles_of(it) + it.rt) * tiles_of(it);
-    const int64_t s1 = s0 + tiles_of(it);
-    const int G = (int)p.sums[1];
-    first = (int)(s0 * G / W);  // the workgroup of step s0
-    while (first_step(W, G, first + 1) <= s0) ++first;
-    while (first > 0 && first_step(W, G, first) > s0) --first;
-    if (first_step(W, G, first + 1) >= s1) return;  // all of it: the result is there
+    const int64_t units = p.sums[0];
+    const int G = (int)p.sums[1], quantum = (int)p.sums[2], each = units_of_item(it, quantum);
+    const int64_t u0 = p.sums[3 + j] + (int64_t)(it.kvh * row_tiles_of(it) + it.rt) * each, u1 = u0 + each;
+    if (units < 1 || G < 1) return;
+    first = min((int)(u0 * G / units), G - 1);  // the workgroup of unit u0
+    while (first + 1 < G && first_unit(units, G, first + 1) <= u0) ++first;
+    while (first > 0 && first_unit(units, G, first) > u0) --first;
+    if (first_unit(units, G, first + 1) >= u1) return;  // all of it: the result is there
     parts = 1;
-    while (first_step(W, G, first + parts) < s1) ++parts;
-    slot0 = 2 * first + (first_step(W, G, first) < s0 ? 1 : 0);
+    while (first + parts < G && first_unit(units, G, first + parts) < u1) ++parts;
+    slot0 = 2 * first + (first_unit(units, G, first) < u0 ? 1 : 0);
   } else {
     if (!find_item(p, head * p.plan.chunks * p.plan.row_tiles + tile % p.plan.row_tiles, it, chunk)) return;
     if (it.broken || it.whole) return;
     parts = (it.total + p.plan.chunk - 1) / p.plan.chunk;
     slot0 = it.slot;
   }
-  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
-  const int v = vb * 4 + (threadIdx.x >> 6);  // vector of the row: 8-column group n * 4 + g
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, own = threadIdx.x >> 6;
+  const int v = SPLIT ? vb : vb * 4 + own;  // vector of the row: 8-column group n * 4 + g
   const int row = (it.rt * waves + wave) * 32 + l32;
-  if (v * 8 >= p.d_v || row >= it.rows) return;
+  if (v * 8 >= p.d_v || (it.rt * waves + wave) * 32 >= it.rows) return;
   // place of part c
   auto at = [&](int c) {
     const int64_t s = c == 0 ? slot0 : EVEN ? 2 * (int64_t)(first + c) : slot0 + (int64_t)c * p.plan.row_tiles;
@@ -992,20 +1085,52 @@ __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks)
   };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + l32;
   const f32x4_t* po = reinterpret_cast<const f32x4_t*>(p.part_o) + v * 64 + lane;
-  float M = NEG_INF;
-  for (int c = 0; c < parts; ++c) M = fmaxf(M, ml[at(c) * 32].x);
-  const float Mu = M == NEG_INF ? 0.0f : M;
-  float l = 0;
+  float M = NEG_INF, l = 0;
   f32x4_t acc = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int c = 0; c < parts; ++c) {
-    const float2 e = ml[at(c) * 32];
-    const f32x4_t x = po[at(c) * (p.d_v * 8)];
-    const float w = exp2_hw(e.x - Mu);
-    l += w * e.y;
+  constexpr int STEP = SPLIT ? 4 : 1, U = 4;  // parts of a batch, loaded together
+  if (row < it.rows) {
+    for (int c0 = 0; c0 < parts; c0 += 8) {
+      float e[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] += w * x[k];
+      for (int u = 0; u < 8; ++u) e[u] = ml[at(min(c0 + u, parts - 1)) * 32].x;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) M = fmaxf(M, e[u]);
+    }
+    const float Mu = M == NEG_INF ? 0.0f : M;
+    for (int c0 = SPLIT ? own : 0; c0 < parts; c0 += STEP * U) {
+      float2 e[U];
+      f32x4_t x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = min(c0 + STEP * u, parts - 1);
+        e[u] = ml[at(c) * 32];
+        x[u] = po[at(c) * (p.d_v * 8)];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c0 + STEP * u >= parts) break;
+        const float w = exp2_hw(e[u].x - Mu);
+        l += w * e[u].y;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += w * x[u][k];
+      }
+    }
   }
+  if constexpr (SPLIT) {
+    __shared__ float sum[4][5][64];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[own][k][lane] = acc[k];
+    sum[own][4][lane] = l;
+    __syncthreads();
+    if (own) return;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += sum[w][k][lane];
+      l += sum[w][4][lane];
+    }
+  }
+  if (row >= it.rows) return;
   const float inv = l == 0 ? 0.0f : 1.0f / l;
   const int i = row / p.group;
   const int h = it.kvh * p.group + row - i * p.group;
@@ -1049,10 +1174,17 @@ hipError_t launch_tree_attn(const AttnParams& p, hipStream_t stream) {
   else launch_dtype<64, 64, false>(p, grid, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.plan.groups > 0 ? p.plan.groups == 1 : p.plan.chunks == 1)) return e;
-  const int vec_blocks = (p.d_v / 8 + 3) / 4;
+  // parts of a row tile, at most (chunks) or on average (even plan)
+  const bool split = (p.plan.groups > 0 ? p.plan.groups / tiles : p.plan.chunks) >= 8;
+  const int vec_blocks = split ? p.d_v / 8 : (p.d_v / 8 + 3) / 4;
   const dim3 join((unsigned)(tiles * p.plan.waves * vec_blocks));
-  if (p.plan.groups > 0) hipLaunchKernelGGL(join_kernel<true>, join, dim3(256), 0, stream, p, vec_blocks);
-  else hipLaunchKernelGGL(join_kernel<false>, join, dim3(256), 0, stream, p, vec_blocks);
+  if (p.plan.groups > 0) {
+    if (split) hipLaunchKernelGGL((join_kernel<true, true>), join, dim3(256), 0, stream, p, vec_blocks);
+    else hipLaunchKernelGGL((join_kernel<true, false>), join, dim3(256), 0, stream, p, vec_blocks);
+  } else {
+    if (split) hipLaunchKernelGGL((join_kernel<false, true>), join, dim3(256), 0, stream, p, vec_blocks);
+    else hipLaunchKernelGGL((join_kernel<false, false>), join, dim3(256), 0, stream, p, vec_blocks);
+  }
   return hipGetLastError();
 }
 
