@@ -442,7 +442,7 @@ mla_status check_attn(const mla_tree_attn_args* a, mla::AttnPlan* plan) {
   // every grid stays within 2^31 work-items
   const double items = (double)a->nseq * a->H_kv * plan->row_tiles * plan->chunks;
   const double joins = (double)a->nseq * a->H_kv * plan->row_tiles * plan->waves * (a->d_v / 8);
-  if (items > (1 << 23) || joins > (double)(1 << 23)) return MLA_EINVAL;
+  if (items > (1 << 23) || joins > (double)(1 << 21)) return MLA_EINVAL;
   return MLA_OK;
 }
 

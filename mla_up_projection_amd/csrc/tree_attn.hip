@@ -117,9 +117,12 @@ __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Item& it,
 __device__ __forceinline__ int64_t first_unit(int64_t units, int G, int b) { return units * b / G; }
 // More workgroups shorten the longest but write more partial results: a step
 // takes 2 us, a partial result (256 KB out and in again) 0.12 us of all
-// workgroups' time, and W 2 / G + 0.12 G is least at G = sqrt(17 W).
-__device__ __forceinline__ int workgroups_for(const AttnParams& p, int64_t W) {
-  return (int)min((int64_t)p.plan.groups, min(W, (int64_t)max(1.0f, sqrtf(17.0f * (float)W))));
+// workgroups' time and 0.2 us more in the join of its item (a single sequence of
+// 65000 rows: 238 parts 44 + 51 us, 110 parts 48 + 28 us). W 2 / G + (0.12 + 0.2 /
+// items) G is least at the square root below.
+__device__ __forceinline__ int workgroups_for(const AttnParams& p, int64_t W, int64_t items) {
+  const float best = sqrtf(2.0f * (float)W / (0.12f + 0.2f / (float)max(items, (int64_t)1)));
+  return (int)min((int64_t)p.plan.groups, min(W, (int64_t)max(1.0f, best)));
 }
 // sum over items of ceil(steps / quantum) <= W / quantum + items <= G
 __device__ __forceinline__ int quantum_for(int64_t W, int64_t items, int G) {
@@ -967,7 +970,7 @@ void tree_attn_even_kernel(AttnParams p) {
     }
   }
   if (W == 0) return;
-  int G = workgroups_for(p, W);
+  int G = workgroups_for(p, W, all_items);
   const int quantum = quantum_for(W, all_items, G);
   int64_t mine = 0, units;
   for (int j = j0; j < j1; ++j) {
@@ -1035,16 +1038,22 @@ void tree_attn_even_kernel(AttnParams p) {
   }
 }
 
-// Joins the partial results of a row tile's wave: out = sum_c 2^(m_c - M) O_c /
-// sum_c 2^(m_c - M) l_c. A thread takes one 4-element vector of one query row of
-// every part, or, where few rows have many parts (SPLIT), of every fourth: four
-// waves then share a vector and add up in LDS. The order of the sum is fixed.
-template <bool EVEN, bool SPLIT>
-__global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks) {
-  const int waves = p.plan.waves;
+// Joins the partial results of 32 query rows (a wave of a row tile): out = sum_c
+// 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the parts c of the cache rows. A
+// lane takes 4-element vectors of one query row. A workgroup's way to its first
+// partial result is a chain of five loads, about 4 us, so there should not be
+// many more of them than run at once (16 blocks for each of 1024 row groups took
+// 47 us for 100 MB, one block 34 us). V = 4: four waves share `vectors_each`
+// vectors, four in flight each. V = 1, for few rows with many parts: a wave takes
+// one vector, and where the workgroup has more than four waves they share the
+// parts and add up in LDS. The order of every sum is fixed.
+template <bool EVEN, int V>
+__global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p, int vectors_each) {
+  const int waves = p.plan.waves, vectors = p.d_v / 8;
+  const int blocks = (vectors + vectors_each - 1) / vectors_each;
   int64_t b = blockIdx.x;
-  const int vb = (int)(b % vec_blocks);
-  b /= vec_blocks;
+  const int vb = (int)(b % blocks) * vectors_each;
+  b /= blocks;
   const int wave = (int)(b % waves);
   const int64_t tile = b / waves;
   const int64_t head = tile / p.plan.row_tiles;
@@ -1075,70 +1084,93 @@ __global__ __launch_bounds__(256) void join_kernel(AttnParams p, int vec_blocks)
     slot0 = it.slot;
   }
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, own = threadIdx.x >> 6;
-  const int v = SPLIT ? vb : vb * 4 + own;  // vector of the row: 8-column group n * 4 + g
   const int row = (it.rt * waves + wave) * 32 + l32;
-  if (v * 8 >= p.d_v || (it.rt * waves + wave) * 32 >= it.rows) return;
+  if ((it.rt * waves + wave) * 32 >= it.rows) return;
   // place of part c
   auto at = [&](int c) {
     const int64_t s = c == 0 ? slot0 : EVEN ? 2 * (int64_t)(first + c) : slot0 + (int64_t)c * p.plan.row_tiles;
     return s * waves + wave;
   };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + l32;
-  const f32x4_t* po = reinterpret_cast<const f32x4_t*>(p.part_o) + v * 64 + lane;
-  float M = NEG_INF, l = 0;
-  f32x4_t acc = {0, 0, 0, 0};
-  constexpr int STEP = SPLIT ? 4 : 1, U = 4;  // parts of a batch, loaded together
-  if (row < it.rows) {
-    for (int c0 = 0; c0 < parts; c0 += 8) {
+  const f32x4_t* po = reinterpret_cast<const f32x4_t*>(p.part_o) + lane;
+  const bool live = row < it.rows;  // (partial results of other rows do not exist)
+  const int i = live ? row / p.group : 0;
+  const int h = it.kvh * p.group + (live ? row - i * p.group : 0);
+  const int64_t t = it.t0 + i;
+  // this wave's parts: their largest reference
+  const int c1 = V == 1 ? own >> 2 : 0, step = V == 1 ? blockDim.x / 256 : 1;
+  constexpr int U = V == 1 ? 8 : 2;  // parts at once
+  float M = NEG_INF;
+  if (live)
+    for (int c0 = c1; c0 < parts; c0 += step * 8) {
       float e[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) e[u] = ml[at(min(c0 + u, parts - 1)) * 32].x;
+      for (int u = 0; u < 8; ++u) e[u] = ml[at(min(c0 + step * u, parts - 1)) * 32].x;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) M = fmaxf(M, e[u]);
+      for (int u = 0; u < 8; ++u)
+        if (c0 + step * u < parts) M = fmaxf(M, e[u]);
     }
-    const float Mu = M == NEG_INF ? 0.0f : M;
-    for (int c0 = SPLIT ? own : 0; c0 < parts; c0 += STEP * U) {
-      float2 e[U];
-      f32x4_t x[U];
+  const float Mu = M == NEG_INF ? 0.0f : M;
+  __shared__ float sum[V == 1 ? 16 : 1][6][64];
+  const int end = min(vb + vectors_each, vectors);
+  for (int v0 = vb + (own & 3); v0 < vb + vectors_each; v0 += 4 * V) {
+    float l = 0;
+    f32x4_t acc[V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = min(c0 + STEP * u, parts - 1);
-        e[u] = ml[at(c) * 32];
-        x[u] = po[at(c) * (p.d_v * 8)];
+    for (int v = 0; v < V; ++v) acc[v] = f32x4_t{0, 0, 0, 0};
+    if (live && v0 < end)
+      for (int c0 = c1; c0 < parts; c0 += step * U) {
+        float2 e[U];
+        f32x4_t x[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t s = at(min(c0 + step * u, parts - 1));
+          e[u] = ml[s * 32];
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[u][v] = po[(s * vectors + min(v0 + 4 * v, end - 1)) * 64];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (c0 + step * u >= parts) break;
+          const float w = exp2_hw(e[u].x - Mu);
+          l += w * e[u].y;
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[v][k] += w * x[u][v][k];
+        }
       }
+    float top = M;
+    if (V == 1 && step > 1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (c0 + STEP * u >= parts) break;
-        const float w = exp2_hw(e[u].x - Mu);
-        l += w * e[u].y;
+      for (int k = 0; k < 4; ++k) sum[own][k][lane] = acc[0][k];
+      sum[own][4][lane] = l;
+      sum[own][5][lane] = M;
+      __syncthreads();
+      if (own >= 4) return;
+      for (int w = 1; w < step; ++w) top = fmaxf(top, sum[own + 4 * w][5][lane]);
+      const float tu = top == NEG_INF ? 0.0f : top;
+      const float f0 = exp2_hw(M - tu);
+      l *= f0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] += w * x[u][k];
+      for (int k = 0; k < 4; ++k) acc[0][k] *= f0;
+      for (int w = 1; w < min(step, parts); ++w) {
+        const float f = exp2_hw(sum[own + 4 * w][5][lane] - tu);
+        l += f * sum[own + 4 * w][4][lane];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[0][k] += f * sum[own + 4 * w][k][lane];
       }
     }
+    if (!live) continue;
+    const float inv = l == 0 ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v0 + 4 * v < end)
+        *reinterpret_cast<uint2*>(p.out + t * p.o_t + h * p.o_h + 8 * (v0 + 4 * v) + 4 * half) =
+            make_uint2(pack_bf16x2(acc[v][0] * inv, acc[v][1] * inv), pack_bf16x2(acc[v][2] * inv, acc[v][3] * inv));
+    if (p.lse && v0 == 0 && half == 0)
+      p.lse[t * p.H + h] = l == 0 ? NEG_INF : (top + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
   }
-  if constexpr (SPLIT) {
-    __shared__ float sum[4][5][64];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum[own][k][lane] = acc[k];
-    sum[own][4][lane] = l;
-    __syncthreads();
-    if (own) return;
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] += sum[w][k][lane];
-      l += sum[w][4][lane];
-    }
-  }
-  if (row >= it.rows) return;
-  const float inv = l == 0 ? 0.0f : 1.0f / l;
-  const int i = row / p.group;
-  const int h = it.kvh * p.group + row - i * p.group;
-  const int64_t t = it.t0 + i;
-  *reinterpret_cast<uint2*>(p.out + t * p.o_t + h * p.o_h + 8 * v + 4 * half) =
-      make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  if (p.lse && v == 0 && half == 0)
-    p.lse[t * p.H + h] = l == 0 ? NEG_INF : (M + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
 }
 
 template <int DK, int DV, bool SHARED, bool MX>
@@ -1174,16 +1206,20 @@ hipError_t launch_tree_attn(const AttnParams& p, hipStream_t stream) {
   else launch_dtype<64, 64, false>(p, grid, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (p.plan.groups > 0 ? p.plan.groups == 1 : p.plan.chunks == 1)) return e;
-  // parts of a row tile, at most (chunks) or on average (even plan)
-  const bool split = (p.plan.groups > 0 ? p.plan.groups / tiles : p.plan.chunks) >= 8;
-  const int vec_blocks = split ? p.d_v / 8 : (p.d_v / 8 + 3) / 4;
-  const dim3 join((unsigned)(tiles * p.plan.waves * vec_blocks));
+  // By the groups of 32 rows: many take all their vectors or a quarter of them in
+  // a workgroup; few take four, and share parts (at most, or on average) over
+  // four times the waves.
+  const int64_t groups = tiles * p.plan.waves;
+  const int64_t parts = p.plan.groups > 0 ? p.plan.groups / tiles : p.plan.chunks;
+  const int vectors = p.d_v / 8, each = groups >= 1024 ? std::min(vectors, 64) : groups >= 64 ? std::min(vectors, 16) : 4;
+  const dim3 grid2((unsigned)(groups * ((vectors + each - 1) / each)));
+  const dim3 threads(each == 4 && parts >= 16 ? 1024 : 256);
   if (p.plan.groups > 0) {
-    if (split) hipLaunchKernelGGL((join_kernel<true, true>), join, dim3(256), 0, stream, p, vec_blocks);
-    else hipLaunchKernelGGL((join_kernel<true, false>), join, dim3(256), 0, stream, p, vec_blocks);
+    if (each > 4) hipLaunchKernelGGL((join_kernel<true, 4>), grid2, threads, 0, stream, p, each);
+    else hipLaunchKernelGGL((join_kernel<true, 1>), grid2, threads, 0, stream, p, each);
   } else {
-    if (split) hipLaunchKernelGGL((join_kernel<false, true>), join, dim3(256), 0, stream, p, vec_blocks);
-    else hipLaunchKernelGGL((join_kernel<false, false>), join, dim3(256), 0, stream, p, vec_blocks);
+    if (each > 4) hipLaunchKernelGGL((join_kernel<false, 4>), grid2, threads, 0, stream, p, each);
+    else hipLaunchKernelGGL((join_kernel<false, 1>), grid2, threads, 0, stream, p, each);
   }
   return hipGetLastError();
 }
