@@ -390,7 +390,7 @@ AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int m
     pl.chunks = 1;
     const double steps = std::max(1.0, (double)nseq * H_kv * (double)tiles * ((max_len + 31) / 32));
     pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(17.0 * steps)) + 1});
-    if (pl.groups > 1) {
+    if (pl.groups > 1 && max_len > 32) {  // (an item of one step has no parts)
       const size_t slots = (size_t)2 * pl.groups * pl.waves;
       pl.part_o = 0;
       pl.part_ml = slots * 32 * (size_t)d_v * 4;

@@ -982,7 +982,7 @@ void tree_attn_even_kernel(AttnParams p) {
   // consecutive runs go to one XCD: row tiles of a sequence share its L2
   const int runs = (G + 7) / 8;
   const int b = (blockIdx.x % 8) * runs + blockIdx.x / 8;
-  if (blockIdx.x == 0 && p.plan.groups > 1) {
+  if (blockIdx.x == 0 && p.plan.total > 0) {
     int64_t at = before;
     for (int j = j0; j < j1; ++j) {
       p.sums[3 + j] = at;
@@ -1205,7 +1205,7 @@ hipError_t launch_tree_attn(const AttnParams& p, hipStream_t stream) {
   else if (p.d_k == 128) launch_dtype<128, 128, false>(p, grid, stream);
   else launch_dtype<64, 64, false>(p, grid, stream);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || (p.plan.groups > 0 ? p.plan.groups == 1 : p.plan.chunks == 1)) return e;
+  if (e != hipSuccess || p.plan.total == 0) return e;  // no item has parts
   // By the groups of 32 rows: many take all their vectors or a quarter of them in
   // a workgroup; few take four, and share parts (at most, or on average) over
   // four times the waves.
