@@ -426,24 +426,38 @@ def mla_kv_rope(kv, k_pe, key, value, *, H, d_nope, d_rope, d_v, cos=None, sin=N
 
 
 # ------------------------------------------------------------------ decoding --
-class _On:
-    """The stream of a call and, while it lasts, its device as the current one
-    (a launch on the default stream goes to the current device)."""
+def _call(where, device, stream, fn, *args):
+    """fn(*args, stream) on `device`: the given stream, or the device's current one, with the device current while
+    the call lasts (a launch on the default stream goes to the current device)."""
+    index = device.index if device is not None and device.type == "cuda" else None
+    if stream is not None:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    elif index is not None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = torch.cuda.current_stream().cuda_stream
+    if index is None or index == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status:
+        raise MlaError(status, where)
 
-    def __init__(self, device, stream):
-        self.guard = None
-        if device is not None and device.type == "cuda" and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.arg = stream
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.arg)
+def _is(t, dtype, numel, device) -> bool:
+    """Whether t is what _Dev would accept; the slow check then says what is wrong with one that is not."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel and t.device == device
+            and t.is_contiguous())
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _i32(chk, t, name, numel):
+    """Device address of an int32 tensor."""
+    if _is(t, _I32, numel, chk.device):
+        return t.data_ptr()
+    if t is None:
+        raise ValueError(f"{chk.where}: {name} must be a torch tensor")
+    return chk(t, name, (_I32,), numel=numel)
 
 
 def mxfp4_quantize(x, codes, scales, stream=None):
@@ -461,8 +475,7 @@ def mxfp4_quantize(x, codes, scales, stream=None):
     dt = DTYPE_FP32 if x.dtype == torch.float32 else DTYPE_BF16
     pc = chk(codes, "codes", (_U8,), numel=rows * cols // 2)
     psc = chk(scales, "scales", (_U8,), numel=rows * cols // 32)
-    with _On(chk.device, stream) as s:
-        _check(lib().mxfp4_quantize(px, dt, rows, cols, ld, pc, psc, s), "mxfp4_quantize")
+    _call("mxfp4_quantize", chk.device, stream, lib().mxfp4_quantize, px, dt, rows, cols, ld, pc, psc)
 
 
 def mla_qup_fwd_w4(x, w, w_scales, out, *, H, d_nope, d_rope, cos=None, sin=None, positions=None, bias=None,
@@ -487,8 +500,7 @@ def mla_qup_fwd_w4(x, w, w_scales, out, *, H, d_nope, d_rope, cos=None, sin=None
     a.out_dtype = DTYPE_MXFP8 if out.dtype == torch.uint8 else DTYPE_BF16
     a.out = chk(out, "out", (_BF16, _U8), numel=T * N)
     a.out_scales = chk(out_scales, "out_scales", (_U8,), numel=T * N // 32)
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_qup_fwd_w4(ctypes.byref(a), s), "mla_qup_fwd_w4")
+    _call("mla_qup_fwd_w4", chk.device, stream, lib().mla_qup_fwd_w4, ctypes.byref(a))
 
 
 class PagePool:
@@ -525,7 +537,7 @@ class PagePool:
             c.buf[k] = chk(b, f"bufs[{k}]", (_BF16, _U8))
             c.page_bytes[k] = b.stride(0) * b.element_size() if n > 1 else b.numel() * b.element_size()
         self.c, self.device = c, chk.device
-        self.ref = ctypes.byref(c)
+        self.ref, self.ptr = ctypes.byref(c), ctypes.pointer(c)
         self.bufs, self.refs, self.table, self.lens, self.held = bufs, refs, table, lens, held
         self.heads, self.d_k = bufs[0].shape[2:]
         self.latent = len(bufs) == (2 if self.mx else 1)
@@ -541,7 +553,16 @@ def _pool_chk(where, pool) -> _Dev:
 
 
 def _workspace(chk, workspace):
-    return chk(workspace, "workspace", (_U8,)), (workspace.numel() if workspace is not None else 0)
+    if workspace is None:
+        return None, 0
+    n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    return (workspace.data_ptr() if _is(workspace, _U8, n, chk.device) else chk(workspace, "workspace", (_U8,))), n
+
+
+def _count(where, t, name) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{where}: {name} must be a torch tensor")
+    return t.numel()
 
 
 def mla_pages_workspace_size(pool) -> int:
@@ -554,59 +575,56 @@ def mla_pages_copy(src, dst, src_ids, dst_ids, stream=None):
     chk = _pool_chk("mla_pages_copy", src)
     if not isinstance(dst, PagePool) or dst.device != src.device:
         raise ValueError("mla_pages_copy: dst must be a PagePool on src's device")
-    n = src_ids.numel()
-    a, b = chk(src_ids, "src_ids", (_I32,)), chk(dst_ids, "dst_ids", (_I32,), numel=n)
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_pages_copy(src.ref, dst.ref, a, b, n, s), "mla_pages_copy")
+    n = _count(chk.where, src_ids, "src_ids")
+    a, b = _i32(chk, src_ids, "src_ids", n), _i32(chk, dst_ids, "dst_ids", n)
+    _call(chk.where, chk.device, stream, lib().mla_pages_copy, src.ref, dst.ref, a, b, n)
 
 
 def mla_pages_reserve(pool, seqs, new_tokens, status, *, workspace, stream=None):
     """Room for new_tokens[i] rows behind sequence seqs[i] (int32 [n] each), copying shared pages on write.
     status int32 [1]: 0 when done, else nothing changed. workspace: mla_pages_workspace_size() bytes."""
     chk = _pool_chk("mla_pages_reserve", pool)
-    n = seqs.numel()
-    a, b = chk(seqs, "seqs", (_I32,)), chk(new_tokens, "new_tokens", (_I32,), numel=n)
-    st = chk(status, "status", (_I32,), numel=1)
+    n = _count(chk.where, seqs, "seqs")
+    a, b = _i32(chk, seqs, "seqs", n), _i32(chk, new_tokens, "new_tokens", n)
+    st = _i32(chk, status, "status", 1)
     w, size = _workspace(chk, workspace)
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_pages_reserve(pool.ref, a, b, n, st, w, size, s), "mla_pages_reserve")
+    _call(chk.where, chk.device, stream, lib().mla_pages_reserve, pool.ref, a, b, n, st, w, size)
 
 
 def mla_pages_fork(pool, src, dst, stream=None):
     """Sequence dst[i] (empty) takes the committed rows of src[i] by sharing its pages."""
     chk = _pool_chk("mla_pages_fork", pool)
-    a, b = chk(src, "src", (_I32,)), chk(dst, "dst", (_I32,), numel=src.numel())
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_pages_fork(pool.ref, a, b, src.numel(), s), "mla_pages_fork")
+    n = _count(chk.where, src, "src")
+    a, b = _i32(chk, src, "src", n), _i32(chk, dst, "dst", n)
+    _call(chk.where, chk.device, stream, lib().mla_pages_fork, pool.ref, a, b, n)
 
 
 def mla_pages_free(pool, seqs, keep=None, stream=None):
     """Cut sequences to keep[i] committed rows (None: none) and drop the pages behind them."""
     chk = _pool_chk("mla_pages_free", pool)
-    a, b = chk(seqs, "seqs", (_I32,)), chk(keep, "keep", (_I32,), numel=seqs.numel())
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_pages_free(pool.ref, a, b, seqs.numel(), s), "mla_pages_free")
+    n = _count(chk.where, seqs, "seqs")
+    a, b = _i32(chk, seqs, "seqs", n), (None if keep is None else _i32(chk, keep, "keep", n))
+    _call(chk.where, chk.device, stream, lib().mla_pages_free, pool.ref, a, b, n)
 
 
 def mla_pages_compact(pool, used, *, workspace, stream=None):
     """Move the pages in use to the front of the pool; used int32 [1] receives their number."""
     chk = _pool_chk("mla_pages_compact", pool)
-    u = chk(used, "used", (_I32,), numel=1)
+    u = _i32(chk, used, "used", 1)
     w, size = _workspace(chk, workspace)
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_pages_compact(pool.ref, u, w, size, s), "mla_pages_compact")
+    _call(chk.where, chk.device, stream, lib().mla_pages_compact, pool.ref, u, w, size)
 
 
 def mla_draft_accept(pool, seqs, path, n_acc, stream=None):
     """Drafted rows path[i, :n_acc[i]] (counted behind the committed ones) of sequence seqs[i] become its next rows."""
     chk = _pool_chk("mla_draft_accept", pool)
-    n = seqs.numel()
-    if path.dim() != 2 or path.shape[0] != n:
+    n = _count(chk.where, seqs, "seqs")
+    if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != n:
         raise ValueError("mla_draft_accept: path must be [n, max_path]")
-    a, b = chk(seqs, "seqs", (_I32,)), chk(path, "path", (_I32,))
-    c = chk(n_acc, "n_acc", (_I32,), numel=n)
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_draft_accept(pool.ref, a, b, c, n, path.shape[1], s), "mla_draft_accept")
+    width = path.shape[1]
+    a, b = _i32(chk, seqs, "seqs", n), _i32(chk, path, "path", n * width)
+    c = _i32(chk, n_acc, "n_acc", n)
+    _call(chk.where, chk.device, stream, lib().mla_draft_accept, pool.ref, a, b, c, n, width)
 
 
 def mla_kv_rope_paged(kv, k_pe, pool, seqs, cu_q, *, H, d_nope, d_rope, d_v, cos=None, sin=None, positions=None,
@@ -619,50 +637,47 @@ def mla_kv_rope_paged(kv, k_pe, pool, seqs, cu_q, *, H, d_nope, d_rope, d_v, cos
     a.kv = chk(kv, "kv", (_BF16,), numel=T * H * (d_nope + d_v))
     a.k_pe = chk(k_pe, "k_pe", (_BF16,), numel=T * d_rope)
     a.H, a.d_nope, a.d_rope, a.d_v, a.T = H, d_nope, d_rope, d_v, T
-    a.nseq = seqs.numel()
-    a.seqs = chk(seqs, "seqs", (_I32,))
-    a.cu_q = chk(cu_q, "cu_q", (_I32,), numel=a.nseq + 1)
+    n = _count(chk.where, seqs, "seqs")
+    a.nseq = n
+    a.seqs, a.cu_q = _i32(chk, seqs, "seqs", n), _i32(chk, cu_q, "cu_q", n + 1)
     a.max_q = max(1, T) if max_q is None else max_q
-    a.positions = chk(positions, "positions", (_I32,), numel=T)
+    a.positions = None if positions is None else _i32(chk, positions, "positions", T)
     a.rope = _rope(chk, cos, sin, d_rope)
     a.cache_dtype = DTYPE_MXFP8 if pool.mx else DTYPE_BF16
-    a.pool = ctypes.pointer(pool.c)
-    with _On(chk.device, stream) as s:
-        _check(lib().mla_kv_rope_paged(ctypes.byref(a), s), "mla_kv_rope_paged")
+    a.pool = pool.ptr
+    _call(chk.where, chk.device, stream, lib().mla_kv_rope_paged, ctypes.byref(a))
 
 
 def make_tree_attn_args(q, pool, out, seqs, cu_q, *, max_q, max_len, scale, lse=None, mask=None,
                         workspace=None) -> mla_tree_attn_args:
     where = "mla_tree_attention"
     chk = _pool_chk(where, pool)
-    a = mla_tree_attn_args()
     if q.dim() != 3 or out.dim() != 3 or q.shape[:2] != out.shape[:2]:
         raise ValueError(f"{where}: q must be [T, H, d_k] and out [T, H, d_v]")
     for t, name in ((q, "q"), (out, "out")):  # token and head strides are free, elements are dense
         if not isinstance(t, torch.Tensor) or t.device != pool.device or t.dtype != _BF16:
             raise ValueError(f"{where}: {name} must be a bf16 tensor on {pool.device}")
-        if t.numel() and t.stride(2) != 1:
+        if t.stride(2) != 1 and t.numel():
             raise ValueError(f"{where}: the elements of a row of {name} must be dense")
     T, H, d_k = q.shape
-    a.q, a.q_stride_t, a.q_stride_h = q.data_ptr(), q.stride(0), q.stride(1)
-    a.out, a.out_stride_t, a.out_stride_h = out.data_ptr(), out.stride(0), out.stride(1)
-    a.T, a.H, a.H_kv, a.d_k, a.d_v = T, H, pool.heads, d_k, out.shape[2]
-    if d_k != pool.d_k or (not pool.latent and a.d_v != pool.d_v):
+    d_v = out.shape[2]
+    if d_k != pool.d_k or (not pool.latent and d_v != pool.d_v):
         raise ValueError(f"{where}: widths of q and out do not fit the cache")
-    a.lse = chk(lse, "lse", (_FP32,), numel=T * H)
-    a.scale = scale
-    a.nseq = seqs.numel()
-    a.seqs = chk(seqs, "seqs", (_I32,))
-    a.cu_q = chk(cu_q, "cu_q", (_I32,), numel=a.nseq + 1)
-    a.max_q, a.max_len = max_q, max_len
+    n = _count(where, seqs, "seqs")
+    words = 0
     if mask is not None:
-        if mask.dim() != 2 or mask.shape[0] != T:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 2 or mask.shape[0] != T:
             raise ValueError(f"{where}: mask must be [T, words]")
-        a.mask, a.mask_words = chk(mask, "mask", (_I32, torch.uint32)), mask.shape[1]
-    a.cache_dtype = DTYPE_MXFP8 if pool.mx else DTYPE_BF16
-    a.pool = ctypes.pointer(pool.c)
-    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
-    return a
+        words = mask.shape[1]
+        mask = mask.data_ptr() if _is(mask, _I32, T * words, pool.device) else chk(mask, "mask", (_I32, torch.uint32))
+    if lse is not None:
+        lse = lse.data_ptr() if _is(lse, _FP32, T * H, pool.device) else chk(lse, "lse", (_FP32,), numel=T * H)
+    ws, ws_bytes = _workspace(chk, workspace)
+    sq, so = q.stride(), out.stride()
+    return mla_tree_attn_args(
+        q.data_ptr(), sq[0], sq[1], out.data_ptr(), so[0], so[1], lse, T, H, pool.heads, d_k, d_v, scale,
+        _i32(chk, seqs, "seqs", n), _i32(chk, cu_q, "cu_q", n + 1), n, max_q, max_len, mask, words,
+        DTYPE_MXFP8 if pool.mx else DTYPE_BF16, pool.ptr, ws, ws_bytes)
 
 
 def mla_tree_attention_workspace_size(q, pool, out, seqs, cu_q, **kw) -> int:
@@ -678,5 +693,4 @@ def mla_tree_attention(q, pool, out, seqs, cu_q, *, stream=None, **kw):
     and the rows, drafts included, of any sequence. lse fp32 [T,H] or None; workspace:
     mla_tree_attention_workspace_size() bytes (None if that is 0)."""
     a = make_tree_attn_args(q, pool, out, seqs, cu_q, **kw)
-    with _On(pool.device, stream) as s:
-        _check(lib().mla_tree_attention(ctypes.byref(a), s), "mla_tree_attention")
+    _call("mla_tree_attention", pool.device, stream, lib().mla_tree_attention, ctypes.byref(a))
