@@ -114,19 +114,34 @@ __device__ __forceinline__ int units_of_item(const Item& it, int quantum) {
 __device__ __forceinline__ int64_t units_of(const AttnParams& p, const Item& it, int quantum) {
   return it.broken || it.n == 0 ? 0 : (int64_t)p.H_kv * row_tiles_of(it) * units_of_item(it, quantum);
 }
-__device__ __forceinline__ int64_t first_unit(int64_t units, int G, int b) { return units * b / G; }
+// a / b for a >= 0, b > 0. The 64-bit division is some hundred instructions, and
+// in a kernel that runs them once their fetch costs more than they do.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (__builtin_expect(((a | b) >> 32) == 0, 1)) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+// G workgroups share `units`: the first `more` take each + 1 of them, the others `each`.
+struct Share {
+  int64_t each, more;
+  __device__ __forceinline__ int64_t first(int b) const { return each * b + min((int64_t)b, more); }
+  __device__ __forceinline__ int of(int64_t unit) const {  // the workgroup that has it
+    const int64_t behind = more * (each + 1);
+    return (int)(unit < behind ? divide(unit, each + 1) : more + divide(unit - behind, each));
+  }
+};
 // More workgroups shorten the longest but write more partial results: a step
 // takes 2 us, a partial result (256 KB out and in again) 0.12 us of all
 // workgroups' time and 0.2 us more in the join of its item (a single sequence of
 // 65000 rows: 238 parts 44 + 51 us, 110 parts 48 + 28 us). W 2 / G + (0.12 + 0.2 /
 // items) G is least at the square root below.
 __device__ __forceinline__ int workgroups_for(const AttnParams& p, int64_t W, int64_t items) {
-  const float best = sqrtf(2.0f * (float)W / (0.12f + 0.2f / (float)max(items, (int64_t)1)));
+  const float part = 0.12f + 0.2f * __builtin_amdgcn_rcpf((float)max(items, (int64_t)1));
+  const float best = __builtin_amdgcn_sqrtf(2.0f * (float)W * __builtin_amdgcn_rcpf(part));
   return (int)min((int64_t)p.plan.groups, min(W, (int64_t)max(1.0f, best)));
 }
 // sum over items of ceil(steps / quantum) <= W / quantum + items <= G
 __device__ __forceinline__ int quantum_for(int64_t W, int64_t items, int G) {
-  return 4 * items <= G ? (int)((W + (G - items) - 1) / (G - items)) : 0;
+  return 4 * items <= G ? (int)divide(W + (G - items) - 1, G - items) : 0;
 }
 
 // Every row of a broken sequence, by one workgroup.
@@ -780,22 +795,35 @@ __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, i
   }
 }
 
+// Bits set by any of the workgroup's threads, to all of them, with one barrier
+// (the place is free again after the next).
+template <int WAVES>
+__device__ __forceinline__ int any_of(bool bit0, bool bit1, int* place) {
+  const int bits = (__any(bit0) ? 1 : 0) | (__any(bit1) ? 2 : 0);
+  if ((threadIdx.x & 63) == 0) place[threadIdx.x >> 6] = bits;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) all |= place[w];
+  return __builtin_amdgcn_readfirstlane(all);
+}
+
 // Page ids of cache rows [tk_begin, tk_end) to s_page, -1 for those outside the
 // pool; returns whether there are any. All threads; the list is complete after.
-template <int THREADS>
+template <int WAVES>
 __device__ __forceinline__ bool fill_pages(const AttnParams& p, const Item& it, int* s_page, int page0, int tk_end) {
   const int pages = (tk_end - 1) / p.pool.page_size - page0 + 1;
   const int held = min(__builtin_amdgcn_readfirstlane(p.pool.held[it.seq]), p.pool.max_pages);
-  int bad = 0;
-  for (int k = threadIdx.x; k < pages; k += THREADS) {
+  bool bad = false;
+  for (int k = threadIdx.x; k < pages; k += 64 * WAVES) {
     int id = page0 + k < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + page0 + k] : -1;
     if (id < 0 || id >= p.pool.num_pages) {
       id = -1;
-      bad = 1;
+      bad = true;
     }
     s_page[k] = id;
   }
-  return __syncthreads_or(bad);
+  return any_of<WAVES>(bad, false, s_page + MAX_CHUNK_PAGES);
 }
 
 // Cache rows [tk_begin, tk_end) of an item, and its result or partial result.
@@ -822,7 +850,7 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     __syncthreads();  // LDS is read
     w.ask_queries();
     w.page0 = tk_begin / p.pool.page_size;
-    bad = fill_pages<S::THREADS>(p, it, s_page, w.page0, min(tk_begin + most, tk_end));  // while they come
+    bad = fill_pages<WAVES>(p, it, s_page, w.page0, min(tk_begin + most, tk_end));  // while they come
     w.take_queries();
   } else {
     const auto r = w.row();
@@ -841,7 +869,7 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
       w.tk_end = end;
       w.page0 = begin / p.pool.page_size;
       __syncthreads();  // LDS is read: the list may change and tiles come in
-      if (!filled || begin > tk_begin) bad = fill_pages<S::THREADS>(p, it, s_page, w.page0, end);
+      if (!filled || begin > tk_begin) bad = fill_pages<WAVES>(p, it, s_page, w.page0, end);
       filled = begin == tk_begin && (!S::WIDE || end == tk_end);  // for a second pass
       slow = bad;
       if (slow) break;
@@ -850,8 +878,9 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
       w.pass((end - begin + TILE - 1) / TILE, full);
       if constexpr (!S::WIDE) break;
     }
-    slow = __syncthreads_or(w.odd) || slow;
-    if (slow || __builtin_expect(!__syncthreads_or(w.top > w.m + LAZY), 1)) break;
+    const int seen = any_of<WAVES>(w.odd, w.top > w.m + LAZY, s_page + MAX_CHUNK_PAGES + WAVES);
+    slow = slow || (seen & 1);
+    if (slow || __builtin_expect(!(seen & 2), 1)) break;
     w.m = w.top;  // the largest score of all: the next pass is the last
   }
   if (__builtin_expect(slow, 0)) {
@@ -897,7 +926,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(1, 4
 void tree_attn_kernel(AttnParams p) {
   using S = Shape<DK, DV, SHARED, MX, WAVES>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
-  __shared__ int s_page[MAX_CHUNK_PAGES];
+  __shared__ int s_page[MAX_CHUNK_PAGES + 8];  // and eight words of any_of
   // consecutive items (row tiles that read the same chunk) go to one XCD's L2
   const int64_t per = gridDim.x / 8;
   Item it;
@@ -913,14 +942,25 @@ void tree_attn_kernel(AttnParams p) {
   run_item<DK, DV, SHARED, MX, WAVES>(p, it, lds, s_page, tk_begin, tk_end, p.plan.chunk);
 }
 
-// Sum of v over the workgroup's earlier threads (256); all: over all of them.
-__device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* lds, int64_t& all) {
+// v of one lane (the same for all that ask), in scalar registers.
+__device__ __forceinline__ int64_t of_lane(int64_t v, int lane) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+
+// Sum of v over the sequences before the thread's own, and over all of them.
+// Up to 64 sequences every wave holds all of them; beyond, the workgroup's 256
+// threads do.
+__device__ __forceinline__ int64_t sum_before(int64_t v, int nseq, int64_t* lds, int64_t& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t inc = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
+  for (int d = 1; d < min(nseq, 64); d <<= 1) {
     const int64_t o = __shfl_up(inc, d);
     if (lane >= d) inc += o;
+  }
+  if (nseq <= 64) {
+    all = of_lane(inc, nseq - 1);
+    return inc - v;
   }
   if (lane == 63) lds[wave] = inc;
   __syncthreads();
@@ -931,6 +971,7 @@ __device__ __forceinline__ int64_t sum_before(int64_t v, int64_t* lds, int64_t& 
     before += w < wave ? lds[w] : 0;
     all += lds[w];
   }
+  all = of_lane(all, 0);
   return before;
 }
 
@@ -942,26 +983,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void tree_attn_even_kernel(AttnParams p) {
   using S = Shape<576, 512, true, MX, 4>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
-  __shared__ int s_page[MAX_CHUNK_PAGES];
-  __shared__ int64_t s_sum[3][4], s_base;
+  __shared__ int s_page[MAX_CHUNK_PAGES + 8];  // and eight words of any_of
+  __shared__ int64_t s_sum[2][4], s_base;
   __shared__ Item s_item;
   const int tid = threadIdx.x;
   Item it;
   // a run of sequences per thread
-  const int per = (p.nseq + 255) / 256;
-  const int j0 = min(tid * per, p.nseq), j1 = min(j0 + per, p.nseq);
-  int64_t steps = 0, items = 0, W, all_items;
+  const bool many = p.nseq > 64;
+  const int per = many ? (p.nseq + 255) / 256 : 1, who = many ? tid : tid & 63;
+  const int j0 = min(who * per, p.nseq), j1 = min(j0 + per, p.nseq);
+  int64_t work = 0, all;  // steps, and above them items (at most 2^23)
   int broken = 0;
   for (int j = j0; j < j1; ++j) {
     load_seq(p, j, it);
     const int64_t n = units_of(p, it, 0);
-    steps += n;
-    items += n ? (int64_t)p.H_kv * row_tiles_of(it) : 0;
+    work += n + (n ? (int64_t)(p.H_kv * row_tiles_of(it)) << 40 : 0);
     broken |= it.broken && it.n > 0;
   }
-  sum_before(items, s_sum[0], all_items);
-  sum_before(steps, s_sum[1], W);
-  if (__syncthreads_or(broken)) {
+  sum_before(work, p.nseq, s_sum[0], all);
+  const int64_t W = all & (((int64_t)1 << 40) - 1), all_items = all >> 40;
+  if (many ? __syncthreads_or(broken) : __any(broken)) {
     Item bad;
     for (int j = blockIdx.x; j < p.nseq; j += gridDim.x) {
       load_seq_uniform(p, j, bad);
@@ -977,12 +1018,14 @@ void tree_attn_even_kernel(AttnParams p) {
     if (per > 1) load_seq(p, j, it);  // (else `it` is that sequence)
     mine += units_of(p, it, quantum);
   }
-  const int64_t before = sum_before(mine, s_sum[2], units);
+  const int64_t before = sum_before(mine, p.nseq, s_sum[1], units);
   if (quantum) G = (int)units;
+  const int64_t each_group = divide(units, G);
+  const Share share{each_group, units - each_group * G};
   // consecutive runs go to one XCD: row tiles of a sequence share its L2
   const int runs = (G + 7) / 8;
   const int b = (blockIdx.x % 8) * runs + blockIdx.x / 8;
-  if (blockIdx.x == 0 && p.plan.total > 0) {
+  if (blockIdx.x == 0 && p.plan.total > 0 && tid == who) {
     int64_t at = before;
     for (int j = j0; j < j1; ++j) {
       p.sums[3 + j] = at;
@@ -990,30 +1033,43 @@ void tree_attn_even_kernel(AttnParams p) {
       at += units_of(p, it, quantum);
     }
     if (tid == 0) {
-      p.sums[0] = units;
-      p.sums[1] = G;
+      p.sums[0] = share.each;
+      p.sums[1] = share.more;
       p.sums[2] = quantum;
     }
   }
   if ((int)(blockIdx.x / 8) >= runs || b >= G) return;
-  const int64_t begin = first_unit(units, G, b), end = first_unit(units, G, b + 1);
-  if (before <= begin && begin < before + mine) {
-    int64_t at = before;
-    for (int j = j0; j < j1; ++j) {
-      if (per > 1) load_seq(p, j, it);
-      const int64_t n = units_of(p, it, quantum);
-      if (begin < at + n) {
-        s_item = it;
-        s_base = at;
-        break;
+  const int64_t begin = share.first(b), end = share.first(b + 1);
+  int64_t base;  // units before the sequence
+  const bool mine_first = before <= begin && begin < before + mine;
+  if (!many) {
+    const int lane = (int)__builtin_ctzll(__ballot(mine_first));
+    it.j = lane;
+    it.t0 = __builtin_amdgcn_readlane(it.t0, lane);
+    it.n = __builtin_amdgcn_readlane(it.n, lane);
+    it.seq = __builtin_amdgcn_readlane(it.seq, lane);
+    it.len = __builtin_amdgcn_readlane(it.len, lane);
+    it.broken = false;
+    base = of_lane(before, lane);
+  } else {
+    if (mine_first) {
+      int64_t at = before;
+      for (int j = j0; j < j1; ++j) {
+        if (per > 1) load_seq(p, j, it);
+        const int64_t n = units_of(p, it, quantum);
+        if (begin < at + n) {
+          s_item = it;
+          s_base = at;
+          break;
+        }
+        at += n;
       }
-      at += n;
     }
+    __syncthreads();
+    it = s_item;
+    base = of_lane(s_base, 0);
   }
-  __syncthreads();
-  it = s_item;
   uniform(p, it);
-  int64_t base = s_base;  // units before the sequence
   for (int64_t unit = begin; unit < end;) {
     const int tiles = tiles_of(it), each = units_of_item(it, quantum);
     const int64_t n = units_of(p, it, quantum);
@@ -1024,11 +1080,11 @@ void tree_attn_even_kernel(AttnParams p) {
       uniform(p, it);
       continue;
     }
-    const int item = __builtin_amdgcn_readfirstlane((int)((unit - base) / each));
+    const int item = __builtin_amdgcn_readfirstlane((int)divide(unit - base, each));
     const int at = __builtin_amdgcn_readfirstlane((int)(unit - base - (int64_t)item * each));
     const int count = quantum ? 1 : (int)min((int64_t)(each - at), end - unit);
-    const int first = quantum ? (int)((int64_t)tiles * at / each) : at;
-    const int last = quantum ? (int)((int64_t)tiles * (at + 1) / each) : at + count;
+    const int first = quantum ? (int)divide((int64_t)tiles * at, each) : at;
+    const int last = quantum ? (int)divide((int64_t)tiles * (at + 1), each) : at + count;
     it.kvh = item / row_tiles_of(it);
     it.rt = item - it.kvh * row_tiles_of(it);
     it.whole = first == 0 && last == tiles;
@@ -1050,13 +1106,12 @@ void tree_attn_even_kernel(AttnParams p) {
 template <bool EVEN, int V>
 __global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p, int vectors_each) {
   const int waves = p.plan.waves, vectors = p.d_v / 8;
-  const int blocks = (vectors + vectors_each - 1) / vectors_each;
-  int64_t b = blockIdx.x;
-  const int vb = (int)(b % blocks) * vectors_each;
-  b /= blocks;
+  const uint32_t blocks = (vectors + vectors_each - 1) / vectors_each;
+  const uint32_t b = blockIdx.x / blocks;
+  const int vb = (int)(blockIdx.x % blocks) * vectors_each;
   const int wave = (int)(b % waves);
-  const int64_t tile = b / waves;
-  const int64_t head = tile / p.plan.row_tiles;
+  const uint32_t tile = b / waves;
+  const uint32_t head = tile / p.plan.row_tiles;
   Item it;
   int chunk = 0, parts, first = 0;  // parts in order: slots at(0) .. at(parts - 1)
   int64_t slot0 = 0;
@@ -1066,19 +1121,16 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p,
     const int j = (int)(head / p.H_kv);
     load_seq_uniform(p, j, it);
     if (it.broken || it.rt >= row_tiles_of(it)) return;
-    const int64_t units = p.sums[0];
-    const int G = (int)p.sums[1], quantum = (int)p.sums[2], each = units_of_item(it, quantum);
-    const int64_t u0 = p.sums[3 + j] + (int64_t)(it.kvh * row_tiles_of(it) + it.rt) * each, u1 = u0 + each;
-    if (units < 1 || G < 1) return;
-    first = min((int)(u0 * G / units), G - 1);  // the workgroup of unit u0
-    while (first + 1 < G && first_unit(units, G, first + 1) <= u0) ++first;
-    while (first > 0 && first_unit(units, G, first) > u0) --first;
-    if (first_unit(units, G, first + 1) >= u1) return;  // all of it: the result is there
-    parts = 1;
-    while (first + parts < G && first_unit(units, G, first + parts) < u1) ++parts;
-    slot0 = 2 * first + (first_unit(units, G, first) < u0 ? 1 : 0);
+    const Share share{p.sums[0], p.sums[1]};
+    const int each = units_of_item(it, (int)p.sums[2]);
+    const int64_t u0 = p.sums[3 + j] + (int64_t)(it.kvh * row_tiles_of(it) + it.rt) * each;
+    // (the bounds keep a workspace that another call writes meanwhile from leading outside it)
+    first = min(max(share.of(u0), 0), p.plan.groups - 1);
+    parts = min(max(share.of(u0 + each - 1) - first, 0), p.plan.groups - 1 - first) + 1;
+    if (parts == 1) return;  // the result is there
+    slot0 = 2 * first + (share.first(first) < u0 ? 1 : 0);
   } else {
-    if (!find_item(p, head * p.plan.chunks * p.plan.row_tiles + tile % p.plan.row_tiles, it, chunk)) return;
+    if (!find_item(p, (int64_t)head * p.plan.chunks * p.plan.row_tiles + tile % p.plan.row_tiles, it, chunk)) return;
     if (it.broken || it.whole) return;
     parts = (it.total + p.plan.chunk - 1) / p.plan.chunk;
     slot0 = it.slot;
