@@ -639,7 +639,8 @@ struct Worker {
       const int after = slot + 1 == S::STAGES ? 0 : slot + 1;
       Next loads;
       if constexpr (!MX) {
-        vm_wait<S::LOADS>();
+        if (i + 2 < tiles) vm_wait<S::LOADS>();
+        else vm_wait<0>();  // nothing younger than tile i + 1 is under way
         barrier_reads_done();
         if (i + 3 < tiles) loads = next_loads(tk_begin + (i + 3) * TILE, third);
       } else {

@@ -340,3 +340,111 @@ def test_same_bits_every_time_on_any_stream_and_in_a_graph():
         assert torch.equal(o2, o3) and torch.equal(l2, l3)
         if k == 0:
             assert torch.equal(o2, out)
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+@pytest.mark.parametrize("n", [65, 300, 600])
+def test_many_sequences(n, mx):
+    """More sequences than lanes and than threads, some without drafts, some listed twice, some outgrown."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 90, (n,), generator=g).tolist()
+    drafts = torch.randint(0, 3, (n,), generator=g).tolist()
+    order = torch.randperm(n, generator=g).tolist()
+    order[7] = order[-1]
+    for shape in ("latent", "latent small"):
+        c = make(shape, lens, drafts, 16, seed=21, mx=mx, heads=2, order=order).tree()
+        want = c.expected()
+        check(*c.run(), want, c.q.shape[2])
+        for j, s in enumerate(order):
+            if lens[s] + drafts[j] > 80:
+                for x in want[:2]:
+                    x[c.cu[j]: c.cu[j + 1]] = math.nan
+        check(*c.run(max_len=80), want, c.q.shape[2])
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+def test_more_row_tiles_than_workgroups(mx):
+    """Several items, and parts of items, to a workgroup."""
+    g = torch.Generator().manual_seed(22)
+    lens = torch.randint(0, 150, (80,), generator=g).tolist()
+    c = make("latent", lens, [1] * 80, 16, seed=22, mx=mx, heads=128)
+    check(*c.run(), c.expected(), 576)
+    c = make("latent", lens[:30], [4, 1, 3] * 10, 16, seed=23, mx=mx, heads=70).tree()
+    check(*c.run(), c.expected(), 576)
+
+
+@pytest.mark.parametrize("shape", ["latent", "per head"])
+def test_drafts_that_see_only_themselves(shape):
+    """Rows whose first tiles are masked as a whole."""
+    c = make(shape, [0, 3, 64], [70, 40, 33], 16, seed=24)
+    c.mask = torch.zeros(c.T, 3, dtype=torch.int64)
+    for j, n in enumerate(c.drafts):
+        for i in range(n):
+            c.mask[c.cu[j] + i, i // 32] = 1 << (i % 32)
+    out, lse = c.run()
+    check(out, lse, c.expected(), c.q.shape[2])
+
+
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+def test_parts_longer_than_the_list_of_pages(mx):
+    """Pages of one row, and parts of more rows than the kernel lists pages at a time, with rows behind the first
+    list that carry all the weight: scores 130 above the others, beyond what the running reference may lag. Eight
+    such rows at distances of 25500 share it; without one of them the outputs change by an eighth."""
+    n, d = 211000, 576
+    g = torch.Generator().manual_seed(25)
+    rows = torch.randn(n, d, generator=g).to(torch.bfloat16)
+    q = normal(26, 1, 1, d)
+    qd = q.double().view(-1)
+    at = [1000 + 25500 * k for k in range(8)]
+    for r in at:
+        v = rows[r].double()
+        rows[r] = (v + qd * ((130 * 24 - v @ qd) / (qd @ qd))).to(torch.bfloat16)
+    c = Case.__new__(Case)
+    c.lens, c.drafts, c.page, c.d_v, c.mx, c.order, c.cu, c.T = [n - 1], [1], 1, 512, mx, [0], [0, 1], 1
+    c.held, c.table = [n], torch.randperm(n, generator=g).to(torch.int32).view(1, n)
+    buf = torch.empty(n, d, dtype=torch.bfloat16)
+    buf[c.table[0].long()] = rows
+    c.bufs = [buf.view(n, 1, 1, d)]
+    if mx:
+        codes, sc = (torch.empty(n, w, dtype=torch.uint8, device=DEV) for w in (d, d // 32))
+        m.mxfp8_quantize(buf.to(DEV), codes, sc)
+        c.bufs = [codes.cpu().view(n, 1, 1, d), sc.cpu().view(n, 1, 1, d // 32)]
+    c.q, c.scale, c.mask, c.max_q, c.max_len = q, 1 / 24, None, 1, n
+    check(*c.run(), c.expected(), d)
+
+
+def test_a_graph_follows_the_lengths_on_the_device():
+    """Captured once, replayed with other lengths, orders of magnitude apart, in the same buffers."""
+    c = make("latent", [700, 90, 5, 0], [3, 2, 4, 1], 48, seed=27, heads=32)
+    pool, seqs, cu, _ = c.device()
+    q = c.q.to(DEV)
+    out, lse = torch.empty(c.T, 32, 512, dtype=torch.bfloat16, device=DEV), torch.empty(c.T, 32, device=DEV)
+    kw = dict(max_q=c.max_q, max_len=c.max_len, scale=c.scale, lse=lse)
+    size = m.mla_tree_attention_workspace_size(q, pool, out, seqs, cu, **kw)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.mla_tree_attention(q, pool, out, seqs, cu, workspace=ws, **kw)
+    for lens in ([700, 90, 5, 0], [0, 0, 0, 0], [31, 28, 5, 0], [650, 1, 0, 0], [700, 90, 5, 0]):
+        pool.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7)
+        lse.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        c.lens = lens
+        check(out.cpu(), lse.cpu(), c.expected(), 576)
+        again = out.clone()
+        ws.fill_(0xFF)
+        m.mla_tree_attention(q, pool, out, seqs, cu, workspace=ws, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(again, out)
+
+
+def test_no_tokens_and_no_sequences():
+    c = make("latent", [40], [0], 16, seed=28, heads=2)
+    out, lse = c.run()
+    assert out.numel() == 0 and lse.numel() == 0
+    c = make("latent", [40], [2], 16, seed=28, heads=2)
+    c.cu, c.order = [0], []
+    out, lse = c.run()
+    assert (out == 7).all() and (lse == 7).all()
