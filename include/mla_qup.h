@@ -543,11 +543,15 @@ typedef struct {
   size_t workspace_bytes;
 } mla_tree_attn_args;
 
-/* Workspace bytes for these arguments: the partial results of the cache's
- * chunks. Never dereferences device pointers; 0 for invalid shapes. */
+/* Workspace bytes for these arguments on the current device: the partial
+ * results of the cache's chunks. Never dereferences device pointers; 0 for invalid shapes. */
 MLA_API size_t mla_tree_attention_workspace_size(const mla_tree_attn_args* args);
 
-/* Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED, MLA_EDEVICE. */
+/* Errors: MLA_EINVAL (also for calls past the launch limits: nseq * H_kv *
+ * ceil(max_q H / H_kv / 32) row tiles, or parts of the cache's rows, of 2^23 and
+ * more), MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED, MLA_EDEVICE. The
+ * workspace belongs to one call at a time: calls that may run at once (two
+ * streams, two graphs) need one each. */
 MLA_API mla_status mla_tree_attention(const mla_tree_attn_args* args, void* stream);
 
 /* Static string naming a status code. */

@@ -683,7 +683,8 @@ def make_tree_attn_args(q, pool, out, seqs, cu_q, *, max_q, max_len, scale, lse=
 def mla_tree_attention_workspace_size(q, pool, out, seqs, cu_q, **kw) -> int:
     kw.pop("stream", None)
     a = make_tree_attn_args(q, pool, out, seqs, cu_q, **kw)
-    return int(lib().mla_tree_attention_workspace_size(ctypes.byref(a)))
+    with torch.cuda.device(pool.device if pool.device.type == "cuda" else -1):  # the plan asks for its compute units
+        return int(lib().mla_tree_attention_workspace_size(ctypes.byref(a)))
 
 
 def mla_tree_attention(q, pool, out, seqs, cu_q, *, stream=None, **kw):

@@ -993,16 +993,16 @@ void tree_attn_even_kernel(AttnParams p) {
   const bool many = p.nseq > 64;
   const int per = many ? (p.nseq + 255) / 256 : 1, who = many ? tid : tid & 63;
   const int j0 = min(who * per, p.nseq), j1 = min(j0 + per, p.nseq);
-  int64_t work = 0, all;  // steps, and above them items (at most 2^23)
+  int64_t work = 0, all;  // steps (fewer than 2^42), and above them items (fewer than 2^21)
   int broken = 0;
   for (int j = j0; j < j1; ++j) {
     load_seq(p, j, it);
     const int64_t n = units_of(p, it, 0);
-    work += n + (n ? (int64_t)(p.H_kv * row_tiles_of(it)) << 40 : 0);
+    work += n + (n ? (int64_t)(p.H_kv * row_tiles_of(it)) << 42 : 0);
     broken |= it.broken && it.n > 0;
   }
   sum_before(work, p.nseq, s_sum[0], all);
-  const int64_t W = all & (((int64_t)1 << 40) - 1), all_items = all >> 40;
+  const int64_t W = all & (((int64_t)1 << 42) - 1), all_items = all >> 42;
   if (many ? __syncthreads_or(broken) : __any(broken)) {
     Item bad;
     for (int j = blockIdx.x; j < p.nseq; j += gridDim.x) {

@@ -232,6 +232,16 @@ def test_attention_refusals(L, over, code):
     assert L.mla_tree_attention(None, None) == bd.MLA_EINVAL
 
 
+def test_attention_limits(L):
+    size = lambda **kw: L.mla_tree_attention_workspace_size(ctypes.byref(attn(**kw)))  # noqa: E731
+    assert size(nseq=1024, max_q=64, mask_words=2) > 0  # 2^16 row tiles of 128
+    assert size(nseq=32768, max_q=63, mask_words=2) > 0  # just below 2^21
+    assert size(nseq=32768, max_q=64, mask_words=2) == 0  # 2^23 groups of 32 rows
+    assert size(nseq=16384, max_q=64, mask_words=2, max_len=(1 << 31) - 1) == 0  # 2^46 steps
+    a = attn(nseq=32768, max_q=64, mask_words=2)
+    assert L.mla_tree_attention(ctypes.byref(a), None) == bd.MLA_EINVAL
+
+
 def test_cache_must_fit_the_widths(L):
     two = dict(nbuf=2, buf__1=addr(6), page_bytes__1=64 * 1024)
     assert L.mla_tree_attention(ctypes.byref(attn(pool=pool(**two))), None) == bd.MLA_EUNSUPPORTED  # (576, 512) with values

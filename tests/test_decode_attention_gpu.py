@@ -448,3 +448,10 @@ def test_no_tokens_and_no_sequences():
     c.cu, c.order = [0], []
     out, lse = c.run()
     assert (out == 7).all() and (lse == 7).all()
+
+
+def test_bounds_far_above_the_call():
+    g = torch.Generator().manual_seed(29)
+    lens = torch.randint(0, 40, (1000,), generator=g).tolist()
+    c = make("latent", lens, [1, 2] * 500, 16, seed=29, heads=8)
+    check(*c.run(max_q=512, max_len=50000), c.expected(), 576)
