@@ -547,9 +547,9 @@ typedef struct {
  * results of the cache's chunks. Never dereferences device pointers; 0 for invalid shapes. */
 MLA_API size_t mla_tree_attention_workspace_size(const mla_tree_attn_args* args);
 
-/* Errors: MLA_EINVAL (also for calls past the launch limits: nseq * H_kv *
- * ceil(max_q H / H_kv / 32) row tiles, or parts of the cache's rows, of 2^23 and
- * more), MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED, MLA_EDEVICE. The
+/* Errors: MLA_EINVAL (also for calls past the launch limits: 2^21 groups of 32
+ * query rows, nseq * H_kv * ceil(max_q H / H_kv / 32), rounded up to tiles of
+ * 64 or 128 rows, or 2^23 of them times parts of the cache), MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED, MLA_EDEVICE. The
  * workspace belongs to one call at a time: calls that may run at once (two
  * streams, two graphs) need one each. */
 MLA_API mla_status mla_tree_attention(const mla_tree_attn_args* args, void* stream);

@@ -441,7 +441,7 @@ mla_status check_attn(const mla_tree_attn_args* a, mla::AttnPlan* plan) {
   *plan = mla::plan_attn(a->T, a->nseq, a->H, a->H_kv, a->d_k, a->d_v, a->max_q, a->max_len, a->pool->page_size);
   // every grid stays below 2^31 work-items, and the even plan's sums within their bits
   const double tiles = (double)a->nseq * a->H_kv * plan->row_tiles;
-  if (tiles * std::max(plan->chunks, plan->waves) >= (double)(1 << 23)) return MLA_EINVAL;
+  if (tiles * plan->chunks >= (double)(1 << 23) || tiles * plan->waves >= (double)(1 << 21)) return MLA_EINVAL;
   if (plan->groups > 0 && tiles * ((a->max_len - 1) / 32 + 1) >= (double)((int64_t)1 << 42)) return MLA_EINVAL;
   return MLA_OK;
 }

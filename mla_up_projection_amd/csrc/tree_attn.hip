@@ -1098,12 +1098,12 @@ void tree_attn_even_kernel(AttnParams p) {
 // Joins the partial results of 32 query rows (a wave of a row tile): out = sum_c
 // 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the parts c of the cache rows. A
 // lane takes 4-element vectors of one query row. A workgroup's way to its first
-// partial result is a chain of five loads, about 4 us, so there should not be
-// many more of them than run at once (16 blocks for each of 1024 row groups took
-// 47 us for 100 MB, one block 34 us). V = 4: four waves share `vectors_each`
-// vectors, four in flight each. V = 1, for few rows with many parts: a wave takes
-// one vector, and where the workgroup has more than four waves they share the
-// parts and add up in LDS. The order of every sum is fixed.
+// partial result is a chain of loads, so many of them should run at once: 1024
+// row groups with 100 MB of partial results took 42 us in one block of 64 vectors
+// each, 32 in four blocks of 16, 34 in eight. V = 4: four waves share
+// `vectors_each` vectors, four in flight each. V = 1, for few rows with many
+// parts: a wave takes one vector, and where the workgroup has more than four
+// waves they share the parts and add up in LDS. The order of every sum is fixed.
 template <bool EVEN, int V>
 __global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p, int vectors_each) {
   const int waves = p.plan.waves, vectors = p.d_v / 8;
@@ -1152,7 +1152,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p,
   const int64_t t = it.t0 + i;
   // this wave's parts: their largest reference
   const int c1 = V == 1 ? own >> 2 : 0, step = V == 1 ? blockDim.x / 256 : 1;
-  constexpr int U = V == 1 ? 8 : 2;  // parts at once
+  constexpr int U = V == 1 ? 8 : 4;  // parts at once
   float M = NEG_INF;
   if (live)
     for (int c0 = c1; c0 < parts; c0 += step * 8) {
@@ -1259,12 +1259,11 @@ hipError_t launch_tree_attn(const AttnParams& p, hipStream_t stream) {
   else launch_dtype<64, 64, false>(p, grid, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.plan.total == 0) return e;  // no item has parts
-  // By the groups of 32 rows: many take all their vectors or a quarter of them in
-  // a workgroup; few take four, and share parts (at most, or on average) over
-  // four times the waves.
+  // By the groups of 32 rows: many take 16 of their vectors in a workgroup; few
+  // take four, and share parts (at most, or on average) over four times the waves.
   const int64_t groups = tiles * p.plan.waves;
   const int64_t parts = p.plan.groups > 0 ? p.plan.groups / tiles : p.plan.chunks;
-  const int vectors = p.d_v / 8, each = groups >= 1024 ? std::min(vectors, 64) : groups >= 64 ? std::min(vectors, 16) : 4;
+  const int vectors = p.d_v / 8, each = groups >= 64 ? std::min(vectors, 16) : 4;
   const dim3 grid2((unsigned)(groups * ((vectors + each - 1) / each)));
   const dim3 threads(each == 4 && parts >= 16 ? 1024 : 256);
   if (p.plan.groups > 0) {

@@ -235,10 +235,10 @@ def test_attention_refusals(L, over, code):
 def test_attention_limits(L):
     size = lambda **kw: L.mla_tree_attention_workspace_size(ctypes.byref(attn(**kw)))  # noqa: E731
     assert size(nseq=1024, max_q=64, mask_words=2) > 0  # 2^16 row tiles of 128
-    assert size(nseq=32768, max_q=63, mask_words=2) > 0  # just below 2^21
-    assert size(nseq=32768, max_q=64, mask_words=2) == 0  # 2^23 groups of 32 rows
-    assert size(nseq=16384, max_q=64, mask_words=2, max_len=(1 << 31) - 1) == 0  # 2^46 steps
-    a = attn(nseq=32768, max_q=64, mask_words=2)
+    assert size(nseq=8192, max_q=63, mask_words=2) > 0
+    assert size(nseq=8192, max_q=64, mask_words=2) == 0  # 2^21 groups of 32 rows
+    assert size(nseq=4096, max_q=64, mask_words=2, max_len=(1 << 31) - 1) == 0  # 2^44 steps
+    a = attn(nseq=8192, max_q=64, mask_words=2)
     assert L.mla_tree_attention(ctypes.byref(a), None) == bd.MLA_EINVAL
 
 
