@@ -19,8 +19,6 @@
 namespace mla {
 namespace {
 
-constexpr int W4_WAVES = 4;   // each takes every fourth 128-wide chunk of K
-
 // Two E2M1 codes (byte SEL of the dword) times scale, in bf16.
 template <int SEL>
 __device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, float scale) {
@@ -40,16 +38,17 @@ __device__ __forceinline__ void dma16_any(const void* p, uint32_t lds_addr) {
                : "memory", "m0");
 }
 
-// A workgroup makes MT tiles of 16 tokens by NT of 16 weight rows. X comes by
+// A workgroup makes MT tiles of 16 tokens by NT of 16 weight rows; its waves take
+// the 128-wide chunks of K in turn and add up in LDS. X comes by
 // direct loads into LDS, whole rows at a time: loaded as fragments (16 rows by 64
 // bytes to an instruction) 16 tokens of the 128-head shape (K 1536) took 11.9 us,
 // 32 took 16.5 and 52 took 27 (one weight tile pair); so they take 9.4, 11.4 and
 // 22. One token takes 8.8 either way: 2.3 TB/s of weights.
-template <int MT, int NT>
-__global__ __launch_bounds__(256) void qup_w4_kernel(W4Params p) {
+template <int MT, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void qup_w4_kernel(W4Params p) {
   constexpr int PITCH = 16 * NT + 4;   // floats per token row of a wave's partial sums
   constexpr int X_LDS = MT * 16 * 256;  // a wave's chunk of X
-  constexpr int LDS = W4_WAVES * std::max(X_LDS, MT * 16 * PITCH * 4);
+  constexpr int LDS = WAVES * std::max(X_LDS, MT * 16 * PITCH * 4);
   __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   float(*red)[MT * 16][PITCH] = reinterpret_cast<float(*)[MT * 16][PITCH]>(lds);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -64,7 +63,7 @@ __global__ __launch_bounds__(256) void qup_w4_kernel(W4Params p) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
     __syncthreads();  // the previous tokens' partial sums are read
-    for (int c = wave; c < chunks; c += W4_WAVES) {
+    for (int c = wave; c < chunks; c += WAVES) {
       u32x4_t w[NT], x[MT][4];
       uint32_t s[NT];
       const int k = c * 128 + 32 * c4;
@@ -123,7 +122,7 @@ __global__ __launch_bounds__(256) void qup_w4_kernel(W4Params p) {
     // Four consecutive threads own 32 columns (an MX block of the output, all of
     // one head) of a token, eight each.
     const TokenMap tm{p.fmt, p.B, p.S, p.cu, p.nseq};
-    for (int i = threadIdx.x; i < MT * 16 * 2 * NT; i += 256) {
+    for (int i = threadIdx.x; i < MT * 16 * 2 * NT; i += 64 * WAVES) {
       const int tl = i / (2 * NT), g = i - tl * (2 * NT);  // token, group of eight columns
       const int64_t t = t0 + tl;
       const int n = n0 + 8 * g;
@@ -132,7 +131,7 @@ __global__ __launch_bounds__(256) void qup_w4_kernel(W4Params p) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = 0;
 #pragma unroll
-      for (int w = 0; w < W4_WAVES; ++w)
+      for (int w = 0; w < WAVES; ++w)
 #pragma unroll
         for (int k = 0; k < 8; k += 4) {
           const f32x4_t r = *reinterpret_cast<const f32x4_t*>(&red[w][tl][8 * g + k]);
@@ -186,11 +185,11 @@ __global__ __launch_bounds__(256) void qup_w4_kernel(W4Params p) {
   }
 }
 
-template <int MT, int NT>
+template <int MT, int NT, int WAVES>
 void launch_w4(const W4Params& p, hipStream_t stream) {
   const int64_t blocks = (p.T + 16 * MT - 1) / (16 * MT);  // the kernel strides over those past the grid
   const dim3 grid((unsigned)((p.N + 16 * NT - 1) / (16 * NT)), (unsigned)std::min<int64_t>(blocks, 4096));
-  hipLaunchKernelGGL((qup_w4_kernel<MT, NT>), grid, dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((qup_w4_kernel<MT, NT, WAVES>), grid, dim3(64 * WAVES), 0, stream, p);
 }
 
 }  // namespace
@@ -200,10 +199,14 @@ hipError_t launch_qup_w4(const W4Params& p, hipStream_t stream) {
   // X is read once per workgroup, so many tokens want many weight rows, as long
   // as a workgroup per CU is left: 52 tokens of 128 heads (N 24576) take 16.6 us
   // with NT = 4 and 21.9 with 2, 64 tokens of 32 heads (N 6144) 13.5 and 10.7.
-  if (p.T <= 16) launch_w4<1, 2>(p, stream);
-  else if (p.T <= 32) launch_w4<2, 2>(p, stream);
-  else if (p.N >= 64 * 256) launch_w4<4, 4>(p, stream);
-  else launch_w4<4, 2>(p, stream);
+  // Eight waves share the chunks of K where workgroups are few and K has more
+  // than four: one token, K 7168, N 12288 29.6 -> 22.3 us, 16 tokens, K 4096, 16
+  // heads of 192 13.5 -> 10.0; but N 24576, K 1536 8.9 -> 11.1, K 512 3.7 -> 4.1.
+  const bool few = p.N < 64 * 256, eight = few && p.K > 512;
+  if (p.T <= 16) eight ? launch_w4<1, 2, 8>(p, stream) : launch_w4<1, 2, 4>(p, stream);
+  else if (p.T <= 32) eight ? launch_w4<2, 2, 8>(p, stream) : launch_w4<2, 2, 4>(p, stream);
+  else if (!few) launch_w4<4, 4, 4>(p, stream);
+  else eight ? launch_w4<4, 2, 8>(p, stream) : launch_w4<4, 2, 4>(p, stream);
   return hipGetLastError();
 }
 

@@ -154,6 +154,14 @@ def test_full_shape():
     run_case(40, 1536, 128, 128, 64, True)
 
 
+@pytest.mark.parametrize("T", [1, 20, 40])
+def test_heads_of_one_block(T):
+    """Weight rows that end inside a workgroup's, few and many."""
+    for H in (1, 511, 513):
+        run_case(T, 96, H, 16, 16, H == 513)
+    run_case(T, 1056, 3, 30, 2, False)
+
+
 def test_positions_outside_the_table():
     run_case(6, 64, 2, 32, 32, False, pos=torch.tensor([0, -1, 4999, 5000, 2 ** 31 - 1, -2 ** 31]))
     run_case(6, 64, 2, 32, 32, True, pos=torch.tensor([0, -1, 4999, 5000, 2 ** 31 - 1, -2 ** 31]))
