@@ -1,7 +1,8 @@
 // C ABI of the decode-side operators: host-side validation, the plan of the
 // attention, then the launches. Argument meanings, layouts and error behaviour
 // are stated in include/mla_qup.h. As in api.hip, validation dereferences no
-// device pointer and makes no HIP call, so every error path runs without a GPU;
+// device pointer, so every error path runs without a GPU (the attention's plan
+// asks for the device's compute units and takes 256 where there is none);
 // nothing here allocates.
 #include <math.h>
 #include <stdint.h>

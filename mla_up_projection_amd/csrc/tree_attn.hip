@@ -13,9 +13,17 @@
 // registers; the cache tile (32 rows) is in LDS, shared by the workgroup's
 // waves, V^T fragments by the transposing LDS read.
 //
-// The cache of a sequence is cut into chunks that different workgroups take;
-// their (m, l, O) are joined by a second kernel in chunk order. A sequence of
-// one chunk is finished at once.
+// The cache of a sequence is cut into parts that different workgroups take;
+// their (m, l, O) are joined by a second kernel in the order of the parts. A
+// sequence of one part is finished at once.
+//
+// What bounds it (rates on the same card: a large copy 4.9 TB/s, a large bf16
+// product 1365 TFLOP/s): per-head caches HBM (4 sequences of 300 to 1500 rows, 128
+// heads of 192 + 128: 62 us and 8 for the join, 4.3 TB/s); the shared 576-wide
+// cache the matrix units, at 2 flops for each of 128 heads and draft to a byte (32
+// sequences of 4096 rows, 16 drafts, 128 heads: 582 us, 1006 TFLOP/s; MXFP8 671);
+// a single token the way through the kernel (one sequence of 517 rows: 18 us, of
+// which the products are 4, and 7 for the join).
 #include <algorithm>
 
 #include "device_common.h"
@@ -132,8 +140,8 @@ struct Share {
 // More workgroups shorten the longest but write more partial results: a step
 // takes 2 us, a partial result (256 KB out and in again) 0.12 us of all
 // workgroups' time and 0.2 us more in the join of its item (a single sequence of
-// 65000 rows: 238 parts 44 + 51 us, 110 parts 48 + 28 us). W 2 / G + (0.12 + 0.2 /
-// items) G is least at the square root below.
+// 65000 rows: 150 parts 44 + 26 us, 113 parts 48 + 21, 101 parts 51 + 19).
+// W 2 / G + (0.12 + 0.2 / items) G is least at the square root below.
 __device__ __forceinline__ int workgroups_for(const AttnParams& p, int64_t W, int64_t items) {
   const float part = 0.12f + 0.2f * __builtin_amdgcn_rcpf((float)max(items, (int64_t)1));
   const float best = __builtin_amdgcn_sqrtf(2.0f * (float)W * __builtin_amdgcn_rcpf(part));
