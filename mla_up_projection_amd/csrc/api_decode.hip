@@ -389,7 +389,7 @@ AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int m
     pl.row_tiles = (int)std::min<int64_t>(tiles, INT32_MAX);
     pl.chunk = (int)most;
     pl.chunks = 1;
-    const double steps = std::max(1.0, (double)nseq * H_kv * (double)tiles * ((max_len + 31) / 32));
+    const double steps = std::max(1.0, (double)nseq * H_kv * (double)tiles * ((max_len - 1) / 32 + 1));
     pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(17.0 * steps)) + 1});
     if (pl.groups > 1 && max_len > 32) {  // (an item of one step has no parts)
       const size_t slots = (size_t)2 * pl.groups * pl.waves;
@@ -406,10 +406,10 @@ AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int m
   const int64_t units = std::max<int64_t>(1, (int64_t)nseq * H_kv * tiles);
   // workgroups to fill the chip twice over with the waves that fit
   const int64_t want = std::max<int64_t>(1, 2 * 256 * 4 / pl.waves / units);
-  const int64_t n = std::min<int64_t>(want, std::max(1, (max_len + 127) / 128));  // four tiles at least
+  const int64_t n = std::min<int64_t>(want, (max_len - 1) / 128 + 1);  // four tiles at least
   const int64_t chunk = std::min((((int64_t)max_len + n - 1) / n + 31) / 32 * 32, most);
   pl.chunk = (int)std::max<int64_t>(chunk, 32);
-  pl.chunks = (max_len + pl.chunk - 1) / pl.chunk;
+  pl.chunks = (max_len - 1) / pl.chunk + 1;
   if (pl.chunks > 1) {
     const size_t slots = (size_t)units * pl.chunks * pl.waves;
     pl.part_o = 0;

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(PT) void reserve_plan_kernel(PoolParams p, const in
     len = p.lens[seq];
     held = p.held[seq];
     const int64_t rows = (int64_t)len + fresh;
-    if (len < 0 || fresh < 0 || rows > (int64_t)p.max_pages * p.page_size) {
+    if (len < 0 || fresh < 0 || held < 0 || rows > (int64_t)p.max_pages * p.page_size) {
       bad = 1;
     } else {
       // (the clamp keeps the sum over 1024 sequences within 32 bits)
@@ -227,7 +227,8 @@ __global__ __launch_bounds__(256) void fork_kernel(PoolParams p, const int32_t* 
   if (listed(dst, i, d) || listed(dst, n, s)) return;
   const int held_d = p.held[d], len = p.lens[s];
   if (held_d > 0) return;
-  const int pages = min((len + p.page_size - 1) / p.page_size, min(p.held[s], p.max_pages));
+  if (len < 0) return;
+  const int pages = max(0, min((int)(((int64_t)len + p.page_size - 1) / p.page_size), min(p.held[s], p.max_pages)));
   for (int k = threadIdx.x; k < pages; k += 256) {
     const int page = p.table[(int64_t)s * p.max_pages + k];
     p.table[(int64_t)d * p.max_pages + k] = page;
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(256) void free_kernel(PoolParams p, const int32_t* 
   if (listed(seqs, i, s)) return;
   const int len = p.lens[s], held = min(p.held[s], p.max_pages);
   const int left = keep ? max(0, min(keep[i], len)) : 0;
-  const int first = min((left + p.page_size - 1) / p.page_size, held);
+  const int first = max(0, min((int)(((int64_t)left + p.page_size - 1) / p.page_size), held));
   for (int k = first + threadIdx.x; k < held; k += 256) {
     int32_t* e = p.table + (int64_t)s * p.max_pages + k;
     const int page = *e;
@@ -391,7 +392,7 @@ __device__ __forceinline__ bool accept_ok(const PoolParams& p, const int32_t* __
                                           int i, int max_path, int& s, int& count) {
   s = seqs[i];
   count = n_acc[i];
-  if (s < 0 || s >= p.max_seqs || count <= 0 || count > max_path) return false;
+  if (s < 0 || s >= p.max_seqs || count <= 0 || count > max_path || p.lens[s] < 0) return false;
   if (listed(seqs, i, s)) return false;
   const int64_t room = (int64_t)min(p.held[s], p.max_pages) * p.page_size - p.lens[s];
   int wrong = 0;

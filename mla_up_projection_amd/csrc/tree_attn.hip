@@ -946,7 +946,7 @@ void tree_attn_kernel(AttnParams p) {
     return;
   }
   const int tk_begin = chunk * p.plan.chunk;
-  const int tk_end = min(tk_begin + p.plan.chunk, it.total);
+  const int tk_end = tk_begin + min(p.plan.chunk, it.total - tk_begin);
   if (it.rt * 32 * WAVES >= it.rows || tk_begin >= tk_end) return;
   run_item<DK, DV, SHARED, MX, WAVES>(p, it, lds, s_page, tk_begin, tk_end, p.plan.chunk);
 }
@@ -1141,7 +1141,7 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p,
   } else {
     if (!find_item(p, (int64_t)head * p.plan.chunks * p.plan.row_tiles + tile % p.plan.row_tiles, it, chunk)) return;
     if (it.broken || it.whole) return;
-    parts = (it.total + p.plan.chunk - 1) / p.plan.chunk;
+    parts = (it.total - 1) / p.plan.chunk + 1;
     slot0 = it.slot;
   }
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5, own = threadIdx.x >> 6;

@@ -238,6 +238,10 @@ def test_attention_limits(L):
     assert size(nseq=8192, max_q=63, mask_words=2) > 0
     assert size(nseq=8192, max_q=64, mask_words=2) == 0  # 2^21 groups of 32 rows
     assert size(nseq=4096, max_q=64, mask_words=2, max_len=(1 << 31) - 1) == 0  # 2^44 steps
+    assert size(max_len=(1 << 31) - 1) > 0
+    heads = pool(nbuf=2, buf__1=addr(6), page_bytes__0=64 * 2 * 384, page_bytes__1=64 * 2 * 256)
+    assert size(pool=heads, H=2, H_kv=2, d_k=192, d_v=128, q_stride_h=192, q_stride_t=384, out_stride_h=128,
+                out_stride_t=256, max_len=(1 << 31) - 1) > 0
     a = attn(nseq=8192, max_q=64, mask_words=2)
     assert L.mla_tree_attention(ctypes.byref(a), None) == bd.MLA_EINVAL
 

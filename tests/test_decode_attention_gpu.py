@@ -455,3 +455,4 @@ def test_bounds_far_above_the_call():
     lens = torch.randint(0, 40, (1000,), generator=g).tolist()
     c = make("latent", lens, [1, 2] * 500, 16, seed=29, heads=8)
     check(*c.run(max_q=512, max_len=50000), c.expected(), 576)
+    check(*c.run(max_len=2 ** 31 - 1), c.expected(), 576)

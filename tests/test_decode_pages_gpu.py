@@ -175,6 +175,25 @@ def test_accept_rules():
     b.accept([2, 1, -7, 5], [pad([1])] * 4, [14, -1, 1, 1])
 
 
+def test_lengths_that_cannot_be():
+    """Lengths outside what the pages hold change nothing but their own sequence."""
+    big = 2 ** 31 - 1
+    for bad in (-1, -big - 1, big):
+        b = Both(30, 4, 6, 6)
+        b.reserve([0, 1], [10, 3])
+        b.pool.lens.copy_(i32([bad, 3, 0, 0, 0, 0]))
+        table, refs = b.pool.table.clone(), b.pool.refs.clone()
+        m.mla_pages_reserve(b.pool, i32([0]), i32([1]), b.status, workspace=b.ws)
+        assert b.status.item() == -1
+        m.mla_draft_accept(b.pool, i32([0]), i32([[0, 1]]), i32([2]))
+        assert b.pool.lens[0].item() == bad and torch.equal(b.pool.table, table) and torch.equal(b.pool.refs, refs)
+        m.mla_pages_fork(b.pool, i32([0]), i32([2]))
+        m.mla_pages_free(b.pool, i32([0]), i32([big]))
+        assert b.pool.held[0].item() == (3 if bad > 0 else 0)
+        assert b.pool.held[2].item() == (3 if bad > 0 else 0)
+        assert torch.equal(b.pool.table[1], table[1]) and (b.pool.table[3:] == -1).all()
+
+
 def test_copy_pages():
     shapes, mx = POOLS["heads mxfp8"]
     for page in (1, 16):
