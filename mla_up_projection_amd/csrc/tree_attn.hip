@@ -22,7 +22,7 @@
 // heads of 192 + 128: 62 us and 8 for the join, 4.3 TB/s); the shared 576-wide
 // cache the matrix units, at 2 flops for each of 128 heads and draft to a byte (32
 // sequences of 4096 rows, 16 drafts, 128 heads: 582 us, 1006 TFLOP/s; MXFP8 671);
-// a single token the way through the kernel (one sequence of 517 rows: 18 us, of
+// a single token the way through the kernel (one sequence of 517 rows: 17 us, of
 // which the products are 4, and 7 for the join).
 #include <algorithm>
 
@@ -47,6 +47,16 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 // consecutive rows, one chunk each) and the transposing reads of V (4 rows, 64
 // bytes each) over all banks.
 __device__ __forceinline__ int swz(int t) { return ((t >> 1) & 1) << 2 | ((t >> 2) & 1) << 1 | ((t >> 3) & 1); }
+
+// v, in a way that lets nothing that follows from it be worked out ahead of its
+// use, where it would occupy registers in between. In the widest kernel addresses
+// of the path for strange values and of the page list, worked out early, went to
+// scratch memory and back on every call's way in: 19.0 us instead of 17.3 for one
+// token.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -257,13 +267,7 @@ struct Worker {
 
   __device__ __forceinline__ Worker(const AttnParams& p_, const Item& it_) : p(p_), it(it_) {}
 
-  // The thread's number, anew: what follows from it is then worked out where it
-  // is used instead of occupying registers all through the loop.
-  __device__ __forceinline__ int thread() const {
-    int t = tid;
-    asm volatile("" : "+v"(t));
-    return t;
-  }
+  __device__ __forceinline__ int thread() const { return opaque(tid); }
 
   // The lane's query row: draft qi, token qt, head h.
   struct Row {
@@ -744,7 +748,7 @@ __device__ __forceinline__ float cache_value(const PoolParams& pool, int b, int6
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, int tk_begin, int tk_end) {
   constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6;
   const int ps = p.pool.page_size;
   const int held = min(p.pool.held[it.seq], p.pool.max_pages);
   const int64_t slot = it.slot * WAVES + wave;
@@ -824,7 +828,7 @@ __device__ __forceinline__ bool fill_pages(const AttnParams& p, const Item& it, 
   const int pages = (tk_end - 1) / p.pool.page_size - page0 + 1;
   const int held = min(__builtin_amdgcn_readfirstlane(p.pool.held[it.seq]), p.pool.max_pages);
   bool bad = false;
-  for (int k = threadIdx.x; k < pages; k += 64 * WAVES) {
+  for (int k = opaque((int)threadIdx.x); k < pages; k += 64 * WAVES) {
     int id = page0 + k < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + page0 + k] : -1;
     if (id < 0 || id >= p.pool.num_pages) {
       id = -1;
