@@ -390,7 +390,9 @@ MLA_API mla_status mla_qup_fwd_w4(const mla_qup_w4_args* args, void* stream);
  * behind them (within the held pages) take drafted tokens. refs[p] counts the
  * table entries that name page p; 0 means free. A new pool has zeros in refs,
  * lens and held and -1 in table. All arrays are device memory. lens may only
- * be lowered through mla_pages_free.
+ * be lowered through mla_pages_free. A call that changes a pool (its arrays or
+ * its rows) must not run at the same time as another call on it: one stream, or
+ * events between two, orders them.
  * Buffers: up to four, buffer b's page p at buf[b] + p*page_bytes[b], its
  * page_size rows one after the other:
  *   bf16 : key [H, D_k], then value [H, D_v] unless D_v = 0

@@ -456,3 +456,22 @@ def test_bounds_far_above_the_call():
     c = make("latent", lens, [1, 2] * 500, 16, seed=29, heads=8)
     check(*c.run(max_q=512, max_len=50000), c.expected(), 576)
     check(*c.run(max_len=2 ** 31 - 1), c.expected(), 576)
+
+
+def test_calls_at_once():
+    """Two streams over one pool, each with its own workspace, several times over."""
+    c = make("latent", [3000, 90, 5, 1200], [3, 2, 4, 1], 48, seed=30, heads=32).tree()
+    pool, seqs, cu, mask = c.device()
+    q = c.q.to(DEV)
+    kw = dict(max_q=c.max_q, max_len=c.max_len, scale=c.scale, mask=mask)
+    outs = [torch.empty(c.T, 32, 512, dtype=torch.bfloat16, device=DEV) for _ in range(9)]
+    size = m.mla_tree_attention_workspace_size(q, pool, outs[0], seqs, cu, **kw)
+    ws = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    m.mla_tree_attention(q, pool, outs[8], seqs, cu, workspace=ws[0], **kw)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(8):
+        m.mla_tree_attention(q, pool, outs[k], seqs, cu, workspace=ws[k % 2], stream=streams[k % 2], **kw)
+    torch.cuda.synchronize()
+    for k in range(8):
+        assert torch.equal(outs[k], outs[8])
