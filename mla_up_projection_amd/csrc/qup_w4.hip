@@ -32,7 +32,7 @@ __device__ __forceinline__ bf16x8_t e2m1x8(uint32_t w, float scale) {
 
 // 16 bytes per lane to LDS bytes [lds_addr + 16 lane, + 16).
 __device__ __forceinline__ void dma16_any(const void* p, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(p)
                : "memory", "m0");

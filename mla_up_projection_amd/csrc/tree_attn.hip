@@ -224,14 +224,14 @@ __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
 
 // 16 bytes per lane from any address to LDS bytes [lds_addr + 16 lane, + 16).
 __device__ __forceinline__ void dma16_far(const void* p, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :
                : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(p)
                : "memory", "m0");
 }
 
 // The same with 4 bytes per lane.
 __device__ __forceinline__ void dma4_far(const void* p, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(p)
                : "memory", "m0");
