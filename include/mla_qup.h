@@ -491,9 +491,8 @@ typedef struct {
   const int32_t* seqs;      /* device int32[nseq] */
   const int32_t* cu_q;      /* device int32[nseq + 1], nondecreasing */
   int32_t nseq;             /* 0 .. MLA_MAX_SEQS */
-  int32_t max_q;            /* positions NULL: bound on the new tokens of a sequence
-                               (documentation of the plan; the table is checked
-                               row by row) */
+  int32_t max_q;            /* bound on the new tokens of a sequence, >= 1: those
+                               past it are not written */
   const int32_t* positions;
   mla_rope rope;
   int32_t cache_dtype;      /* MLA_DTYPE_BF16 or MLA_DTYPE_MXFP8 */

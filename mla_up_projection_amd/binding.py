@@ -630,7 +630,8 @@ def mla_draft_accept(pool, seqs, path, n_acc, stream=None):
 def mla_kv_rope_paged(kv, k_pe, pool, seqs, cu_q, *, H, d_nope, d_rope, d_v, cos=None, sin=None, positions=None,
                       max_q=None, stream=None):
     """Key and value rows of new tokens into the cache: kv bf16 [T,H,d_nope+d_v], k_pe bf16 [T,d_rope]; token
-    cu_q[j] + i becomes row lens[seqs[j]] + i. positions int32 [T] or None for the rows themselves."""
+    cu_q[j] + i becomes row lens[seqs[j]] + i, i < max_q (None: all). positions int32 [T] or None for the rows
+    themselves."""
     chk = _pool_chk("mla_kv_rope_paged", pool)
     a = mla_kv_paged_args()
     T = kv.shape[0]

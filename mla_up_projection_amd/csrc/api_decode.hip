@@ -353,6 +353,7 @@ mla_status mla_kv_rope_paged(const mla_kv_paged_args* a, void* stream) {
   p.seqs = a->seqs;
   p.cu = a->cu_q;
   p.nseq = a->nseq;
+  p.max_q = a->max_q;
   p.positions = a->positions;
   p.cos = a->rope.cos;
   p.sin = a->rope.sin;
@@ -374,9 +375,7 @@ bool attn_shape_supported(int d_k, int d_v, bool shared) {
   return (d_k == 192 && d_v == 128) || (d_k == 128 && d_v == 128) || (d_k == 64 && d_v == 64);
 }
 
-AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int max_q, int max_len, int page_size) {
-  (void)T;
-  (void)d_k;
+AttnPlan plan_attn(int nseq, int H, int H_kv, int d_v, int max_q, int max_len, int page_size) {
   AttnPlan pl{};
   const int64_t rows = (int64_t)max_q * (H / H_kv);
   // the pages of a chunk fit the kernel's list (with one more at each end)
@@ -439,7 +438,7 @@ mla_status check_attn(const mla_tree_attn_args* a, mla::AttnPlan* plan) {
   if (a->cache_dtype == MLA_DTYPE_MXFP8 && a->d_k == 576 && a->pool->num_pages * a->pool->page_bytes[1] % 4)
     return MLA_EINVAL;
   if ((int64_t)a->max_q * (a->H / a->H_kv) > INT32_MAX / 2) return MLA_EINVAL;
-  *plan = mla::plan_attn(a->T, a->nseq, a->H, a->H_kv, a->d_k, a->d_v, a->max_q, a->max_len, a->pool->page_size);
+  *plan = mla::plan_attn(a->nseq, a->H, a->H_kv, a->d_v, a->max_q, a->max_len, a->pool->page_size);
   // every grid stays below 2^31 work-items, and the even plan's sums within their bits
   const double tiles = (double)a->nseq * a->H_kv * plan->row_tiles;
   if (tiles * plan->chunks >= (double)(1 << 23) || tiles * plan->waves >= (double)(1 << 21)) return MLA_EINVAL;

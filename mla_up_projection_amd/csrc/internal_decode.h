@@ -49,7 +49,7 @@ struct KvPagedParams {
   int H, d_nope, d_rope, d_v;
   const int32_t* seqs;
   const int32_t* cu;
-  int nseq;
+  int nseq, max_q;
   const int32_t* positions;
   const float* cos;
   const float* sin;
@@ -114,11 +114,11 @@ struct AttnParams {
   uint32_t page_magic;  // ceil(2^32 / page_size): quotient of small rows by a high product
   float* part_o;
   float* part_ml;
-  int64_t* sums;  // even plan: units, workgroups, quantum, units before each sequence
+  int64_t* sums;  // even plan: how units are shared (each, more), quantum, units before each sequence
   AttnPlan plan;
 };
 bool attn_shape_supported(int d_k, int d_v, bool shared);
-AttnPlan plan_attn(int64_t T, int nseq, int H, int H_kv, int d_k, int d_v, int max_q, int max_len, int page_size);
+AttnPlan plan_attn(int nseq, int H, int H_kv, int d_v, int max_q, int max_len, int page_size);
 hipError_t launch_tree_attn(const AttnParams& p, hipStream_t stream);
 
 }  // namespace mla

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void kv_paged_kernel(KvPagedParams p, int tok)
           const int64_t at = (int64_t)p.pool.lens[seq] + (t - p.cu[lo]);
           const int64_t k = at / p.pool.page_size;
           pos = (int)min(at, (int64_t)0x7FFFFFFF);
-          if (at >= 0 && k < min(p.pool.held[seq], p.pool.max_pages)) {
+          if (at >= 0 && k < min(p.pool.held[seq], p.pool.max_pages) && t - p.cu[lo] < p.max_q) {
             const int page = p.pool.table[(int64_t)seq * p.pool.max_pages + k];
             if (page >= 0 && page < p.pool.num_pages)
               row = (int64_t)page * p.pool.page_size + (at - k * p.pool.page_size);

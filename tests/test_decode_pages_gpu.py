@@ -337,6 +337,19 @@ def test_append_what_is_not_written():
                 assert torch.equal(got[p, r].view(torch.int16), before[p, r].view(torch.int16))
 
 
+def test_append_stops_at_max_q():
+    b = Both(20, 4, 4, 5)
+    b.reserve([0, 1], [8, 8])
+    kv = torch.ones(9, 1, 96, dtype=torch.bfloat16, device=DEV)
+    before = b.bufs[0].clone()
+    m.mla_kv_rope_paged(kv, None, b.pool, i32([1, 0]), i32([0, 3, 9]), H=1, d_nope=96, d_rope=0, d_v=0, max_q=4)
+    rows = {b.ref.at(1, r) for r in range(3)} | {b.ref.at(0, r) for r in range(4)}
+    for p in range(20):
+        for r in range(4):
+            want = torch.ones_like(before[p, r]) if (p, r) in rows else before[p, r]
+            assert torch.equal(b.bufs[0][p, r].view(torch.int16), want.view(torch.int16))
+
+
 def test_many_tokens_one_sequence_many_sequences():
     """More chunks than one workgroup's, and the longest list of sequences."""
     for nseq, each in ((1, 5000), (1024, 2)):
