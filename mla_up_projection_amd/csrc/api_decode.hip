@@ -389,7 +389,7 @@ AttnPlan plan_attn(int nseq, int H, int H_kv, int d_v, int max_q, int max_len, i
     pl.chunk = (int)most;
     pl.chunks = 1;
     const double steps = std::max(1.0, (double)nseq * H_kv * (double)tiles * ((max_len - 1) / 32 + 1));
-    pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(17.0 * steps)) + 1});
+    pl.groups = (int)std::min({(double)device_cu_count(), steps, std::floor(std::sqrt(17.0 * steps + 84.0 * nseq * H_kv * (double)tiles)) + 1});
     if (pl.groups > 1 && max_len > 32) {  // (an item of one step has no parts)
       const size_t slots = (size_t)2 * pl.groups * pl.waves;
       pl.part_o = 0;
