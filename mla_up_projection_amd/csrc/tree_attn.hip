@@ -123,8 +123,9 @@ __device__ __forceinline__ bool find_item(const AttnParams& p, int64_t item, Ite
 //  - few: the steps are numbered through, and workgroup b of G takes the steps
 //    [b W / G, (b + 1) W / G), so that all end at the same time; but an item of at
 //    most SHORT steps is not cut: who has its first step takes it all (64
-//    sequences of 100 to 400 rows, 4 drafts, 128 heads: 93 -> 71 us, 27 short ones
-//    with 22 drafts each 226 -> 165; up to 8 steps only the latter gains).
+//    sequences of 100 to 400 rows, 4 drafts, 128 heads: 71 us instead of 93, 27
+//    short ones with 22 drafts each 165 instead of 226; with a limit of 8 steps 93
+//    and 164).
 // Units below are parts (quantum > 0, one per workgroup) or steps.
 constexpr int WIDE_ROWS = 128, SHORT = 16;
 __device__ __forceinline__ int row_tiles_of(const Item& it) { return (it.rows + WIDE_ROWS - 1) / WIDE_ROWS; }
