@@ -735,80 +735,160 @@ struct Worker {
   }
 };
 
-// One element of a cache row (bf16, or E4M3 times its scale) in fp32.
+// Eight elements of a cache row, c .. c + 7, as bf16 pairs.
 template <bool MX>
-__device__ __forceinline__ float cache_value(const PoolParams& pool, int b, int64_t row, int d, int c) {
-  if constexpr (!MX) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(pool.buf[b])[row * d + c]);
-  const uint32_t code = pool.buf[2 * b][row * d + c], sc = pool.buf[2 * b + 1][row * (d / 32) + c / 32];
-  const uint32_t v = __builtin_bit_cast(
-      uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, __uint_as_float(sc << 23), false));
-  return bf16_bits_to_f32(v & 0xFFFFu);
+__device__ __forceinline__ u32x4_t cache_eight(const PoolParams& pool, int b, int64_t row, int d, int c) {
+  if constexpr (!MX) return *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(pool.buf[b]) + row * d + c);
+  const uint2 code = *reinterpret_cast<const uint2*>(pool.buf[2 * b] + row * d + c);
+  const float f = __uint_as_float((uint32_t)pool.buf[2 * b + 1][row * (d / 32) + c / 32] << 23);
+  return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, f, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, true))};
 }
 
-// The workgroup's rows without the matrix units, for chunks where a page id
-// lies outside the pool or a row must not see what another sees (an infinite
-// or NaN value: no weight keeps it out of a product). A wave takes its rows one
-// by one, a lane every 64th column; a row that is not seen is not looked at.
-// Writes what the fast path writes.
+// Cache row of token `tok` of a sequence that holds `held` pages; `bad` if its
+// page lies outside the pool.
+__device__ __forceinline__ int64_t find_row(const AttnParams& p, const Item& it, int held, uint32_t tok, bool& bad) {
+  const uint32_t ps = (uint32_t)p.pool.page_size, pk = tok / ps;
+  const int page = (int)pk < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + pk] : -1;
+  bad = page < 0 || page >= p.pool.num_pages;
+  return ((bad ? 0 : (int64_t)page) * ps + (tok - pk * ps)) * p.H_kv + it.kvh;
+}
+
+// Cache rows [tk_begin, tk_end) for one query row by one wave, without the matrix
+// units: for what those cannot do, an infinite or NaN value that some rows must
+// not see (no weight keeps it out of a product) and a page id outside the pool (the
+// row's result is NaN). Of 64 cache rows, eight lanes take a row's scores, then LANES
+// lanes a row's values, eight columns each, all loads of 16 bytes with several in
+// flight. A row that is not seen adds nothing. o: the lane's columns, 8 (lane %
+// LANES) on. All of a workgroup's rows come here, so it costs: one stray NaN among 8
+// sequences of 2000 rows, 4 drafts, 16 heads makes 1.4 ms of 30 us (5.5 with a lane
+// for every 64th column and one cache row at a time).
+template <int DK, bool MX, int LANES>
+__device__ __forceinline__ void slow_row(const AttnParams& p, const Item& it, int row, int tk_begin, int tk_end,
+                                         float (&o)[8], float& m, float& l) {
+  constexpr int CHUNKS = (DK + 63) / 64, PASS = 64 / LANES, AHEAD = LANES == 64 ? 8 : 2;  // 16-byte chunks of a key to a lane
+  const int lane = opaque((int)threadIdx.x) & 63, part = lane & 7, of8 = lane >> 3;
+  const bool shared = p.pool.nbuf == (MX ? 2 : 1);
+  const int vb = shared ? 0 : 1, vd = shared ? DK : p.d_v;
+  const int held = min(p.pool.held[it.seq], p.pool.max_pages);
+  const int qi = row / p.group, h = it.kvh * p.group + row - qi * p.group;
+  const int64_t qt = it.t0 + qi;
+  u32x4_t q[CHUNKS];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int d = 8 * (part + 8 * c);
+    q[c] = u32x4_t{0, 0, 0, 0};
+    if (DK % 64 == 0 || d < DK) q[c] = *reinterpret_cast<const u32x4_t*>(p.q + qt * p.q_t + h * p.q_h + d);
+  }
+  m = NEG_INF;
+  l = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) o[k] = 0;
+  for (uint32_t tk = (uint32_t)tk_begin; tk < (uint32_t)tk_end; tk += 64) {
+    const uint32_t tok = tk + lane;
+    const bool see = tok < (uint32_t)tk_end && (visible(p, it, qt, qi, (int)(tk + (lane & 32))) >> (lane & 31)) & 1;
+    bool bad;
+    const int64_t crow = find_row(p, it, held, min(tok, (uint32_t)tk_end - 1), bad);
+    float s = 0;
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+      const int64_t r = __shfl(crow, 8 * g + of8);
+      float sum = 0;
+      u32x4_t a[CHUNKS];
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+        if (DK % 64 == 0 || 8 * (part + 8 * c) < DK) a[c] = cache_eight<MX>(p.pool, 0, r, DK, 8 * (part + 8 * c));
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+        if (DK % 64 == 0 || 8 * (part + 8 * c) < DK)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sum = __builtin_fmaf(bf16_bits_to_f32(a[c][k] & 0xFFFFu), bf16_bits_to_f32(q[c][k] & 0xFFFFu), sum);
+            sum = __builtin_fmaf(bf16_bits_to_f32(a[c][k] >> 16), bf16_bits_to_f32(q[c][k] >> 16), sum);
+          }
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
+      sum = __shfl(sum, 8 * part);
+      if (of8 == g) s = sum;
+    }
+    s = !see ? NEG_INF : bad ? __builtin_nanf("") : s * p.scale_log2;
+    if (__any(__builtin_isnan(s))) {  // and so is everything that follows
+      m = l = __builtin_nanf("");
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = m;
+      return;
+    }
+    float top = s;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if (top == NEG_INF) continue;
+    if (top > m) {
+      const float f = exp2_hw(m - top);  // 0 for the first
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] *= f;
+    }
+    const float w = see ? exp2_hw(s - m) : 0.0f;
+    l += w;
+#pragma unroll 1
+    for (int j = 0; j < 64; j += PASS * AHEAD) {
+      u32x4_t v[AHEAD];
+      float wj[AHEAD];
+      bool sj[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int from = j + u * PASS + lane / LANES;
+        wj[u] = __shfl(w, from);
+        sj[u] = __shfl((int)see, from);
+        v[u] = cache_eight<MX>(p.pool, vb, __shfl(crow, from), vd, 8 * (lane % LANES));
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (sj[u])
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[2 * k] += wj[u] * bf16_bits_to_f32(v[u][k] & 0xFFFFu);
+            o[2 * k + 1] += wj[u] * bf16_bits_to_f32(v[u][k] >> 16);
+          }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+#pragma unroll
+  for (int d = LANES; d < 64; d <<= 1)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] += __shfl_xor(o[k], d);
+}
+
+// The workgroup's rows by slow_row, a wave its 32 one by one. Writes what the fast
+// path writes.
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, int tk_begin, int tk_end) {
-  constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64;
-  const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6;
-  const int ps = p.pool.page_size;
-  const int held = min(p.pool.held[it.seq], p.pool.max_pages);
+  const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6, v = lane % (DV / 8);
   const int64_t slot = it.slot * WAVES + wave;
+#pragma unroll 1
   for (int r32 = 0; r32 < 32; ++r32) {
-    const int row = (it.rt * WAVES + wave) * 32 + r32;
+    const int row = __builtin_amdgcn_readfirstlane((it.rt * WAVES + wave) * 32 + r32);
     if (row >= it.rows) return;
+    float o[8], m, l;
+    slow_row<DK, MX, DV / 8>(p, it, row, tk_begin, tk_end, o, m, l);
     const int qi = row / p.group, h = it.kvh * p.group + row - qi * p.group;
     const int64_t qt = it.t0 + qi;
-    float q[NQ], o[NO], m = NEG_INF, l = 0;
-#pragma unroll
-    for (int k = 0; k < NQ; ++k)
-      q[k] = lane + 64 * k < DK ? bf16_bits_to_f32(p.q[qt * p.q_t + h * p.q_h + lane + 64 * k]) : 0.0f;
-#pragma unroll
-    for (int k = 0; k < NO; ++k) o[k] = 0;
-    uint32_t vis = 0;
-    for (int tk = tk_begin; tk < tk_end; ++tk) {
-      if (((tk - tk_begin) & 31) == 0) vis = visible(p, it, qt, qi, tk);
-      if (!((vis >> ((tk - tk_begin) & 31)) & 1)) continue;
-      const int pk = tk / ps;
-      int64_t page = pk < held ? p.pool.table[(int64_t)it.seq * p.pool.max_pages + pk] : -1;
-      if (page >= p.pool.num_pages) page = -1;
-      const int64_t crow = (max(page, (int64_t)0) * ps + tk - pk * ps) * p.H_kv + it.kvh;
-      float s = 0;
-#pragma unroll
-      for (int k = 0; k < NQ; ++k)
-        if (lane + 64 * k < DK) s += q[k] * cache_value<MX>(p.pool, 0, crow, DK, lane + 64 * k);
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-      s = page < 0 ? __builtin_nanf("") : s * p.scale_log2;
-      const float mn = s > m || __builtin_isnan(s) ? s : m;  // NaN stays
-      const float f = m == NEG_INF ? 0.0f : exp2_hw(m - mn), w = s == NEG_INF ? 0.0f : exp2_hw(s - mn);
-      m = mn;
-      l = (f == 1.0f ? l : l * f) + w;
-#pragma unroll
-      for (int k = 0; k < NO; ++k)
-        if (lane + 64 * k < DV) {
-          const float v = cache_value<MX>(p.pool, SHARED ? 0 : 1, crow, SHARED ? DK : DV, lane + 64 * k);
-          o[k] = (f == 1.0f ? o[k] : m == NEG_INF ? 0.0f : o[k] * f) + w * v;
-        }
-    }
     const float inv = l == 0 ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int k = 0; k < NO; ++k) {
-      const int c = lane + 64 * k;
-      if (c >= DV) continue;
-      if (it.whole)
-        p.out[qt * p.o_t + h * p.o_h + c] = (uint16_t)f32_to_bf16_bits(o[k] * inv);
-      else  // column 32 n + 8 g + 4 half + e
-        p.part_o[(slot * (DV * 8) + (c >> 3) * 64 + ((c >> 2) & 1) * 32 + r32) * 4 + (c & 3)] = o[k];
-    }
-    if (lane == 0) {
-      if (!it.whole)
-        reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r32] = make_float2(m, l);
-      else if (p.lse)
-        p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    if (lane >= DV / 8) continue;
+    if (it.whole) {
+      *reinterpret_cast<uint4*>(p.out + qt * p.o_t + h * p.o_h + 8 * v) =
+          make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                     pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+      if (lane == 0 && p.lse) p.lse[qt * p.H + h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    } else {  // column 32 n + 8 g + 4 half + e
+      f32x4_t* po = reinterpret_cast<f32x4_t*>(p.part_o) + slot * (DV * 8) + v * 64 + r32;
+      po[0] = f32x4_t{o[0], o[1], o[2], o[3]};
+      po[32] = f32x4_t{o[4], o[5], o[6], o[7]};
+      if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r32] = make_float2(m, l);
     }
   }
 }
@@ -966,9 +1046,10 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
   if (r.half == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r.l32] = make_float2(m, l);
 }
 
-// Chunked plan: a workgroup an item.
+// Chunked plan: a workgroup an item. (The fewest waves of a SIMD are those that the
+// matrix path alone would have; without them slow_rows takes registers from it.)
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(1, 4)))
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(DK == 64 ? 4 : DK == 96 ? 3 : 2, 4)))
 void tree_attn_kernel(AttnParams p) {
   using S = Shape<DK, DV, SHARED, MX, WAVES>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
