@@ -511,7 +511,10 @@ MLA_API mla_status mla_kv_rope_paged(const mla_kv_paged_args* args, void* stream
  * A token that sees no row gets out = 0 and lse = -inf. What lies in rows that
  * a token does not see, NaN and infinities included, has no influence on it.
  * Statistics and sums are fp32; the weights e^(s - max) are rounded to bf16
- * for the product with the values. Results do not depend on timing.
+ * for the product with the values. Results do not depend on timing. Values may
+ * be as large as bf16 holds (up to 2^127: a result is a mean of values, and half
+ * a rounding step more is still finite): where a sum leaves fp32's range on the
+ * way to a mean that lies in it, the row is done again, slowly.
  * Widths (D_k, D_v): latent cache (no value buffer, value = the key's first
  * D_v elements): (576, 512), (96, 64); with values: (192, 128), (128, 128),
  * (64, 64). Others: MLA_EUNSUPPORTED. bf16 or MXFP8 cache; queries are bf16.

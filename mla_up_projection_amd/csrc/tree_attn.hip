@@ -40,6 +40,7 @@ constexpr float LAZY = 64.0f;    // how many powers of two a score may lie above
 constexpr float NEG_INF = -__builtin_huge_valf();
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // Position of 16-byte chunk c of cache row t within the row's 128 bytes. A row
 // spans half the 64 banks, so rows t, t + 2, .. would share theirs; moving
@@ -56,6 +57,15 @@ __device__ __forceinline__ int swz(int t) { return ((t >> 1) & 1) << 2 | ((t >> 
 __device__ __forceinline__ int opaque(int v) {
   asm volatile("" : "+v"(v));
   return v;
+}
+
+// n < 2^bits_of(n)
+__device__ __forceinline__ int bits_of(int n) { return 32 - __builtin_clz(n); }
+
+// max(x, |a|, |b|), NaN if one of them is.
+__device__ __forceinline__ float widest(float x, float a, float b) {
+  asm("v_maximum3_f32 %0, |%1|, |%2|, %0" : "+v"(x) : "v"(a), "v"(b));
+  return x;
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -491,7 +501,8 @@ struct Worker {
   // row's first tile with a row it sees. Weights above 1 cost nothing: fp32 and
   // bf16 both reach 2^127, and a row's weights keep their precision relative to
   // each other. So O is never rescaled on the way; a row whose scores rise more
-  // than 2^LAZY above m (top says so at the end) is done again with m = top.
+  // than 2^LAZY above m (top says so at the end) is done again with m = top. With
+  // values so large that O leaves fp32's range all the same: out_of_range().
   __device__ __forceinline__ void weights(f32x16_t& s) {
     float t = s[0];
 #pragma unroll
@@ -747,6 +758,16 @@ __device__ __forceinline__ u32x4_t cache_eight(const PoolParams& pool, int b, in
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, true))};
 }
 
+// sum + the products of eight bf16 and eight others.
+__device__ __forceinline__ float dot8(u32x4_t a, u32x4_t b, float sum) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sum = __builtin_fmaf(bf16_bits_to_f32(a[k] & 0xFFFFu), bf16_bits_to_f32(b[k] & 0xFFFFu), sum);
+    sum = __builtin_fmaf(bf16_bits_to_f32(a[k] >> 16), bf16_bits_to_f32(b[k] >> 16), sum);
+  }
+  return sum;
+}
+
 // Cache row of token `tok` of a sequence that holds `held` pages; `bad` if its
 // page lies outside the pool.
 __device__ __forceinline__ int64_t find_row(const AttnParams& p, const Item& it, int held, uint32_t tok, bool& bad) {
@@ -762,26 +783,30 @@ __device__ __forceinline__ int64_t find_row(const AttnParams& p, const Item& it,
 // row's result is NaN). Of 64 cache rows, eight lanes take a row's scores, then LANES
 // lanes a row's values, eight columns each, all loads of 16 bytes with several in
 // flight. A row that is not seen adds nothing. o: the lane's columns, 8 (lane %
-// LANES) on. All of a workgroup's rows come here, so it costs: one stray NaN among 8
+// LANES) on; the reference lies so far above the largest score that the weights'
+// sum stays below 1 and finite values give finite sums. All of a workgroup's rows come here, so it costs: one stray NaN among 8
 // sequences of 2000 rows, 4 drafts, 16 heads makes 1.4 ms of 30 us (5.5 with a lane
 // for every 64th column and one cache row at a time).
+// The columns may also be some eights of them, first + step (lane % LANES). DK 0: any
+// width, in few registers.
 template <int DK, bool MX, int LANES>
 __device__ __forceinline__ void slow_row(const AttnParams& p, const Item& it, int row, int tk_begin, int tk_end,
-                                         float (&o)[8], float& m, float& l) {
-  constexpr int CHUNKS = (DK + 63) / 64, PASS = 64 / LANES, AHEAD = LANES == 64 ? 8 : 2;  // 16-byte chunks of a key to a lane
+                                         float (&o)[8], float& m, float& l, int first = 0, int step = 1) {
+  constexpr int CHUNKS = (DK + 63) / 64;  // 16-byte chunks of a key to a lane
+  constexpr int PASS = 64 / LANES, AHEAD = LANES == 64 ? 8 : LANES == 1 ? 1 : 2;  // rows to a load, loads in flight
   const int lane = opaque((int)threadIdx.x) & 63, part = lane & 7, of8 = lane >> 3;
   const bool shared = p.pool.nbuf == (MX ? 2 : 1);
-  const int vb = shared ? 0 : 1, vd = shared ? DK : p.d_v;
+  const int dk = DK ? DK : p.d_k;
+  const float above = (float)bits_of(tk_end - tk_begin);
+  const int vb = shared ? 0 : 1, vd = shared ? p.d_k : p.d_v;
   const int held = min(p.pool.held[it.seq], p.pool.max_pages);
   const int qi = row / p.group, h = it.kvh * p.group + row - qi * p.group;
   const int64_t qt = it.t0 + qi;
-  u32x4_t q[CHUNKS];
+  const uint16_t* query = p.q + qt * p.q_t + h * p.q_h;
+  u32x4_t q[CHUNKS + 1];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
-    const int d = 8 * (part + 8 * c);
-    q[c] = u32x4_t{0, 0, 0, 0};
-    if (DK % 64 == 0 || d < DK) q[c] = *reinterpret_cast<const u32x4_t*>(p.q + qt * p.q_t + h * p.q_h + d);
-  }
+  for (int c = 0; c < CHUNKS; ++c)
+    if (DK % 64 == 0 || 8 * (part + 8 * c) < DK) q[c] = *reinterpret_cast<const u32x4_t*>(query + 8 * (part + 8 * c));
   m = NEG_INF;
   l = 0;
 #pragma unroll
@@ -796,18 +821,17 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, const Item& it, in
     for (int g = 0; g < 8; ++g) {
       const int64_t r = __shfl(crow, 8 * g + of8);
       float sum = 0;
-      u32x4_t a[CHUNKS];
+      u32x4_t a[CHUNKS + 1];
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c)
-        if (DK % 64 == 0 || 8 * (part + 8 * c) < DK) a[c] = cache_eight<MX>(p.pool, 0, r, DK, 8 * (part + 8 * c));
+        if (DK % 64 == 0 || 8 * (part + 8 * c) < DK) a[c] = cache_eight<MX>(p.pool, 0, r, dk, 8 * (part + 8 * c));
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c)
-        if (DK % 64 == 0 || 8 * (part + 8 * c) < DK)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sum = __builtin_fmaf(bf16_bits_to_f32(a[c][k] & 0xFFFFu), bf16_bits_to_f32(q[c][k] & 0xFFFFu), sum);
-            sum = __builtin_fmaf(bf16_bits_to_f32(a[c][k] >> 16), bf16_bits_to_f32(q[c][k] >> 16), sum);
-          }
+        if (DK % 64 == 0 || 8 * (part + 8 * c) < DK) sum = dot8(a[c], q[c], sum);
+      if (DK == 0)
+#pragma unroll 1
+        for (int d = 8 * part; d < dk; d += 64)
+          sum = dot8(cache_eight<MX>(p.pool, 0, r, dk, d), *reinterpret_cast<const u32x4_t*>(query + d), sum);
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor(sum, d);
       sum = __shfl(sum, 8 * part);
@@ -824,6 +848,7 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, const Item& it, in
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     if (top == NEG_INF) continue;
+    top += above;
     if (top > m) {
       const float f = exp2_hw(m - top);  // 0 for the first
       m = top;
@@ -843,7 +868,7 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, const Item& it, in
         const int from = j + u * PASS + lane / LANES;
         wj[u] = __shfl(w, from);
         sj[u] = __shfl((int)see, from);
-        v[u] = cache_eight<MX>(p.pool, vb, __shfl(crow, from), vd, 8 * (lane % LANES));
+        v[u] = cache_eight<MX>(p.pool, vb, __shfl(crow, from), vd, 8 * min(first + step * (lane % LANES), p.d_v / 8 - 1));
       }
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
@@ -890,6 +915,39 @@ __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, i
       po[32] = f32x4_t{o[4], o[5], o[6], o[7]};
       if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[slot * 32 + r32] = make_float2(m, l);
     }
+  }
+}
+
+// Rows of an item (bits of `rows`, from row `at` on) whose result over all cache rows
+// came out infinite or NaN although their scores are finite. Either a committed
+// value is not finite, and the rows, which all see it, have what the formula gives;
+// or sums left fp32's range on the way to a mean that lies in it, and the rows are
+// done again by slow_row. For a wave, and the columns 8 (first + step v), v < LANES.
+template <int DK, bool MX, int LANES>
+__device__ __forceinline__ void out_of_range(const AttnParams& p, const Item& it, int at, uint32_t rows, int first,
+                                             int step) {
+  const int lane = opaque((int)threadIdx.x) & 63;
+  const bool shared = p.pool.nbuf == (MX ? 2 : 1);
+  const int held = min(p.pool.held[it.seq], p.pool.max_pages), c = 8 * min(first + step * (lane % LANES), p.d_v / 8 - 1);
+#pragma unroll 1
+  for (uint32_t tk = 0; tk < (uint32_t)it.len; tk += 64 / LANES) {
+    bool bad;
+    const int64_t r = find_row(p, it, held, min(tk + lane / LANES, (uint32_t)it.len - 1), bad);
+    const u32x4_t v = cache_eight<MX>(p.pool, shared ? 0 : 1, r, shared ? p.d_k : p.d_v, c);
+    if (__any(not_finite_pair(v[0]) || not_finite_pair(v[1]) || not_finite_pair(v[2]) || not_finite_pair(v[3]))) return;
+  }
+  vm_wait<0>();  // what this wave wrote
+#pragma unroll 1
+  for (; rows; rows &= rows - 1) {
+    const int row = __builtin_amdgcn_readfirstlane(at + __builtin_ctz(rows));
+    float o[8], m, l;
+    slow_row<DK, MX, LANES>(p, it, row, 0, it.total, o, m, l, first, step);
+    const int qi = row / p.group, h = it.kvh * p.group + row - qi * p.group;
+    const float inv = l == 0 ? 0.0f : 1.0f / l;
+    if (lane < LANES)
+      *reinterpret_cast<uint4*>(p.out + (int64_t)(it.t0 + qi) * p.o_t + h * p.o_h + c) =
+          make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                     pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
   }
 }
 
@@ -1008,8 +1066,14 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     const int at = (it.rt * WAVES + wave) * 32;
     int qi = at / p.group, h = at - qi * p.group;
     uint16_t* dst = p.out + (int64_t)(it.t0 + qi) * p.o_t + (int64_t)(it.kvh * p.group + h) * p.o_h + 8 * lane;
-    for (int k = 0; k < min(32, it.rows - at); ++k) {
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(rows + k * (DV * 2) + ((lane ^ k) << 4));
+    const int live = min(32, it.rows - at);
+    u16x2_t most = {0, 0};  // magnitudes
+    for (int k = 0; k < live; ++k) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(rows + k * (DV * 2) + ((lane ^ k) << 4));
+      *reinterpret_cast<u32x4_t*>(dst) = v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, v[i] & 0x7FFF7FFFu));
       dst += p.o_h;
       if (++h == p.group) {
         h = 0;
@@ -1018,23 +1082,41 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     }
     if (p.lse && r.live && r.half == 0)
       p.lse[r.qt * p.H + r.h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    if (__builtin_expect(__any(most[0] >= 0x7F80 || most[1] >= 0x7F80), 0)) {
+      uint32_t strange = 0;
+      for (int k = 0; k < live; ++k) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(rows + k * (DV * 2) + ((lane ^ k) << 4));
+        if (__any(not_finite_pair(v[0]) || not_finite_pair(v[1]) || not_finite_pair(v[2]) || not_finite_pair(v[3])))
+          strange |= 1u << k;
+      }
+      strange &= (uint32_t)__ballot(l < __builtin_huge_valf());
+      if (strange) out_of_range<DK, MX, DV / 8>(p, it, at, strange, 0, 1);
+    }
     return;
   }
-  if (!r.live) return;
   if (it.whole) {
     const float inv = l == 0 ? 0.0f : 1.0f / l;
     uint16_t* dst = p.out + r.qt * p.o_t + r.h * p.o_h;
+    float x = 0;
+    if (r.live) {
 #pragma unroll
-    for (int n = 0; n < S::NT; ++n)
+      for (int n = 0; n < S::NT; ++n)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * r.half) =
-            make_uint2(pack_bf16x2(w.o[n][4 * g] * inv, w.o[n][4 * g + 1] * inv),
-                       pack_bf16x2(w.o[n][4 * g + 2] * inv, w.o[n][4 * g + 3] * inv));
-    if (p.lse && r.half == 0)
-      p.lse[r.qt * p.H + r.h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+        for (int g = 0; g < 4; ++g) {
+          x = widest(widest(x, w.o[n][4 * g], w.o[n][4 * g + 1]), w.o[n][4 * g + 2], w.o[n][4 * g + 3]);
+          *reinterpret_cast<uint2*>(dst + 32 * n + 8 * g + 4 * r.half) =
+              make_uint2(pack_bf16x2(w.o[n][4 * g] * inv, w.o[n][4 * g + 1] * inv),
+                         pack_bf16x2(w.o[n][4 * g + 2] * inv, w.o[n][4 * g + 3] * inv));
+        }
+      if (p.lse && r.half == 0)
+        p.lse[r.qt * p.H + r.h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    }
+    const uint64_t strange = __ballot(!(x < __builtin_huge_valf()) && l < __builtin_huge_valf());
+    if (__builtin_expect(strange != 0, 0))
+      out_of_range<DK, MX, DV / 8>(p, it, (it.rt * WAVES + wave) * 32, (uint32_t)(strange | strange >> 32), 0, 1);
     return;
   }
+  if (!r.live) return;
   // partial result, in register order: [slot][wave][32 DV floats as NT * 4 vectors of 64 lanes]
   const int64_t slot = it.slot * WAVES + wave;
   f32x4_t* po = reinterpret_cast<f32x4_t*>(p.part_o) + slot * (DV * 8);
@@ -1234,9 +1316,12 @@ void tree_attn_even_kernel(AttnParams p) {
 // each, 32 in four blocks of 16, 34 in eight. V = 4: four waves share
 // `vectors_each` vectors, four in flight each. V = 1, for few rows with many
 // parts: a wave takes one vector, and where the workgroup has more than four
-// waves they share the parts and add up in LDS. The order of every sum is fixed.
+// waves they share the parts and add up in LDS. The order of every sum is fixed. (The
+// waves of a SIMD are those that out_of_range, which hardly runs, may not lower much.)
 template <bool EVEN, int V>
-__global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p, int vectors_each) {
+__global__ __launch_bounds__(V == 1 ? 1024 : 256)
+__attribute__((amdgpu_waves_per_eu(EVEN ? (V == 1 ? 8 : 6) : (V == 1 ? 7 : 5))))
+void join_kernel(AttnParams p, int vectors_each) {
   const int waves = p.plan.waves, vectors = p.d_v / 8;
   const uint32_t blocks = (vectors + vectors_each - 1) / vectors_each;
   const uint32_t b = blockIdx.x / blocks;
@@ -1298,63 +1383,71 @@ __global__ __launch_bounds__(V == 1 ? 1024 : 256) void join_kernel(AttnParams p,
   const float Mu = M == NEG_INF ? 0.0f : M;
   __shared__ float sum[V == 1 ? 16 : 1][6][64];
   const int end = min(vb + vectors_each, vectors);
-  for (int v0 = vb + (own & 3); v0 < vb + vectors_each; v0 += 4 * V) {
-    float l = 0;
-    f32x4_t acc[V];
+  const int v0 = __builtin_amdgcn_readfirstlane(vb + (own & 3));  // the wave's vectors: V from here on, four apart
+  float l = 0;
+  f32x4_t acc[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = f32x4_t{0, 0, 0, 0};
-    if (live && v0 < end)
-      for (int c0 = c1; c0 < parts; c0 += step * U) {
-        float2 e[U];
-        f32x4_t x[U][V];
+  for (int v = 0; v < V; ++v) acc[v] = f32x4_t{0, 0, 0, 0};
+  if (live)
+    for (int c0 = c1; c0 < parts; c0 += step * U) {
+      float2 e[U];
+      f32x4_t x[U][V];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t s = at(min(c0 + step * u, parts - 1));
-          e[u] = ml[s * 32];
+      for (int u = 0; u < U; ++u) {
+        const int64_t s = at(min(c0 + step * u, parts - 1));
+        e[u] = ml[s * 32];
 #pragma unroll
-          for (int v = 0; v < V; ++v) x[u][v] = po[(s * vectors + min(v0 + 4 * v, end - 1)) * 64];
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (c0 + step * u >= parts) break;
-          const float w = exp2_hw(e[u].x - Mu);
-          l += w * e[u].y;
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[v][k] += w * x[u][v][k];
-        }
+        for (int v = 0; v < V; ++v) x[u][v] = po[(s * vectors + min(v0 + 4 * v, end - 1)) * 64];
       }
-    float top = M;
-    if (V == 1 && step > 1) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sum[own][k][lane] = acc[0][k];
-      sum[own][4][lane] = l;
-      sum[own][5][lane] = M;
-      __syncthreads();
-      if (own >= 4) return;
-      for (int w = 1; w < step; ++w) top = fmaxf(top, sum[own + 4 * w][5][lane]);
-      const float tu = top == NEG_INF ? 0.0f : top;
-      const float f0 = exp2_hw(M - tu);
-      l *= f0;
+      for (int u = 0; u < U; ++u) {
+        if (c0 + step * u >= parts) break;
+        const float w = exp2_hw(e[u].x - Mu);
+        l += w * e[u].y;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[0][k] *= f0;
-      for (int w = 1; w < min(step, parts); ++w) {
-        const float f = exp2_hw(sum[own + 4 * w][5][lane] - tu);
-        l += f * sum[own + 4 * w][4][lane];
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[0][k] += f * sum[own + 4 * w][k][lane];
+          for (int k = 0; k < 4; ++k) acc[v][k] += w * x[u][v][k];
       }
     }
-    if (!live) continue;
-    const float inv = l == 0 ? 0.0f : 1.0f / l;
+  float top = M;
+  if (V == 1 && step > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v0 + 4 * v < end)
-        *reinterpret_cast<uint2*>(p.out + t * p.o_t + h * p.o_h + 8 * (v0 + 4 * v) + 4 * half) =
-            make_uint2(pack_bf16x2(acc[v][0] * inv, acc[v][1] * inv), pack_bf16x2(acc[v][2] * inv, acc[v][3] * inv));
-    if (p.lse && v0 == 0 && half == 0)
-      p.lse[t * p.H + h] = l == 0 ? NEG_INF : (top + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+    for (int k = 0; k < 4; ++k) sum[own][k][lane] = acc[0][k];
+    sum[own][4][lane] = l;
+    sum[own][5][lane] = M;
+    __syncthreads();
+    if (own >= 4) return;
+    for (int w = 1; w < step; ++w) top = fmaxf(top, sum[own + 4 * w][5][lane]);
+    const float tu = top == NEG_INF ? 0.0f : top;
+    const float f0 = exp2_hw(M - tu);
+    l *= f0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[0][k] *= f0;
+    for (int w = 1; w < min(step, parts); ++w) {
+      const float f = exp2_hw(sum[own + 4 * w][5][lane] - tu);
+      l += f * sum[own + 4 * w][4][lane];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[0][k] += f * sum[own + 4 * w][k][lane];
+    }
+  }
+  const float inv = l == 0 ? 0.0f : 1.0f / l;
+  float x = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) x = widest(widest(x, acc[v][0], acc[v][1]), acc[v][2], acc[v][3]);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (live && v0 + 4 * v < end)
+      *reinterpret_cast<uint2*>(p.out + t * p.o_t + h * p.o_h + 8 * (v0 + 4 * v) + 4 * half) =
+          make_uint2(pack_bf16x2(acc[v][0] * inv, acc[v][1] * inv), pack_bf16x2(acc[v][2] * inv, acc[v][3] * inv));
+  if (p.lse && live && v0 == 0 && half == 0)
+    p.lse[t * p.H + h] = l == 0 ? NEG_INF : (top + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
+  const uint64_t strange = __ballot(!(x < __builtin_huge_valf()) && l < __builtin_huge_valf());
+  if (__builtin_expect(strange != 0, 0)) {
+    const int at = (it.rt * waves + wave) * 32;
+    const uint32_t rows = (uint32_t)(strange | strange >> 32);
+    if (p.mx) out_of_range<0, true, V>(p, it, at, rows, v0, 4);
+    else out_of_range<0, false, V>(p, it, at, rows, v0, 4);
   }
 }
 
