@@ -440,8 +440,8 @@ MLA_API mla_status mla_pages_copy(const mla_pool* src, const mla_pool* dst, cons
  * ascending order of their ids, in the order of seqs, a copied page before the
  * added ones.
  *   status: device int32[1], 0 when done. Otherwise nothing has changed: the
- *   number of pages missing, or -1 if a new_tokens is negative or a sequence
- *   would exceed max_pages.
+ *   number of pages missing (at most 2^31 - 1), or -1 if a new_tokens is
+ *   negative or a sequence would exceed max_pages.
  * Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EDEVICE. */
 MLA_API mla_status mla_pages_reserve(const mla_pool* pool, const int32_t* seqs, const int32_t* new_tokens,
                                      int32_t n, int32_t* status, void* workspace, size_t workspace_bytes,

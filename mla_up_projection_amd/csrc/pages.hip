@@ -96,6 +96,7 @@ __global__ __launch_bounds__(PT) void reserve_plan_kernel(PoolParams p, const in
                                                           int32_t* __restrict__ status, int32_t* __restrict__ ws) {
   __shared__ int seq_key[HASH], seq_first[HASH], page_key[HASH], page_count[HASH], page_last[HASH];
   __shared__ int sums[PT / 64], bad, nwide;
+  __shared__ unsigned long long wanted;
   __shared__ int w_seq[PT], w_held[PT], w_at[PT], w_add[PT];
   const int tid = threadIdx.x;
   for (int k = tid; k < HASH; k += PT) {
@@ -103,9 +104,12 @@ __global__ __launch_bounds__(PT) void reserve_plan_kernel(PoolParams p, const in
     seq_first[k] = 0x7FFFFFFF;
     page_count[k] = 0;
   }
-  if (tid == 0) bad = nwide = 0;
+  if (tid == 0) {
+    bad = nwide = 0;
+    wanted = 0;
+  }
   __syncthreads();
-  int seq = -1, len = 0, held = 0, add = 0, slot = 0, page = -1, copy = 0, fresh = 0;
+  int seq = -1, len = 0, held = 0, add = 0, need = 0, slot = 0, page = -1, copy = 0, fresh = 0;
   if (tid < n) {
     seq = seqs[tid];
     fresh = new_tokens[tid];
@@ -124,8 +128,9 @@ __global__ __launch_bounds__(PT) void reserve_plan_kernel(PoolParams p, const in
     if (len < 0 || fresh < 0 || held < 0 || rows > (int64_t)p.max_pages * p.page_size) {
       bad = 1;
     } else {
-      // (the clamp keeps the sum over 1024 sequences within 32 bits)
-      add = min(max(0, (int)((rows + p.page_size - 1) / p.page_size) - held), p.num_pages + 1);
+      // (the clamp keeps the sum over 1024 sequences within 32 bits; more than there are is refused)
+      need = max(0, (int)((rows + p.page_size - 1) / p.page_size) - held);
+      add = min(need, p.num_pages + 1);
       const int k = len / p.page_size;
       if (fresh > 0 && len % p.page_size != 0 && k < held) {
         page = p.table[(int64_t)seq * p.max_pages + k];
@@ -164,14 +169,19 @@ __global__ __launch_bounds__(PT) void reserve_plan_kernel(PoolParams p, const in
   }
   __syncthreads();  // `taken` is written
   const bool enough = found >= total;
-  if (tid == 0) status[0] = enough ? 0 : total - found;
+  if (!enough && seq >= 0) atomicAdd(&wanted, (unsigned long long)need + copy);
   if (tid < n) {
     const bool moves = enough && seq >= 0 && copy;
     ws[PW_PAIRS + 3 * tid] = page;
     ws[PW_PAIRS + 3 * tid + 1] = moves ? taken[at] : -1;
     ws[PW_PAIRS + 3 * tid + 2] = moves ? len % p.page_size : 0;
   }
-  if (!enough) return;
+  if (!enough) {  // `found` is all that is free
+    __syncthreads();
+    if (tid == 0) status[0] = (int)min(wanted - found, (unsigned long long)0x7FFFFFFF);
+    return;
+  }
+  if (tid == 0) status[0] = 0;
   if (seq >= 0) {
     if (copy) {
       p.table[(int64_t)seq * p.max_pages + len / p.page_size] = taken[at];
