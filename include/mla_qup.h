@@ -520,7 +520,8 @@ MLA_API mla_status mla_kv_rope_paged(const mla_kv_paged_args* args, void* stream
  * (64, 64). Others: MLA_EUNSUPPORTED. bf16 or MXFP8 cache; queries are bf16.
  * A 576-wide MXFP8 cache must hold an even number of rows (num_pages *
  * page_size * H_kv): its scale buffer is read in words of 4 bytes.
- * A sequence that outgrows max_q or max_len, and a page id outside the pool,
+ * A sequence that outgrows max_q or max_len, has more committed rows than its
+ * held pages or more than 2^31 - 2^17 rows in all, and a page id outside the pool,
  * give NaN in the rows concerned, never a read out of bounds. Query rows
  * behind cu_q[nseq] are left as they are. */
 typedef struct {

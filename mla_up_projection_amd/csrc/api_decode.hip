@@ -505,7 +505,7 @@ mla_status mla_tree_attention(const mla_tree_attn_args* a, void* stream) {
   p.cu = a->cu_q;
   p.nseq = a->nseq;
   p.max_q = a->max_q;
-  p.max_len = a->max_len;
+  p.max_len = std::min(a->max_len, mla::kLongestSeq);
   p.mask = a->mask;
   p.mask_words = a->mask ? a->mask_words : 0;
   p.mx = a->cache_dtype == MLA_DTYPE_MXFP8;

@@ -95,6 +95,10 @@ struct AttnPlan {
                                         // plan's sums; bytes in all
 };
 
+// Longest sequence that the attention takes: positions of the tiles that it asks
+// for ahead and the next part of a long one (65536 rows) stay within 31 bits.
+constexpr int32_t kLongestSeq = INT32_MAX - (1 << 17);
+
 struct AttnParams {
   const uint16_t* q;
   int64_t q_t, q_h;

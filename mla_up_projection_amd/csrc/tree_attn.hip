@@ -80,7 +80,9 @@ struct Item {
   int64_t slot;         // else the place of its partial result
 };
 
-// Sequence j of the call. Any lane may ask for any j.
+// Sequence j of the call. Any lane may ask for any j. Committed rows behind the
+// held pages are nowhere, and every token sees them, so the sequence is broken at
+// once: a length that means nothing must not be worked through.
 __device__ __forceinline__ void load_seq(const AttnParams& p, int j, Item& it) {
   const int T = (int)p.T;
   it.j = j;
@@ -90,7 +92,9 @@ __device__ __forceinline__ void load_seq(const AttnParams& p, int j, Item& it) {
   it.seq = p.seqs[j];
   it.broken = it.seq < 0 || it.seq >= p.pool.max_seqs || it.n > p.max_q;
   it.len = it.broken ? 0 : p.pool.lens[it.seq];
-  it.broken |= it.len < 0 || it.len > p.max_len - it.n;
+  const int held = it.broken ? 0 : p.pool.held[it.seq];
+  it.broken |= it.len < 0 || it.len > p.max_len - it.n ||
+               it.len > (int64_t)max(min(held, p.pool.max_pages), 0) * p.pool.page_size;
   it.total = it.len + it.n;
 }
 // What all lanes agree on goes to scalar registers.
