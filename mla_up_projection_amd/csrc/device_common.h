@@ -99,9 +99,10 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float x0, float x1, float x2, flo
 // ---------------------------------------------------------------------------
 
 // 16 bytes per lane: lane i of the wave writes LDS bytes [lds_addr + 16 i,
-// +16) from global sbase + voff (sbase wave-uniform).
+// +16) from global sbase + voff (sbase wave-uniform). The load reads m0, which
+// takes a wait state after the instruction that sets it.
 __device__ __forceinline__ void dma16(const void* sbase, uint32_t voff, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds_addr), "v"(voff), "s"(sbase)
                : "memory", "m0");
