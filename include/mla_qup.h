@@ -381,7 +381,8 @@ typedef struct {
   uint8_t* out_scales;      /* MXFP8: BHSD [.., D/32]; else NULL */
 } mla_qup_w4_args;
 
-/* Errors: as mla_qup_fwd (W may span any size). */
+/* Errors: as mla_qup_fwd; MLA_EUNSUPPORTED for 2^29 output columns (H*D) or
+ * more. */
 MLA_API mla_status mla_qup_fwd_w4(const mla_qup_w4_args* args, void* stream);
 
 /* A cache of num_pages pages of page_size token rows. Sequence i holds the

@@ -160,6 +160,7 @@ mla_status mla_qup_fwd_w4(const mla_qup_w4_args* a, void* stream) {
   if (T == 0) return MLA_OK;
   const int D = a->d_nope + a->d_rope;
   const int64_t N = (int64_t)a->H * D;
+  if (N >= (int64_t)1 << 29) return MLA_EUNSUPPORTED;  // 8 work-items a column, 2^32 in a grid's dimension
   if (!a->x || !a->w || !a->w_scales || !a->out) return MLA_EINVAL;
   const bool mx = a->out_dtype == MLA_DTYPE_MXFP8;
   if (mx && !a->out_scales) return MLA_EINVAL;
