@@ -534,7 +534,7 @@ typedef struct {
   float* lse;               /* fp32 [T, H] or NULL */
   int64_t T;                /* query rows */
   int32_t H, H_kv, d_k, d_v; /* H a multiple of H_kv */
-  float scale;              /* finite */
+  float scale;              /* finite, and so is scale * log2 e in fp32 */
   const int32_t* seqs;      /* device int32[nseq] */
   const int32_t* cu_q;      /* device int32[nseq + 1], nondecreasing from 0 */
   int32_t nseq;             /* 0 .. 65535 */

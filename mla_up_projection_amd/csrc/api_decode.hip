@@ -423,13 +423,16 @@ AttnPlan plan_attn(int nseq, int H, int H_kv, int d_v, int max_q, int max_len, i
 
 namespace {
 
+// The factor that makes scores powers of two.
+float scale_log2(const mla_tree_attn_args* a) { return (float)((double)a->scale * 1.4426950408889634); }
+
 mla_status check_attn(const mla_tree_attn_args* a, mla::AttnPlan* plan) {
   if (a == nullptr) return MLA_EINVAL;
   mla_status st = check_pool(a->pool);
   if (st) return st;
   if (a->T < 0 || a->T > (int64_t)INT32_MAX || a->H < 1 || a->H_kv < 1 || a->H % a->H_kv) return MLA_EINVAL;
   if (a->nseq < 0 || a->nseq > 65535 || a->max_q < 1 || a->max_len < 1) return MLA_EINVAL;
-  if (!isfinite(a->scale)) return MLA_EINVAL;
+  if (!isfinite(scale_log2(a))) return MLA_EINVAL;
   if (a->cache_dtype != MLA_DTYPE_BF16 && a->cache_dtype != MLA_DTYPE_MXFP8) return MLA_EINVAL;
   if (a->d_k < 1 || a->d_v < 1 || a->d_k > 65536 || a->d_v > 65536) return MLA_EINVAL;
   const bool shared = a->pool->nbuf == (a->cache_dtype == MLA_DTYPE_MXFP8 ? 2 : 1);
@@ -501,7 +504,7 @@ mla_status mla_tree_attention(const mla_tree_attn_args* a, void* stream) {
   p.group = a->H / a->H_kv;
   p.d_k = a->d_k;
   p.d_v = a->d_v;
-  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2(a);
   p.seqs = a->seqs;
   p.cu = a->cu_q;
   p.nseq = a->nseq;
