@@ -219,7 +219,7 @@ __device__ __forceinline__ bool not_finite_pair(uint32_t v) {
 // and a ring of STAGES tiles in LDS. The widest shape always has four waves, one
 // to a SIMD: waves without rows only help to load (with one wave of rows a CU
 // still takes a tile in less time than HBM delivers it). The others: four waves
-// keep three or four tiles, two waves two and one wave one, so that several
+// keep three tiles (MXFP8 two), two waves two and one wave one, so that several
 // workgroups share a CU and hide each other's loads.
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
 struct Shape {
@@ -229,7 +229,7 @@ struct Shape {
   static constexpr int KK = DK / 16, NT = DV / 32;
   static constexpr int TILE_LDS = NB * BLK;
   static constexpr bool WIDE = DK == 576 && DV == 512;  // the products are written out (tree_attn_wide.h)
-  static constexpr int STAGES = WIDE ? (MX ? 3 : 4) : MX ? (WAVES == 1 ? 1 : 2) : WAVES == 4 ? (NB > 5 ? 4 : 3) : WAVES;
+  static constexpr int STAGES = WIDE ? (MX ? 3 : 4) : MX ? (WAVES == 1 ? 1 : 2) : WAVES == 4 ? 3 : WAVES;
   // WIDE MXFP8, two places each: codes of a tile, 4.5 blocks of 128 bytes a row, and scales, five words a row
   static constexpr int RAW_LDS = 5 * BLK, SCALE_LDS = TILE * 20;
   static constexpr int LDS = STAGES * TILE_LDS + (WIDE && MX ? 2 * (RAW_LDS + SCALE_LDS) : 0);
