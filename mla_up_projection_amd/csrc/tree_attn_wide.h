@@ -1,4 +1,5 @@
-// The products of a 576/512-wide tile for one wave, written out.
+// The products of a 576/512-wide tile for one wave, written out (by
+// tree_attn_wide_gen.py, where changes are made).
 //
 // A wave that owns 32 query rows holds 144 registers of Q and 256 of O: all
 // accumulation registers and more than half of the others, and the wave is alone
@@ -26,7 +27,11 @@
 #pragma once
 
 // The registers that the blocks use by name.
-#define WIDE_CLOBBERS   "v208", "v209", "v210", "v211", "v212", "v213", "v214", "v215", "v216", "v217", "v218", "v219",   "v220", "v221", "v222", "v223", "v224", "v225", "v226", "v227", "v228", "v229", "v230", "v231",   "v232", "v233", "v234", "v235", "v236", "v237", "v238", "v239", "v240", "v241", "v242", "v243",   "v244", "v245", "v246", "v247", "v248", "v249", "v250", "v251", "v252", "v253", "v254", "v255"
+#define WIDE_CLOBBERS \
+  "v208", "v209", "v210", "v211", "v212", "v213", "v214", "v215", "v216", "v217", "v218", "v219", \
+  "v220", "v221", "v222", "v223", "v224", "v225", "v226", "v227", "v228", "v229", "v230", "v231", \
+  "v232", "v233", "v234", "v235", "v236", "v237", "v238", "v239", "v240", "v241", "v242", "v243", \
+  "v244", "v245", "v246", "v247", "v248", "v249", "v250", "v251", "v252", "v253", "v254", "v255"
 
 // Scores (s, not scaled) of a tile.
 #define WIDE_SCORES \
