@@ -40,7 +40,6 @@ constexpr float LAZY = 64.0f;    // how many powers of two a score may lie above
 constexpr float NEG_INF = -__builtin_huge_valf();
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 // Position of 16-byte chunk c of cache row t within the row's 128 bytes. A row
 // spans half the 64 banks, so rows t, t + 2, .. would share theirs; moving
@@ -66,6 +65,14 @@ __device__ __forceinline__ int bits_of(int n) { return 32 - __builtin_clz(n); }
 __device__ __forceinline__ float widest(float x, float a, float b) {
   asm("v_maximum3_f32 %0, |%1|, |%2|, %0" : "+v"(x) : "v"(a), "v"(b));
   return x;
+}
+
+// The kernel's arguments, read again where they are used: of the paths that hardly
+// run, so that nothing of theirs is worked out ahead and kept.
+__device__ __forceinline__ const AttnParams& arguments() {
+  auto* p = (const __attribute__((address_space(4))) AttnParams*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnParams*)p;
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -208,6 +215,14 @@ __device__ __forceinline__ uint32_t visible(const AttnParams& p, const Item& it,
   }
   const int left = it.n - d;  // rows of the sequence from bit 0 on
   return left >= 32 ? bits : left <= 0 ? 0 : bits & ((1u << left) - 1);
+}
+
+// The maximum of three pairs in fp16: a bf16 that is infinite or NaN is a NaN there
+// (the exponent's upper five bits are all of fp16's, the others lie in its mantissa),
+// which stays whatever the others are.
+__device__ __forceinline__ uint32_t widest_pairs(uint32_t x, uint32_t a, uint32_t b) {
+  asm("v_pk_maximum3_f16 %0, %1, %2, %0" : "+v"(x) : "v"(a), "v"(b));
+  return x;
 }
 
 // Whether one of two bf16 is infinite or NaN.
@@ -895,7 +910,8 @@ __device__ __forceinline__ void slow_row(const AttnParams& p, const Item& it, in
 // The workgroup's rows by slow_row, a wave its 32 one by one. Writes what the fast
 // path writes.
 template <int DK, int DV, bool SHARED, bool MX, int WAVES>
-__device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, int tk_begin, int tk_end) {
+__device__ __forceinline__ void slow_rows(const Item& it, int tk_begin, int tk_end) {
+  const AttnParams& p = arguments();
   const int tid = opaque((int)threadIdx.x), lane = tid & 63, wave = tid >> 6, v = lane % (DV / 8);
   const int64_t slot = it.slot * WAVES + wave;
 #pragma unroll 1
@@ -928,8 +944,8 @@ __device__ __forceinline__ void slow_rows(const AttnParams& p, const Item& it, i
 // or sums left fp32's range on the way to a mean that lies in it, and the rows are
 // done again by slow_row. For a wave, and the columns 8 (first + step v), v < LANES.
 template <int DK, bool MX, int LANES>
-__device__ __forceinline__ void out_of_range(const AttnParams& p, const Item& it, int at, uint32_t rows, int first,
-                                             int step) {
+__device__ __forceinline__ void out_of_range(const Item& it, int at, uint32_t rows, int first, int step) {
+  const AttnParams& p = arguments();
   const int lane = opaque((int)threadIdx.x) & 63;
   const bool shared = p.pool.nbuf == (MX ? 2 : 1);
   const int held = min(p.pool.held[it.seq], p.pool.max_pages), c = 8 * min(first + step * (lane % LANES), p.d_v / 8 - 1);
@@ -1044,7 +1060,7 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     w.m = w.top;  // the largest score of all: the next pass is the last
   }
   if (__builtin_expect(slow, 0)) {
-    slow_rows<DK, DV, SHARED, MX, WAVES>(p, it, tk_begin, tk_end);
+    slow_rows<DK, DV, SHARED, MX, WAVES>(it, tk_begin, tk_end);
     return;
   }
   const float m = w.m;
@@ -1071,13 +1087,11 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     int qi = at / p.group, h = at - qi * p.group;
     uint16_t* dst = p.out + (int64_t)(it.t0 + qi) * p.o_t + (int64_t)(it.kvh * p.group + h) * p.o_h + 8 * lane;
     const int live = min(32, it.rows - at);
-    u16x2_t most = {0, 0};  // magnitudes
+    uint32_t largest = 0;
     for (int k = 0; k < live; ++k) {
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(rows + k * (DV * 2) + ((lane ^ k) << 4));
       *reinterpret_cast<u32x4_t*>(dst) = v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, v[i] & 0x7FFF7FFFu));
+      largest = widest_pairs(widest_pairs(largest, v[0], v[1]), v[2], v[3]);
       dst += p.o_h;
       if (++h == p.group) {
         h = 0;
@@ -1086,7 +1100,7 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     }
     if (p.lse && r.live && r.half == 0)
       p.lse[r.qt * p.H + r.h] = l == 0 ? NEG_INF : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
-    if (__builtin_expect(__any(most[0] >= 0x7F80 || most[1] >= 0x7F80), 0)) {
+    if (__builtin_expect(__any((largest & 0x7C00u) == 0x7C00u || (largest & 0x7C000000u) == 0x7C000000u), 0)) {
       uint32_t strange = 0;
       for (int k = 0; k < live; ++k) {
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(rows + k * (DV * 2) + ((lane ^ k) << 4));
@@ -1094,7 +1108,7 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
           strange |= 1u << k;
       }
       strange &= (uint32_t)__ballot(l < __builtin_huge_valf());
-      if (strange) out_of_range<DK, MX, DV / 8>(p, it, at, strange, 0, 1);
+      if (strange) out_of_range<DK, MX, DV / 8>(it, at, strange, 0, 1);
     }
     return;
   }
@@ -1117,7 +1131,7 @@ __device__ __forceinline__ void run_item(const AttnParams& p, const Item& it, ui
     }
     const uint64_t strange = __ballot(!(x < __builtin_huge_valf()) && l < __builtin_huge_valf());
     if (__builtin_expect(strange != 0, 0))
-      out_of_range<DK, MX, DV / 8>(p, it, (it.rt * WAVES + wave) * 32, (uint32_t)(strange | strange >> 32), 0, 1);
+      out_of_range<DK, MX, DV / 8>(it, (it.rt * WAVES + wave) * 32, (uint32_t)(strange | strange >> 32), 0, 1);
     return;
   }
   if (!r.live) return;
@@ -1450,8 +1464,8 @@ void join_kernel(AttnParams p, int vectors_each) {
   if (__builtin_expect(strange != 0, 0)) {
     const int at = (it.rt * waves + wave) * 32;
     const uint32_t rows = (uint32_t)(strange | strange >> 32);
-    if (p.mx) out_of_range<0, true, V>(p, it, at, rows, v0, 4);
-    else out_of_range<0, false, V>(p, it, at, rows, v0, 4);
+    if (p.mx) out_of_range<0, true, V>(it, at, rows, v0, 4);
+    else out_of_range<0, false, V>(it, at, rows, v0, 4);
   }
 }
 
