@@ -511,8 +511,9 @@ MLA_API mla_status mla_kv_rope_paged(const mla_kv_paged_args* args, void* stream
  *   out = sum_r e^(s_r) value_r / sum_r e^(s_r),   lse = ln sum_r e^(s_r).
  * A token that sees no row gets out = 0 and lse = -inf. What lies in rows that
  * a token does not see, NaN and infinities included, has no influence on it.
- * Statistics and sums are fp32; the weights e^(s - max) are rounded to bf16
- * for the product with the values. Results do not depend on timing. Values may
+ * Scores, statistics and sums are fp32; the weights e^(s - max) are rounded to
+ * bf16 for the product with the values, and MXFP8 rows are taken as bf16, which
+ * holds them exactly down to 2^-133. Results do not depend on timing. Values may
  * be as large as bf16 holds (up to 2^127: a result is a mean of values, and half
  * a rounding step more is still finite): where a sum leaves fp32's range on the
  * way to a mean that lies in it, the row is done again, slowly.

@@ -19,11 +19,11 @@
 //
 // What bounds it (rates on the same card: a large copy 4.9 TB/s, a large bf16
 // product 1365 TFLOP/s): per-head caches HBM (4 sequences of 300 to 1500 rows, 128
-// heads of 192 + 128: 62 us and 8 for the join, 4.3 TB/s); the shared 576-wide
+// heads of 192 + 128: 62 us and 7 for the join, 4.3 TB/s); the shared 576-wide
 // cache the matrix units, at 2 flops for each of 128 heads and draft to a byte (32
-// sequences of 4096 rows, 16 drafts, 128 heads: 582 us, 1006 TFLOP/s; MXFP8 671);
-// a single token the way through the kernel (one sequence of 517 rows: 17 us, of
-// which the products are 4, and 7 for the join).
+// sequences of 4096 rows, 16 drafts, 128 heads: 560 to 580 us, 1010 to 1045
+// TFLOP/s; MXFP8 650 to 665); a single token the way through the kernel (one
+// sequence of 517 rows: 18 us, of which the products are 4, and 7 for the join).
 #include <algorithm>
 
 #include "device_common.h"
@@ -804,7 +804,7 @@ __device__ __forceinline__ int64_t find_row(const AttnParams& p, const Item& it,
 // flight. A row that is not seen adds nothing. o: the lane's columns, 8 (lane %
 // LANES) on; the reference lies so far above the largest score that the weights'
 // sum stays below 1 and finite values give finite sums. All of a workgroup's rows come here, so it costs: one stray NaN among 8
-// sequences of 2000 rows, 4 drafts, 16 heads makes 1.4 ms of 30 us (5.5 with a lane
+// sequences of 2000 rows, 4 drafts, 16 heads makes 1.4 ms of 35 us (5.5 with a lane
 // for every 64th column and one cache row at a time).
 // The columns may also be some eights of them, first + step (lane % LANES). DK 0: any
 // width, in few registers.
