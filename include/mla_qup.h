@@ -509,8 +509,9 @@ MLA_API mla_status mla_kv_rope_paged(const mla_kv_paged_args* args, void* stream
  * mask[t*mask_words + k/32] set (NULL: k <= i, a chain). Per head h, with its
  * key head h / (H / H_kv), s_r = scale q.key_r over the rows seen:
  *   out = sum_r e^(s_r) value_r / sum_r e^(s_r),   lse = ln sum_r e^(s_r).
- * A token that sees no row gets out = 0 and lse = -inf. What lies in rows that
- * a token does not see, NaN and infinities included, has no influence on it.
+ * A token that sees no row, or none with a score above -inf, gets out = 0 and
+ * lse = -inf. What lies in rows that a token does not see, NaN and infinities
+ * included, has no influence on it.
  * Scores, statistics and sums are fp32; the weights e^(s - max) are rounded to
  * bf16 for the product with the values, and MXFP8 rows are taken as bf16, which
  * holds them exactly down to 2^-133. Results do not depend on timing. Values may
