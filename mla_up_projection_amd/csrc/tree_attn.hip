@@ -560,12 +560,16 @@ struct Worker {
   }
   // Values that some rows do not see may be anything, and the product would make
   // NaN of 0 times infinity, so this thread's share of the tile's values is
-  // looked over: if one is not finite, slow_rows() takes over.
-  __device__ __forceinline__ void look_over(const uint8_t* tile) {
-    const int tid = thread();
+  // looked over: if one of a draft, or of the last row (which the places behind it
+  // repeat), is not finite, slow_rows() takes over. Committed rows are seen by all.
+  __device__ __forceinline__ void look_over(const uint8_t* tile, int tk) {
+    const int tid = thread(), first = min(it.len, tk_end - 1) - tk;
     const uint8_t* vals = tile + (SHARED ? 0 : S::NBK * BLK);
+    constexpr bool ONE_ROW = S::THREADS == 8 * TILE;  // a thread's pieces are all of one row
+    if (ONE_ROW && (tid >> 3) < first) return;
 #pragma unroll 1
     for (int i = tid; i < DV * TILE / 8; i += S::THREADS) {  // 16 bytes each, in any order
+      if (!ONE_ROW && (i >> 3) % TILE < first) continue;
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(vals + 16 * i);
 #pragma unroll
       for (int k = 0; k < 4; ++k) odd |= not_finite_pair(v[k]);
@@ -587,7 +591,7 @@ struct Worker {
     f32x16_t s = scores(tile);
     if (__builtin_expect(i >= full, 0)) {
       mask(s, tk_begin + i * TILE);
-      look_over(tile);
+      look_over(tile, tk_begin + i * TILE);
     }
     weights(s);
     values(tile, s);
@@ -701,7 +705,7 @@ struct Worker {
       }
       if (__builtin_expect(i >= full, 0)) {
         if (active) mask(s, tk_begin + i * TILE);
-        look_over(lds + slot * S::TILE_LDS);
+        look_over(lds + slot * S::TILE_LDS, tk_begin + i * TILE);
       }
       // (behind the last tile the scores of what lies there are not used)
       if (active) step_ahead(lds + slot * S::TILE_LDS, lds + after * S::TILE_LDS, s, loads);
@@ -950,11 +954,20 @@ __device__ __forceinline__ void out_of_range(const Item& it, int at, uint32_t ro
   const bool shared = p.pool.nbuf == (MX ? 2 : 1);
   const int held = min(p.pool.held[it.seq], p.pool.max_pages), c = 8 * min(first + step * (lane % LANES), p.d_v / 8 - 1);
 #pragma unroll 1
-  for (uint32_t tk = 0; tk < (uint32_t)it.len; tk += 64 / LANES) {
-    bool bad;
-    const int64_t r = find_row(p, it, held, min(tk + lane / LANES, (uint32_t)it.len - 1), bad);
-    const u32x4_t v = cache_eight<MX>(p.pool, shared ? 0 : 1, r, shared ? p.d_k : p.d_v, c);
-    if (__any(not_finite_pair(v[0]) || not_finite_pair(v[1]) || not_finite_pair(v[2]) || not_finite_pair(v[3]))) return;
+  for (uint32_t tk = 0; tk < (uint32_t)it.len; tk += 4 * (64 / LANES)) {
+    u32x4_t v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      bool bad;
+      const int64_t r = find_row(p, it, held, min(tk + u * (64 / LANES) + lane / LANES, (uint32_t)it.len - 1), bad);
+      v[u] = cache_eight<MX>(p.pool, shared ? 0 : 1, r, shared ? p.d_k : p.d_v, c);
+    }
+    bool strange = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) strange |= not_finite_pair(v[u][k]);
+    if (__any(strange)) return;
   }
   vm_wait<0>();  // what this wave wrote
 #pragma unroll 1
