@@ -67,8 +67,10 @@ __device__ __forceinline__ float widest(float x, float a, float b) {
   return x;
 }
 
-// The kernel's arguments, read again where they are used: of the paths that hardly
-// run, so that nothing of theirs is worked out ahead and kept.
+// The kernel's arguments (the first of every kernel here), read again: for the paths
+// that hardly run, so that nothing of theirs is worked out ahead and kept. With the
+// others' copy a call of one step took 17.1 us, not 17.0, and 27 short sequences
+// with 22 drafts 104, not 100.
 __device__ __forceinline__ const AttnParams& arguments() {
   auto* p = (const __attribute__((address_space(4))) AttnParams*)__builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(p));
