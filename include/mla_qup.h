@@ -66,7 +66,7 @@ enum {
                             library's static scratch (MLA_BWD_SCRATCH_BYTES) */
 };
 
-enum { MLA_DTYPE_BF16 = 0, MLA_DTYPE_FP32 = 1, MLA_DTYPE_MXFP8 = 2 };
+enum { MLA_DTYPE_BF16 = 0, MLA_DTYPE_FP32 = 1, MLA_DTYPE_MXFP8 = 2, MLA_DTYPE_INT8 = 3 };
 
 /* Token formats: rows of X (and of dQ) are tokens.
  *   BSHD: row t = b*S + s, position s.
@@ -561,6 +561,208 @@ MLA_API size_t mla_tree_attention_workspace_size(const mla_tree_attn_args* args)
  * workspace belongs to one call at a time: calls that may run at once (two
  * streams, two graphs) need one each. */
 MLA_API mla_status mla_tree_attention(const mla_tree_attn_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Around the projection in a layer: the RMS norm of the rows in front of it,
+ * the projection in 8-bit integers, and attention of a prompt or a training
+ * batch over the keys and values of mla_kv_rope, with the gradients of norm and
+ * attention: mla_rmsnorm_fwd -> mla_qup_fwd / mla_qup_fwd_i8 -> mla_attn_fwd,
+ * and back mla_attn_bwd -> mla_qup_bwd -> mla_rmsnorm_bwd.
+ * ------------------------------------------------------------------------ */
+
+/* RMS norm of token rows, with the addition of the residual in front of it:
+ *   h = x + res (rounded to the residual's type; h = x without one),
+ *   rstd = (mean_k h^2 + eps)^(-1/2),  y = h * rstd * gamma.
+ * y is written as bf16 (y), as 8-bit codes (codes, scales), or both; the codes
+ * come from the fp32 values:
+ *   MXFP8: as mxfp8_quantize; the operand of mla_qup_fwd.
+ *   INT8 : scales[t] = amax / 127 of the row, code = the integer nearest to
+ *          y * (127 / amax), ties to even; the operand of mla_qup_fwd_i8. A row of
+ *          zeros, or with amax <= 127 * 2^-128, has scale 0 and codes 0; one that
+ *          holds NaN or an infinity has scale NaN and codes 0.
+ * Sums are fp32. */
+typedef struct {
+  const void* x;        /* bf16 [T, K], row t at x + t*ld_x elements; 16-B aligned */
+  int64_t ld_x;         /* >= K, a multiple of 8 */
+  const void* res;      /* [T, K] in res_dtype, or NULL; 16-B aligned */
+  int32_t res_dtype;    /* MLA_DTYPE_BF16 or MLA_DTYPE_FP32 */
+  const void* gamma;    /* [K] in gamma_dtype, or NULL (ones); 16-B aligned */
+  int32_t gamma_dtype;  /* MLA_DTYPE_BF16 or MLA_DTYPE_FP32 */
+  float eps;            /* >= 0, finite */
+  int64_t T;            /* 0 .. 2^31 - 1 */
+  int32_t K;            /* a multiple of 8 (MXFP8 codes: of 32), 8 .. 32768 */
+  void* h;              /* out: [T, K] in res_dtype; NULL: not written. Needs res. 16-B aligned */
+  float* rstd;          /* out: [T] or NULL */
+  void* y;              /* out: bf16 [T, K] or NULL; 16-B aligned */
+  int32_t q_dtype;      /* with codes: MLA_DTYPE_MXFP8 or MLA_DTYPE_INT8 */
+  void* codes;          /* out: [T, K] or NULL; 8-B aligned */
+  void* scales;         /* out: MXFP8 uint8 [T, K/32], INT8 fp32 [T]; NULL without codes */
+} mla_rmsnorm_args;
+
+/* Errors: MLA_EINVAL (also where neither y nor codes nor h nor rstd is asked
+ * for), MLA_EALIAS, MLA_EDEVICE. */
+MLA_API mla_status mla_rmsnorm_fwd(const mla_rmsnorm_args* args, void* stream);
+
+/* Its backward. With xhat = h rstd and g = gamma dy:
+ *   d = dh + rstd (g - xhat mean_k(g xhat)),  dgamma = sum_t dy xhat.
+ * d is the gradient of x and of res alike: dx takes it as bf16, dres as fp32.
+ * Sums are fp32 and taken in a fixed order. */
+typedef struct {
+  const void* dy;       /* bf16 [T, K]; 16-B aligned */
+  const void* h;        /* the forward's h (or its x), row t at h + t*ld_h elements; 16-B aligned */
+  int32_t h_dtype;      /* MLA_DTYPE_BF16 or MLA_DTYPE_FP32 */
+  int64_t ld_h;         /* >= K, a multiple of 8 */
+  const float* rstd;    /* [T], the forward's */
+  const void* gamma;    /* as the forward's */
+  int32_t gamma_dtype;
+  const void* dh;       /* [T, K] in h_dtype: the gradient that reaches h on other ways, or NULL; 16-B aligned */
+  int64_t T;
+  int32_t K;
+  void* dx;             /* out: bf16 [T, K] or NULL; 16-B aligned */
+  float* dres;          /* out: fp32 [T, K] or NULL; 16-B aligned */
+  float* dgamma;        /* out: fp32 [K] or NULL */
+  void* workspace;      /* mla_rmsnorm_bwd_workspace_size() bytes, 256-B aligned; needed for dgamma */
+  size_t workspace_bytes;
+} mla_rmsnorm_bwd_args;
+
+/* Workspace bytes of the backward for these sizes; 0 for invalid ones. */
+MLA_API size_t mla_rmsnorm_bwd_workspace_size(int64_t T, int32_t K);
+
+/* T = 0 writes zeros to dgamma. Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE,
+ * MLA_EDEVICE. */
+MLA_API mla_status mla_rmsnorm_bwd(const mla_rmsnorm_bwd_args* args, void* stream);
+
+/* Quantize the rows of a matrix to int8 with one scale each, by the rule of
+ * mla_rmsnorm_fwd: the weights of mla_qup_fwd_i8 (a scale for each output
+ * channel), or its activations.
+ *   x      : as mxfp8_quantize. rows: 0 .. 2^24; cols: a multiple of 8, > 0.
+ *   codes  : device int8[rows*cols], 8-byte aligned. scales: device float[rows].
+ * Errors: MLA_EINVAL, MLA_EALIAS, MLA_EDEVICE. */
+MLA_API mla_status int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                                 int8_t* codes, float* scales, void* stream);
+
+/* The forward in 8-bit integers: Q[t, n] = x_scales[t] * w_scales[n] *
+ * sum_k x[t, k] w[n, k] (+ bias[n]), rotated and stored as mla_qup_fwd does. The
+ * sums are exact (32-bit integers), the rest fp32. H = 1, d_rope = 0 and B = 1 make
+ * it a plain product [T, N].
+ *   positions: as mla_qup_fwd_w4's. */
+typedef struct {
+  const int8_t* x;          /* [T, K]; 16-B aligned */
+  const float* x_scales;    /* [T] */
+  const int8_t* w;          /* [N, K]; 16-B aligned */
+  const float* w_scales;    /* [N] */
+  const void* bias;         /* bf16 [N] or NULL; 8-B aligned */
+  int32_t K;                /* a multiple of 64, 64 .. 65536 */
+  int32_t H, d_nope, d_rope; /* as the forward's */
+  mla_tokens tokens;
+  const int32_t* positions;
+  mla_rope rope;
+  int32_t out_dtype;        /* MLA_DTYPE_BF16 or MLA_DTYPE_MXFP8 */
+  void* out;                /* BHSD; 16-B aligned */
+  uint8_t* out_scales;      /* MXFP8: BHSD [.., D/32]; else NULL */
+} mla_qup_i8_args;
+
+/* Errors: as mla_qup_fwd; MLA_EUNSUPPORTED where X or W spans more than 4 GiB or
+ * there are 2^29 output columns or more. */
+MLA_API mla_status mla_qup_fwd_i8(const mla_qup_i8_args* args, void* stream);
+
+/* Which keys a query row sees in mla_attn_fwd: those of one span [lo, hi) of its
+ * batch entry's keys. A span per row says causal, document, prefix, window and
+ * padding masks alike; this call writes the usual ones.
+ *   packed (cu_q given): documents packed back to back in one batch entry (B = 1),
+ *     query rows cu_q[j] .. cu_q[j+1] and key rows cu_k[j] .. cu_k[j+1] belonging
+ *     to document j. cu_k NULL: cu_q.
+ *   else: one sequence per batch entry, its first len_q[b] query rows and len_k[b]
+ *     key rows (NULL: all).
+ * With l_q queries and l_k keys a sequence's queries are its last tokens: query i
+ * of it stands at its key i + l_k - l_q. It sees the sequence's keys
+ *   causal: up to itself, and the first prefix[j] (NULL: 0) whatever it is;
+ *   else  : all;
+ *   window > 0: of those only the ones less than `window` behind it or after it.
+ * A row that belongs to no sequence sees nothing. Sequence bounds outside the
+ * rows that there are, are cut to them. */
+typedef struct {
+  int32_t* spans;           /* out: [B, Sq, 2] (lo, hi); 8-B aligned */
+  int32_t* at;              /* out: [B, Sq], each row's place among the keys, or NULL */
+  int32_t B, Sq, Sk;
+  const int32_t* cu_q;      /* [nseq + 1], nondecreasing, or NULL */
+  const int32_t* cu_k;
+  int32_t nseq;             /* packed: documents, >= 1; else ignored */
+  const int32_t* len_q;     /* [B] or NULL */
+  const int32_t* len_k;
+  const int32_t* prefix;    /* [nseq] or [B], or NULL */
+  int32_t causal;           /* 0 or 1 */
+  int32_t window;           /* 0: none */
+} mla_attn_spans_args;
+
+/* Errors: MLA_EINVAL, MLA_EALIAS, MLA_EDEVICE. */
+MLA_API mla_status mla_attn_spans(const mla_attn_spans_args* args, void* stream);
+
+/* Rows of bf16: element (b, h, s, d) at p[b*stride_b + h*stride_h + s*stride_s + d].
+ * p 16-byte aligned; strides >= 0 and multiples of 8, stride_s < 2^22. BHSD, token-major
+ * and slices of wider rows are all such rows. */
+typedef struct {
+  void* p;
+  int64_t stride_b, stride_h, stride_s;
+} mla_attn_rows;
+
+/* Attention of Sq query rows over Sk keys, per batch entry b and head h with its
+ * key head h / (H / H_kv):
+ *   s_ij = c(scale q_i . k_j) - slopes[h] |at_i - j|,  c(x) = cap tanh(x / cap) or x,
+ *   out_i = sum_j e^(s_ij) v_j / sum_j e^(s_ij),  lse_i = ln sum_j e^(s_ij),
+ * over the keys j of row i's span. A row that sees no key, or none with a score
+ * above -inf, gets out = 0 and lse = -inf. What lies in rows that a query does not
+ * see, NaN and infinities included, has no influence on it.
+ * Scores, statistics and sums are fp32; the weights are rounded to bf16 for the
+ * product with v, as every attention on these matrix units does. */
+typedef struct {
+  mla_attn_rows q;          /* [B, H, Sq, d_k] */
+  mla_attn_rows k;          /* [B, H_kv, Sk, d_k] */
+  mla_attn_rows v;          /* [B, H_kv, Sk, d_v] */
+  mla_attn_rows out;        /* out: [B, H, Sq, d_v]; rows may not meet */
+  float* lse;               /* out: [B, H, Sq], or NULL */
+  int32_t B, H, H_kv;       /* H a multiple of H_kv */
+  int32_t Sq, Sk;           /* Sq >= 0, Sk >= 0, each at most 2^27 */
+  int32_t d_k, d_v;         /* multiples of 8; d_k <= 192, d_v <= 128 */
+  float scale;              /* finite */
+  float cap;                /* 0: none; else > 0 and finite */
+  const float* slopes;      /* [H] or NULL */
+  const int32_t* spans;     /* [B, Sq, 2] (lo, hi) or NULL: every key; cut to [0, Sk); 8-B aligned */
+  const int32_t* at;        /* [B, Sq] or NULL: i + Sk - Sq; only read with slopes */
+  void* workspace;          /* mla_attn_fwd_workspace_size() bytes, 256-B aligned */
+  size_t workspace_bytes;
+} mla_attn_args;
+
+/* Workspace bytes for these arguments on the current device (0 if none): the
+ * partial results of keys that are divided because query rows are few. Reads the
+ * sizes only. The workspace belongs to one call at a time. */
+MLA_API size_t mla_attn_fwd_workspace_size(const mla_attn_args* args);
+
+/* Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED (wider rows,
+ * or 2^22 and more tiles of query rows), MLA_EDEVICE. */
+MLA_API mla_status mla_attn_fwd(const mla_attn_args* args, void* stream);
+
+/* Its backward, from the forward's out and lse:
+ *   P = e^(s - lse), dP = dout v^T, delta_i = dout_i . out_i,
+ *   dS = P (dP - delta) c'(scale q k),  dq = scale dS k, dk = scale dS^T q, dv = P^T dout.
+ * Heads that share a key head add their gradients. P and dS are rounded to bf16 for
+ * the matrix products, sums are fp32 in a fixed order, results do not depend on
+ * timing. dq, dk and dv are written whole: zeros where nothing is seen. The slopes
+ * are constants. `fwd.workspace` is not used. */
+typedef struct {
+  mla_attn_args fwd;        /* the forward's arguments; out and lse are inputs here */
+  mla_attn_rows dout;       /* [B, H, Sq, d_v] */
+  mla_attn_rows dq;         /* out: [B, H, Sq, d_k] */
+  mla_attn_rows dk;         /* out: [B, H_kv, Sk, d_k] */
+  mla_attn_rows dv;         /* out: [B, H_kv, Sk, d_v] */
+  void* workspace;          /* mla_attn_bwd_workspace_size() bytes, 256-B aligned */
+  size_t workspace_bytes;
+} mla_attn_bwd_args;
+
+MLA_API size_t mla_attn_bwd_workspace_size(const mla_attn_bwd_args* args);
+
+/* Errors: as mla_attn_fwd. */
+MLA_API mla_status mla_attn_bwd(const mla_attn_bwd_args* args, void* stream);
 
 /* Static string naming a status code. */
 MLA_API const char* mla_status_str(mla_status status);

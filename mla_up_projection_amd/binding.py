@@ -20,7 +20,7 @@ MLA_FWD_FP8_MFMA = 1
 (MLA_OK, MLA_EINVAL, MLA_EROPE_TABLE, MLA_EALIAS, MLA_EUNSUPPORTED, MLA_EDEVICE, MLA_EWORKSPACE,
  MLA_ESCRATCH) = range(8)
 MLA_BWD_SCRATCH_BYTES = 64 << 20
-DTYPE_BF16, DTYPE_FP32, DTYPE_MXFP8 = 0, 1, 2
+DTYPE_BF16, DTYPE_FP32, DTYPE_MXFP8, DTYPE_INT8 = 0, 1, 2, 3
 FMT_BSHD, FMT_SBHD, FMT_THD = 0, 1, 2
 
 FUNCTIONS = ("rope_cache_build", "mxfp8_quantize", "mxfp8_quantize_t", "mla_qup_fwd", "mla_qup_bwd",
@@ -29,7 +29,9 @@ FUNCTIONS = ("rope_cache_build", "mxfp8_quantize", "mxfp8_quantize_t", "mla_qup_
              "mxfp4_quantize", "mla_qup_fwd_w4", "mla_pages_workspace_size", "mla_pages_copy",
              "mla_pages_reserve", "mla_pages_fork", "mla_pages_free", "mla_pages_compact",
              "mla_draft_accept", "mla_kv_rope_paged", "mla_tree_attention",
-             "mla_tree_attention_workspace_size")
+             "mla_tree_attention_workspace_size", "mla_rmsnorm_fwd", "mla_rmsnorm_bwd",
+             "mla_rmsnorm_bwd_workspace_size", "int8_quantize", "mla_qup_fwd_i8", "mla_attn_spans",
+             "mla_attn_fwd", "mla_attn_fwd_workspace_size", "mla_attn_bwd", "mla_attn_bwd_workspace_size")
 
 
 class mla_tokens(Structure):
@@ -100,6 +102,48 @@ class mla_tree_attn_args(Structure):
                 ("pool", POINTER(mla_pool)), ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
 
 
+class mla_rmsnorm_args(Structure):
+    _fields_ = [("x", c_void_p), ("ld_x", c_int64), ("res", c_void_p), ("res_dtype", c_int32), ("gamma", c_void_p),
+                ("gamma_dtype", c_int32), ("eps", c_float), ("T", c_int64), ("K", c_int32), ("h", c_void_p),
+                ("rstd", c_void_p), ("y", c_void_p), ("q_dtype", c_int32), ("codes", c_void_p), ("scales", c_void_p)]
+
+
+class mla_rmsnorm_bwd_args(Structure):
+    _fields_ = [("dy", c_void_p), ("h", c_void_p), ("h_dtype", c_int32), ("ld_h", c_int64), ("rstd", c_void_p),
+                ("gamma", c_void_p), ("gamma_dtype", c_int32), ("dh", c_void_p), ("T", c_int64), ("K", c_int32),
+                ("dx", c_void_p), ("dres", c_void_p), ("dgamma", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
+class mla_qup_i8_args(Structure):
+    _fields_ = [("x", c_void_p), ("x_scales", c_void_p), ("w", c_void_p), ("w_scales", c_void_p), ("bias", c_void_p),
+                ("K", c_int32), ("H", c_int32), ("d_nope", c_int32), ("d_rope", c_int32), ("tokens", mla_tokens),
+                ("positions", c_void_p), ("rope", mla_rope), ("out_dtype", c_int32), ("out", c_void_p),
+                ("out_scales", c_void_p)]
+
+
+class mla_attn_spans_args(Structure):
+    _fields_ = [("spans", c_void_p), ("at", c_void_p), ("B", c_int32), ("Sq", c_int32), ("Sk", c_int32),
+                ("cu_q", c_void_p), ("cu_k", c_void_p), ("nseq", c_int32), ("len_q", c_void_p), ("len_k", c_void_p),
+                ("prefix", c_void_p), ("causal", c_int32), ("window", c_int32)]
+
+
+class mla_attn_rows(Structure):
+    _fields_ = [("p", c_void_p), ("stride_b", c_int64), ("stride_h", c_int64), ("stride_s", c_int64)]
+
+
+class mla_attn_args(Structure):
+    _fields_ = [("q", mla_attn_rows), ("k", mla_attn_rows), ("v", mla_attn_rows), ("out", mla_attn_rows),
+                ("lse", c_void_p), ("B", c_int32), ("H", c_int32), ("H_kv", c_int32), ("Sq", c_int32), ("Sk", c_int32),
+                ("d_k", c_int32), ("d_v", c_int32), ("scale", c_float), ("cap", c_float), ("slopes", c_void_p),
+                ("spans", c_void_p), ("at", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
+class mla_attn_bwd_args(Structure):
+    _fields_ = [("fwd", mla_attn_args), ("dout", mla_attn_rows), ("dq", mla_attn_rows), ("dk", mla_attn_rows),
+                ("dv", mla_attn_rows), ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
 _lib = None
 
 
@@ -143,6 +187,21 @@ def lib() -> ctypes.CDLL:
         L.mla_tree_attention.argtypes = [POINTER(mla_tree_attn_args), c_void_p]
         L.mla_tree_attention_workspace_size.argtypes = [POINTER(mla_tree_attn_args)]
         L.mla_tree_attention_workspace_size.restype = c_size_t
+        L.mla_rmsnorm_fwd.argtypes = [POINTER(mla_rmsnorm_args), c_void_p]
+        L.mla_rmsnorm_bwd.argtypes = [POINTER(mla_rmsnorm_bwd_args), c_void_p]
+        L.mla_rmsnorm_bwd_workspace_size.argtypes = [c_int64, c_int32]
+        L.int8_quantize.argtypes = L.mxfp8_quantize.argtypes
+        L.mla_qup_fwd_i8.argtypes = [POINTER(mla_qup_i8_args), c_void_p]
+        L.mla_attn_spans.argtypes = [POINTER(mla_attn_spans_args), c_void_p]
+        L.mla_attn_fwd.argtypes = [POINTER(mla_attn_args), c_void_p]
+        L.mla_attn_fwd_workspace_size.argtypes = [POINTER(mla_attn_args)]
+        L.mla_attn_bwd.argtypes = [POINTER(mla_attn_bwd_args), c_void_p]
+        L.mla_attn_bwd_workspace_size.argtypes = [POINTER(mla_attn_bwd_args)]
+        for f in ("mla_rmsnorm_bwd_workspace_size", "mla_attn_fwd_workspace_size", "mla_attn_bwd_workspace_size"):
+            getattr(L, f).restype = c_size_t
+        for f in ("mla_rmsnorm_fwd", "mla_rmsnorm_bwd", "int8_quantize", "mla_qup_fwd_i8", "mla_attn_spans",
+                  "mla_attn_fwd", "mla_attn_bwd"):
+            getattr(L, f).restype = c_int32
         for f in ("mxfp4_quantize", "mla_qup_fwd_w4", "mla_pages_copy", "mla_pages_reserve", "mla_pages_fork",
                   "mla_pages_free", "mla_pages_compact", "mla_draft_accept", "mla_kv_rope_paged",
                   "mla_tree_attention"):
@@ -696,3 +755,231 @@ def mla_tree_attention(q, pool, out, seqs, cu_q, *, stream=None, **kw):
     mla_tree_attention_workspace_size() bytes (None if that is 0)."""
     a = make_tree_attn_args(q, pool, out, seqs, cu_q, **kw)
     _call("mla_tree_attention", pool.device, stream, lib().mla_tree_attention, ctypes.byref(a))
+
+
+# ----------------------------------------------------- around the projection --
+_I8 = torch.int8
+_FLOATS = (_BF16, _FP32)
+
+
+def _dtype_of(t) -> int:
+    return DTYPE_FP32 if t is not None and t.dtype == _FP32 else DTYPE_BF16
+
+
+def _opt(chk, t, name, dtype, numel):
+    """Device address of a tensor that may be missing."""
+    if t is None:
+        return None
+    if chk.device is not None and _is(t, dtype, numel, chk.device):
+        return t.data_ptr()
+    return chk(t, name, (dtype,), numel=numel)
+
+
+def _row_view(chk, t, name, dtypes):
+    """Address and row stride of a 2-D tensor whose rows are dense."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (t.stride(1) != 1 and t.numel() and t.shape[1] > 1):
+        raise ValueError(f"{chk.where}: {name} must be 2-D with contiguous rows")
+    rows, cols = t.shape
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{chk.where}: the rows of {name} overlap")
+    ld = t.stride(0) if rows > 1 else cols
+    chk(t[:0], name, dtypes)
+    return t.data_ptr(), ld
+
+
+def mla_rmsnorm_fwd(x, gamma, *, eps=1e-6, res=None, h=None, y=None, codes=None, scales=None, rstd=None, stream=None):
+    """RMS norm of x bf16 [T,K] (row stride may exceed K), to which res bf16/fp32 [T,K] is added first. Outputs, each
+    optional: h [T,K] like res (the sum), y bf16 [T,K], rstd fp32 [T], and 8-bit codes of y: uint8 [T,K] with scales
+    uint8 [T,K/32] (MXFP8), or int8 [T,K] with scales fp32 [T]. gamma bf16/fp32 [K] or None (ones)."""
+    chk = _Dev("mla_rmsnorm_fwd")
+    a = mla_rmsnorm_args()
+    a.x, a.ld_x = _row_view(chk, x, "x", (_BF16,))
+    T, K = x.shape
+    a.res = chk(res, "res", _FLOATS, numel=T * K)
+    a.res_dtype = _dtype_of(res)
+    a.gamma = chk(gamma, "gamma", _FLOATS, numel=K)
+    a.gamma_dtype = _dtype_of(gamma)
+    a.eps, a.T, a.K = eps, T, K
+    a.h = _opt(chk, h, "h", _FP32 if a.res_dtype == DTYPE_FP32 else _BF16, T * K)
+    a.rstd = _opt(chk, rstd, "rstd", _FP32, T)
+    a.y = _opt(chk, y, "y", _BF16, T * K)
+    if codes is not None:
+        a.codes = chk(codes, "codes", (_U8, _I8), numel=T * K)
+        a.q_dtype = DTYPE_INT8 if codes.dtype == _I8 else DTYPE_MXFP8
+    if a.q_dtype == DTYPE_INT8:
+        a.scales = _opt(chk, scales, "scales", _FP32, T)
+    else:
+        a.scales = _opt(chk, scales, "scales", _U8, T * K // 32)
+    _call(chk.where, chk.device, stream, lib().mla_rmsnorm_fwd, ctypes.byref(a))
+
+
+def mla_rmsnorm_bwd_workspace_size(T, K) -> int:
+    return int(lib().mla_rmsnorm_bwd_workspace_size(T, K))
+
+
+def mla_rmsnorm_bwd(dy, h, rstd, gamma, *, dh=None, dx=None, dres=None, dgamma=None, workspace=None, stream=None):
+    """Backward of mla_rmsnorm_fwd: dy bf16 [T,K]; h bf16/fp32 [T,K], the forward's sum (or its x; the row stride may
+    exceed K); rstd fp32 [T]; dh [T,K] like h, the gradient that reaches h on other ways, or None. Outputs, each
+    optional: the gradient of x and res as dx bf16 [T,K] and dres fp32 [T,K], and dgamma fp32 [K], which needs a
+    workspace of mla_rmsnorm_bwd_workspace_size(T, K) bytes."""
+    chk = _Dev("mla_rmsnorm_bwd")
+    a = mla_rmsnorm_bwd_args()
+    a.h, a.ld_h = _row_view(chk, h, "h", _FLOATS)
+    T, K = h.shape
+    a.h_dtype = _dtype_of(h)
+    a.dy = chk(dy, "dy", (_BF16,), numel=T * K)
+    a.rstd = chk(rstd, "rstd", (_FP32,), numel=T)
+    a.gamma = chk(gamma, "gamma", _FLOATS, numel=K)
+    a.gamma_dtype = _dtype_of(gamma)
+    a.dh = chk(dh, "dh", (h.dtype,), numel=T * K)
+    a.T, a.K = T, K
+    a.dx = _opt(chk, dx, "dx", _BF16, T * K)
+    a.dres = _opt(chk, dres, "dres", _FP32, T * K)
+    a.dgamma = _opt(chk, dgamma, "dgamma", _FP32, K)
+    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
+    _call(chk.where, chk.device, stream, lib().mla_rmsnorm_bwd, ctypes.byref(a))
+
+
+def int8_quantize(x, codes, scales, stream=None):
+    """x [rows, cols] bf16/fp32 (row stride may exceed cols) -> codes int8 [rows, cols], scales fp32 [rows]."""
+    chk = _Dev("int8_quantize")
+    px, ld = _row_view(chk, x, "x", _FLOATS)
+    rows, cols = x.shape
+    pc = chk(codes, "codes", (_I8,), numel=rows * cols)
+    ps = chk(scales, "scales", (_FP32,), numel=rows)
+    _call(chk.where, chk.device, stream, lib().int8_quantize, px, _dtype_of(x), rows, cols, ld, pc, ps)
+
+
+def mla_qup_fwd_i8(x, x_scales, w, w_scales, out, *, H, d_nope, d_rope, cos=None, sin=None, positions=None, bias=None,
+                   out_scales=None, fmt=FMT_BSHD, B=1, S=None, cu_seqlens=None, max_seqlen=None, stream=None):
+    """Forward in 8-bit integers: x int8 [T,K] with x_scales fp32 [T] (mla_rmsnorm_fwd, int8_quantize), w int8 [N,K]
+    with w_scales fp32 [N] (int8_quantize); out and out_scales as mla_qup_fwd's. positions int32 [T]: each token's
+    position, in place of the format's."""
+    chk = _Dev("mla_qup_fwd_i8")
+    a = mla_qup_i8_args()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("mla_qup_fwd_i8: x must be [T, K]")
+    T, K = x.shape
+    N = H * (d_nope + d_rope)
+    a.x = chk(x, "x", (_I8,))
+    a.x_scales = chk(x_scales, "x_scales", (_FP32,), numel=T)
+    a.w = chk(w, "w", (_I8,), numel=N * K)
+    a.w_scales = chk(w_scales, "w_scales", (_FP32,), numel=N)
+    a.bias = chk(bias, "bias", (_BF16,), numel=N)
+    a.K, a.H, a.d_nope, a.d_rope = K, H, d_nope, d_rope
+    a.tokens = _tokens(chk, T, fmt, B, S, cu_seqlens, max_seqlen)
+    a.positions = chk(positions, "positions", (_I32,), numel=T)
+    a.rope = _rope(chk, cos, sin, d_rope)
+    a.out_dtype = DTYPE_MXFP8 if out.dtype == torch.uint8 else DTYPE_BF16
+    a.out = chk(out, "out", (_BF16, _U8), numel=T * N)
+    a.out_scales = chk(out_scales, "out_scales", (_U8,), numel=T * N // 32)
+    _call(chk.where, chk.device, stream, lib().mla_qup_fwd_i8, ctypes.byref(a))
+
+
+def mla_attn_spans(spans, at=None, *, Sk, cu_q=None, cu_k=None, len_q=None, len_k=None, prefix=None, causal=True,
+                   window=0, stream=None):
+    """The keys that each query row of mla_attn_fwd sees: spans int32 [B,Sq,2], and the rows' places among the keys,
+    at int32 [B,Sq] or None. Packed documents: cu_q int32 [n+1] (and cu_k, None: the same); else one sequence per batch
+    entry with len_q / len_k int32 [B] (None: all rows). prefix int32 [n or B]: keys that all rows of a sequence see.
+    window: how far back a row sees (0: all the way)."""
+    chk = _Dev("mla_attn_spans")
+    a = mla_attn_spans_args()
+    if not isinstance(spans, torch.Tensor) or spans.dim() != 3 or spans.shape[2] != 2:
+        raise ValueError("mla_attn_spans: spans must be [B, Sq, 2]")
+    a.B, a.Sq, a.Sk = spans.shape[0], spans.shape[1], Sk
+    a.spans = chk(spans, "spans", (_I32,))
+    a.at = _opt(chk, at, "at", _I32, a.B * a.Sq)
+    n = a.B
+    if cu_q is not None:
+        a.cu_q = chk(cu_q, "cu_q", (_I32,), min_numel=2)
+        a.nseq = n = cu_q.numel() - 1
+        a.cu_k = _opt(chk, cu_k, "cu_k", _I32, n + 1)
+    elif cu_k is not None:
+        raise ValueError("mla_attn_spans: cu_k without cu_q")
+    a.len_q, a.len_k = _opt(chk, len_q, "len_q", _I32, n), _opt(chk, len_k, "len_k", _I32, n)
+    a.prefix = _opt(chk, prefix, "prefix", _I32, n)
+    a.causal, a.window = 1 if causal else 0, window
+    _call(chk.where, chk.device, stream, lib().mla_attn_spans, ctypes.byref(a))
+
+
+def _attn_rows(chk, t, name, shape):
+    """A bf16 [B, H, S, d] view whose rows are dense; other strides are free."""
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
+        raise ValueError(f"{chk.where}: {name} must be {list(shape)}")
+    if t.dtype is not _BF16 or t.device != chk.device:
+        chk(t[:0], name, (_BF16,))
+    s = t.stride()
+    if s[3] != 1 and shape[3] > 1 and t.numel():
+        raise ValueError(f"{chk.where}: the elements of a row of {name} must be dense")
+    # the stride of an axis of one entry says nothing
+    return mla_attn_rows(t.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
+
+
+def _attn_args(where, q, k, v, out, lse, scale, cap, slopes, spans, at, workspace):
+    chk = _Dev(where)
+    if not all(isinstance(t, torch.Tensor) and t.dim() == 4 for t in (q, k, v)):
+        raise ValueError(f"{where}: q, k and v must be [B, H, S, d]")
+    chk(q[:0], "q", (_BF16,))
+    (B, H, Sq, d_k), (_, H_kv, Sk, d_v) = q.shape, v.shape
+    a = mla_attn_args()
+    a.q = _attn_rows(chk, q, "q", (B, H, Sq, d_k))
+    a.k = _attn_rows(chk, k, "k", (B, H_kv, Sk, d_k))
+    a.v = _attn_rows(chk, v, "v", (B, H_kv, Sk, d_v))
+    a.out = _attn_rows(chk, out, "out", (B, H, Sq, d_v))
+    a.lse = _opt(chk, lse, "lse", _FP32, B * H * Sq)
+    a.B, a.H, a.H_kv, a.Sq, a.Sk, a.d_k, a.d_v = B, H, H_kv, Sq, Sk, d_k, d_v
+    a.scale, a.cap = scale, cap
+    a.slopes = _opt(chk, slopes, "slopes", _FP32, H)
+    a.spans = _opt(chk, spans, "spans", _I32, B * Sq * 2)
+    a.at = _opt(chk, at, "at", _I32, B * Sq)
+    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
+    return chk, a
+
+
+def _size_on(device, fn, *args) -> int:
+    """A workspace size on `device`: plans ask for its compute units."""
+    if device.type != "cuda" or device.index == torch._C._cuda_getDevice():
+        return int(fn(*args))
+    with torch.cuda.device(device):
+        return int(fn(*args))
+
+
+def mla_attn_fwd_workspace_size(q, k, v, out, *, scale, cap=0.0, slopes=None, spans=None, at=None, lse=None) -> int:
+    chk, a = _attn_args("mla_attn_fwd", q, k, v, out, lse, scale, cap, slopes, spans, at, None)
+    return _size_on(chk.device, lib().mla_attn_fwd_workspace_size, ctypes.byref(a))
+
+
+def mla_attn_fwd(q, k, v, out, *, scale, lse=None, cap=0.0, slopes=None, spans=None, at=None, workspace=None,
+                 stream=None):
+    """Attention: q bf16 [B,H,Sq,d_k], k [B,H_kv,Sk,d_k], v [B,H_kv,Sk,d_v] -> out bf16 [B,H,Sq,d_v] and lse fp32
+    [B,H,Sq] (None: not wanted). Rows are dense, all other strides free (a transposed token-major tensor will do).
+    cap: scores go through cap tanh(./cap); slopes fp32 [H]: minus slope times distance; spans and at from
+    mla_attn_spans (None: every key). workspace: mla_attn_fwd_workspace_size() bytes (None if that is 0)."""
+    chk, a = _attn_args("mla_attn_fwd", q, k, v, out, lse, scale, cap, slopes, spans, at, workspace)
+    _call(chk.where, chk.device, stream, lib().mla_attn_fwd, ctypes.byref(a))
+
+
+def _attn_bwd_args(dout, q, k, v, out, lse, dq, dk, dv, scale, cap, slopes, spans, at, workspace):
+    a = mla_attn_bwd_args()
+    chk, a.fwd = _attn_args("mla_attn_bwd", q, k, v, out, lse, scale, cap, slopes, spans, at, None)
+    a.dout = _attn_rows(chk, dout, "dout", tuple(out.shape))
+    a.dq = _attn_rows(chk, dq, "dq", tuple(q.shape))
+    a.dk = _attn_rows(chk, dk, "dk", tuple(k.shape))
+    a.dv = _attn_rows(chk, dv, "dv", tuple(v.shape))
+    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
+    return chk, a
+
+
+def mla_attn_bwd_workspace_size(dout, q, k, v, out, lse, dq, dk, dv, *, scale, cap=0.0, slopes=None, spans=None,
+                                at=None) -> int:
+    chk, a = _attn_bwd_args(dout, q, k, v, out, lse, dq, dk, dv, scale, cap, slopes, spans, at, None)
+    return _size_on(chk.device, lib().mla_attn_bwd_workspace_size, ctypes.byref(a))
+
+
+def mla_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, scale, cap=0.0, slopes=None, spans=None, at=None,
+                 workspace=None, stream=None):
+    """Backward of mla_attn_fwd from its out and lse: dout like out -> dq like q, dk like k, dv like v (heads that
+    share a key head add up). Strides are free as in the forward: dq may be the token-major [T,H,D] that mla_qup_bwd
+    reads. workspace: mla_attn_bwd_workspace_size() bytes."""
+    chk, a = _attn_bwd_args(dout, q, k, v, out, lse, dq, dk, dv, scale, cap, slopes, spans, at, workspace)
+    _call(chk.where, chk.device, stream, lib().mla_attn_bwd, ctypes.byref(a))

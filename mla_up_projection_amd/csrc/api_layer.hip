@@ -1,0 +1,470 @@
+// C ABI of the operators around the up-projection in a layer (RMS norm, int8
+// projection, attention over documents): host-side validation, then the launches.
+// Argument meanings and error behaviour are stated in include/mla_qup.h. As in
+// api.hip, validation dereferences no device pointer, so every error path runs
+// without a GPU; nothing here allocates.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "api_checks.h"
+#include "internal_layer.h"
+
+namespace {
+
+struct LayerRanges {
+  Range in[16], out[16];
+  int nin = 0, nout = 0;
+  void input(const void* p, size_t bytes) {
+    if (p && bytes) in[nin++] = rng(p, bytes);
+  }
+  void output(const void* p, size_t bytes) {
+    if (p && bytes) out[nout++] = rng(p, bytes);
+  }
+  bool overlap() const {
+    const auto meet = [](const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; };
+    for (int i = 0; i < nout; ++i) {
+      for (int j = 0; j < nin; ++j)
+        if (meet(out[i], in[j])) return true;
+      for (int j = i + 1; j < nout; ++j)
+        if (meet(out[i], out[j])) return true;
+    }
+    return false;
+  }
+};
+
+bool float_type(int32_t t) { return t == MLA_DTYPE_BF16 || t == MLA_DTYPE_FP32; }
+size_t float_size(int32_t t) { return t == MLA_DTYPE_FP32 ? 4 : 2; }
+size_t span_bytes(int64_t T, int64_t ld, int64_t K, size_t es) { return T ? ((size_t)(T - 1) * ld + K) * es : 0; }
+
+mla_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return MLA_OK;
+  if (ws == nullptr || have < need) return MLA_EWORKSPACE;
+  return aligned(ws, 256) ? MLA_OK : MLA_EINVAL;
+}
+
+constexpr int32_t kNormMaxK = 32768;
+
+bool norm_sizes(int64_t T, int32_t K) {
+  return T >= 0 && T <= (int64_t)INT32_MAX && K >= 8 && K <= kNormMaxK && K % 8 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_rmsnorm_fwd(const mla_rmsnorm_args* a, void* stream) {
+  if (a == nullptr || !norm_sizes(a->T, a->K)) return MLA_EINVAL;
+  if (a->ld_x < a->K || a->ld_x % 8 || a->ld_x > ((int64_t)1 << 40)) return MLA_EINVAL;
+  if (!(a->eps >= 0) || !isfinite(a->eps)) return MLA_EINVAL;
+  if (a->T == 0) return MLA_OK;
+  if (!a->y && !a->codes && !a->h && !a->rstd) return MLA_EINVAL;
+  if ((a->res || a->h) && !float_type(a->res_dtype)) return MLA_EINVAL;
+  if (a->gamma && !float_type(a->gamma_dtype)) return MLA_EINVAL;
+  if (a->h && !a->res) return MLA_EINVAL;
+  if (a->codes) {
+    if (a->q_dtype != MLA_DTYPE_MXFP8 && a->q_dtype != MLA_DTYPE_INT8) return MLA_EINVAL;
+    if (a->q_dtype == MLA_DTYPE_MXFP8 && a->K % 32) return MLA_EINVAL;
+  }
+  if ((a->codes == nullptr) != (a->scales == nullptr)) return MLA_EINVAL;
+  const bool i8 = a->q_dtype == MLA_DTYPE_INT8;
+  if (!a->x || !aligned(a->x, 16) || !aligned(a->res, 16) || !aligned(a->gamma, 16) || !aligned(a->h, 16) ||
+      !aligned(a->y, 16) || !aligned(a->codes, 8) || !aligned(a->rstd, 4) || (a->scales && i8 && !aligned(a->scales, 4)))
+    return MLA_EINVAL;
+  const size_t n = (size_t)a->T * a->K;
+  LayerRanges r;
+  r.input(a->x, span_bytes(a->T, a->ld_x, a->K, 2));
+  r.input(a->res, n * float_size(a->res_dtype));
+  r.input(a->gamma, (size_t)a->K * float_size(a->gamma_dtype));
+  r.output(a->h, n * float_size(a->res_dtype));
+  r.output(a->rstd, (size_t)a->T * 4);
+  r.output(a->y, n * 2);
+  r.output(a->codes, n);
+  r.output(a->scales, i8 ? (size_t)a->T * 4 : n / 32);
+  if (r.overlap()) return MLA_EALIAS;
+  mla::NormParams p{};
+  p.x = (const uint16_t*)a->x;
+  p.ld_x = a->ld_x;
+  p.res = a->res;
+  p.res_f32 = a->res_dtype == MLA_DTYPE_FP32;
+  p.gamma = a->gamma;
+  p.gamma_f32 = a->gamma_dtype == MLA_DTYPE_FP32;
+  p.eps = a->eps;
+  p.T = a->T;
+  p.K = a->K;
+  p.h = a->h;
+  p.rstd = a->rstd;
+  p.y = (uint16_t*)a->y;
+  p.q_dtype = a->q_dtype;
+  p.codes = (uint8_t*)a->codes;
+  p.scales = a->scales;
+  return launched(mla::launch_rmsnorm(p, (hipStream_t)stream));
+}
+
+size_t mla_rmsnorm_bwd_workspace_size(int64_t T, int32_t K) {
+  if (!norm_sizes(T, K)) return 0;
+  return (size_t)mla::rmsnorm_bwd_groups(T, K) * K * 4;
+}
+
+mla_status mla_rmsnorm_bwd(const mla_rmsnorm_bwd_args* a, void* stream) {
+  if (a == nullptr || !norm_sizes(a->T, a->K)) return MLA_EINVAL;
+  if (a->ld_h < a->K || a->ld_h % 8 || a->ld_h > ((int64_t)1 << 40) || !float_type(a->h_dtype)) return MLA_EINVAL;
+  if (a->gamma && !float_type(a->gamma_dtype)) return MLA_EINVAL;
+  if (a->T == 0 && !a->dgamma) return MLA_OK;
+  if (!a->dx && !a->dres && !a->dgamma) return MLA_EINVAL;
+  if (a->T > 0 && (!a->dy || !a->h || !a->rstd)) return MLA_EINVAL;
+  if (!aligned(a->dy, 16) || !aligned(a->h, 16) || !aligned(a->rstd, 4) || !aligned(a->gamma, 16) || !aligned(a->dh, 16) ||
+      !aligned(a->dx, 16) || !aligned(a->dres, 16) || !aligned(a->dgamma, 4))
+    return MLA_EINVAL;
+  const size_t need = a->dgamma ? mla_rmsnorm_bwd_workspace_size(a->T, a->K) : 0;
+  mla_status st = check_ws(a->workspace, a->workspace_bytes, need);
+  if (st) return st;
+  const size_t n = (size_t)a->T * a->K, es = float_size(a->h_dtype);
+  LayerRanges r;
+  r.input(a->dy, n * 2);
+  r.input(a->h, span_bytes(a->T, a->ld_h, a->K, es));
+  r.input(a->rstd, (size_t)a->T * 4);
+  r.input(a->gamma, (size_t)a->K * float_size(a->gamma_dtype));
+  r.input(a->dh, n * es);
+  r.output(a->dx, n * 2);
+  r.output(a->dres, n * 4);
+  r.output(a->dgamma, (size_t)a->K * 4);
+  r.output(a->workspace, need);
+  if (r.overlap()) return MLA_EALIAS;
+  mla::NormBwdParams p{};
+  p.dy = (const uint16_t*)a->dy;
+  p.h = a->h;
+  p.ld_h = a->ld_h;
+  p.h_f32 = a->h_dtype == MLA_DTYPE_FP32;
+  p.rstd = a->rstd;
+  p.gamma = a->gamma;
+  p.gamma_f32 = a->gamma_dtype == MLA_DTYPE_FP32;
+  p.dh = a->dh;
+  p.T = a->T;
+  p.K = a->K;
+  p.dx = (uint16_t*)a->dx;
+  p.dres = a->dres;
+  p.dgamma = a->dgamma;
+  p.part = (float*)a->workspace;
+  p.groups = mla::rmsnorm_bwd_groups(a->T, a->K);
+  return launched(mla::launch_rmsnorm_bwd(p, (hipStream_t)stream));
+}
+
+mla_status int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
+                         float* scales, void* stream) {
+  if (!float_type(x_dtype)) return MLA_EINVAL;
+  if (rows < 0 || rows > ((int64_t)1 << 24) || cols <= 0 || cols % 8 || ld < cols || ld > ((int64_t)1 << 40)) return MLA_EINVAL;
+  if (rows == 0) return MLA_OK;
+  if (rows > ((int64_t)1 << 36) / cols) return MLA_EINVAL;
+  const size_t es = float_size(x_dtype);
+  if (!x || !codes || !scales) return MLA_EINVAL;
+  if (!aligned(x, 16) || (size_t)ld * es % 16 || !aligned(codes, 8) || !aligned(scales, 4)) return MLA_EINVAL;
+  LayerRanges r;
+  r.input(x, span_bytes(rows, ld, cols, es));
+  r.output(codes, (size_t)rows * cols);
+  r.output(scales, (size_t)rows * 4);
+  if (r.overlap()) return MLA_EALIAS;
+  return launched(mla::launch_int8_quantize(x, x_dtype == MLA_DTYPE_FP32, rows, cols, ld, codes, scales, (hipStream_t)stream));
+}
+
+mla_status mla_qup_fwd_i8(const mla_qup_i8_args* a, void* stream) {
+  if (a == nullptr) return MLA_EINVAL;
+  mla_status st = check_head_shape(a->K, a->H, a->d_nope, a->d_rope);
+  if (st) return st;
+  if (a->K % 64 || a->K > 65536) return MLA_EINVAL;
+  int64_t max_pos = 0;
+  if ((st = check_tokens(a->tokens, &max_pos))) return st;
+  if (a->out_dtype != MLA_DTYPE_BF16 && a->out_dtype != MLA_DTYPE_MXFP8) return MLA_EINVAL;
+  const int64_t T = a->tokens.T, D = (int64_t)a->d_nope + a->d_rope, N = a->H * D;
+  const bool mx = a->out_dtype == MLA_DTYPE_MXFP8;
+  if ((a->out_scales != nullptr) != mx && T > 0) return MLA_EINVAL;
+  // given positions may be anything: one outside the table makes NaN
+  if ((st = check_rope(a->rope, a->d_rope, a->positions ? 0 : max_pos))) return st;
+  if (N >= ((int64_t)1 << 29) || N * a->K > (int64_t)UINT32_MAX || T * a->K > (int64_t)UINT32_MAX) return MLA_EUNSUPPORTED;
+  if (T == 0) return MLA_OK;
+  if (!a->x || !a->x_scales || !a->w || !a->w_scales || !a->out) return MLA_EINVAL;
+  if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->out, 16) || !aligned(a->bias, 8) || !aligned(a->x_scales, 4) ||
+      !aligned(a->w_scales, 4) || !aligned(a->positions, 4))
+    return MLA_EINVAL;
+  LayerRanges r;
+  r.input(a->x, (size_t)T * a->K);
+  r.input(a->x_scales, (size_t)T * 4);
+  r.input(a->w, (size_t)N * a->K);
+  r.input(a->w_scales, (size_t)N * 4);
+  r.input(a->bias, (size_t)N * 2);
+  r.input(a->positions, (size_t)T * 4);
+  if (a->tokens.fmt == MLA_FMT_THD) r.input(a->tokens.cu_seqlens, ((size_t)a->tokens.nseq + 1) * 4);
+  r.input(a->rope.cos, rope_bytes(a->rope, a->d_rope));
+  r.input(a->rope.sin, rope_bytes(a->rope, a->d_rope));
+  r.output(a->out, (size_t)T * N * (mx ? 1 : 2));
+  if (mx) r.output(a->out_scales, (size_t)T * N / 32);
+  if (r.overlap()) return MLA_EALIAS;
+  mla::I8Params p{};
+  p.x = a->x;
+  p.xs = a->x_scales;
+  p.w = a->w;
+  p.ws = a->w_scales;
+  p.bias = (const uint16_t*)a->bias;
+  p.T = T;
+  p.K = a->K;
+  p.N = (int)N;
+  p.H = a->H;
+  p.D = (int)D;
+  p.d_nope = a->d_nope;
+  p.d_rope = a->d_rope;
+  fill_token_map(a->tokens, p.fmt, p.B, p.S, p.cu, p.nseq);
+  p.positions = a->positions;
+  p.cos = a->rope.cos;
+  p.sin = a->rope.sin;
+  p.rope_rows = a->rope.rows;
+  p.rope_pairs = a->rope.pairs;
+  p.out_mx = mx;
+  p.out = a->out;
+  p.out_scales = a->out_scales;
+  return launched(mla::launch_qup_i8(p, (hipStream_t)stream));
+}
+
+mla_status mla_attn_spans(const mla_attn_spans_args* a, void* stream) {
+  if (a == nullptr || a->B < 1 || a->Sq < 0 || a->Sk < 0 || a->Sq > (1 << 27) || a->Sk > (1 << 27)) return MLA_EINVAL;
+  if ((int64_t)a->B * a->Sq > (int64_t)INT32_MAX / 2) return MLA_EINVAL;
+  if (a->window < 0 || (a->causal != 0 && a->causal != 1)) return MLA_EINVAL;
+  const bool packed = a->cu_q != nullptr;
+  if (packed ? a->B != 1 || a->nseq < 1 || a->len_q || a->len_k : a->cu_k != nullptr) return MLA_EINVAL;
+  if (packed && !a->cu_k && a->Sq != a->Sk) return MLA_EINVAL;
+  if (!aligned(a->spans, 8) || !aligned(a->at, 4) || !aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_q, 4) ||
+      !aligned(a->len_k, 4) || !aligned(a->prefix, 4))
+    return MLA_EINVAL;
+  const size_t rows = (size_t)a->B * a->Sq, n = packed ? (size_t)a->nseq : (size_t)a->B;
+  if (rows == 0) return MLA_OK;
+  if (!a->spans) return MLA_EINVAL;
+  LayerRanges r;
+  r.input(a->cu_q, (n + 1) * 4);
+  r.input(a->cu_k, (n + 1) * 4);
+  r.input(a->len_q, n * 4);
+  r.input(a->len_k, n * 4);
+  r.input(a->prefix, n * 4);
+  r.output(a->spans, rows * 8);
+  r.output(a->at, rows * 4);
+  if (r.overlap()) return MLA_EALIAS;
+  mla::SpanParams p{};
+  p.spans = a->spans;
+  p.at = a->at;
+  p.B = a->B;
+  p.Sq = a->Sq;
+  p.Sk = a->Sk;
+  p.nseq = packed ? a->nseq : 0;
+  p.cu_q = a->cu_q;
+  p.cu_k = a->cu_k ? a->cu_k : a->cu_q;
+  p.len_q = a->len_q;
+  p.len_k = a->len_k;
+  p.prefix = a->prefix;
+  p.causal = a->causal;
+  p.window = a->window;
+  return launched(mla::launch_attn_spans(p, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// One side of the attention: its sizes and rows.
+struct Side {
+  const mla_attn_rows* rows;
+  int64_t B, H, S, d;
+  int64_t last() const {  // elements from the first to behind the last
+    return B && H && S ? (B - 1) * rows->stride_b + (H - 1) * rows->stride_h + (S - 1) * rows->stride_s + d : 0;
+  }
+};
+
+// Whether rows of `width` elements with these strides and counts lie apart: each
+// stride steps over what lies inside it.
+bool rows_apart(const mla_attn_rows& r, int64_t B, int64_t H, int64_t S, int64_t width) {
+  struct Step {
+    int64_t stride, n;
+  } st[3] = {{r.stride_b, B}, {r.stride_h, H}, {r.stride_s, S}};
+  std::sort(st, st + 3, [](const Step& a, const Step& b) { return a.stride < b.stride; });
+  for (const Step& t : st) {
+    if (t.n <= 1) continue;
+    if (t.stride < width) return false;
+    width += (t.n - 1) * t.stride;
+  }
+  return true;
+}
+
+mla_status check_rows(const Side& s, bool out) {
+  const mla_attn_rows& r = *s.rows;
+  for (int64_t v : {r.stride_b, r.stride_h, r.stride_s})
+    if (v < 0 || v % 8 || v > ((int64_t)1 << 40)) return MLA_EINVAL;
+  if (r.stride_s >= (1 << 22)) return MLA_EUNSUPPORTED;
+  if (s.last() == 0) return MLA_OK;
+  if (!r.p || !aligned(r.p, 16)) return MLA_EINVAL;
+  return out && !rows_apart(r, s.B, s.H, s.S, s.d) ? MLA_EINVAL : MLA_OK;
+}
+
+// Whether two sets of rows share memory. Slices of the same wider rows (equal
+// strides, one beside the other) do not.
+bool rows_meet(Side a, Side b) {
+  if (!a.last() || !b.last()) return false;
+  if (reinterpret_cast<uintptr_t>(a.rows->p) > reinterpret_cast<uintptr_t>(b.rows->p)) std::swap(a, b);
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.rows->p), pb = reinterpret_cast<uintptr_t>(b.rows->p);
+  if (pb - pa >= (size_t)a.last() * 2) return false;
+  const mla_attn_rows &x = *a.rows, &y = *b.rows;
+  const auto same = [](int64_t s, int64_t t, int64_t n, int64_t m) { return s == t || n <= 1 || m <= 1; };
+  const int64_t apart = (int64_t)(pb - pa) / 2;
+  if (!same(x.stride_b, y.stride_b, a.B, b.B) || !same(x.stride_h, y.stride_h, a.H, b.H) ||
+      !same(x.stride_s, y.stride_s, a.S, b.S) || apart < a.d)
+    return true;
+  const mla_attn_rows both{nullptr, std::max(x.stride_b, y.stride_b), std::max(x.stride_h, y.stride_h),
+                           std::max(x.stride_s, y.stride_s)};
+  return !rows_apart(both, std::max(a.B, b.B), std::max(a.H, b.H), std::max(a.S, b.S), apart + b.d);
+}
+
+mla_status check_layer_attn(const mla_attn_args* a) {
+  if (a == nullptr || a->B < 1 || a->H < 1 || a->H_kv < 1 || a->H % a->H_kv) return MLA_EINVAL;
+  if (a->Sq < 0 || a->Sk < 0 || a->Sq > (1 << 27) || a->Sk > (1 << 27)) return MLA_EINVAL;
+  if (a->d_k < 8 || a->d_v < 8 || a->d_k % 8 || a->d_v % 8) return MLA_EINVAL;
+  if (a->d_k > 192 || a->d_v > 128) return MLA_EUNSUPPORTED;
+  if (!isfinite(a->scale) || !isfinite(a->cap) || !(a->cap >= 0)) return MLA_EINVAL;
+  if (!isfinite(a->scale * 1.4427f) || !isfinite(a->cap * 1.4427f)) return MLA_EINVAL;
+  if (a->cap > 0 && !isfinite(2 * a->scale / a->cap * 1.4427f)) return MLA_EINVAL;
+  const int64_t tiles = (int64_t)a->B * a->H * ((std::max(a->Sq, a->Sk) + 31) / 32);
+  if (tiles >= (1 << 22)) return MLA_EUNSUPPORTED;
+  return MLA_OK;
+}
+
+mla_status check_attn_sides(const mla_attn_args* a, bool backward) {
+  if (!aligned(a->lse, 4) || !aligned(a->slopes, 4) || !aligned(a->spans, 8) || !aligned(a->at, 4)) return MLA_EINVAL;
+  const Side sides[4] = {{&a->q, a->B, a->H, a->Sq, a->d_k},
+                         {&a->k, a->B, a->H_kv, a->Sk, a->d_k},
+                         {&a->v, a->B, a->H_kv, a->Sk, a->d_v},
+                         {&a->out, a->B, a->H, a->Sq, a->d_v}};
+  for (int i = 0; i < 4; ++i)
+    if (mla_status st = check_rows(sides[i], i == 3 && !backward)) return st;
+  return MLA_OK;
+}
+
+// Outputs of an attention call against its inputs and each other; the ranges hold
+// what is not rows.
+bool attn_alias(LayerRanges& r, const mla_attn_args* a, std::initializer_list<Side> in, std::initializer_list<Side> out) {
+  r.input(a->slopes, (size_t)a->H * 4);
+  r.input(a->spans, (size_t)a->B * a->Sq * 8);
+  r.input(a->at, (size_t)a->B * a->Sq * 4);
+  if (r.overlap()) return true;
+  const auto range = [](const Side& s) { return rng(s.rows->p, (size_t)s.last() * 2); };
+  const auto meet = [](const Range& x, const Range& y) { return x.lo < y.hi && y.lo < x.hi && x.lo < x.hi && y.lo < y.hi; };
+  for (const Side* o = out.begin(); o != out.end(); ++o) {
+    for (int k = 0; k < r.nin; ++k)
+      if (meet(range(*o), r.in[k])) return true;
+    for (int k = 0; k < r.nout; ++k)
+      if (meet(range(*o), r.out[k])) return true;
+    for (const Side& i : in)
+      if (rows_meet(*o, i)) return true;
+    for (const Side* q = o + 1; q != out.end(); ++q)
+      if (rows_meet(*o, *q)) return true;
+  }
+  for (const Side& i : in)
+    for (int k = 0; k < r.nout; ++k)
+      if (meet(range(i), r.out[k])) return true;
+  return false;
+}
+
+mla::AttnRows rows_of(const mla_attn_rows& r) { return mla::AttnRows{(uint16_t*)r.p, r.stride_b, r.stride_h, r.stride_s}; }
+
+mla::LayerAttnParams attn_params(const mla_attn_args* a) {
+  mla::LayerAttnParams p{};
+  p.q = rows_of(a->q);
+  p.k = rows_of(a->k);
+  p.v = rows_of(a->v);
+  p.out = rows_of(a->out);
+  p.lse = a->lse;
+  p.B = a->B;
+  p.H = a->H;
+  p.H_kv = a->H_kv;
+  p.group = a->H / a->H_kv;
+  p.Sq = a->Sq;
+  p.Sk = a->Sk;
+  p.d_k = a->d_k;
+  p.d_v = a->d_v;
+  p.scale = a->scale;
+  p.cap = a->cap;
+  p.slopes = a->slopes;
+  p.spans = a->spans;
+  p.at = a->at;
+  return p;
+}
+
+int attn_cus() {
+  const int n = mla::device_cu_count();
+  return n > 0 ? n : 256;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_attn_fwd_workspace_size(const mla_attn_args* a) {
+  if (check_layer_attn(a)) return 0;
+  return mla::plan_layer_attn(a->B, a->H, a->Sq, a->Sk, a->d_v, attn_cus()).total;
+}
+
+mla_status mla_attn_fwd(const mla_attn_args* a, void* stream) {
+  mla_status st = check_layer_attn(a);
+  if (st || (st = check_attn_sides(a, false))) return st;
+  if (a->Sq == 0) return MLA_OK;
+  const mla::AttnPlanFwd plan = mla::plan_layer_attn(a->B, a->H, a->Sq, a->Sk, a->d_v, attn_cus());
+  if ((st = check_ws(a->workspace, a->workspace_bytes, plan.total))) return st;
+  LayerRanges r;
+  r.output(a->lse, (size_t)a->B * a->H * a->Sq * 4);
+  r.output(a->workspace, plan.total);
+  if (attn_alias(r, a,
+                 {{&a->q, a->B, a->H, a->Sq, a->d_k}, {&a->k, a->B, a->H_kv, a->Sk, a->d_k}, {&a->v, a->B, a->H_kv, a->Sk, a->d_v}},
+                 {{&a->out, a->B, a->H, a->Sq, a->d_v}}))
+    return MLA_EALIAS;
+  mla::LayerAttnParams p = attn_params(a);
+  p.plan = plan;
+  p.part_o = (float*)((uint8_t*)a->workspace + plan.part_o);
+  p.part_ml = (float*)((uint8_t*)a->workspace + plan.part_ml);
+  return launched(mla::launch_layer_attn(p, (hipStream_t)stream));
+}
+
+size_t mla_attn_bwd_workspace_size(const mla_attn_bwd_args* a) {
+  if (a == nullptr || check_layer_attn(&a->fwd)) return 0;
+  return mla::plan_layer_attn_bwd(a->fwd.B, a->fwd.H, a->fwd.Sq).total;
+}
+
+mla_status mla_attn_bwd(const mla_attn_bwd_args* a, void* stream) {
+  if (a == nullptr) return MLA_EINVAL;
+  const mla_attn_args* f = &a->fwd;
+  mla_status st = check_layer_attn(f);
+  if (st || (st = check_attn_sides(f, true))) return st;
+  if (f->Sq > 0 && !f->lse) return MLA_EINVAL;
+  const Side dout{&a->dout, f->B, f->H, f->Sq, f->d_v}, dq{&a->dq, f->B, f->H, f->Sq, f->d_k},
+      dk{&a->dk, f->B, f->H_kv, f->Sk, f->d_k}, dv{&a->dv, f->B, f->H_kv, f->Sk, f->d_v};
+  if ((st = check_rows(dout, false)) || (st = check_rows(dq, true)) || (st = check_rows(dk, true)) ||
+      (st = check_rows(dv, true)))
+    return st;
+  const mla::AttnBwdPlan plan = mla::plan_layer_attn_bwd(f->B, f->H, f->Sq);
+  if ((st = check_ws(a->workspace, a->workspace_bytes, plan.total))) return st;
+  LayerRanges r;
+  r.input(f->lse, (size_t)f->B * f->H * f->Sq * 4);
+  r.output(a->workspace, plan.total);
+  if (attn_alias(r, f,
+                 {{&f->q, f->B, f->H, f->Sq, f->d_k}, {&f->k, f->B, f->H_kv, f->Sk, f->d_k}, {&f->v, f->B, f->H_kv, f->Sk, f->d_v},
+                  {&f->out, f->B, f->H, f->Sq, f->d_v}, dout},
+                 {dq, dk, dv}))
+    return MLA_EALIAS;
+  mla::LayerAttnBwdParams p{};
+  p.f = attn_params(f);
+  p.dout = rows_of(a->dout);
+  p.dq = rows_of(a->dq);
+  p.dk = rows_of(a->dk);
+  p.dv = rows_of(a->dv);
+  p.plan = plan;
+  p.records = (float*)((uint8_t*)a->workspace + plan.records);
+  p.tiles = (int32_t*)((uint8_t*)a->workspace + plan.tiles);
+  return launched(mla::launch_layer_attn_bwd(p, (hipStream_t)stream));
+}
+
+}  // extern "C"

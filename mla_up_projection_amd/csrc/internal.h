@@ -46,6 +46,11 @@ struct FwdParams {
   int64_t split_stride;
   void* out;
   uint8_t* out_scales;
+  // int8 operands: scales of the rows of X and of W, and positions in place of
+  // the token format's (or nullptr)
+  const float* x_row_scales;
+  const float* w_row_scales;
+  const int32_t* positions;
 };
 
 struct BwdParams {
@@ -130,6 +135,7 @@ hipError_t launch_mxfp8_quantize(const void* x, int x_fp32, int64_t rows, int64_
                                  hipStream_t stream);
 hipError_t launch_qup_fwd_bf16(const FwdParams& p, hipStream_t stream);
 hipError_t launch_qup_fwd_mx(const FwdParams& p, hipStream_t stream);
+hipError_t launch_qup_fwd_i8(const FwdParams& p, hipStream_t stream);  // K % 64 == 0
 // MXFP8 x MXFP8 product out[t][n] = sum_k X[t][k] W[n][k] in the plain form
 // (FwdParams: x, xs, w, ws, T, K, N, mx_fp8_mfma, out, out_f32, k_splits,
 // split_stride; K % 128 == 0).

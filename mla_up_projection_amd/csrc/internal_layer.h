@@ -1,0 +1,138 @@
+// Internal launch interface of the operators around the up-projection in a
+// layer: the RMS norm in front of it, the projection in 8-bit integers, and
+// attention over documents with its backward. Every launcher assumes that
+// api_layer.hip has validated its arguments.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mla_qup.h"
+
+namespace mla {
+
+struct NormParams {
+  const uint16_t* x;
+  int64_t ld_x;
+  const void* res;        // nullptr: no residual
+  int res_f32;
+  const void* gamma;      // nullptr: ones
+  int gamma_f32;
+  float eps;
+  int64_t T;
+  int K;
+  void* h;
+  float* rstd;
+  uint16_t* y;
+  int q_dtype;            // MLA_DTYPE_MXFP8 or MLA_DTYPE_INT8 where codes are wanted
+  uint8_t* codes;
+  void* scales;
+};
+hipError_t launch_rmsnorm(const NormParams& p, hipStream_t stream);
+
+struct NormBwdParams {
+  const uint16_t* dy;
+  const void* h;
+  int64_t ld_h;
+  int h_f32;
+  const float* rstd;
+  const void* gamma;
+  int gamma_f32;
+  const void* dh;         // in h's type, or nullptr
+  int64_t T;
+  int K;
+  uint16_t* dx;
+  float* dres;
+  float* dgamma;
+  float* part;            // [groups, K]
+  int groups;
+};
+// Workgroups of the backward: each sums dgamma over its own rows.
+int rmsnorm_bwd_groups(int64_t T, int K);
+hipError_t launch_rmsnorm_bwd(const NormBwdParams& p, hipStream_t stream);
+
+hipError_t launch_int8_quantize(const void* x, int x_f32, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
+                                float* scales, hipStream_t stream);
+
+struct I8Params {
+  const int8_t* x;
+  const float* xs;
+  const int8_t* w;
+  const float* ws;
+  const uint16_t* bias;
+  int64_t T;
+  int K, N, H, D, d_nope, d_rope;
+  int fmt, B, S;
+  const int32_t* cu;
+  int nseq;
+  const int32_t* positions;
+  const float* cos;
+  const float* sin;
+  int rope_rows, rope_pairs;
+  int out_mx;
+  void* out;
+  uint8_t* out_scales;
+};
+hipError_t launch_qup_i8(const I8Params& p, hipStream_t stream);
+
+struct SpanParams {
+  int32_t* spans;         // [B, Sq, 2]
+  int32_t* at;            // [B, Sq] or nullptr
+  int B, Sq, Sk;
+  int nseq;               // packed: documents; 0: one sequence per batch row
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* len_q;
+  const int32_t* len_k;
+  const int32_t* prefix;
+  int causal, window;
+};
+hipError_t launch_attn_spans(const SpanParams& p, hipStream_t stream);
+
+// Rows of 16-bit elements: element (b, h, s, d) at p[b * sb + h * sh + s * ss + d].
+struct AttnRows {
+  uint16_t* p;
+  int64_t sb, sh, ss;
+};
+
+struct AttnPlanFwd {
+  int rows;               // query rows of a workgroup (32 per wave)
+  int tiles_q;
+  int splits;             // parts that a tile's keys are divided into
+  int64_t groups;         // workgroups before splitting: B * H * tiles_q
+  size_t part_o, part_ml, total;
+};
+
+struct LayerAttnParams {
+  AttnRows q, k, v, out;
+  float* lse;             // [B, H, Sq] or nullptr
+  int B, H, H_kv, group, Sq, Sk, d_k, d_v;
+  float scale, cap;
+  const float* slopes;
+  const int32_t* spans;   // nullptr: every key
+  const int32_t* at;      // nullptr: i + Sk - Sq
+  AttnPlanFwd plan;
+  float* part_o;          // [slot][row][d_v] sums that are not divided yet
+  float* part_ml;         // [slot][row][2] running maximum (a power of two's exponent) and sum
+};
+AttnPlanFwd plan_layer_attn(int B, int H, int Sq, int Sk, int d_v, int cus);
+hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream);
+
+// What the backward needs of 64 query rows of a head, in one record of floats and
+// ints: lse in powers of two, delta, lo, hi, and the rows' places (64 each).
+struct AttnBwdPlan {
+  int tiles_q;            // of 64 query rows
+  size_t records, tiles, total;
+};
+constexpr int ATTN_RECORD = 512;  // words of a record
+struct LayerAttnBwdParams {
+  LayerAttnParams f;
+  AttnRows dout, dq, dk, dv;
+  float* records;         // [B, H, tiles_q, ATTN_RECORD]
+  int32_t* tiles;         // [B, tiles_q, 4]: smallest lo, largest hi, largest lo, smallest hi
+  AttnBwdPlan plan;
+};
+AttnBwdPlan plan_layer_attn_bwd(int B, int H, int Sq);
+hipError_t launch_layer_attn_bwd(const LayerAttnBwdParams& p, hipStream_t stream);
+
+}  // namespace mla

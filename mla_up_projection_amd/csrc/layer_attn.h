@@ -1,0 +1,220 @@
+// What the forward and backward of attention over documents share: tiles of
+// rows in LDS and their fragments, the scores' form, and the slow but exact way
+// for single rows.
+//
+// A tile of R rows (keys, or queries) lies in LDS as blocks of 64 columns: block b
+// holds R rows of 128 bytes, 16-byte chunk c of row r at place c ^ swz(r). swz is
+// made so that both ways of reading a fragment meet every bank once:
+//   row_frag: 32 rows by 16 columns, a lane eight consecutive columns of a row
+//             (ds_read_b128; 16 rows and one chunk to a pass),
+//   col_frag: the transpose, a lane eight rows of a column (ds_read_b64_tr_b16;
+//             four rows by 64 bytes to a pass).
+// The matrix instruction's sum over rows takes them in the order in which the
+// lanes of a 32 x 32 result hold them, so that results become operands as they
+// lie: lane half g holds rows 8 u + 4 g + 0..3, u = 0, 1 of each 16.
+#pragma once
+
+#include "device_common.h"
+#include "internal_layer.h"
+
+namespace mla {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int tile_swz(int r) { return ((r & 2) << 1) | ((r >> 2) & 3); }
+
+typedef short la_i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) la_i16x4 la_lds_i16x4;
+typedef __attribute__((address_space(3))) const u32x4_t la_lds_u32x4;
+
+// Byte addresses of a lane's row fragments inside a tile: columns 16 j + 8 half,
+// j = 0..3 of a block, rows l % 32 (32 rows further: 4096 bytes).
+struct RowAddr {
+  uint32_t a[4];
+};
+__device__ __forceinline__ RowAddr row_addr(int lane) {
+  RowAddr r;
+  const int row = lane & 31, c0 = (lane >> 5) ^ tile_swz(row);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r.a[j] = (uint32_t)(row * 128 + ((c0 ^ (2 * j)) << 4));
+  return r;
+}
+// R rows per tile; step j counts 16 columns, kb 32 rows.
+template <int R>
+__device__ __forceinline__ bf16x8_t row_frag(uint32_t tile, const RowAddr& ra, int j, int kb) {
+  const uint32_t at = tile + ra.a[j & 3] + (uint32_t)((j >> 2) * R * 128 + kb * 4096);
+  return __builtin_bit_cast(bf16x8_t, *(la_lds_u32x4*)(uintptr_t)at);
+}
+
+// The same for transposed fragments: columns 32 n + l % 32, rows of step c (16).
+struct ColAddr {
+  uint32_t a[2][2];  // [first or second four rows][n odd]
+};
+__device__ __forceinline__ ColAddr col_addr(int lane) {
+  ColAddr r;
+  const int s = lane & 15, g = (lane >> 4) & 1, half = lane >> 5, e = s >> 2;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int row = 8 * u + 4 * half + e, chunk = 2 * g + ((s & 3) >> 1);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      r.a[u][n] = (uint32_t)(row * 128 + (((chunk + 4 * n) ^ tile_swz(row)) << 4) + (s & 1) * 8);
+  }
+  return r;
+}
+template <int R>
+__device__ __forceinline__ bf16x8_t col_frag(uint32_t tile, const ColAddr& ca, int n, int c) {
+  const uint32_t off = tile + (uint32_t)((n >> 1) * R * 128 + c * 2048);
+  const la_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_i16x4*)(uintptr_t)(ca.a[0][n & 1] + off));
+  const la_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_i16x4*)(uintptr_t)(ca.a[1][n & 1] + off));
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// Eight values of a 32 x 32 result as the operand of step c & 1 of its rows.
+__device__ __forceinline__ bf16x8_t pack_frag(const f32x16_t& s, int c) {
+  u32x4_t o;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = pack_bf16x2(s[8 * c + 2 * k], s[8 * c + 2 * k + 1]);
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+
+__device__ __forceinline__ f32x16_t zero16() {
+  f32x16_t z;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) z[r] = 0.0f;
+  return z;
+}
+
+__device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return reinterpret_cast<const uint16_t*>((uint64_t)hi << 32 | lo);
+}
+
+// Rows row0 .. row0 + R - 1 of `width` columns into a tile of W columns by direct
+// loads; WAVES waves share them. Rows from `rows` on repeat the last one and
+// columns from `width` on the row's first: what they hold meets zeros or is
+// masked. `base`: the first row of this batch entry and head.
+template <int R, int W, int WAVES>
+__device__ __forceinline__ void load_tile(const uint16_t* base, uint32_t stride_bytes, int row0, int rows, int width,
+                                          uint32_t tile, int wave, int lane) {
+  const uint16_t* from = uniform(base + (int64_t)row0 * (stride_bytes >> 1));
+  const int last = rows - 1 - row0;
+  constexpr int LOADS = R / 8 * (W / 64);
+#pragma unroll
+  for (int i = 0; i < (LOADS + WAVES - 1) / WAVES; ++i) {
+    const int j = i * WAVES + wave, b = j / (R / 8), r8 = (j % (R / 8)) * 8;
+    if (LOADS % WAVES == 0 || j < LOADS) {
+      const int r = r8 + (lane >> 3);
+      int c = 64 * b + 8 * ((lane & 7) ^ tile_swz(r));
+      if (c >= width) c = 0;
+      dma16(from, (uint32_t)min(r, last) * stride_bytes + 2 * c, __builtin_amdgcn_readfirstlane(tile + j * 1024));
+    }
+  }
+}
+
+// A lane's fragments of one row kept in registers: columns 16 j + 8 half of
+// the row, zeros past its width.
+template <int W>
+__device__ __forceinline__ void load_row_frags(const uint16_t* row, int width, int half, bf16x8_t (&f)[W / 16]) {
+#pragma unroll
+  for (int j = 0; j < W / 16; ++j) {
+    const int c = 16 * j + 8 * half;
+    u32x4_t v = {0, 0, 0, 0};
+    if (c < width) v = *reinterpret_cast<const u32x4_t*>(row + c);
+    f[j] = __builtin_bit_cast(bf16x8_t, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Scores. t = q . k scale; the scores are kept in powers of two (times log2 e).
+// ---------------------------------------------------------------------------
+struct ScoreForm {
+  float scale2;       // scale log2 e, or 2 scale log2 e / cap where there is a cap
+  float cap2;         // cap log2 e; 0: none
+  float slope2;       // slope log2 e of the head
+};
+__device__ __forceinline__ ScoreForm score_form(const LayerAttnParams& p, int h) {
+  ScoreForm f;
+  f.cap2 = p.cap * LOG2E;
+  f.scale2 = p.cap > 0 ? 2 * p.scale / p.cap * LOG2E : p.scale * LOG2E;
+  f.slope2 = p.slopes ? p.slopes[h] * LOG2E : 0.0f;
+  return f;
+}
+// tanh(x) from e = 2^(2 x log2 e): 1 - 2 / (1 + e), which is -1 and 1 at its ends.
+__device__ __forceinline__ float tanh_of(float x2) {
+  return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x2));
+}
+
+struct Span {
+  int lo, hi;
+};
+__device__ __forceinline__ Span row_span(const LayerAttnParams& p, int b, int i) {
+  if (i >= p.Sq) return Span{0, 0};
+  if (!p.spans) return Span{0, p.Sk};
+  const int2 s = *reinterpret_cast<const int2*>(p.spans + 2 * ((int64_t)b * p.Sq + i));
+  const int lo = max(s.x, 0), hi = min(s.y, p.Sk);
+  return lo < hi ? Span{lo, hi} : Span{0, 0};
+}
+__device__ __forceinline__ int row_place(const LayerAttnParams& p, int b, int i) {
+  return p.at ? p.at[(int64_t)b * p.Sq + i] : i + p.Sk - p.Sq;
+}
+
+__device__ __forceinline__ const uint16_t* row_of(const AttnRows& r, int b, int h, int64_t s) {
+  return r.p + b * r.sb + h * r.sh + s * r.ss;
+}
+
+// Workgroup g of a grid of n units, rounded up to a multiple of 8, on the chip's
+// eight dies: consecutive units share a die, and with it that die's L2. -1: none.
+__device__ __forceinline__ int die_order(uint32_t g, uint32_t n) {
+  const uint32_t per = (n + 7) / 8, u = (g & 7) * per + (g >> 3);
+  return u < n ? (int)u : -1;
+}
+
+// ---------------------------------------------------------------------------
+// The slow way, for rows whose result is not finite: what a row does not see takes
+// no part in it at all. A wave works on one row; 64 keys (queries) at a time, a
+// lane scores one of them, and then the lanes share the columns.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float dot_rows(const uint16_t* a, const uint16_t* b, int d) {
+  float s = 0;
+  for (int c = 0; c < d; c += 8) {
+    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(a + c), y = *reinterpret_cast<const u32x4_t*>(b + c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      s = __builtin_fmaf(bf16_bits_to_f32(x[k] & 0xFFFFu), bf16_bits_to_f32(y[k] & 0xFFFFu), s);
+      s = __builtin_fmaf(__uint_as_float(x[k] & 0xFFFF0000u), __uint_as_float(y[k] & 0xFFFF0000u), s);
+    }
+  }
+  return s;
+}
+
+// Score in powers of two of a query at place `at` and key j, and the derivative
+// of the cap there.
+__device__ __forceinline__ float score_of(const ScoreForm& f, float dot, int at, int j, float& slope) {
+  float s = dot * f.scale2;
+  slope = 1.0f;
+  if (f.cap2 > 0) {
+    const float t = tanh_of(s);
+    slope = 1.0f - t * t;
+    s = f.cap2 * t;
+  }
+  if (f.slope2 != 0) s -= f.slope2 * fabsf((float)(at - j));
+  return s;
+}
+
+__device__ __forceinline__ float la_wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ float la_wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+}  // namespace mla

@@ -1,0 +1,456 @@
+// Attention over documents, backward, for gfx950. With P = e^(s - lse) from the
+// forward's statistics and delta = rowsum(dout out):
+//   dV = P^T dO,  dS = P (dO V^T - delta) c',  dK = scale dS^T Q,  dQ = scale dS K.
+//
+// Two kernels, so that every sum stays in registers and no atomics are needed: one
+// owns 128 keys and goes through the queries that see them (dK and dV; heads that
+// share the keys one after the other), one owns 128 queries and goes through their
+// keys (dQ). Both make S and dP again, at 32 + 32 matrix products of the 26 that one
+// pass with atomics would take, but with results that do not depend on timing.
+// As in the forward the matrix unit's results, transposed by the choice of its
+// operands, are the operands of the next products as they lie.
+#include <algorithm>
+
+#include "layer_attn.h"
+
+namespace mla {
+namespace {
+
+constexpr int TT = 64;  // rows of a streamed tile: queries here, keys there
+
+// delta and the records of 64 query rows; the heads' first writes the tile's bounds.
+__global__ __launch_bounds__(256) void attn_bwd_prep_kernel(LayerAttnBwdParams p) {
+  const LayerAttnParams& f = p.f;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tq = blockIdx.x % p.plan.tiles_q, bh = blockIdx.x / p.plan.tiles_q;
+  const int b = bh / f.H, h = bh - b * f.H;
+  float* rec = p.records + (int64_t)blockIdx.x * ATTN_RECORD;
+  const int c = (lane & 15) * 8;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = 16 * wave + 4 * k + (lane >> 4), i = tq * TT + r;
+    float s = 0;
+    if (i < f.Sq && c < f.d_v) {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(row_of(p.dout, b, h, i) + c);
+      const u32x4_t y = *reinterpret_cast<const u32x4_t*>(row_of(f.out, b, h, i) + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        s = __builtin_fmaf(bf16_bits_to_f32(x[q] & 0xFFFFu), bf16_bits_to_f32(y[q] & 0xFFFFu), s);
+        s = __builtin_fmaf(__uint_as_float(x[q] & 0xFFFF0000u), __uint_as_float(y[q] & 0xFFFF0000u), s);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o);
+    if ((lane & 15) == 0) rec[TT + r] = s;
+  }
+  if (wave == 0) {
+    const int i = tq * TT + lane;
+    const Span sp = row_span(f, b, i);
+    // a row that sees nothing has weights 2^(s - inf) = 0
+    float l2 = __builtin_inff();
+    if (i < f.Sq) {
+      const float l = f.lse[(int64_t)bh * f.Sq + i];
+      l2 = l == -__builtin_inff() ? __builtin_inff() : l * LOG2E;
+    }
+    rec[lane] = l2;
+    rec[2 * TT + lane] = __int_as_float(sp.lo);
+    rec[3 * TT + lane] = __int_as_float(sp.hi);
+    rec[4 * TT + lane] = __int_as_float(f.slopes && i < f.Sq ? row_place(f, b, i) : 0);
+    if (h == 0) {
+      int lo = sp.lo < sp.hi ? sp.lo : INT32_MAX, hi = sp.hi, lo_all = sp.lo, hi_all = sp.hi;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        lo = min(lo, __shfl_xor(lo, o));
+        hi = max(hi, __shfl_xor(hi, o));
+        lo_all = max(lo_all, __shfl_xor(lo_all, o));
+        hi_all = min(hi_all, __shfl_xor(hi_all, o));
+      }
+      if (lane == 0) *reinterpret_cast<int4*>(p.tiles + 4 * ((int64_t)b * p.plan.tiles_q + tq)) = make_int4(lo, hi, lo_all, hi_all);
+    }
+  }
+}
+
+// What a query and a key give each other, the slow way.
+struct Weights {
+  float p, ds;
+};
+__device__ __forceinline__ Weights pair_weights(const LayerAttnBwdParams& p, const ScoreForm& f, int b, int h, int i, int j,
+                                                const float* rec) {
+  const int hk = h / p.f.group;
+  float slope;
+  const float s = score_of(f, dot_rows(row_of(p.f.q, b, h, i), row_of(p.f.k, b, hk, j), p.f.d_k),
+                           __float_as_int(rec[4 * TT + i % TT]), j, slope);
+  const float w = __builtin_amdgcn_exp2f(s - rec[i % TT]);
+  const float dp = dot_rows(row_of(p.dout, b, h, i), row_of(p.f.v, b, hk, j), p.f.d_v);
+  return Weights{w, w * (dp - rec[TT + i % TT]) * slope};
+}
+__device__ __forceinline__ const float* record(const LayerAttnBwdParams& p, int b, int h, int tq) {
+  return p.records + (((int64_t)b * p.f.H + h) * p.plan.tiles_q + tq) * ATTN_RECORD;
+}
+__device__ __forceinline__ void store_row(const AttnRows& to, int b, int h, int s, const float* o, int d, float times, int lane) {
+  uint16_t* out = const_cast<uint16_t*>(row_of(to, b, h, s));
+#pragma unroll
+  for (int c = 0; c < 3; ++c)
+    if (lane + 64 * c < d) out[lane + 64 * c] = (uint16_t)f32_to_bf16_bits(o[c] * times);
+}
+
+__device__ __forceinline__ void slow_dq(const LayerAttnBwdParams& p, int b, int h, int i, int lane) {
+  const Span sp = row_span(p.f, b, i);
+  const ScoreForm f = score_form(p.f, h);
+  const float* rec = record(p, b, h, i / TT);
+  float o[3] = {0, 0, 0};
+  for (int j0 = sp.lo; j0 < sp.hi; j0 += 64) {
+    Weights w{0, 0};
+    if (j0 + lane < sp.hi) w = pair_weights(p, f, b, h, i, j0 + lane, rec);
+    const int n = min(64, sp.hi - j0);
+    for (int r = 0; r < n; ++r) {
+      const float ds = __shfl(w.ds, r);
+      if (ds == 0 && __shfl(w.p, r) == 0) continue;
+      const uint16_t* k = row_of(p.f.k, b, h / p.f.group, j0 + r);
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+        if (lane + 64 * c < p.f.d_k) o[c] = __builtin_fmaf(ds, bf16_bits_to_f32(k[lane + 64 * c]), o[c]);
+    }
+  }
+  store_row(p.dq, b, h, i, o, p.f.d_k, p.f.scale, lane);
+}
+
+__device__ __forceinline__ void slow_dkdv(const LayerAttnBwdParams& p, int b, int hk, int j, int lane) {
+  float ok[3] = {0, 0, 0}, ov[3] = {0, 0, 0};
+  for (int h = hk * p.f.group; h < (hk + 1) * p.f.group; ++h) {
+    const ScoreForm f = score_form(p.f, h);
+    for (int tq = 0; tq < p.plan.tiles_q; ++tq) {
+      const int4 bounds = *reinterpret_cast<const int4*>(p.tiles + 4 * ((int64_t)b * p.plan.tiles_q + tq));
+      if (j < bounds.x || j >= bounds.y) continue;
+      const float* rec = record(p, b, h, tq);
+      const bool sees = j >= __float_as_int(rec[2 * TT + lane]) && j < __float_as_int(rec[3 * TT + lane]);
+      Weights w{0, 0};
+      if (sees) w = pair_weights(p, f, b, h, tq * TT + lane, j, rec);
+      uint64_t live = __builtin_amdgcn_ballot_w64(sees && !(w.p == 0 && w.ds == 0));
+      while (live) {
+        const int r = __builtin_ctzll(live);
+        live &= live - 1;
+        const float wp = __shfl(w.p, r), ds = __shfl(w.ds, r);
+        const uint16_t *q = row_of(p.f.q, b, h, tq * TT + r), *d = row_of(p.dout, b, h, tq * TT + r);
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (lane + 64 * c < p.f.d_k) ok[c] = __builtin_fmaf(ds, bf16_bits_to_f32(q[lane + 64 * c]), ok[c]);
+          if (lane + 64 * c < p.f.d_v) ov[c] = __builtin_fmaf(wp, bf16_bits_to_f32(d[lane + 64 * c]), ov[c]);
+        }
+      }
+    }
+  }
+  store_row(p.dk, b, hk, j, ok, p.f.d_k, p.f.scale, lane);
+  store_row(p.dv, b, hk, j, ov, p.f.d_v, 1.0f, lane);
+}
+
+// Columns of a lane's row out of the transposed sums, as bf16. Returns whether one
+// is not finite (nothing is stored then).
+template <int NB>
+__device__ __forceinline__ uint32_t not_finite(const f32x16_t (&o)[NB], int width, int half) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (32 * n + 8 * (r / 4) + 4 * half < width) odd |= abs_bits(o[n][r]) >= 0x7F800000u;
+  const u32x2_t x = swap_halves(odd, odd);
+  return x[0] | x[1];
+}
+template <int NB>
+__device__ __forceinline__ void store_cols(uint16_t* out, const f32x16_t (&o)[NB], int width, int half, bool live, float times) {
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[n][2 * k] * times, o[n][2 * k + 1] * times);
+    u32x2_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = swap_halves(w[k], w[4 + k]);
+    const int d = 32 * n + 16 * half;
+    if (live) {
+      if (d < width) *reinterpret_cast<u32x4_t*>(out + d) = u32x4_t{x[0][0], x[1][0], x[0][1], x[1][1]};
+      if (d + 8 < width) *reinterpret_cast<u32x4_t*>(out + d + 8) = u32x4_t{x[2][0], x[3][0], x[2][1], x[3][1]};
+    }
+  }
+}
+
+// P and dS out of products and dP. Element r of a block: row 8 (r / 4) + 4 half + r %
+// 4 of the streamed tile's 32, column the lane's own.
+template <bool EXTRA>
+__device__ __forceinline__ void weights(const ScoreForm& sf, f32x16_t& s, f32x16_t& dp, int r, int away, float lse2,
+                                        float delta, bool sees) {
+  float slope = 1.0f, x;
+  if (EXTRA) {
+    x = s[r] * sf.scale2;
+    if (sf.cap2 > 0) {
+      const float t = tanh_of(x);
+      slope = 1.0f - t * t;
+      x = sf.cap2 * t;
+    }
+    x = x - sf.slope2 * fabsf((float)away) - lse2;
+  } else {
+    x = __builtin_fmaf(s[r], sf.scale2, -lse2);
+  }
+  const float w = __builtin_amdgcn_exp2f(x);
+  float ds = w * (dp[r] - delta);
+  if (EXTRA) ds *= slope;
+  s[r] = sees ? w : 0.0f;
+  dp[r] = sees ? ds : 0.0f;
+}
+
+template <int DK, int DV, bool EXTRA>
+__global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p) {
+  constexpr int QB = TT * 2 * DK, OB = TT * 2 * DV, RB = 2048, SB = QB + OB + RB;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SB];
+  const LayerAttnParams& f = p.f;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5;
+  const int tiles_k = (f.Sk + 127) / 128;
+  const int u = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k));
+  if (u < 0) return;
+  const int bh = u / tiles_k, k0 = (u - bh * tiles_k) * 128;
+  const int b = bh / f.H_kv, hk = bh - b * f.H_kv;
+  const int j = k0 + 32 * wave + (lane & 31);  // this lane's key
+  bf16x8_t kf[DK / 16], vf[DV / 16];
+  load_row_frags<DK>(row_of(f.k, b, hk, min(j, f.Sk - 1)), f.d_k, half, kf);
+  load_row_frags<DV>(row_of(f.v, b, hk, min(j, f.Sk - 1)), f.d_v, half, vf);
+  const RowAddr ra = row_addr(lane);
+  const ColAddr ca = col_addr(lane);
+  const uint32_t ring = lds_u32(lds);
+  f32x16_t dk[DK / 32], dv[DV / 32];
+#pragma unroll
+  for (int n = 0; n < DK / 32; ++n) dk[n] = zero16();
+#pragma unroll
+  for (int n = 0; n < DV / 32; ++n) dv[n] = zero16();
+
+  // Query tiles that see any of the keys, and whether all their rows see all of
+  // them, looked at 64 tiles at a time: a load in each step would wait for the
+  // tile that is on its way.
+  int h = hk * f.group, word = -1;
+  uint64_t left = 0, whole = 0;
+  bool all_next = false;
+  const auto next = [&]() {
+    while (!left) {
+      if (++word * 64 >= p.plan.tiles_q) {
+        word = 0;
+        if (++h >= (hk + 1) * f.group) return -1;
+      }
+      const int tq = word * 64 + lane;
+      bool some = false, all = false;
+      if (tq < p.plan.tiles_q) {
+        const int4 x = *reinterpret_cast<const int4*>(p.tiles + 4 * ((int64_t)b * p.plan.tiles_q + tq));
+        some = x.x < k0 + 128 && x.y > k0;
+        all = x.z <= k0 && x.w >= k0 + 128;
+      }
+      left = __builtin_amdgcn_ballot_w64(some);
+      whole = __builtin_amdgcn_ballot_w64(all);
+    }
+    const int r = __builtin_ctzll(left);
+    left &= left - 1;
+    all_next = (whole >> r) & 1;
+    return word * 64 + r;
+  };
+  const auto issue = [&](int tq, int head, int slot) {
+    const uint32_t at = ring + slot * SB;
+    load_tile<TT, DK, 4>(row_of(f.q, b, head, 0), (uint32_t)(f.q.ss * 2), tq * TT, f.Sq, f.d_k, at, wave, lane);
+    load_tile<TT, DV, 4>(row_of(p.dout, b, head, 0), (uint32_t)(p.dout.ss * 2), tq * TT, f.Sq, f.d_v, at + QB, wave, lane);
+    const float* rec = record(p, b, head, tq);
+    if (wave < (EXTRA ? 2 : 1))
+      dma16(uniform(reinterpret_cast<const uint16_t*>(rec)), wave * 1024 + lane * 16,
+            __builtin_amdgcn_readfirstlane(at + QB + OB + wave * 1024));
+  };
+  int tq = next(), slot = 0;
+  vm_wait<0>();
+  if (tq >= 0) issue(tq, h, 0);
+  ScoreForm sf = score_form(f, min(h, f.H - 1));
+  while (tq >= 0) {
+    const ScoreForm form = sf;
+    const bool all = all_next;
+    const int head = h;
+    tq = next();
+    if (EXTRA && tq >= 0 && h != head) sf = score_form(f, h);
+    vm_wait<0>();
+    barrier();
+    if (tq >= 0) issue(tq, h, slot ^ 1);
+    const uint32_t qt = ring + slot * SB, ot = qt + QB;
+    const uint8_t* rec = lds + slot * SB + QB + OB;
+    slot ^= 1;
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+      f32x16_t s = zero16(), dp = zero16();
+#pragma unroll
+      for (int c = 0; c < DK / 16; ++c)
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(qt, ra, c, qb), kf[c], s, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < DV / 16; ++c)
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(ot, ra, c, qb), vf[c], dp, 0, 0, 0);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int row = 32 * qb + 8 * g + 4 * half;
+        const f32x4_t lse2 = *reinterpret_cast<const f32x4_t*>(rec + 4 * row);
+        const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(rec + 4 * (TT + row));
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        i32x4 lo = {0, 0, 0, 0}, hi = lo, at = lo;
+        if (!all) {
+          lo = *reinterpret_cast<const i32x4*>(rec + 4 * (2 * TT + row));
+          hi = *reinterpret_cast<const i32x4*>(rec + 4 * (3 * TT + row));
+        }
+        if (EXTRA) at = *reinterpret_cast<const i32x4*>(rec + 4 * (4 * TT + row));
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          weights<EXTRA>(form, s, dp, 4 * g + r, at[r] - j, lse2[r], delta[r], all || (j >= lo[r] && j < hi[r]));
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8_t w = pack_frag(s, c), d = pack_frag(dp, c);
+#pragma unroll
+        for (int n = 0; n < DV / 32; ++n)
+          dv[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TT>(ot, ca, n, 2 * qb + c), w, dv[n], 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < DK / 32; ++n)
+          dk[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TT>(qt, ca, n, 2 * qb + c), d, dk[n], 0, 0, 0);
+      }
+    }
+  }
+  const bool live = j < f.Sk;
+  const uint32_t odd = not_finite(dk, f.d_k, half) | not_finite(dv, f.d_v, half);
+  store_cols(const_cast<uint16_t*>(row_of(p.dk, b, hk, min(j, f.Sk - 1))), dk, f.d_k, half, live && !odd, f.scale);
+  store_cols(const_cast<uint16_t*>(row_of(p.dv, b, hk, min(j, f.Sk - 1))), dv, f.d_v, half, live && !odd, 1.0f);
+  uint64_t bad = __builtin_amdgcn_ballot_w64(live && odd) & 0xFFFFFFFFull;
+  while (bad) {
+    const int r = __builtin_ctzll(bad);
+    bad &= bad - 1;
+    slow_dkdv(p, b, hk, k0 + 32 * wave + r, lane);
+  }
+}
+
+template <int DK, int DV, bool EXTRA>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
+  constexpr int KB = TT * 2 * DK, VB = TT * 2 * DV, SB = KB + VB;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SB];
+  const LayerAttnParams& f = p.f;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5;
+  const int tiles = (f.Sq + 127) / 128;
+  const int u = die_order(blockIdx.x, (uint32_t)(f.B * f.H * tiles));
+  if (u < 0) return;
+  const int bh = u / tiles, t0 = tiles - 1 - (u - bh * tiles);  // the last rows first
+  const int b = bh / f.H, h = bh - b * f.H, hk = h / f.group;
+  const int i = t0 * 128 + 32 * wave + (lane & 31);
+  const Span sp = row_span(f, b, i);
+  int lo = INT32_MAX, hi = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (2 * t0 + k < p.plan.tiles_q) {
+      const int4 x = *reinterpret_cast<const int4*>(p.tiles + 4 * ((int64_t)b * p.plan.tiles_q + 2 * t0 + k));
+      lo = min(lo, x.x), hi = max(hi, x.y);
+    }
+  int lo_all = sp.lo, hi_all = sp.hi;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    lo_all = max(lo_all, __shfl_xor(lo_all, o));
+    hi_all = min(hi_all, __shfl_xor(hi_all, o));
+  }
+  const int wlo_all = __builtin_amdgcn_readfirstlane(lo_all), whi_all = __builtin_amdgcn_readfirstlane(hi_all);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const int first = lo < hi ? lo / TT : 0, last = lo < hi ? (hi + TT - 1) / TT : 0;
+  const ScoreForm sf = score_form(f, h);
+  const int ic = min(i, f.Sq - 1);
+  const float* rec = record(p, b, h, ic / TT);
+  const float lse2 = rec[ic % TT], delta = rec[TT + ic % TT];
+  const int place = EXTRA ? __float_as_int(rec[4 * TT + ic % TT]) : 0;
+  bf16x8_t q[DK / 16], d[DV / 16];
+  load_row_frags<DK>(row_of(f.q, b, h, ic), f.d_k, half, q);
+  load_row_frags<DV>(row_of(p.dout, b, h, ic), f.d_v, half, d);
+  const RowAddr ra = row_addr(lane);
+  const ColAddr ca = col_addr(lane);
+  const uint32_t ring = lds_u32(lds);
+  const uint16_t *kb = row_of(f.k, b, hk, 0), *vb = row_of(f.v, b, hk, 0);
+  const auto issue = [&](int t, int slot) {
+    load_tile<TT, DK, 4>(kb, (uint32_t)(f.k.ss * 2), t * TT, f.Sk, f.d_k, ring + slot * SB, wave, lane);
+    load_tile<TT, DV, 4>(vb, (uint32_t)(f.v.ss * 2), t * TT, f.Sk, f.d_v, ring + slot * SB + KB, wave, lane);
+  };
+  f32x16_t dq[DK / 32];
+#pragma unroll
+  for (int n = 0; n < DK / 32; ++n) dq[n] = zero16();
+  vm_wait<0>();
+  if (first < last) issue(first, 0);
+  for (int t = first; t < last; ++t) {
+    const int slot = (t - first) & 1;
+    vm_wait<0>();
+    barrier();
+    if (t + 1 < last) issue(t + 1, slot ^ 1);
+    const uint32_t kt = ring + slot * SB, vt = kt + KB;
+    const bool all = t * TT >= wlo_all && (t + 1) * TT <= whi_all;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      f32x16_t s = zero16(), dp = zero16();
+#pragma unroll
+      for (int c = 0; c < DK / 16; ++c)
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(kt, ra, c, k), q[c], s, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < DV / 16; ++c)
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(vt, ra, c, k), d[c], dp, 0, 0, 0);
+      const int j0 = t * TT + 32 * k + 4 * half;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int j = j0 + 8 * (r / 4) + r % 4;
+        weights<EXTRA>(sf, s, dp, r, place - j, lse2, delta, all || (uint32_t)(j - sp.lo) < (uint32_t)(sp.hi - sp.lo));
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8_t w = pack_frag(dp, c);
+#pragma unroll
+        for (int n = 0; n < DK / 32; ++n)
+          dq[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TT>(kt, ca, n, 2 * k + c), w, dq[n], 0, 0, 0);
+      }
+    }
+  }
+  const bool live = i < f.Sq;
+  const uint32_t odd = not_finite(dq, f.d_k, half);
+  store_cols(const_cast<uint16_t*>(row_of(p.dq, b, h, ic)), dq, f.d_k, half, live && !odd, f.scale);
+  uint64_t bad = __builtin_amdgcn_ballot_w64(live && odd) & 0xFFFFFFFFull;
+  while (bad) {
+    const int r = __builtin_ctzll(bad);
+    bad &= bad - 1;
+    slow_dq(p, b, h, t0 * 128 + 32 * wave + r, lane);
+  }
+}
+
+template <int DK, int DV, bool EXTRA>
+void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
+  const LayerAttnParams& f = p.f;
+  const int64_t keys = (int64_t)f.B * f.H_kv * ((f.Sk + 127) / 128), rows = (int64_t)f.B * f.H * ((f.Sq + 127) / 128);
+  if (keys)
+    hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, EXTRA>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(256), 0, stream, p);
+  if (rows)
+    hipLaunchKernelGGL((attn_dq_kernel<DK, DV, EXTRA>), dim3((unsigned)((rows + 7) / 8 * 8)), dim3(256), 0, stream, p);
+}
+template <int DK, int DV>
+void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
+  p.f.cap > 0 || p.f.slopes ? bwd<DK, DV, true>(p, stream) : bwd<DK, DV, false>(p, stream);
+}
+
+}  // namespace
+
+AttnBwdPlan plan_layer_attn_bwd(int B, int H, int Sq) {
+  AttnBwdPlan pl{};
+  pl.tiles_q = (Sq + TT - 1) / TT;
+  pl.records = 0;
+  pl.tiles = (size_t)B * H * pl.tiles_q * ATTN_RECORD * 4;
+  pl.total = pl.tiles + (size_t)B * pl.tiles_q * 16;
+  return pl;
+}
+
+hipError_t launch_layer_attn_bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
+  const int64_t blocks = (int64_t)p.f.B * p.f.H * p.plan.tiles_q;
+  if (blocks) hipLaunchKernelGGL(attn_bwd_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  if (p.f.d_k <= 64 && p.f.d_v <= 64) bwd<64, 64>(p, stream);
+  else if (p.f.d_k <= 128) bwd<128, 128>(p, stream);
+  else bwd<192, 128>(p, stream);
+  return hipGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,393 @@
+// Attention over documents, forward, for gfx950: one pass over the keys with the
+// running maximum and sum of the softmax.
+//
+// A workgroup owns 32 query rows per wave of one head. S^T = K Q^T comes from the
+// matrix units with a query to a lane (column) and keys along its registers, so a
+// row's maximum and sum are within a lane and its partner in the other half of the
+// wave; P^T, rounded to bf16, is the operand of O^T += V^T P^T as it lies. K and V
+// stream through a ring of two 64-key tiles by direct loads, a tile ahead. Q stays
+// in registers.
+#include <algorithm>
+
+#include "layer_attn.h"
+
+namespace mla {
+namespace {
+
+constexpr int TK = 64;  // keys of a tile
+
+// Output row (b, h, i), and its lse where that is wanted, the slow way.
+__device__ __forceinline__ void slow_forward(const LayerAttnParams& p, int b, int h, int i, bool want_lse, int lane) {
+  const Span sp = row_span(p, b, i);
+  const ScoreForm f = score_form(p, h);
+  const int hk = h / p.group, at = p.slopes ? row_place(p, b, i) : 0;
+  const uint16_t* q = row_of(p.q, b, h, i);
+  float m = -__builtin_inff(), l = 0, o[2] = {0, 0};
+  for (int j0 = sp.lo; j0 < sp.hi; j0 += 64) {
+    const int j = j0 + lane;
+    float s = -__builtin_inff(), g;
+    if (j < sp.hi) s = score_of(f, dot_rows(q, row_of(p.k, b, hk, j), p.d_k), at, j, g);
+    const float mt = la_wave_max(s);
+    const float mn = fmaxf(m, mt), mu = mn == -__builtin_inff() ? 0.0f : mn;
+    const float a = __builtin_amdgcn_exp2f(m - mu);
+    float w = __builtin_amdgcn_exp2f(s - mu);  // (NaN scores make NaN here)
+    m = mn;
+    l = l * a + la_wave_sum(w);
+    o[0] *= a;
+    o[1] *= a;
+    const int n = min(64, sp.hi - j0);
+    for (int r = 0; r < n; ++r) {
+      const float wr = __shfl(w, r);
+      const uint16_t* v = row_of(p.v, b, hk, j0 + r);
+      // a key whose score is -inf is not seen
+      if (wr != 0 || __shfl(s, r) != -__builtin_inff()) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (lane + 64 * c < p.d_v) o[c] = __builtin_fmaf(wr, bf16_bits_to_f32(v[lane + 64 * c]), o[c]);
+      }
+    }
+  }
+  const bool none = m == -__builtin_inff() && l == 0;
+  uint16_t* out = const_cast<uint16_t*>(row_of(p.out, b, h, i));
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (lane + 64 * c < p.d_v) out[lane + 64 * c] = (uint16_t)f32_to_bf16_bits(none ? 0.0f : o[c] / l);
+  if (p.lse && want_lse && lane == 0)
+    p.lse[((int64_t)b * p.H + h) * p.Sq + i] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
+}
+
+template <int DK, int DV>
+struct Fwd {
+  static constexpr int KB = TK * 2 * DK, VB = TK * 2 * DV, SB = KB + VB;
+  static constexpr int NJ = DK / 16, NV = DV / 32;
+};
+
+// EXTRA: scores have a cap, depend on distance or fall as the product rises; else
+// they are the products times a positive scale, which the exponent's one fused
+// multiply-add brings in.
+template <int DK, int DV, int WAVES, bool EXTRA>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kernel(LayerAttnParams p) {
+  using F = Fwd<DK, DV>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * F::SB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5;
+  const int u = die_order(blockIdx.x, (uint32_t)(p.plan.groups * p.plan.splits));
+  if (u < 0) return;
+  const int split = u % p.plan.splits, g = u / p.plan.splits;
+  // the last query tiles, whose rows see the most under a causal mask, go first
+  const int bh = g / p.plan.tiles_q, tq = p.plan.tiles_q - 1 - (g - bh * p.plan.tiles_q);
+  const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
+  const int i = tq * (32 * WAVES) + 32 * wave + (lane & 31);  // this lane's query
+  const Span sp = row_span(p, b, i);
+
+  // keys that any row of the workgroup sees, and those that all do
+  int lo = sp.lo < sp.hi ? sp.lo : INT32_MAX, hi = sp.hi, lo_all = sp.lo, hi_all = sp.hi;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    lo = min(lo, __shfl_xor(lo, o));
+    hi = max(hi, __shfl_xor(hi, o));
+    lo_all = max(lo_all, __shfl_xor(lo_all, o));
+    hi_all = min(hi_all, __shfl_xor(hi_all, o));
+  }
+  const int wlo_all = __builtin_amdgcn_readfirstlane(lo_all), whi_all = __builtin_amdgcn_readfirstlane(hi_all);
+  if (WAVES > 1) {
+    int* red = reinterpret_cast<int*>(lds);
+    if (lane == 0) red[2 * wave] = lo, red[2 * wave + 1] = hi;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) lo = min(lo, red[2 * w]), hi = max(hi, red[2 * w + 1]);
+    __syncthreads();
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  int first = lo < hi ? lo / TK : 0, last = lo < hi ? (hi + TK - 1) / TK : 0;  // tiles
+  if (p.plan.splits > 1) {
+    const int per = (last - first + p.plan.splits - 1) / p.plan.splits;
+    const int f0 = first + split * per;
+    last = min(last, f0 + per);
+    first = f0;
+  }
+
+  const ScoreForm sf = score_form(p, h);
+  const int place = EXTRA && p.slopes && i < p.Sq ? row_place(p, b, i) : 0;
+  bf16x8_t q[F::NJ];
+  load_row_frags<DK>(row_of(p.q, b, h, min(i, p.Sq - 1)), p.d_k, half, q);
+  const uint16_t* kb = row_of(p.k, b, hk, 0);
+  const uint16_t* vb = row_of(p.v, b, hk, 0);
+  const uint32_t ks = (uint32_t)(p.k.ss * 2), vs = (uint32_t)(p.v.ss * 2);
+  const uint32_t ring = lds_u32(lds);
+  const auto issue = [&](int t, int slot) {
+    load_tile<TK, DK, WAVES>(kb, ks, t * TK, p.Sk, p.d_k, ring + slot * F::SB, wave, lane);
+    load_tile<TK, DV, WAVES>(vb, vs, t * TK, p.Sk, p.d_v, ring + slot * F::SB + F::KB, wave, lane);
+  };
+  const RowAddr ra = row_addr(lane);
+  const ColAddr ca = col_addr(lane);
+  f32x16_t o[F::NV];
+#pragma unroll
+  for (int n = 0; n < F::NV; ++n) o[n] = zero16();
+  float m = -__builtin_inff(), l = 0;
+  vm_wait<0>();
+  if (first < last) issue(first, 0);
+  for (int t = first; t < last; ++t) {
+    const int slot = (t - first) & 1;
+    vm_wait<0>();
+    barrier();
+    if (t + 1 < last) issue(t + 1, slot ^ 1);
+    const uint32_t kt = ring + slot * F::SB, vt = kt + F::KB;
+    f32x16_t s[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      s[k] = zero16();
+#pragma unroll
+      for (int j = 0; j < F::NJ; ++j)
+        s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TK>(kt, ra, j, k), q[j], s[k], 0, 0, 0);
+    }
+    // element r of block k: key t TK + 32 k + 8 (r / 4) + 4 half + r % 4
+    const int j0 = t * TK + 4 * half;
+    if (EXTRA) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          float x = s[k][r] * sf.scale2;
+          if (p.cap > 0) x = sf.cap2 * tanh_of(x);
+          s[k][r] = x - sf.slope2 * fabsf((float)(place - (j0 + 32 * k + 8 * (r / 4) + r % 4)));
+        }
+    }
+    if (t * TK < wlo_all || (t + 1) * TK > whi_all) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if ((uint32_t)(j0 + 32 * k + 8 * (r / 4) + r % 4 - sp.lo) >= (uint32_t)(sp.hi - sp.lo)) s[k][r] = -__builtin_inff();
+    }
+    float mt = s[0][0];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[k][r]);
+    {
+      const u32x2_t x = swap_halves(__float_as_uint(mt), __float_as_uint(mt));
+      mt = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
+    const float sc = EXTRA ? 1.0f : sf.scale2;
+    mt *= sc;
+    // The sums are rescaled only where the maximum rises by more than 2^8: weights
+    // up to that lose nothing in bf16 and fp32.
+    const bool rise = mt > m + 8.0f || (m == -__builtin_inff() && mt > m);
+    if (__builtin_amdgcn_ballot_w64(rise)) {
+      const float mn = fmaxf(m, mt);
+      const float a = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= a;
+#pragma unroll
+      for (int n = 0; n < F::NV; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[n][r] *= a;
+    }
+    const float mu = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[k][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][r], sc, -mu));
+        l += s[k][r];
+      }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const bf16x8_t w = pack_frag(s[c >> 1], c & 1);
+#pragma unroll
+      for (int n = 0; n < F::NV; ++n)
+        o[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TK>(vt, ca, n, c), w, o[n], 0, 0, 0);
+    }
+  }
+  {
+    const u32x2_t x = swap_halves(__float_as_uint(l), __float_as_uint(l));
+    l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  const bool live = i < p.Sq;
+  if (p.plan.splits > 1) {
+    if (!live) return;
+    const int64_t row = ((int64_t)g * p.plan.splits + split) * (32 * WAVES) + 32 * wave + (lane & 31);
+    if (half == 0) *reinterpret_cast<float2*>(p.part_ml + 2 * row) = make_float2(m, l);
+#pragma unroll
+    for (int n = 0; n < F::NV; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int d = 32 * n + 8 * k + 4 * half;
+        if (d < p.d_v)
+          *reinterpret_cast<float4*>(p.part_o + row * p.d_v + d) =
+              make_float4(o[n][4 * k], o[n][4 * k + 1], o[n][4 * k + 2], o[n][4 * k + 3]);
+      }
+    return;
+  }
+  const bool none = l == 0;
+  const float inv = none ? 0.0f : 1.0f / l;
+  const bool fine = l < __builtin_inff();  // (values that are not finite leave l and lse as they are)
+  uint32_t odd = !fine;
+#pragma unroll
+  for (int n = 0; n < F::NV; ++n)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      o[n][r] *= inv;
+      if (32 * n + 8 * (r / 4) + 4 * half < p.d_v) odd |= abs_bits(o[n][r]) >= 0x7F800000u;
+    }
+  {
+    const u32x2_t x = swap_halves(odd, odd);
+    odd = x[0] | x[1];
+  }
+  uint16_t* out = const_cast<uint16_t*>(row_of(p.out, b, h, min(i, p.Sq - 1)));
+#pragma unroll
+  for (int n = 0; n < F::NV; ++n) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[n][2 * k], o[n][2 * k + 1]);
+    u32x2_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = swap_halves(w[k], w[4 + k]);
+    // lower lane: columns 0..15 of the block, upper lane: 16..31
+    const int d = 32 * n + 16 * half;
+    if (live && !odd) {
+      if (d < p.d_v) *reinterpret_cast<u32x4_t*>(out + d) = u32x4_t{x[0][0], x[1][0], x[0][1], x[1][1]};
+      if (d + 8 < p.d_v) *reinterpret_cast<u32x4_t*>(out + d + 8) = u32x4_t{x[2][0], x[3][0], x[2][1], x[3][1]};
+    }
+  }
+  if (p.lse && live && fine && half == 0)
+    p.lse[(int64_t)bh * p.Sq + i] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
+  uint64_t bad = __builtin_amdgcn_ballot_w64(live && odd) & 0xFFFFFFFFull;
+  while (bad) {
+    const int r = __builtin_ctzll(bad);
+    bad &= bad - 1;
+    slow_forward(p, b, h, tq * (32 * WAVES) + 32 * wave + r, !(__shfl(l, r) < __builtin_inff()), lane);
+  }
+}
+
+// Parts of a row joined: a wave to a row, four rows to a workgroup.
+__global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= (int64_t)p.B * p.H * p.Sq) return;
+  const int64_t bh = row / p.Sq;
+  const int i = (int)(row - bh * p.Sq), b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
+  const int rows = p.plan.rows, tq = i / rows;
+  const int64_t g = bh * p.plan.tiles_q + (p.plan.tiles_q - 1 - tq);
+  const int64_t slot0 = g * p.plan.splits * rows + i % rows;
+  float m = -__builtin_inff();
+  for (int s = 0; s < p.plan.splits; ++s) m = fmaxf(m, p.part_ml[2 * (slot0 + (int64_t)s * rows)]);
+  const float mu = m == -__builtin_inff() ? 0.0f : m;
+  float l = 0, o[2] = {0, 0};
+  for (int s = 0; s < p.plan.splits; ++s) {
+    const int64_t at = slot0 + (int64_t)s * rows;
+    const float w = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - mu);
+    l = __builtin_fmaf(p.part_ml[2 * at + 1], w, l);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (lane + 64 * c < p.d_v) o[c] = __builtin_fmaf(p.part_o[at * p.d_v + lane + 64 * c], w, o[c]);
+  }
+  const bool none = l == 0;
+  const float inv = none ? 0.0f : 1.0f / l;
+  const bool fine = l < __builtin_inff();
+  if (p.lse && fine && lane == 0) p.lse[row] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
+  bool odd = !fine;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    o[c] *= inv;
+    odd |= abs_bits(o[c]) >= 0x7F800000u;
+  }
+  if (__builtin_amdgcn_ballot_w64(odd)) {
+    slow_forward(p, b, h, i, !fine, lane);
+    return;
+  }
+  uint16_t* out = const_cast<uint16_t*>(row_of(p.out, b, h, i));
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (lane + 64 * c < p.d_v) out[lane + 64 * c] = (uint16_t)f32_to_bf16_bits(o[c]);
+}
+
+__global__ __launch_bounds__(256) void spans_kernel(SpanParams p) {
+  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (row >= (int64_t)p.B * p.Sq) return;
+  const int b = (int)(row / p.Sq), i = (int)(row - (int64_t)b * p.Sq);
+  int q0 = 0, q1, k0 = 0, k1, j = b;
+  if (p.nseq) {
+    // the last document that starts at or before row i
+    int lo = 0, hi = p.nseq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu_q[mid] <= i) lo = mid; else hi = mid;
+    }
+    j = lo;
+    q0 = p.cu_q[j], q1 = p.cu_q[j + 1];
+    k0 = p.cu_k[j], k1 = p.cu_k[j + 1];
+  } else {
+    q1 = p.len_q ? p.len_q[b] : p.Sq;
+    k1 = p.len_k ? p.len_k[b] : p.Sk;
+  }
+  q0 = min(max(q0, 0), p.Sq), q1 = min(max(q1, q0), p.Sq);
+  k0 = min(max(k0, 0), p.Sk), k1 = min(max(k1, k0), p.Sk);
+  const int at = k1 - (q1 - i);  // the queries are the sequence's last tokens
+  int lo = k0, hi = k1;
+  if (p.causal) {
+    const int prefix = p.prefix ? min(max(p.prefix[j], 0), k1 - k0) : 0;
+    hi = min(k1, max(at + 1, k0 + prefix));
+  }
+  if (p.window) lo = max(lo, at - p.window + 1);
+  if (i < q0 || i >= q1 || lo >= hi) lo = hi = 0;
+  *reinterpret_cast<int2*>(p.spans + 2 * row) = make_int2(lo, hi);
+  if (p.at) p.at[row] = at;
+}
+
+template <int DK, int DV, int WAVES>
+void fwd(const LayerAttnParams& p, hipStream_t stream) {
+  const int64_t units = p.plan.groups * p.plan.splits;
+  const dim3 grid((unsigned)((units + 7) / 8 * 8)), block(64 * WAVES);
+  if (p.cap > 0 || p.slopes || !(p.scale > 0)) hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, false>), grid, block, 0, stream, p);
+}
+template <int DK, int DV>
+void fwd(const LayerAttnParams& p, hipStream_t stream) {
+  p.plan.rows == 32 ? fwd<DK, DV, 1>(p, stream) : fwd<DK, DV, 4>(p, stream);
+}
+
+}  // namespace
+
+AttnPlanFwd plan_layer_attn(int B, int H, int Sq, int Sk, int d_v, int cus) {
+  AttnPlanFwd pl{};
+  pl.rows = Sq <= 64 ? 32 : 128;
+  pl.tiles_q = (Sq + pl.rows - 1) / pl.rows;
+  pl.groups = (int64_t)B * H * pl.tiles_q;
+  pl.splits = 1;
+  if (pl.groups > 0) {
+    // two workgroups to a compute unit, four tiles of keys to a part at least
+    const int64_t want = (2 * (int64_t)cus + pl.groups - 1) / pl.groups;
+    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, (Sk + 4 * TK - 1) / (4 * TK), 64}));
+  }
+  if (pl.splits > 1) {
+    const size_t rows = (size_t)pl.groups * pl.splits * pl.rows;
+    pl.part_o = 0;
+    pl.part_ml = rows * (size_t)d_v * 4;
+    pl.total = pl.part_ml + rows * 8;
+  }
+  return pl;
+}
+
+hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream) {
+  if (p.plan.groups == 0) return hipSuccess;
+  if (p.d_k <= 64 && p.d_v <= 64) fwd<64, 64>(p, stream);
+  else if (p.d_k <= 128) fwd<128, 128>(p, stream);
+  else fwd<192, 128>(p, stream);
+  if (p.plan.splits > 1) {
+    const int64_t rows = (int64_t)p.B * p.H * p.Sq;
+    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_spans(const SpanParams& p, hipStream_t stream) {
+  const int64_t rows = (int64_t)p.B * p.Sq;
+  if (rows == 0) return hipSuccess;
+  hipLaunchKernelGGL(spans_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,60 @@
+// The end of an up-projection of few tokens: bias, rotation, quantization and
+// store of eight columns of a token.
+#pragma once
+
+#include "device_common.h"
+
+namespace mla {
+
+// v: columns n .. n + 7 of token t. Four consecutive lanes hold 32 columns of one
+// head and come here together; `first` marks the one that stores their scale.
+// live: there are such a token and column.
+template <class P>
+__device__ __forceinline__ void finish8(const P& p, const TokenMap& tm, int64_t t, int n, bool live, bool first,
+                                        float (&v)[8]) {
+  int pos = 0, bb = 0, ss = 0;
+  const int h = n / p.D, d0 = n - h * p.D;
+  if (live) {
+    token_coords(tm, t, pos, bb, ss);
+    if (p.positions) pos = p.positions[t];
+    if (p.bias)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += bf16_bits_to_f32(p.bias[n + k]);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      if (d0 + k >= p.d_nope) {
+        const bool ok = pos >= 0 && pos < p.rope_rows;
+        const int64_t ti = (int64_t)(ok ? pos : 0) * p.rope_pairs + (d0 + k - p.d_nope) / 2;
+        const float cs = ok ? p.cos[ti] : __builtin_nanf(""), sn = ok ? p.sin[ti] : __builtin_nanf("");
+        const float a = v[k], b = v[k + 1];
+        v[k] = a * cs - b * sn;
+        v[k + 1] = a * sn + b * cs;
+      }
+  }
+  const int64_t o = (((int64_t)bb * p.H + h) * p.S + ss) * p.D + d0;
+  if (!p.out_mx) {
+    if (live)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o) =
+          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7]));
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[k]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    uint32_t c0 = 0x7F7F7F7Fu, c1 = 0x7F7F7F7Fu, sc = 0xFF;
+    if (m < 0x7F800000u) {
+      const int E = mx_block_exp(m);
+      c0 = e4m3_pack4(v[0], v[1], v[2], v[3], E);
+      c1 = e4m3_pack4(v[4], v[5], v[6], v[7], E);
+      sc = (uint32_t)(E + 127);
+    }
+    if (live) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + o) = make_uint2(c0, c1);
+      if (first) p.out_scales[o / 32] = (uint8_t)sc;
+    }
+  }
+}
+
+}  // namespace mla

@@ -55,20 +55,24 @@ constexpr int ROPE_TAB_HALF = TILE_T * ROPE_ROW_BYTES;  // cos rows, then sin ro
 // epilogue spread over the banks.
 __device__ __forceinline__ int rope_swz(int r) { return (r >> 1) & 7; }
 
-enum { MODE_BF16 = 0, MODE_MX_EXACT = 1, MODE_MX_FP8 = 2, MODE_BF16_R64 = 3 };
+enum { MODE_BF16 = 0, MODE_MX_EXACT = 1, MODE_MX_FP8 = 2, MODE_BF16_R64 = 3, MODE_I8 = 4, MODE_I8_R64 = 5 };
 enum { EPI_MLA = 0, EPI_PLAIN = 1 };  // fused RoPE/quantize/BHSD epilogue, or a plain row-major store
 
 // Stage layout per mode: a ring slot holds ROWB bytes of each of the tile's
 // TILE_T X rows and TILE_N W rows. 128-byte row slices (whole cache lines per
-// request: 64 bf16 or 128 E4M3 K-values) in a 2-slot ring, except BF16 with
-// K % 64 == 32, which uses 64-byte slices in 4 slots. Every mode takes 80 KB
-// of LDS; E4M3 operand scales travel in registers (see StageScales).
+// request: 64 bf16 or 128 E4M3 or int8 K-values) in a 2-slot ring, except BF16
+// with K % 64 == 32 and int8 with K % 128 == 64, which use 64-byte slices in 4
+// slots. Every mode takes 80 KB of LDS; E4M3 operand scales travel in registers
+// (see StageScales), those of int8 tokens and channels meet the sums after the
+// last stage.
 template <int MODE>
 struct Tile {
   static constexpr bool MX = MODE == MODE_MX_EXACT || MODE == MODE_MX_FP8;
-  static constexpr int ROWB = MODE == MODE_BF16_R64 ? 64 : 128;
-  static constexpr int KPS = MX ? ROWB : ROWB / 2;  // K-values per stage
-  static constexpr int STAGES = MODE == MODE_BF16_R64 ? 4 : 2;
+  static constexpr bool I8 = MODE == MODE_I8 || MODE == MODE_I8_R64;
+  static constexpr bool R64 = MODE == MODE_BF16_R64 || MODE == MODE_I8_R64;
+  static constexpr int ROWB = R64 ? 64 : 128;
+  static constexpr int KPS = MX || I8 ? ROWB : ROWB / 2;  // K-values per stage
+  static constexpr int STAGES = R64 ? 4 : 2;
   static constexpr int XSB = TILE_T * ROWB;         // X part of a slot
   static constexpr int WSB = TILE_N * ROWB;         // W part of a slot
   static constexpr int SB = XSB + WSB;
@@ -109,12 +113,15 @@ struct TokInfo {
 
 // t: this lane's token, in the wave's run of 32 consecutive tokens starting at
 // t - (lane & 31).
+// GIVEN: the positions may be given, in place of the format's.
+template <bool GIVEN>
 __device__ __forceinline__ TokInfo tok_info(const FwdParams& p, const TokenMap& tm, int64_t t, int lane) {
   TokInfo ti{t < p.T, 0, 0};
   if (ti.ok) {
     int b, s;
     const int base = (int)t - (lane & 31);
     token_coords_run(tm, t, base, base + 31, ti.pos, b, s);
+    if (GIVEN && p.positions) ti.pos = p.positions[t];
     ti.row = (int64_t)b * p.H * p.S + s;
   }
   return ti;
@@ -274,12 +281,12 @@ __device__ __forceinline__ void epilogue_one(const FwdParams& p, const TokInfo& 
   sc[NB] = n_blk < p.N ? epilogue_block(p, ti, acc[NB][TB], n_blk, lane, !packed, tab, tok) : 0u;
 }
 
-template <int TB, int... NBs>
+template <bool GIVEN, int TB, int... NBs>
 __device__ __forceinline__ void epilogue_tok(const FwdParams& p, const TokenMap& tm,
                                              const f32x16_t (&acc)[WBLK_N][WBLK_T], int n0, int64_t t_lane,
                                              int lane, RopeTab tab, int tok0,
                                              std::integer_sequence<int, NBs...>) {
-  const TokInfo ti = tok_info(p, tm, t_lane + 32 * TB, lane);
+  const TokInfo ti = tok_info<GIVEN>(p, tm, t_lane + 32 * TB, lane);
   // When the tile is exactly one head, the head's D/32 scale bytes of this
   // token are contiguous: store them as 16-bit pairs, right after the token
   // row's codes, instead of one byte per block.
@@ -300,19 +307,20 @@ __device__ __forceinline__ void epilogue_tok(const FwdParams& p, const TokenMap&
   }
 }
 
-template <int... TBs>
+template <bool GIVEN, int... TBs>
 __device__ __forceinline__ void epilogue_all(const FwdParams& p, const TokenMap& tm,
                                              const f32x16_t (&acc)[WBLK_N][WBLK_T], int n0, int64_t t_lane,
                                              int lane, RopeTab tab, int tok0,
                                              std::integer_sequence<int, TBs...>) {
-  (epilogue_tok<TBs>(p, tm, acc, n0, t_lane, lane, tab, tok0, std::make_integer_sequence<int, WBLK_N>{}), ...);
+  (epilogue_tok<GIVEN, TBs>(p, tm, acc, n0, t_lane, lane, tab, tok0, std::make_integer_sequence<int, WBLK_N>{}), ...);
 }
 
 // t_lane: this lane's first token; tok0: its row inside the tile (for tab).
+template <bool GIVEN>
 __device__ __forceinline__ void epilogue_tile(const FwdParams& p, const TokenMap& tm,
                                               const f32x16_t (&acc)[WBLK_N][WBLK_T], int n0, int64_t t_lane,
                                               int lane, RopeTab tab, int tok0) {
-  epilogue_all(p, tm, acc, n0, t_lane, lane, tab, tok0, std::make_integer_sequence<int, WBLK_T>{});
+  epilogue_all<GIVEN>(p, tm, acc, n0, t_lane, lane, tab, tok0, std::make_integer_sequence<int, WBLK_T>{});
 }
 
 // The tile's cos and sin table rows (d_rope = 64: the first 32 pairs of
@@ -321,6 +329,7 @@ __device__ __forceinline__ void epilogue_tile(const FwdParams& p, const TokenMap
 // 8j .. 8j + 7 of both tables; lane i writes row 8j + i / 8, chunk position
 // i % 8. Positions outside the table (and rows past T) read row 0; the
 // epilogue turns those tokens into NaN as it does for direct table loads.
+template <bool GIVEN>
 __device__ __forceinline__ void stage_rope_rows(const FwdParams& p, const TokenMap& tm, int64_t t0,
                                                 uint32_t dst, int wave, int lane) {
 #pragma unroll
@@ -333,6 +342,7 @@ __device__ __forceinline__ void stage_rope_rows(const FwdParams& p, const TokenM
     const int run0 = (int)min(t0 + 8 * j, p.T - 1), run1 = (int)min(t0 + 8 * j + 7, p.T - 1);
     int pos, b, s;
     token_coords_run(tm, t, run0, run1, pos, b, s);
+    if (GIVEN && p.positions) pos = p.positions[t];
     if (pos < 0 || pos >= p.rope_rows) pos = 0;
     const uint32_t off = (uint32_t)pos * (uint32_t)(p.rope_pairs * 4) + (uint32_t)(((lane & 7) ^ rope_swz(r)) * 16);
     dma16(p.cos, off, dst + j * 1024);
@@ -633,6 +643,35 @@ __device__ __forceinline__ StageScales quad_stage(const QuadScales& q, int kt) {
   return sc;
 }
 
+// The sums' type: int8 products add up in 32-bit integers, exactly.
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+template <bool I8>
+struct AccOf {
+  typedef f32x16_t type;
+};
+template <>
+struct AccOf<true> {
+  typedef i32x16_t type;
+};
+
+__device__ __forceinline__ f32x16_t mma16(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// 32 k of int8: a fragment is 16 consecutive bytes of a row here too
+__device__ __forceinline__ i32x16_t mma16(bf16x8_t a, bf16x8_t b, i32x16_t c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+}
+
+// Sums times the scales of token and channel, in fp32: one rounding of the sum
+// (of those past 2^24) and one for each product.
+__device__ __forceinline__ f32x16_t i8_scaled(const i32x16_t& acc, float xs, const float (&ws)[16]) {
+  f32x16_t o;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) o[r] = (float)acc[r] * xs * ws[r];
+  return o;
+}
+
 // Scales of stage kt of the current pair.
 template <bool FP8>
 __device__ __forceinline__ StageScales stage_scales(const PairScales& ps, int kt) {
@@ -645,14 +684,14 @@ __device__ __forceinline__ StageScales stage_scales(const PairScales& ps, int kt
   return sc;
 }
 
-template <int MODE>
-__device__ __forceinline__ void mma_stage(f32x16_t (&acc)[WBLK_N][WBLK_T], const uint8_t* cur,
+template <int MODE, class ACC>
+__device__ __forceinline__ void mma_stage(ACC (&acc)[WBLK_N][WBLK_T], const uint8_t* cur,
                                           const StageScales& sc, int arow0, int brow0, int half) {
   using TL = Tile<MODE>;
-  if (!TL::MX) {
-    // all fragments of the stage's k16 steps first, so the later steps' LDS
+  if constexpr (!TL::MX) {
+    // all fragments of the stage's k16 (int8: k32) steps first, so the later steps' LDS
     // reads are in flight while the first step's MFMAs run
-    constexpr int NJS = TL::KPS / 16;
+    constexpr int NJS = TL::ROWB / 32;
     bf16x8_t a[NJS][WBLK_N], b[NJS][WBLK_T];
 #pragma unroll
     for (int j = 0; j < NJS; ++j) {
@@ -670,8 +709,8 @@ __device__ __forceinline__ void mma_stage(f32x16_t (&acc)[WBLK_N][WBLK_T], const
       for (int tb = 0; tb < WBLK_T; ++tb)
 #pragma unroll
         for (int nb = 0; nb < WBLK_N; ++nb)
-          acc[nb][tb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j][nb], b[j][tb], acc[nb][tb], 0, 0, 0);
-  } else if (MODE == MODE_MX_EXACT) {
+          acc[nb][tb] = mma16(a[j][nb], b[j][tb], acc[nb][tb]);
+  } else if constexpr (MODE == MODE_MX_EXACT) {
     // E4M3 expanded exactly to bf16 (code * 2^(scale-127)) per fragment; the
     // bf16 MFMA then multiplies exactly and accumulates in fp32. K is walked
     // in a permuted but identical order for both operands: for K-block jb of
@@ -846,7 +885,7 @@ void qup_fwd_kernel(FwdParams p) {
 
   const TileGrid grid{(int)((p.T + TILE_T - 1) / TILE_T), (p.N + TILE_N - 1) / TILE_N, 0};
   const TileGrid g{grid.tiles_t, grid.tiles_n, grid.tiles_t * grid.tiles_n};
-  const int row_bytes = MX ? p.K : 2 * p.K;
+  const int row_bytes = MX || TL::I8 ? p.K : 2 * p.K;
   const int nk_all = p.K / KPS;
   const int units = EPI == EPI_PLAIN ? g.total * p.k_splits : g.total;
   const uint32_t ring = lds_u32(lds);
@@ -889,13 +928,13 @@ void qup_fwd_kernel(FwdParams p) {
     sc_raw = load_pair(p, sr, 0, nk, half);  // MX: STAGES == 2
 
   for (;;) {
-    f32x16_t acc[WBLK_N][WBLK_T];
+    typename AccOf<TL::I8>::type acc[WBLK_N][WBLK_T];
 #pragma unroll
     for (int i = 0; i < WBLK_N; ++i)
 #pragma unroll
       for (int j = 0; j < WBLK_T; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
     for (int kt = 0; kt < nk; ++kt) {
       vm_wait<(STAGES - 2) * TL::LPS>();
@@ -905,7 +944,7 @@ void qup_fwd_kernel(FwdParams p) {
       // (kt + STAGES - 1) % STAGES was read in iteration kt - 1 and every
       // wave has passed the barrier since.
       if (tab_lds && kt == nk - 1)
-        stage_rope_rows(p, tm, t0, ring + (uint32_t)((sb + nk) % STAGES) * TL::SB, wave, lane);
+        stage_rope_rows<TL::I8>(p, tm, t0, ring + (uint32_t)((sb + nk) % STAGES) * TL::SB, wave, lane);
       else
         issue_stage<MODE>(dp, xb, wb, kt + STAGES - 1, nk, sb + kt + STAGES - 1, ring, wave);
       if (QUAD) {
@@ -959,11 +998,30 @@ void qup_fwd_kernel(FwdParams p) {
           sc_raw = load_pair(p, sr, 0, nk, half);
       }
     }
-    if (EPI == EPI_PLAIN)
+    if constexpr (TL::I8) {
+      const int64_t t_lane = t0c + 32 * WBLK_T * wt + (lane & 31);
+      f32x16_t q[WBLK_N][WBLK_T];
+      float xs[WBLK_T];
+#pragma unroll
+      for (int tb = 0; tb < WBLK_T; ++tb) xs[tb] = p.x_row_scales[min(t_lane + 32 * tb, p.T - 1)];
+#pragma unroll
+      for (int nb = 0; nb < WBLK_N; ++nb) {
+        float ws[16];  // rows 8g + 4 half + 0..3 of the block
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int n = min(n0c + 32 * WBLK_N * wn + 32 * nb, p.N - 32) + 8 * g + 4 * half;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ws[4 * g + k] = p.w_row_scales[n + k];
+        }
+#pragma unroll
+        for (int tb = 0; tb < WBLK_T; ++tb) q[nb][tb] = i8_scaled(acc[nb][tb], xs[tb], ws);
+      }
+      epilogue_tile<true>(p, tm, q, n0c + 32 * WBLK_N * wn, t_lane, lane, tab, 32 * WBLK_T * wt + (lane & 31));
+    } else if constexpr (EPI == EPI_PLAIN)
       plain_tile(p, static_cast<uint8_t*>(p.out) + (int64_t)split_c * p.split_stride, acc,
                  n0c + 32 * WBLK_N * wn, t0c + 32 * WBLK_T * wt + (lane & 31), lane);
     else
-      epilogue_tile(p, tm, acc, n0c + 32 * WBLK_N * wn, t0c + 32 * WBLK_T * wt + (lane & 31), lane, tab,
+      epilogue_tile<false>(p, tm, acc, n0c + 32 * WBLK_N * wn, t0c + 32 * WBLK_T * wt + (lane & 31), lane, tab,
                     32 * WBLK_T * wt + (lane & 31));
     if (!more) break;
     u = un;
@@ -1021,6 +1079,20 @@ hipError_t launch_qup_fwd_mx(const FwdParams& p_in, hipStream_t stream) {
     else
       hipLaunchKernelGGL((qup_fwd_kernel<MODE_MX_EXACT, EPI_MLA>), grid, dim3(NTHREADS), 0, stream, p);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_qup_fwd_i8(const FwdParams& p_in, hipStream_t stream) {
+  FwdParams p = p_in;
+  p.rope_lds = rope_rows_fit_lds(p);
+  const dim3 grid(fwd_grid(p, device_cu_count()));
+  if (p.K % 128 == 0) {
+    if (p.rope_lds)
+      hipLaunchKernelGGL((qup_fwd_kernel<MODE_I8, EPI_MLA, true>), grid, dim3(NTHREADS), 0, stream, p);
+    else
+      hipLaunchKernelGGL((qup_fwd_kernel<MODE_I8, EPI_MLA>), grid, dim3(NTHREADS), 0, stream, p);
+  } else
+    hipLaunchKernelGGL((qup_fwd_kernel<MODE_I8_R64, EPI_MLA>), grid, dim3(NTHREADS), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -1,0 +1,363 @@
+// RMS norm of token rows in front of the up-projection, with the residual's
+// addition and an output in bf16, MXFP8 or int8, and its backward, for gfx950.
+//
+//   h = x + res,  rstd = (mean_k h^2 + eps)^(-1/2),  y = h rstd gamma
+//   dh = dh_in + rstd (g - xhat mean_k(g xhat)),  g = gamma dy,  xhat = h rstd
+//   dgamma = sum_t dy xhat
+//
+// Bound by HBM: every row is read once, stays in registers between the sum of
+// squares and the outputs, and is written once. A row belongs to WPR waves of
+// a workgroup, each lane holding up to CH chunks of eight elements, so loads
+// and stores are 16 bytes to a lane and contiguous over a wave.
+#include <algorithm>
+
+#include "device_common.h"
+#include "internal_layer.h"
+
+namespace mla {
+namespace {
+
+constexpr int THREADS = 256;
+
+struct F8 {
+  float v[8];
+};
+
+__device__ __forceinline__ F8 from_bf16(uint4 u) {
+  F8 r;
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    r.v[2 * k] = bf16_bits_to_f32(w[k] & 0xFFFFu);
+    r.v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  }
+  return r;
+}
+__device__ __forceinline__ uint4 to_bf16(const F8& a) {
+  return make_uint4(pack_bf16x2(a.v[0], a.v[1]), pack_bf16x2(a.v[2], a.v[3]), pack_bf16x2(a.v[4], a.v[5]),
+                    pack_bf16x2(a.v[6], a.v[7]));
+}
+__device__ __forceinline__ F8 load8(const void* p, int64_t at, bool f32) {
+  if (!f32) return from_bf16(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+  F8 r;
+  const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+  const float4 a = s[0], b = s[1];
+  r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
+  r.v[4] = b.x, r.v[5] = b.y, r.v[6] = b.z, r.v[7] = b.w;
+  return r;
+}
+__device__ __forceinline__ void store8_f32(float* p, const F8& a) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+  return v;
+}
+
+// Sum (or unsigned maximum) over the WPR waves of a row; `red` holds a value per
+// wave, and calls alternate between two of them so that one barrier does.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* red, int wave) {
+  v = wave_sum(v);
+  if (WPR == 1) return v;
+  red[wave] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) v += red[wave / WPR * WPR + w];
+  return v;
+}
+template <int WPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int wave) {
+  v = wave_max(v);
+  if (WPR == 1) return v;
+  red[wave] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) v = max(v, red[wave / WPR * WPR + w]);
+  return v;
+}
+
+// Eight codes of one token row: |code| <= 127, the nearest to y / scale with ties
+// to even.
+__device__ __forceinline__ uint2 int8x8(const F8& y, float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    w[k] = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float r = __builtin_amdgcn_fmed3f(__builtin_rintf(y.v[4 * k + q] * inv), -127.0f, 127.0f);
+      w[k] |= ((uint32_t)(int)r & 0xFFu) << (8 * q);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A row's scale amax / 127 and its inverse. A row of zeros (or one so small that
+// the scale leaves fp32's range) has scale 0 and codes 0; one that holds NaN or
+// an infinity has scale NaN and codes 0.
+__device__ __forceinline__ void int8_scale(uint32_t amax_bits, float& scale, float& inv) {
+  const float a = __uint_as_float(amax_bits);
+  scale = a / 127.0f;
+  inv = 127.0f / a;
+  if (amax_bits >= 0x7F800000u) {
+    scale = __builtin_nanf("");
+    inv = 0;
+  } else if (!(inv < __builtin_inff())) {
+    scale = 0;
+    inv = 0;
+  }
+}
+
+template <int WPR, int CH>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : THREADS) void rmsnorm_kernel(NormParams p) {
+  constexpr int WAVES = WPR > 4 ? WPR : THREADS / 64;
+  __shared__ float red[2][WAVES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * (WAVES / WPR) + wave / WPR;
+  const bool row = t < p.T;
+  const int chunks = p.K / 8, first = (wave % WPR) * 64 + lane;
+  F8 h[CH];
+  float ss = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int at = first + c * 64 * WPR;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[c].v[k] = 0;
+    if (row && at < chunks) {
+      h[c] = load8(p.x, t * p.ld_x + 8 * at, false);
+      if (p.res) {
+        const F8 r = load8(p.res, t * p.K + 8 * at, p.res_f32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[c].v[k] += r.v[k];
+        // the sum that is normalised is the one that is stored, rounded to its type
+        if (!p.res_f32) h[c] = from_bf16(to_bf16(h[c]));
+      }
+      if (p.h) {
+        if (p.res_f32) store8_f32(static_cast<float*>(p.h) + t * p.K + 8 * at, h[c]);
+        else *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h) + t * p.K + 8 * at) = to_bf16(h[c]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[c].v[k], h[c].v[k], ss);
+  }
+  ss = row_sum<WPR>(ss, red[0], wave);
+  const float rstd = 1.0f / __builtin_sqrtf(ss / (float)p.K + p.eps);
+  if (row && p.rstd && lane == 0 && wave % WPR == 0) p.rstd[t] = rstd;
+  uint32_t amax = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int at = first + c * 64 * WPR;
+    if (row && at < chunks) {
+      F8 g;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g.v[k] = 1.0f;
+      if (p.gamma) g = load8(p.gamma, 8 * at, p.gamma_f32);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        h[c].v[k] = h[c].v[k] * rstd * g.v[k];
+        amax = max(amax, abs_bits(h[c].v[k]));
+      }
+      if (p.y) *reinterpret_cast<uint4*>(p.y + t * p.K + 8 * at) = to_bf16(h[c]);
+    }
+    if (p.codes && p.q_dtype == MLA_DTYPE_MXFP8) {
+      // four neighbouring lanes hold a block of 32
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max(m, abs_bits(h[c].v[k]));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+      uint2 code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+      uint32_t sc = 0xFF;
+      if (m < 0x7F800000u) {
+        const int E = mx_block_exp(m);
+        code = make_uint2(e4m3_pack4(h[c].v[0], h[c].v[1], h[c].v[2], h[c].v[3], E),
+                          e4m3_pack4(h[c].v[4], h[c].v[5], h[c].v[6], h[c].v[7], E));
+        sc = (uint32_t)(E + 127);
+      }
+      if (row && at < chunks) {
+        *reinterpret_cast<uint2*>(p.codes + t * p.K + 8 * at) = code;
+        if ((lane & 3) == 0) static_cast<uint8_t*>(p.scales)[(t * p.K + 8 * at) / 32] = (uint8_t)sc;
+      }
+    }
+  }
+  if (p.codes && p.q_dtype == MLA_DTYPE_INT8) {
+    amax = row_max<WPR>(amax, reinterpret_cast<uint32_t*>(red[1]), wave);
+    float scale, inv;
+    int8_scale(amax, scale, inv);
+    if (row && lane == 0 && wave % WPR == 0) static_cast<float*>(p.scales)[t] = scale;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = first + c * 64 * WPR;
+      if (row && at < chunks) {
+        const uint2 code = int8x8(h[c], inv);
+        *reinterpret_cast<uint2*>(p.codes + t * p.K + 8 * at) = inv == 0 ? make_uint2(0, 0) : code;
+      }
+    }
+  }
+}
+
+// Rows of any length are walked in strides of the workgroup: once for the
+// maximum, once (out of L2) for the codes.
+template <bool F32>
+__global__ __launch_bounds__(THREADS) void int8_quantize_kernel(const void* x, int64_t cols, int64_t ld, int8_t* codes,
+                                                                float* scales) {
+  __shared__ uint32_t red[4];
+  const int wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  uint32_t m = 0;
+  for (int64_t c = threadIdx.x * 8; c < cols; c += THREADS * 8) {
+    const F8 v = load8(x, t * ld + c, F32);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v.v[k]));
+  }
+  m = row_max<4>(m, red, wave);
+  float scale, inv;
+  int8_scale(m, scale, inv);
+  if (threadIdx.x == 0) scales[t] = scale;
+  for (int64_t c = threadIdx.x * 8; c < cols; c += THREADS * 8) {
+    const uint2 code = int8x8(load8(x, t * ld + c, F32), inv);
+    *reinterpret_cast<uint2*>(codes + t * cols + c) = inv == 0 ? make_uint2(0, 0) : code;
+  }
+}
+
+// Each workgroup walks rows in strides of the grid and keeps the sums of
+// dgamma of its columns in registers; the partial sums are added afterwards in
+// a fixed order.
+template <int WAVES, int CH>
+__global__ __launch_bounds__(64 * WAVES) void rmsnorm_bwd_kernel(NormBwdParams p) {
+  __shared__ float red[2][WAVES];
+  const int wave = threadIdx.x >> 6;
+  const int chunks = p.K / 8;
+  F8 gamma[CH], dg[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int at = (int)threadIdx.x + c * 64 * WAVES;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) gamma[c].v[k] = 1.0f, dg[c].v[k] = 0;
+    if (p.gamma && at < chunks) gamma[c] = load8(p.gamma, 8 * at, p.gamma_f32);
+  }
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+    const float rstd = p.rstd[t];
+    F8 xh[CH], dy[CH];
+    float dot = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = (int)threadIdx.x + c * 64 * WAVES;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) xh[c].v[k] = dy[c].v[k] = 0;
+      if (at < chunks) {
+        xh[c] = load8(p.h, t * p.ld_h + 8 * at, p.h_f32);
+        dy[c] = load8(p.dy, t * p.K + 8 * at, false);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        xh[c].v[k] *= rstd;
+        dg[c].v[k] = __builtin_fmaf(dy[c].v[k], xh[c].v[k], dg[c].v[k]);
+        dy[c].v[k] *= gamma[c].v[k];
+        dot = __builtin_fmaf(dy[c].v[k], xh[c].v[k], dot);
+      }
+    }
+    dot = row_sum<WAVES>(dot, red[turn], wave) / (float)p.K;
+    if (p.dx || p.dres)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int at = (int)threadIdx.x + c * 64 * WAVES;
+        if (at < chunks) {
+          F8 o;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o.v[k] = (dy[c].v[k] - xh[c].v[k] * dot) * rstd;
+          if (p.dh) {
+            const F8 d = load8(p.dh, t * p.K + 8 * at, p.h_f32);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o.v[k] += d.v[k];
+          }
+          if (p.dx) *reinterpret_cast<uint4*>(p.dx + t * p.K + 8 * at) = to_bf16(o);
+          if (p.dres) store8_f32(p.dres + t * p.K + 8 * at, o);
+        }
+      }
+  }
+  if (p.dgamma)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = (int)threadIdx.x + c * 64 * WAVES;
+      if (at < chunks) store8_f32(p.part + (int64_t)blockIdx.x * p.K + 8 * at, dg[c]);
+    }
+}
+
+// Column sums of the partial sums: eight columns to a workgroup's wave row, the
+// rows divided over its threads and joined in a fixed order.
+__global__ __launch_bounds__(THREADS) void dgamma_kernel(const float* part, int groups, int K, float* dgamma) {
+  __shared__ float red[16][17];
+  const int col = threadIdx.x & 15, sub = threadIdx.x >> 4;
+  const int k = blockIdx.x * 16 + col;
+  float s = 0;
+  if (k < K)
+    for (int g = sub; g < groups; g += 16) s += part[(int64_t)g * K + k];
+  red[sub][col] = s;
+  __syncthreads();
+  if (sub == 0 && k < K) {
+    s = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) s += red[q][col];
+    dgamma[k] = s;
+  }
+}
+
+template <int WPR, int CH>
+void norm(const NormParams& p, hipStream_t stream) {
+  constexpr int rows = WPR > 4 ? 1 : THREADS / 64 / WPR;
+  hipLaunchKernelGGL((rmsnorm_kernel<WPR, CH>), dim3((unsigned)((p.T + rows - 1) / rows)),
+                     dim3(WPR > 4 ? 64 * WPR : THREADS), 0, stream, p);
+}
+template <int WAVES, int CH>
+void norm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((rmsnorm_bwd_kernel<WAVES, CH>), dim3((unsigned)p.groups), dim3(64 * WAVES), 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormParams& p, hipStream_t stream) {
+  if (p.T == 0) return hipSuccess;
+  if (p.K <= 512) norm<1, 1>(p, stream);
+  else if (p.K <= 2048) norm<1, 4>(p, stream);
+  else if (p.K <= 8192) norm<4, 4>(p, stream);
+  else norm<16, 4>(p, stream);
+  return hipGetLastError();
+}
+
+int rmsnorm_bwd_groups(int64_t T, int K) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(T, K <= 2048 ? 2048 : K <= 8192 ? 1024 : 256));
+}
+
+hipError_t launch_rmsnorm_bwd(const NormBwdParams& p, hipStream_t stream) {
+  if (p.K <= 512) norm_bwd<1, 1>(p, stream);
+  else if (p.K <= 2048) norm_bwd<4, 1>(p, stream);
+  else if (p.K <= 8192) norm_bwd<4, 4>(p, stream);
+  else norm_bwd<16, 4>(p, stream);
+  if (p.dgamma)
+    hipLaunchKernelGGL(dgamma_kernel, dim3((unsigned)((p.K + 15) / 16)), dim3(THREADS), 0, stream, p.part, p.groups, p.K,
+                       p.dgamma);
+  return hipGetLastError();
+}
+
+hipError_t launch_int8_quantize(const void* x, int x_f32, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
+                                float* scales, hipStream_t stream) {
+  const dim3 grid((unsigned)rows);
+  if (x_f32) hipLaunchKernelGGL((int8_quantize_kernel<true>), grid, dim3(THREADS), 0, stream, x, cols, ld, codes, scales);
+  else hipLaunchKernelGGL((int8_quantize_kernel<false>), grid, dim3(THREADS), 0, stream, x, cols, ld, codes, scales);
+  return hipGetLastError();
+}
+
+}  // namespace mla
