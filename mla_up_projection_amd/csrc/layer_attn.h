@@ -28,22 +28,22 @@ typedef short la_i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) la_i16x4 la_lds_i16x4;
 typedef __attribute__((address_space(3))) const u32x4_t la_lds_u32x4;
 
-// Byte addresses of a lane's row fragments inside a tile: columns 16 j + 8 half,
-// j = 0..3 of a block, rows l % 32 (32 rows further: 4096 bytes).
+// Byte addresses of a lane's row fragments: columns 16 j + 8 half, j = 0..3 of a
+// block, rows l % 32 (32 rows further: 4096 bytes). The four differ in two bits, so
+// only the first is kept between tiles (`tile` a multiple of 128).
 struct RowAddr {
   uint32_t a[4];
 };
-__device__ __forceinline__ RowAddr row_addr(int lane) {
-  RowAddr r;
-  const int row = lane & 31, c0 = (lane >> 5) ^ tile_swz(row);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r.a[j] = (uint32_t)(row * 128 + ((c0 ^ (2 * j)) << 4));
-  return r;
+__device__ __forceinline__ uint32_t row_base(int lane) {
+  const int row = lane & 31;
+  return (uint32_t)(row * 128 + (((lane >> 5) ^ tile_swz(row)) << 4));
 }
-// R rows per tile; step j counts 16 columns, kb 32 rows.
+__device__ __forceinline__ RowAddr row_addr(uint32_t base) { return RowAddr{{base, base ^ 32, base ^ 64, base ^ 96}}; }
+// R rows per tile; step j counts 16 columns, kb 32 rows. `off` is a constant, like
+// the rest of what is added to the four addresses: it goes into the instruction.
 template <int R>
-__device__ __forceinline__ bf16x8_t row_frag(uint32_t tile, const RowAddr& ra, int j, int kb) {
-  const uint32_t at = tile + ra.a[j & 3] + (uint32_t)((j >> 2) * R * 128 + kb * 4096);
+__device__ __forceinline__ bf16x8_t row_frag(const RowAddr& ra, int off, int j, int kb) {
+  const uint32_t at = ra.a[j & 3] + (uint32_t)(off + (j >> 2) * R * 128 + kb * 4096);
   return __builtin_bit_cast(bf16x8_t, *(la_lds_u32x4*)(uintptr_t)at);
 }
 
@@ -51,26 +51,35 @@ __device__ __forceinline__ bf16x8_t row_frag(uint32_t tile, const RowAddr& ra, i
 struct ColAddr {
   uint32_t a[2][2];  // [first or second four rows][n odd]
 };
-__device__ __forceinline__ ColAddr col_addr(int lane) {
-  ColAddr r;
-  const int s = lane & 15, g = (lane >> 4) & 1, half = lane >> 5, e = s >> 2;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int row = 8 * u + 4 * half + e, chunk = 2 * g + ((s & 3) >> 1);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-      r.a[u][n] = (uint32_t)(row * 128 + (((chunk + 4 * n) ^ tile_swz(row)) << 4) + (s & 1) * 8);
-  }
-  return r;
+__device__ __forceinline__ uint32_t col_base(int lane) {
+  const int s = lane & 15, row = 4 * (lane >> 5) + (s >> 2), chunk = 2 * ((lane >> 4) & 1) + ((s & 3) >> 1);
+  return (uint32_t)(row * 128 + ((chunk ^ tile_swz(row)) << 4) + (s & 1) * 8);
+}
+__device__ __forceinline__ ColAddr col_addr(uint32_t base) {
+  const uint32_t next = (base + 1024) ^ 32;  // eight rows on
+  return ColAddr{{{base, base ^ 64}, {next, next ^ 64}}};
 }
 template <int R>
-__device__ __forceinline__ bf16x8_t col_frag(uint32_t tile, const ColAddr& ca, int n, int c) {
-  const uint32_t off = tile + (uint32_t)((n >> 1) * R * 128 + c * 2048);
-  const la_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_i16x4*)(uintptr_t)(ca.a[0][n & 1] + off));
-  const la_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_i16x4*)(uintptr_t)(ca.a[1][n & 1] + off));
+__device__ __forceinline__ bf16x8_t col_frag(const ColAddr& ca, int off, int n, int c) {
+  off += (n >> 1) * R * 128 + c * 2048;
+  const la_i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_i16x4*)(uintptr_t)(ca.a[0][n & 1] + (uint32_t)off));
+  const la_i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((la_lds_i16x4*)(uintptr_t)(ca.a[1][n & 1] + (uint32_t)off));
   typedef short i16x8 __attribute__((ext_vector_type(8)));
   const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// A phase of M matrix instructions, each followed by D LDS reads and V vector
+// instructions: the reads of the next phase and the arithmetic of this one go
+// between the matrix instructions instead of in front of them.
+template <int M, int D, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (D) __builtin_amdgcn_sched_group_barrier(0x100, D, 0);
+    if (V) __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+  }
 }
 
 // Eight values of a 32 x 32 result as the operand of step c & 1 of its rows.
@@ -102,17 +111,30 @@ template <int R, int W, int WAVES>
 __device__ __forceinline__ void load_tile(const uint16_t* base, uint32_t stride_bytes, int row0, int rows, int width,
                                           uint32_t tile, int wave, int lane) {
   const uint16_t* from = uniform(base + (int64_t)row0 * (stride_bytes >> 1));
-  const int last = rows - 1 - row0;
+  const int last = rows - 1 - row0, r0 = lane >> 3;
   constexpr int LOADS = R / 8 * (W / 64);
+  static_assert(LOADS % WAVES == 0, "every wave loads as much");
+  if (last >= R - 1 && width == W) {
+    // eight rows to a load: what differs between loads is the same for all lanes
+    // but for one bit of the rows' places
+    const uint32_t row = (uint32_t)r0 * stride_bytes;
+    const uint32_t at[2] = {row + (uint32_t)(((lane & 7) ^ tile_swz(r0)) << 4), row + (uint32_t)(((lane & 7) ^ tile_swz(r0 + 8)) << 4)};
 #pragma unroll
-  for (int i = 0; i < (LOADS + WAVES - 1) / WAVES; ++i) {
-    const int j = i * WAVES + wave, b = j / (R / 8), r8 = (j % (R / 8)) * 8;
-    if (LOADS % WAVES == 0 || j < LOADS) {
-      const int r = r8 + (lane >> 3);
-      int c = 64 * b + 8 * ((lane & 7) ^ tile_swz(r));
-      if (c >= width) c = 0;
-      dma16(from, (uint32_t)min(r, last) * stride_bytes + 2 * c, __builtin_amdgcn_readfirstlane(tile + j * 1024));
+    for (int i = 0; i < LOADS / WAVES; ++i) {
+      const int j = i * WAVES + wave, b = j / (R / 8), r8 = (j % (R / 8)) * 8;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(from) + (int64_t)((uint32_t)r8 * stride_bytes) + 128 * b;
+      dma16(uniform(reinterpret_cast<const uint16_t*>(src)), r8 & 8 ? at[1] : at[0],
+            __builtin_amdgcn_readfirstlane(tile + j * 1024));
     }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < LOADS / WAVES; ++i) {
+    const int j = i * WAVES + wave, b = j / (R / 8), r8 = (j % (R / 8)) * 8;
+    const int r = r8 + r0;
+    int c = 64 * b + 8 * ((lane & 7) ^ tile_swz(r));
+    if (c >= width) c = 0;
+    dma16(from, (uint32_t)min(r, last) * stride_bytes + 2 * c, __builtin_amdgcn_readfirstlane(tile + j * 1024));
   }
 }
 
@@ -128,6 +150,21 @@ __device__ __forceinline__ void load_row_frags(const uint16_t* row, int width, i
     f[j] = __builtin_bit_cast(bf16x8_t, v);
   }
 }
+
+// The registers hold their loaded values from here on: the compiler's wait for them
+// stands here, not at their first use in a loop, where it would wait for the tile
+// on its way in every step.
+template <int N>
+__device__ __forceinline__ void arrived(bf16x8_t (&f)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    u32x4_t v = __builtin_bit_cast(u32x4_t, f[j]);
+    asm volatile("" : "+v"(v));
+    f[j] = __builtin_bit_cast(bf16x8_t, v);
+  }
+}
+__device__ __forceinline__ void arrived(float& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void arrived(int& x) { asm volatile("" : "+v"(x)); }
 
 // ---------------------------------------------------------------------------
 // Scores. t = q . k scale; the scores are kept in powers of two (times log2 e).

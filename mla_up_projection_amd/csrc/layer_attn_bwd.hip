@@ -175,28 +175,24 @@ __device__ __forceinline__ void store_cols(uint16_t* out, const f32x16_t (&o)[NB
   }
 }
 
-// P and dS out of products and dP. Element r of a block: row 8 (r / 4) + 4 half + r %
-// 4 of the streamed tile's 32, column the lane's own.
+// P out of products, and with a cap its derivative. Element r of a block: row 8 (r /
+// 4) + 4 half + r % 4 of the streamed tile's 32, column the lane's own.
 template <bool EXTRA>
-__device__ __forceinline__ void weights(const ScoreForm& sf, f32x16_t& s, f32x16_t& dp, int r, int away, float lse2,
-                                        float delta, bool sees) {
-  float slope = 1.0f, x;
+__device__ __forceinline__ void probability(const ScoreForm& sf, f32x16_t& s, f32x16_t& slope, int r, int away, float lse2) {
+  float x;
   if (EXTRA) {
     x = s[r] * sf.scale2;
+    slope[r] = 1.0f;
     if (sf.cap2 > 0) {
       const float t = tanh_of(x);
-      slope = 1.0f - t * t;
+      slope[r] = 1.0f - t * t;
       x = sf.cap2 * t;
     }
     x = x - sf.slope2 * fabsf((float)away) - lse2;
   } else {
     x = __builtin_fmaf(s[r], sf.scale2, -lse2);
   }
-  const float w = __builtin_amdgcn_exp2f(x);
-  float ds = w * (dp[r] - delta);
-  if (EXTRA) ds *= slope;
-  s[r] = sees ? w : 0.0f;
-  dp[r] = sees ? ds : 0.0f;
+  s[r] = __builtin_amdgcn_exp2f(x);
 }
 
 template <int DK, int DV, bool EXTRA>
@@ -215,8 +211,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
   bf16x8_t kf[DK / 16], vf[DV / 16];
   load_row_frags<DK>(row_of(f.k, b, hk, min(j, f.Sk - 1)), f.d_k, half, kf);
   load_row_frags<DV>(row_of(f.v, b, hk, min(j, f.Sk - 1)), f.d_v, half, vf);
-  const RowAddr ra = row_addr(lane);
-  const ColAddr ca = col_addr(lane);
+  const uint32_t rb = row_base(lane), cb = col_base(lane);
   const uint32_t ring = lds_u32(lds);
   f32x16_t dk[DK / 32], dv[DV / 32];
 #pragma unroll
@@ -261,6 +256,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
             __builtin_amdgcn_readfirstlane(at + QB + OB + wave * 1024));
   };
   int tq = next(), slot = 0;
+  arrived(kf);
+  arrived(vf);
   vm_wait<0>();
   if (tq >= 0) issue(tq, h, 0);
   ScoreForm sf = score_form(f, min(h, f.H - 1));
@@ -273,44 +270,89 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
     vm_wait<0>();
     barrier();
     if (tq >= 0) issue(tq, h, slot ^ 1);
-    const uint32_t qt = ring + slot * SB, ot = qt + QB;
+    const RowAddr rows = row_addr(rb + (ring + slot * SB));
+    const ColAddr cols = col_addr(cb + (ring + slot * SB));
     const uint8_t* rec = lds + slot * SB + QB + OB;
     slot ^= 1;
+    // Four phases for 32 queries: the products for S, dP, dV and dK. Each reads the
+    // next one's operands while its own matrix instructions run.
+    bf16x8_t qr[DK / 16];
+#pragma unroll
+    for (int c = 0; c < DK / 16; ++c) qr[c] = row_frag<TT>(rows, 0, c, 0);
 #pragma unroll
     for (int qb = 0; qb < 2; ++qb) {
-      f32x16_t s = zero16(), dp = zero16();
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      f32x16_t s, dp;
+      bf16x8_t dr[DV / 16], dc[DV / 32][2], qc[DK / 32][2];
+      f32x4_t lse2[4], delta[4];
+      i32x4 lo[4], hi[4], at[4];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = 0; c < DK / 16; ++c)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(qt, ra, c, qb), kf[c], s, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < DV / 16; ++c)
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(ot, ra, c, qb), vf[c], dp, 0, 0, 0);
+      for (int c = 0; c < DV / 16; ++c) dr[c] = row_frag<TT>(rows, QB, c, qb);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int row = 32 * qb + 8 * g + 4 * half;
-        const f32x4_t lse2 = *reinterpret_cast<const f32x4_t*>(rec + 4 * row);
-        const f32x4_t delta = *reinterpret_cast<const f32x4_t*>(rec + 4 * (TT + row));
-        typedef int i32x4 __attribute__((ext_vector_type(4)));
-        i32x4 lo = {0, 0, 0, 0}, hi = lo, at = lo;
-        if (!all) {
-          lo = *reinterpret_cast<const i32x4*>(rec + 4 * (2 * TT + row));
-          hi = *reinterpret_cast<const i32x4*>(rec + 4 * (3 * TT + row));
+        lse2[g] = *reinterpret_cast<const f32x4_t*>(rec + 4 * row);
+        delta[g] = *reinterpret_cast<const f32x4_t*>(rec + 4 * (TT + row));
+        lo[g] = hi[g] = at[g] = i32x4{0, 0, 0, 0};
+        if (EXTRA) at[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (4 * TT + row));
+      }
+#pragma unroll
+      for (int c = 0; c < DK / 16; ++c) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qr[c], kf[c], c ? s : zero16(), 0, 0, 0);
+      interleave<DK / 16, 2, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      if (!all)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int row = 32 * qb + 8 * g + 4 * half;
+          lo[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (2 * TT + row));
+          hi[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (3 * TT + row));
         }
-        if (EXTRA) at = *reinterpret_cast<const i32x4*>(rec + 4 * (4 * TT + row));
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          weights<EXTRA>(form, s, dp, 4 * g + r, at[r] - j, lse2[r], delta[r], all || (j >= lo[r] && j < hi[r]));
-      }
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bf16x8_t w = pack_frag(s, c), d = pack_frag(dp, c);
+        for (int n = 0; n < DV / 32; ++n) dc[n][c] = col_frag<TT>(cols, QB, n, 2 * qb + c);
 #pragma unroll
-        for (int n = 0; n < DV / 32; ++n)
-          dv[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TT>(ot, ca, n, 2 * qb + c), w, dv[n], 0, 0, 0);
+      for (int c = 0; c < DV / 16; ++c) dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(dr[c], vf[c], c ? dp : zero16(), 0, 0, 0);
+      f32x16_t slope;
 #pragma unroll
-        for (int n = 0; n < DK / 32; ++n)
-          dk[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TT>(qt, ca, n, 2 * qb + c), d, dk[n], 0, 0, 0);
-      }
+      for (int r = 0; r < 16; ++r)
+        probability<EXTRA>(form, s, slope, r, at[r / 4][r % 4] - j, lse2[r / 4][r % 4]);
+      if (!all)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = j >= lo[r / 4][r % 4] && j < hi[r / 4][r % 4] ? s[r] : 0.0f;
+      const bf16x8_t w[2] = {pack_frag(s, 0), pack_frag(s, 1)};
+      interleave<DV / 16, 2, 8>();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int n = 0; n < DK / 32; ++n) qc[n][c] = col_frag<TT>(cols, 0, n, 2 * qb + c);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int n = 0; n < DV / 32; ++n) dv[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(dc[n][c], w[c], dv[n], 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta[r / 4][r % 4]);
+      if (EXTRA)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
+      if (!all)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] = j >= lo[r / 4][r % 4] && j < hi[r / 4][r % 4] ? dp[r] : 0.0f;
+      const bf16x8_t d[2] = {pack_frag(dp, 0), pack_frag(dp, 1)};
+      interleave<DV / 16, 3, 6>();
+      __builtin_amdgcn_sched_barrier(0);
+      if (qb == 0)
+#pragma unroll
+        for (int c = 0; c < DK / 16; ++c) qr[c] = row_frag<TT>(rows, 0, c, 1);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int n = 0; n < DK / 32; ++n) dk[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qc[n][c], d[c], dk[n], 0, 0, 0);
+      interleave<DK / 16, 1, 0>();
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   const bool live = j < f.Sk;
@@ -359,13 +401,12 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   const ScoreForm sf = score_form(f, h);
   const int ic = min(i, f.Sq - 1);
   const float* rec = record(p, b, h, ic / TT);
-  const float lse2 = rec[ic % TT], delta = rec[TT + ic % TT];
-  const int place = EXTRA ? __float_as_int(rec[4 * TT + ic % TT]) : 0;
+  float lse2 = rec[ic % TT], delta = rec[TT + ic % TT];
+  int place = EXTRA ? __float_as_int(rec[4 * TT + ic % TT]) : 0;
   bf16x8_t q[DK / 16], d[DV / 16];
   load_row_frags<DK>(row_of(f.q, b, h, ic), f.d_k, half, q);
   load_row_frags<DV>(row_of(p.dout, b, h, ic), f.d_v, half, d);
-  const RowAddr ra = row_addr(lane);
-  const ColAddr ca = col_addr(lane);
+  const uint32_t rb = row_base(lane), cb = col_base(lane);
   const uint32_t ring = lds_u32(lds);
   const uint16_t *kb = row_of(f.k, b, hk, 0), *vb = row_of(f.v, b, hk, 0);
   const auto issue = [&](int t, int slot) {
@@ -375,6 +416,11 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   f32x16_t dq[DK / 32];
 #pragma unroll
   for (int n = 0; n < DK / 32; ++n) dq[n] = zero16();
+  arrived(q);
+  arrived(d);
+  arrived(lse2);
+  arrived(delta);
+  arrived(place);
   vm_wait<0>();
   if (first < last) issue(first, 0);
   for (int t = first; t < last; ++t) {
@@ -382,30 +428,65 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
     vm_wait<0>();
     barrier();
     if (t + 1 < last) issue(t + 1, slot ^ 1);
-    const uint32_t kt = ring + slot * SB, vt = kt + KB;
+    const RowAddr rows = row_addr(rb + (ring + slot * SB));
+    const ColAddr cols = col_addr(cb + (ring + slot * SB));
     const bool all = t * TT >= wlo_all && (t + 1) * TT <= whi_all;
+    // The operands of a block of 32 keys are one stream: K by rows for S, V by rows
+    // for dP, K by columns for dQ, read AHEAD matrix instructions before their use.
+    constexpr int NS = DK / 16, NP = DV / 16, NQ = DK / 16, N = NS + NP + NQ, AHEAD = 4;
+    bf16x8_t op[AHEAD];
+    const auto read = [&](int x) {
+      const int k = x / N, y = x % N;
+      op[x % AHEAD] = y < NS ? row_frag<TT>(rows, 0, y, k)
+                      : y < NS + NP ? row_frag<TT>(rows, KB, y - NS, k)
+                                    : col_frag<TT>(cols, 0, (y - NS - NP) % (DK / 32), 2 * k + (y - NS - NP) / (DK / 32));
+    };
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) read(x);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      f32x16_t s = zero16(), dp = zero16();
+      f32x16_t s, dp, slope;
 #pragma unroll
-      for (int c = 0; c < DK / 16; ++c)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(kt, ra, c, k), q[c], s, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < DV / 16; ++c)
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TT>(vt, ra, c, k), d[c], dp, 0, 0, 0);
+      for (int c = 0; c < NS; ++c) {
+        const int x = k * N + c;
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], q[c], c ? s : zero16(), 0, 0, 0);
+        read(x + AHEAD);
+      }
+      interleave<NS, 1, 0>();
+      __builtin_amdgcn_sched_barrier(0);
       const int j0 = t * TT + 32 * k + 4 * half;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int j = j0 + 8 * (r / 4) + r % 4;
-        weights<EXTRA>(sf, s, dp, r, place - j, lse2, delta, all || (uint32_t)(j - sp.lo) < (uint32_t)(sp.hi - sp.lo));
+      for (int c = 0; c < NP; ++c) {
+        const int x = k * N + NS + c;
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], d[c], c ? dp : zero16(), 0, 0, 0);
+        read(x + AHEAD);
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bf16x8_t w = pack_frag(dp, c);
+      for (int r = 0; r < 16; ++r) probability<EXTRA>(sf, s, slope, r, place - (j0 + 8 * (r / 4) + r % 4), lse2);
+      interleave<NP - AHEAD, 1, 4>();
+      interleave<AHEAD, 2, 4>();
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = 0; n < DK / 32; ++n)
-          dq[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TT>(kt, ca, n, 2 * k + c), w, dq[n], 0, 0, 0);
+      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
+      if (EXTRA)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
+      if (!all)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if ((uint32_t)(j0 + 8 * (r / 4) + r % 4 - sp.lo) >= (uint32_t)(sp.hi - sp.lo)) dp[r] = 0.0f;
+      const bf16x8_t w[2] = {pack_frag(dp, 0), pack_frag(dp, 1)};
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < NQ; ++c) {
+        const int x = k * N + NS + NP + c;
+        dq[c % (DK / 32)] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], w[c / (DK / 32)], dq[c % (DK / 32)], 0, 0, 0);
+        if (x + AHEAD < 2 * N) read(x + AHEAD);
       }
+      interleave<NQ - AHEAD, 2, 0>();
+      interleave<AHEAD, 1, 0>();
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   const bool live = i < f.Sq;

@@ -109,7 +109,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   }
 
   const ScoreForm sf = score_form(p, h);
-  const int place = EXTRA && p.slopes && i < p.Sq ? row_place(p, b, i) : 0;
+  int place = EXTRA && p.slopes && i < p.Sq ? row_place(p, b, i) : 0;
+  arrived(place);
   bf16x8_t q[F::NJ];
   load_row_frags<DK>(row_of(p.q, b, h, min(i, p.Sq - 1)), p.d_k, half, q);
   const uint16_t* kb = row_of(p.k, b, hk, 0);
@@ -120,12 +121,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     load_tile<TK, DK, WAVES>(kb, ks, t * TK, p.Sk, p.d_k, ring + slot * F::SB, wave, lane);
     load_tile<TK, DV, WAVES>(vb, vs, t * TK, p.Sk, p.d_v, ring + slot * F::SB + F::KB, wave, lane);
   };
-  const RowAddr ra = row_addr(lane);
-  const ColAddr ca = col_addr(lane);
+  const uint32_t rb = row_base(lane), cb = col_base(lane);
   f32x16_t o[F::NV];
 #pragma unroll
   for (int n = 0; n < F::NV; ++n) o[n] = zero16();
   float m = -__builtin_inff(), l = 0;
+  arrived(q);
   vm_wait<0>();
   if (first < last) issue(first, 0);
   for (int t = first; t < last; ++t) {
@@ -133,15 +134,30 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     vm_wait<0>();
     barrier();
     if (t + 1 < last) issue(t + 1, slot ^ 1);
-    const uint32_t kt = ring + slot * F::SB, vt = kt + F::KB;
+    const RowAddr kt = row_addr(rb + (ring + slot * F::SB));
+    const ColAddr vt = col_addr(cb + (ring + slot * F::SB));
+    // The operands of a tile are one stream: K by rows for S, then V by columns for O,
+    // read AHEAD matrix instructions before their use.
+    constexpr int NS = 2 * F::NJ, NO = 4 * F::NV, AHEAD = 6;
+    static_assert(F::NV <= 4 && NS >= AHEAD, "the first AHEAD of V are read in the products for S");
+    bf16x8_t op[AHEAD];
+    const auto read = [&](int x) {
+      if (x < NS) op[x % AHEAD] = row_frag<TK>(kt, 0, x % F::NJ, x / F::NJ);
+      else op[x % AHEAD] = col_frag<TK>(vt, F::KB, (x - NS) % F::NV, (x - NS) / F::NV);
+    };
     f32x16_t s[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      s[k] = zero16();
+    for (int x = 0; x < AHEAD; ++x) read(x);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < F::NJ; ++j)
-        s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(row_frag<TK>(kt, ra, j, k), q[j], s[k], 0, 0, 0);
+    for (int x = 0; x < NS; ++x) {
+      const int k = x / F::NJ, j = x % F::NJ;
+      s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], q[j], j ? s[k] : zero16(), 0, 0, 0);
+      read(x + AHEAD);
     }
+    interleave<NS - AHEAD, 1, 0>();
+    interleave<AHEAD, 2, 0>();
+    __builtin_amdgcn_sched_barrier(0);
     // element r of block k: key t TK + 32 k + 8 (r / 4) + 4 half + r % 4
     const int j0 = t * TK + 4 * half;
     if (EXTRA) {
@@ -193,13 +209,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
         s[k][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][r], sc, -mu));
         l += s[k][r];
       }
+    bf16x8_t w[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const bf16x8_t w = pack_frag(s[c >> 1], c & 1);
+    for (int c = 0; c < 4; ++c) w[c] = pack_frag(s[c >> 1], c & 1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int n = 0; n < F::NV; ++n)
-        o[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(col_frag<TK>(vt, ca, n, c), w, o[n], 0, 0, 0);
+    for (int y = 0; y < NO; ++y) {
+      const int x = NS + y, n = y % F::NV;
+      o[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], w[y / F::NV], o[n], 0, 0, 0);
+      if (y + AHEAD < NO) read(x + AHEAD);
     }
+    interleave<NO - AHEAD, 2, 0>();
+    interleave<AHEAD, 1, 0>();
+    __builtin_amdgcn_sched_barrier(0);
   }
   {
     const u32x2_t x = swap_halves(__float_as_uint(l), __float_as_uint(l));
