@@ -90,6 +90,10 @@ __device__ __forceinline__ bf16x8_t pack_frag(const f32x16_t& s, int c) {
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
+// At the head of a branch that hardly runs: keeps its arithmetic from being done in
+// every case and selected afterwards.
+__device__ __forceinline__ void rare() { asm volatile(""); }
+
 __device__ __forceinline__ f32x16_t zero16() {
   f32x16_t z;
 #pragma unroll

@@ -285,7 +285,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
       f32x16_t s, dp;
       bf16x8_t dr[DV / 16], dc[DV / 32][2], qc[DK / 32][2];
       f32x4_t lse2[4], delta[4];
-      i32x4 lo[4], hi[4], at[4];
+      i32x4 at[4];
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int c = 0; c < DV / 16; ++c) dr[c] = row_frag<TT>(rows, QB, c, qb);
@@ -294,20 +294,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
         const int row = 32 * qb + 8 * g + 4 * half;
         lse2[g] = *reinterpret_cast<const f32x4_t*>(rec + 4 * row);
         delta[g] = *reinterpret_cast<const f32x4_t*>(rec + 4 * (TT + row));
-        lo[g] = hi[g] = at[g] = i32x4{0, 0, 0, 0};
         if (EXTRA) at[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (4 * TT + row));
       }
 #pragma unroll
       for (int c = 0; c < DK / 16; ++c) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qr[c], kf[c], c ? s : zero16(), 0, 0, 0);
       interleave<DK / 16, 2, 0>();
-      __builtin_amdgcn_sched_barrier(0);
-      if (!all)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int row = 32 * qb + 8 * g + 4 * half;
-          lo[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (2 * TT + row));
-          hi[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (3 * TT + row));
-        }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -318,12 +309,22 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
       f32x16_t slope;
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        probability<EXTRA>(form, s, slope, r, at[r / 4][r % 4] - j, lse2[r / 4][r % 4]);
-      if (!all)
+        probability<EXTRA>(form, s, slope, r, EXTRA ? at[r / 4][r % 4] - j : 0, lse2[r / 4][r % 4]);
+      interleave<DV / 16, 2, 6>();
+      __builtin_amdgcn_sched_barrier(0);
+      if (!all) {
+        // (dS is 0 with P, unless dP is not finite, which the results then show)
+        rare();
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = j >= lo[r / 4][r % 4] && j < hi[r / 4][r % 4] ? s[r] : 0.0f;
+        for (int g = 0; g < 4; ++g) {
+          const int row = 32 * qb + 8 * g + 4 * half;
+          const i32x4 lo = *reinterpret_cast<const i32x4*>(rec + 4 * (2 * TT + row));
+          const i32x4 hi = *reinterpret_cast<const i32x4*>(rec + 4 * (3 * TT + row));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[4 * g + r] = j >= lo[r] && j < hi[r] ? s[4 * g + r] : 0.0f;
+        }
+      }
       const bf16x8_t w[2] = {pack_frag(s, 0), pack_frag(s, 1)};
-      interleave<DV / 16, 2, 8>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -338,9 +339,6 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
       if (EXTRA)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
-      if (!all)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) dp[r] = j >= lo[r / 4][r % 4] && j < hi[r / 4][r % 4] ? dp[r] : 0.0f;
       const bf16x8_t d[2] = {pack_frag(dp, 0), pack_frag(dp, 1)};
       interleave<DV / 16, 3, 6>();
       __builtin_amdgcn_sched_barrier(0);
@@ -472,10 +470,12 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
       if (EXTRA)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
-      if (!all)
+      if (!all) {
+        rare();
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if ((uint32_t)(j0 + 8 * (r / 4) + r % 4 - sp.lo) >= (uint32_t)(sp.hi - sp.lo)) dp[r] = 0.0f;
+      }
       const bf16x8_t w[2] = {pack_frag(dp, 0), pack_frag(dp, 1)};
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -171,6 +171,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
         }
     }
     if (t * TK < wlo_all || (t + 1) * TK > whi_all) {
+      rare();
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -192,6 +193,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     // up to that lose nothing in bf16 and fp32.
     const bool rise = mt > m + 8.0f || (m == -__builtin_inff() && mt > m);
     if (__builtin_amdgcn_ballot_w64(rise)) {
+      rare();
       const float mn = fmaxf(m, mt);
       const float a = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
