@@ -108,39 +108,44 @@ __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
 }
 
 // Rows row0 .. row0 + R - 1 of `width` columns into a tile of W columns by direct
-// loads; WAVES waves share them. Rows from `rows` on repeat the last one and
-// columns from `width` on the row's first: what they hold meets zeros or is
-// masked. `base`: the first row of this batch entry and head.
+// loads of eight rows by 64 columns; WAVES waves share them, PIECES each. Rows from
+// `rows` on repeat the last one and columns from `width` on the row's first: what
+// they hold meets zeros or is masked. The pieces are issued one at a time, between
+// matrix instructions.
 template <int R, int W, int WAVES>
-__device__ __forceinline__ void load_tile(const uint16_t* base, uint32_t stride_bytes, int row0, int rows, int width,
-                                          uint32_t tile, int wave, int lane) {
-  const uint16_t* from = uniform(base + (int64_t)row0 * (stride_bytes >> 1));
-  const int last = rows - 1 - row0, r0 = lane >> 3;
-  constexpr int LOADS = R / 8 * (W / 64);
-  static_assert(LOADS % WAVES == 0, "every wave loads as much");
-  if (last >= R - 1 && width == W) {
-    // eight rows to a load: what differs between loads is the same for all lanes
-    // but for one bit of the rows' places
-    const uint32_t row = (uint32_t)r0 * stride_bytes;
-    const uint32_t at[2] = {row + (uint32_t)(((lane & 7) ^ tile_swz(r0)) << 4), row + (uint32_t)(((lane & 7) ^ tile_swz(r0 + 8)) << 4)};
+struct TileLoads {
+  static constexpr int PIECES = R / 8 * (W / 64) / WAVES;
+  static constexpr int KINDS = WAVES == 1 ? 2 : 1;  // (places alternate between groups of eight rows)
+  static_assert(R % 16 == 0 && (R / 8) % WAVES == 0 && (WAVES == 1 || WAVES % 2 == 0), "every wave loads as much");
+  uint32_t col[KINDS][W / 64];  // bytes into the row
+  const uint16_t* from;
+  uint32_t stride;
+  int last, wave, r0;
+
+  __device__ __forceinline__ TileLoads(int width, uint32_t stride_bytes, int w, int lane) : stride(stride_bytes), wave(w), r0(lane >> 3) {
 #pragma unroll
-    for (int i = 0; i < LOADS / WAVES; ++i) {
-      const int j = i * WAVES + wave, b = j / (R / 8), r8 = (j % (R / 8)) * 8;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(from) + (int64_t)((uint32_t)r8 * stride_bytes) + 128 * b;
-      dma16(uniform(reinterpret_cast<const uint16_t*>(src)), r8 & 8 ? at[1] : at[0],
-            __builtin_amdgcn_readfirstlane(tile + j * 1024));
-    }
-    return;
-  }
+    for (int k = 0; k < KINDS; ++k)
 #pragma unroll
-  for (int i = 0; i < LOADS / WAVES; ++i) {
-    const int j = i * WAVES + wave, b = j / (R / 8), r8 = (j % (R / 8)) * 8;
-    const int r = r8 + r0;
-    int c = 64 * b + 8 * ((lane & 7) ^ tile_swz(r));
-    if (c >= width) c = 0;
-    dma16(from, (uint32_t)min(r, last) * stride_bytes + 2 * c, __builtin_amdgcn_readfirstlane(tile + j * 1024));
+      for (int b = 0; b < W / 64; ++b) {
+        const int c = 64 * b + 8 * ((lane & 7) ^ tile_swz(r0 + 8 * (WAVES == 1 ? k : w & 1)));
+        col[k][b] = c < width ? 2 * c : 0;
+      }
   }
-}
+  // base: the first row of the batch entry and head
+  __device__ __forceinline__ void begin(const uint16_t* base, int row0, int rows) {
+    from = uniform(base + (int64_t)row0 * (stride >> 1));
+    last = rows - 1 - row0;
+  }
+  __device__ __forceinline__ void piece(int i, uint32_t tile) const {
+    const int j = i * WAVES + wave, b = i * WAVES / (R / 8), r8 = (j % (R / 8)) * 8;
+    const uint32_t row = (uint32_t)min(r0 + r8, last);
+    dma16(from, __umul24(row, stride) + col[WAVES == 1 ? i & 1 : 0][b], __builtin_amdgcn_readfirstlane(tile + j * 1024));
+  }
+  __device__ __forceinline__ void all(uint32_t tile) const {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) piece(i, tile);
+  }
+};
 
 // A lane's fragments of one row kept in registers: columns 16 j + 8 half of
 // the row, zeros past its width.

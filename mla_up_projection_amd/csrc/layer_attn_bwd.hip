@@ -246,20 +246,29 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
     all_next = (whole >> r) & 1;
     return word * 64 + r;
   };
-  const auto issue = [&](int tq, int head, int slot) {
-    const uint32_t at = ring + slot * SB;
-    load_tile<TT, DK, 4>(row_of(f.q, b, head, 0), (uint32_t)(f.q.ss * 2), tq * TT, f.Sq, f.d_k, at, wave, lane);
-    load_tile<TT, DV, 4>(row_of(p.dout, b, head, 0), (uint32_t)(p.dout.ss * 2), tq * TT, f.Sq, f.d_v, at + QB, wave, lane);
-    const float* rec = record(p, b, head, tq);
+  TileLoads<TT, DK, 4> ql(f.d_k, (uint32_t)(f.q.ss * 2), wave, lane);
+  TileLoads<TT, DV, 4> ol(f.d_v, (uint32_t)(p.dout.ss * 2), wave, lane);
+  const float* rec_from = nullptr;
+  const auto begin = [&](int tq, int head) {
+    ql.begin(row_of(f.q, b, head, 0), tq * TT, f.Sq);
+    ol.begin(row_of(p.dout, b, head, 0), tq * TT, f.Sq);
+    rec_from = record(p, b, head, tq);
+  };
+  const auto load_record = [&](uint32_t at) {
     if (wave < (EXTRA ? 2 : 1))
-      dma16(uniform(reinterpret_cast<const uint16_t*>(rec)), wave * 1024 + lane * 16,
+      dma16(uniform(reinterpret_cast<const uint16_t*>(rec_from)), wave * 1024 + lane * 16,
             __builtin_amdgcn_readfirstlane(at + QB + OB + wave * 1024));
   };
   int tq = next(), slot = 0;
   arrived(kf);
   arrived(vf);
   vm_wait<0>();
-  if (tq >= 0) issue(tq, h, 0);
+  if (tq >= 0) {
+    begin(tq, h);
+    ql.all(ring);
+    ol.all(ring + QB);
+    load_record(ring);
+  }
   ScoreForm sf = score_form(f, min(h, f.H - 1));
   while (tq >= 0) {
     const ScoreForm form = sf;
@@ -269,7 +278,9 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
     if (EXTRA && tq >= 0 && h != head) sf = score_form(f, h);
     vm_wait<0>();
     barrier();
-    if (tq >= 0) issue(tq, h, slot ^ 1);
+    const bool more = tq >= 0;
+    const uint32_t fill = ring + (slot ^ 1) * SB;
+    if (more) begin(tq, h);
     const RowAddr rows = row_addr(rb + (ring + slot * SB));
     const ColAddr cols = col_addr(cb + (ring + slot * SB));
     const uint8_t* rec = lds + slot * SB + QB + OB;
@@ -297,8 +308,21 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
         if (EXTRA) at[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (4 * TT + row));
       }
 #pragma unroll
-      for (int c = 0; c < DK / 16; ++c) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qr[c], kf[c], c ? s : zero16(), 0, 0, 0);
-      interleave<DK / 16, 2, 0>();
+      for (int c = 0; c < DK / 16; ++c) {
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qr[c], kf[c], c ? s : zero16(), 0, 0, 0);
+        if (qb == 0) {  // the next tile's loads, one behind each
+          __builtin_amdgcn_sched_barrier(0);
+          constexpr int PQ = decltype(ql)::PIECES, PO = decltype(ol)::PIECES;
+          static_assert(PQ + PO <= DK / 16, "a load between two matrix instructions");
+          if (more) {
+            if (c < PQ) ql.piece(c, fill);
+            else if (c < PQ + PO) ol.piece(c - PQ, fill + QB);
+            if (c == 0) load_record(fill);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (qb == 1) interleave<DK / 16, 2, 0>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -407,10 +431,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   const uint32_t rb = row_base(lane), cb = col_base(lane);
   const uint32_t ring = lds_u32(lds);
   const uint16_t *kb = row_of(f.k, b, hk, 0), *vb = row_of(f.v, b, hk, 0);
-  const auto issue = [&](int t, int slot) {
-    load_tile<TT, DK, 4>(kb, (uint32_t)(f.k.ss * 2), t * TT, f.Sk, f.d_k, ring + slot * SB, wave, lane);
-    load_tile<TT, DV, 4>(vb, (uint32_t)(f.v.ss * 2), t * TT, f.Sk, f.d_v, ring + slot * SB + KB, wave, lane);
-  };
+  TileLoads<TT, DK, 4> kl(f.d_k, (uint32_t)(f.k.ss * 2), wave, lane);
+  TileLoads<TT, DV, 4> vl(f.d_v, (uint32_t)(f.v.ss * 2), wave, lane);
   f32x16_t dq[DK / 32];
 #pragma unroll
   for (int n = 0; n < DK / 32; ++n) dq[n] = zero16();
@@ -420,12 +442,24 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   arrived(delta);
   arrived(place);
   vm_wait<0>();
-  if (first < last) issue(first, 0);
+  if (first < last) {
+    kl.begin(kb, first * TT, f.Sk);
+    vl.begin(vb, first * TT, f.Sk);
+    kl.all(ring);
+    vl.all(ring + KB);
+  }
   for (int t = first; t < last; ++t) {
     const int slot = (t - first) & 1;
+    const uint32_t fill = ring + (slot ^ 1) * SB;
     vm_wait<0>();
     barrier();
-    if (t + 1 < last) issue(t + 1, slot ^ 1);
+    const bool more = t + 1 < last;
+    if (more) {
+      kl.begin(kb, (t + 1) * TT, f.Sk);
+      vl.begin(vb, (t + 1) * TT, f.Sk);
+      kl.all(fill);
+      vl.all(fill + KB);
+    }
     const RowAddr rows = row_addr(rb + (ring + slot * SB));
     const ColAddr cols = col_addr(cb + (ring + slot * SB));
     const bool all = t * TT >= wlo_all && (t + 1) * TT <= whi_all;

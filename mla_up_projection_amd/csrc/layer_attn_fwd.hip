@@ -115,12 +115,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   load_row_frags<DK>(row_of(p.q, b, h, min(i, p.Sq - 1)), p.d_k, half, q);
   const uint16_t* kb = row_of(p.k, b, hk, 0);
   const uint16_t* vb = row_of(p.v, b, hk, 0);
-  const uint32_t ks = (uint32_t)(p.k.ss * 2), vs = (uint32_t)(p.v.ss * 2);
   const uint32_t ring = lds_u32(lds);
-  const auto issue = [&](int t, int slot) {
-    load_tile<TK, DK, WAVES>(kb, ks, t * TK, p.Sk, p.d_k, ring + slot * F::SB, wave, lane);
-    load_tile<TK, DV, WAVES>(vb, vs, t * TK, p.Sk, p.d_v, ring + slot * F::SB + F::KB, wave, lane);
-  };
+  TileLoads<TK, DK, WAVES> kl(p.d_k, (uint32_t)(p.k.ss * 2), wave, lane);
+  TileLoads<TK, DV, WAVES> vl(p.d_v, (uint32_t)(p.v.ss * 2), wave, lane);
   const uint32_t rb = row_base(lane), cb = col_base(lane);
   f32x16_t o[F::NV];
 #pragma unroll
@@ -128,12 +125,22 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   float m = -__builtin_inff(), l = 0;
   arrived(q);
   vm_wait<0>();
-  if (first < last) issue(first, 0);
+  if (first < last) {
+    kl.begin(kb, first * TK, p.Sk);
+    vl.begin(vb, first * TK, p.Sk);
+    kl.all(ring);
+    vl.all(ring + F::KB);
+  }
   for (int t = first; t < last; ++t) {
     const int slot = (t - first) & 1;
+    const uint32_t fill = ring + (slot ^ 1) * F::SB;
     vm_wait<0>();
     barrier();
-    if (t + 1 < last) issue(t + 1, slot ^ 1);
+    const bool more = t + 1 < last;
+    if (more) {
+      kl.begin(kb, (t + 1) * TK, p.Sk);
+      vl.begin(vb, (t + 1) * TK, p.Sk);
+    }
     const RowAddr kt = row_addr(rb + (ring + slot * F::SB));
     const ColAddr vt = col_addr(cb + (ring + slot * F::SB));
     // The operands of a tile are one stream: K by rows for S, then V by columns for O,
@@ -142,21 +149,34 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     static_assert(F::NV <= 4 && NS >= AHEAD, "the first AHEAD of V are read in the products for S");
     bf16x8_t op[AHEAD];
     const auto read = [&](int x) {
-      if (x < NS) op[x % AHEAD] = row_frag<TK>(kt, 0, x % F::NJ, x / F::NJ);
+      if (x < NS) op[x % AHEAD] = row_frag<TK>(kt, 0, x / 2, x & 1);
       else op[x % AHEAD] = col_frag<TK>(vt, F::KB, (x - NS) % F::NV, (x - NS) / F::NV);
     };
     f32x16_t s[2];
 #pragma unroll
     for (int x = 0; x < AHEAD; ++x) read(x);
     __builtin_amdgcn_sched_barrier(0);
+    constexpr int PK = decltype(kl)::PIECES, PV = decltype(vl)::PIECES, EVERY = NS / (PK + PV);
+    static_assert(EVERY >= 1 || WAVES == 1, "a load between two matrix instructions");
 #pragma unroll
     for (int x = 0; x < NS; ++x) {
-      const int k = x / F::NJ, j = x % F::NJ;
+      const int k = x & 1, j = x / 2;  // two sums in turn
       s[k] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], q[j], j ? s[k] : zero16(), 0, 0, 0);
       read(x + AHEAD);
+      if (EVERY >= 1 ? x % EVERY == 0 : true) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+          constexpr int EACH = EVERY >= 1 ? 1 : (PK + PV + NS - 1) / NS;
+          const int i0 = EVERY >= 1 ? x / EVERY : x * EACH;
+#pragma unroll
+          for (int i = i0; i < i0 + EACH; ++i) {
+            if (i < PK) kl.piece(i, fill);
+            else if (i < PK + PV) vl.piece(i - PK, fill + F::KB);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    interleave<NS - AHEAD, 1, 0>();
-    interleave<AHEAD, 2, 0>();
     __builtin_amdgcn_sched_barrier(0);
     // element r of block k: key t TK + 32 k + 8 (r / 4) + 4 half + r % 4
     const int j0 = t * TK + 4 * half;
