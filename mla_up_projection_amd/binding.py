@@ -767,12 +767,23 @@ def _dtype_of(t) -> int:
 
 
 def _opt(chk, t, name, dtype, numel):
-    """Device address of a tensor that may be missing."""
+    """Device address of a tensor that may be missing; _Dev's checks, and its words where one fails."""
     if t is None:
         return None
-    if chk.device is not None and _is(t, dtype, numel, chk.device):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel and t.device == chk.device
+            and t.is_contiguous()):
         return t.data_ptr()
     return chk(t, name, (dtype,), numel=numel)
+
+
+def _float(chk, t, name, numel):
+    """The same for a bf16 or fp32 tensor, and its type."""
+    if t is None:
+        return None, DTYPE_BF16
+    if isinstance(t, torch.Tensor) and t.dtype is _FP32:
+        return _opt(chk, t, name, _FP32, numel), DTYPE_FP32
+    return (_opt(chk, t, name, _BF16, numel) if isinstance(t, torch.Tensor) and t.dtype is _BF16
+            else chk(t, name, _FLOATS, numel=numel)), DTYPE_BF16
 
 
 def _row_view(chk, t, name, dtypes):
@@ -780,10 +791,12 @@ def _row_view(chk, t, name, dtypes):
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or (t.stride(1) != 1 and t.numel() and t.shape[1] > 1):
         raise ValueError(f"{chk.where}: {name} must be 2-D with contiguous rows")
     rows, cols = t.shape
-    if rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{chk.where}: the rows of {name} overlap")
     ld = t.stride(0) if rows > 1 else cols
-    chk(t[:0], name, dtypes)
+    if ld < cols:
+        raise ValueError(f"{chk.where}: the rows of {name} overlap")
+    if t.dtype not in dtypes or t.device.type != DEVICE_TYPE or (chk.device is not None and t.device != chk.device):
+        chk(t[:0], name, dtypes)
+    chk.device = t.device
     return t.data_ptr(), ld
 
 
@@ -792,24 +805,23 @@ def mla_rmsnorm_fwd(x, gamma, *, eps=1e-6, res=None, h=None, y=None, codes=None,
     optional: h [T,K] like res (the sum), y bf16 [T,K], rstd fp32 [T], and 8-bit codes of y: uint8 [T,K] with scales
     uint8 [T,K/32] (MXFP8), or int8 [T,K] with scales fp32 [T]. gamma bf16/fp32 [K] or None (ones)."""
     chk = _Dev("mla_rmsnorm_fwd")
-    a = mla_rmsnorm_args()
-    a.x, a.ld_x = _row_view(chk, x, "x", (_BF16,))
+    px, ld = _row_view(chk, x, "x", (_BF16,))
     T, K = x.shape
-    a.res = chk(res, "res", _FLOATS, numel=T * K)
-    a.res_dtype = _dtype_of(res)
-    a.gamma = chk(gamma, "gamma", _FLOATS, numel=K)
-    a.gamma_dtype = _dtype_of(gamma)
-    a.eps, a.T, a.K = eps, T, K
-    a.h = _opt(chk, h, "h", _FP32 if a.res_dtype == DTYPE_FP32 else _BF16, T * K)
-    a.rstd = _opt(chk, rstd, "rstd", _FP32, T)
-    a.y = _opt(chk, y, "y", _BF16, T * K)
+    n = T * K
+    pr, res_dtype = _float(chk, res, "res", n)
+    pg, gamma_dtype = _float(chk, gamma, "gamma", K)
+    pc = ps = None
+    q_dtype = DTYPE_BF16
     if codes is not None:
-        a.codes = chk(codes, "codes", (_U8, _I8), numel=T * K)
-        a.q_dtype = DTYPE_INT8 if codes.dtype == _I8 else DTYPE_MXFP8
-    if a.q_dtype == DTYPE_INT8:
-        a.scales = _opt(chk, scales, "scales", _FP32, T)
-    else:
-        a.scales = _opt(chk, scales, "scales", _U8, T * K // 32)
+        i8 = isinstance(codes, torch.Tensor) and codes.dtype is _I8
+        q_dtype = DTYPE_INT8 if i8 else DTYPE_MXFP8
+        pc = _opt(chk, codes, "codes", _I8 if i8 else _U8, n)
+        ps = _opt(chk, scales, "scales", _FP32, T) if i8 else _opt(chk, scales, "scales", _U8, n // 32)
+    elif scales is not None:
+        raise ValueError("mla_rmsnorm_fwd: scales without codes")
+    a = mla_rmsnorm_args(px, ld, pr, res_dtype, pg, gamma_dtype, eps, T, K,
+                         _opt(chk, h, "h", _FP32 if res_dtype == DTYPE_FP32 else _BF16, n),
+                         _opt(chk, rstd, "rstd", _FP32, T), _opt(chk, y, "y", _BF16, n), q_dtype, pc, ps)
     _call(chk.where, chk.device, stream, lib().mla_rmsnorm_fwd, ctypes.byref(a))
 
 
@@ -823,20 +835,16 @@ def mla_rmsnorm_bwd(dy, h, rstd, gamma, *, dh=None, dx=None, dres=None, dgamma=N
     optional: the gradient of x and res as dx bf16 [T,K] and dres fp32 [T,K], and dgamma fp32 [K], which needs a
     workspace of mla_rmsnorm_bwd_workspace_size(T, K) bytes."""
     chk = _Dev("mla_rmsnorm_bwd")
-    a = mla_rmsnorm_bwd_args()
-    a.h, a.ld_h = _row_view(chk, h, "h", _FLOATS)
+    ph, ld = _row_view(chk, h, "h", _FLOATS)
     T, K = h.shape
-    a.h_dtype = _dtype_of(h)
-    a.dy = chk(dy, "dy", (_BF16,), numel=T * K)
-    a.rstd = chk(rstd, "rstd", (_FP32,), numel=T)
-    a.gamma = chk(gamma, "gamma", _FLOATS, numel=K)
-    a.gamma_dtype = _dtype_of(gamma)
-    a.dh = chk(dh, "dh", (h.dtype,), numel=T * K)
-    a.T, a.K = T, K
-    a.dx = _opt(chk, dx, "dx", _BF16, T * K)
-    a.dres = _opt(chk, dres, "dres", _FP32, T * K)
-    a.dgamma = _opt(chk, dgamma, "dgamma", _FP32, K)
-    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
+    n = T * K
+    pg, gamma_dtype = _float(chk, gamma, "gamma", K)
+    ws, ws_bytes = _workspace(chk, workspace)
+    if dy is None or rstd is None:
+        raise ValueError("mla_rmsnorm_bwd: dy and rstd must be torch tensors")
+    a = mla_rmsnorm_bwd_args(_opt(chk, dy, "dy", _BF16, n), ph, _dtype_of(h), ld, _opt(chk, rstd, "rstd", _FP32, T), pg,
+                             gamma_dtype, _opt(chk, dh, "dh", h.dtype, n), T, K, _opt(chk, dx, "dx", _BF16, n),
+                             _opt(chk, dres, "dres", _FP32, n), _opt(chk, dgamma, "dgamma", _FP32, K), ws, ws_bytes)
     _call(chk.where, chk.device, stream, lib().mla_rmsnorm_bwd, ctypes.byref(a))
 
 
@@ -845,8 +853,7 @@ def int8_quantize(x, codes, scales, stream=None):
     chk = _Dev("int8_quantize")
     px, ld = _row_view(chk, x, "x", _FLOATS)
     rows, cols = x.shape
-    pc = chk(codes, "codes", (_I8,), numel=rows * cols)
-    ps = chk(scales, "scales", (_FP32,), numel=rows)
+    pc, ps = _opt(chk, codes, "codes", _I8, rows * cols), _opt(chk, scales, "scales", _FP32, rows)
     _call(chk.where, chk.device, stream, lib().int8_quantize, px, _dtype_of(x), rows, cols, ld, pc, ps)
 
 
@@ -856,23 +863,29 @@ def mla_qup_fwd_i8(x, x_scales, w, w_scales, out, *, H, d_nope, d_rope, cos=None
     with w_scales fp32 [N] (int8_quantize); out and out_scales as mla_qup_fwd's. positions int32 [T]: each token's
     position, in place of the format's."""
     chk = _Dev("mla_qup_fwd_i8")
-    a = mla_qup_i8_args()
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("mla_qup_fwd_i8: x must be [T, K]")
     T, K = x.shape
     N = H * (d_nope + d_rope)
-    a.x = chk(x, "x", (_I8,))
-    a.x_scales = chk(x_scales, "x_scales", (_FP32,), numel=T)
-    a.w = chk(w, "w", (_I8,), numel=N * K)
-    a.w_scales = chk(w_scales, "w_scales", (_FP32,), numel=N)
-    a.bias = chk(bias, "bias", (_BF16,), numel=N)
-    a.K, a.H, a.d_nope, a.d_rope = K, H, d_nope, d_rope
-    a.tokens = _tokens(chk, T, fmt, B, S, cu_seqlens, max_seqlen)
-    a.positions = chk(positions, "positions", (_I32,), numel=T)
-    a.rope = _rope(chk, cos, sin, d_rope)
-    a.out_dtype = DTYPE_MXFP8 if out.dtype == torch.uint8 else DTYPE_BF16
-    a.out = chk(out, "out", (_BF16, _U8), numel=T * N)
-    a.out_scales = chk(out_scales, "out_scales", (_U8,), numel=T * N // 32)
+    if x.dtype is not _I8 or x.device.type != DEVICE_TYPE or not x.is_contiguous():
+        chk(x, "x", (_I8,))
+    chk.device = x.device
+    px = x.data_ptr()
+    tk = mla_tokens(FMT_BSHD, B, S if S is not None else (T // B if B else 0), T) if fmt == FMT_BSHD else \
+        _tokens(chk, T, fmt, B, S, cu_seqlens, max_seqlen)
+    rope = mla_rope()
+    if cos is not None or sin is not None:
+        if (cos is not None and sin is not None and cos.dim() == 2 and cos.shape == sin.shape
+                and _is(cos, _FP32, cos.numel(), chk.device) and _is(sin, _FP32, cos.numel(), chk.device)):
+            rope = mla_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], cos.shape[1])
+        else:
+            rope = _rope(chk, cos, sin, d_rope)
+    mx = out.dtype is _U8
+    a = mla_qup_i8_args(px, _opt(chk, x_scales, "x_scales", _FP32, T), _opt(chk, w, "w", _I8, N * K),
+                        _opt(chk, w_scales, "w_scales", _FP32, N), _opt(chk, bias, "bias", _BF16, N), K, H, d_nope, d_rope,
+                        tk, _opt(chk, positions, "positions", _I32, T), rope, DTYPE_MXFP8 if mx else DTYPE_BF16,
+                        _opt(chk, out, "out", _U8 if mx else _BF16, T * N),
+                        _opt(chk, out_scales, "out_scales", _U8, T * N // 32))
     _call(chk.where, chk.device, stream, lib().mla_qup_fwd_i8, ctypes.byref(a))
 
 
@@ -883,56 +896,57 @@ def mla_attn_spans(spans, at=None, *, Sk, cu_q=None, cu_k=None, len_q=None, len_
     entry with len_q / len_k int32 [B] (None: all rows). prefix int32 [n or B]: keys that all rows of a sequence see.
     window: how far back a row sees (0: all the way)."""
     chk = _Dev("mla_attn_spans")
-    a = mla_attn_spans_args()
     if not isinstance(spans, torch.Tensor) or spans.dim() != 3 or spans.shape[2] != 2:
         raise ValueError("mla_attn_spans: spans must be [B, Sq, 2]")
-    a.B, a.Sq, a.Sk = spans.shape[0], spans.shape[1], Sk
-    a.spans = chk(spans, "spans", (_I32,))
-    a.at = _opt(chk, at, "at", _I32, a.B * a.Sq)
-    n = a.B
+    B, Sq = spans.shape[:2]
+    if spans.dtype is not _I32 or spans.device.type != DEVICE_TYPE or not spans.is_contiguous():
+        chk(spans, "spans", (_I32,))
+    chk.device = spans.device
+    n, nseq, pq = B, 0, None
     if cu_q is not None:
-        a.cu_q = chk(cu_q, "cu_q", (_I32,), min_numel=2)
-        a.nseq = n = cu_q.numel() - 1
-        a.cu_k = _opt(chk, cu_k, "cu_k", _I32, n + 1)
+        pq = chk(cu_q, "cu_q", (_I32,), min_numel=2)
+        nseq = n = cu_q.numel() - 1
     elif cu_k is not None:
         raise ValueError("mla_attn_spans: cu_k without cu_q")
-    a.len_q, a.len_k = _opt(chk, len_q, "len_q", _I32, n), _opt(chk, len_k, "len_k", _I32, n)
-    a.prefix = _opt(chk, prefix, "prefix", _I32, n)
-    a.causal, a.window = 1 if causal else 0, window
+    a = mla_attn_spans_args(spans.data_ptr(), _opt(chk, at, "at", _I32, B * Sq), B, Sq, Sk, pq,
+                            _opt(chk, cu_k, "cu_k", _I32, n + 1), nseq, _opt(chk, len_q, "len_q", _I32, n),
+                            _opt(chk, len_k, "len_k", _I32, n), _opt(chk, prefix, "prefix", _I32, n),
+                            1 if causal else 0, window)
     _call(chk.where, chk.device, stream, lib().mla_attn_spans, ctypes.byref(a))
 
 
 def _attn_rows(chk, t, name, shape):
     """A bf16 [B, H, S, d] view whose rows are dense; other strides are free."""
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
         raise ValueError(f"{chk.where}: {name} must be {list(shape)}")
     if t.dtype is not _BF16 or t.device != chk.device:
         chk(t[:0], name, (_BF16,))
-    s = t.stride()
-    if s[3] != 1 and shape[3] > 1 and t.numel():
+    b, h, s, d = t.stride()
+    if d != 1 and shape[3] > 1 and t.numel():
         raise ValueError(f"{chk.where}: the elements of a row of {name} must be dense")
     # the stride of an axis of one entry says nothing
-    return mla_attn_rows(t.data_ptr(), s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
+    return t.data_ptr(), b if shape[0] > 1 else 0, h if shape[1] > 1 else 0, s if shape[2] > 1 else 0
+
+
+def _attn_sizes(where, q, k, v):
+    if not all(isinstance(t, torch.Tensor) and t.dim() == 4 for t in (q, k, v)):
+        raise ValueError(f"{where}: q, k and v must be [B, H, S, d]")
+    B, H, Sq, d_k = q.shape
+    _, H_kv, Sk, d_v = v.shape
+    return B, H, H_kv, Sq, Sk, d_k, d_v
 
 
 def _attn_args(where, q, k, v, out, lse, scale, cap, slopes, spans, at, workspace):
     chk = _Dev(where)
-    if not all(isinstance(t, torch.Tensor) and t.dim() == 4 for t in (q, k, v)):
-        raise ValueError(f"{where}: q, k and v must be [B, H, S, d]")
-    chk(q[:0], "q", (_BF16,))
-    (B, H, Sq, d_k), (_, H_kv, Sk, d_v) = q.shape, v.shape
-    a = mla_attn_args()
-    a.q = _attn_rows(chk, q, "q", (B, H, Sq, d_k))
-    a.k = _attn_rows(chk, k, "k", (B, H_kv, Sk, d_k))
-    a.v = _attn_rows(chk, v, "v", (B, H_kv, Sk, d_v))
-    a.out = _attn_rows(chk, out, "out", (B, H, Sq, d_v))
-    a.lse = _opt(chk, lse, "lse", _FP32, B * H * Sq)
-    a.B, a.H, a.H_kv, a.Sq, a.Sk, a.d_k, a.d_v = B, H, H_kv, Sq, Sk, d_k, d_v
-    a.scale, a.cap = scale, cap
-    a.slopes = _opt(chk, slopes, "slopes", _FP32, H)
-    a.spans = _opt(chk, spans, "spans", _I32, B * Sq * 2)
-    a.at = _opt(chk, at, "at", _I32, B * Sq)
-    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
+    sizes = B, H, H_kv, Sq, Sk, d_k, d_v = _attn_sizes(where, q, k, v)
+    if q.device.type != DEVICE_TYPE:
+        chk(q[:0], "q", (_BF16,))
+    chk.device = q.device
+    ws, ws_bytes = _workspace(chk, workspace)
+    a = mla_attn_args(_attn_rows(chk, q, "q", (B, H, Sq, d_k)), _attn_rows(chk, k, "k", (B, H_kv, Sk, d_k)),
+                      _attn_rows(chk, v, "v", (B, H_kv, Sk, d_v)), _attn_rows(chk, out, "out", (B, H, Sq, d_v)),
+                      _opt(chk, lse, "lse", _FP32, B * H * Sq), *sizes, scale, cap, _opt(chk, slopes, "slopes", _FP32, H),
+                      _opt(chk, spans, "spans", _I32, B * Sq * 2), _opt(chk, at, "at", _I32, B * Sq), ws, ws_bytes)
     return chk, a
 
 
@@ -944,9 +958,17 @@ def _size_on(device, fn, *args) -> int:
         return int(fn(*args))
 
 
-def mla_attn_fwd_workspace_size(q, k, v, out, *, scale, cap=0.0, slopes=None, spans=None, at=None, lse=None) -> int:
-    chk, a = _attn_args("mla_attn_fwd", q, k, v, out, lse, scale, cap, slopes, spans, at, None)
-    return _size_on(chk.device, lib().mla_attn_fwd_workspace_size, ctypes.byref(a))
+def _sizes_only(where, q, k, v, scale, cap):
+    a = mla_attn_args()
+    a.B, a.H, a.H_kv, a.Sq, a.Sk, a.d_k, a.d_v = _attn_sizes(where, q, k, v)
+    a.scale, a.cap = scale, cap
+    return a
+
+
+def mla_attn_fwd_workspace_size(q, k, v, out=None, *, scale, cap=0.0, **_) -> int:
+    """Of the arguments (those of the call) the sizes and the device of q, k and v count."""
+    a = _sizes_only("mla_attn_fwd", q, k, v, scale, cap)
+    return _size_on(q.device, lib().mla_attn_fwd_workspace_size, ctypes.byref(a))
 
 
 def mla_attn_fwd(q, k, v, out, *, scale, lse=None, cap=0.0, slopes=None, spans=None, at=None, workspace=None,
@@ -959,21 +981,11 @@ def mla_attn_fwd(q, k, v, out, *, scale, lse=None, cap=0.0, slopes=None, spans=N
     _call(chk.where, chk.device, stream, lib().mla_attn_fwd, ctypes.byref(a))
 
 
-def _attn_bwd_args(dout, q, k, v, out, lse, dq, dk, dv, scale, cap, slopes, spans, at, workspace):
+def mla_attn_bwd_workspace_size(dout, q, k, v, out=None, lse=None, dq=None, dk=None, dv=None, *, scale, cap=0.0, **_) -> int:
+    """As mla_attn_fwd_workspace_size."""
     a = mla_attn_bwd_args()
-    chk, a.fwd = _attn_args("mla_attn_bwd", q, k, v, out, lse, scale, cap, slopes, spans, at, None)
-    a.dout = _attn_rows(chk, dout, "dout", tuple(out.shape))
-    a.dq = _attn_rows(chk, dq, "dq", tuple(q.shape))
-    a.dk = _attn_rows(chk, dk, "dk", tuple(k.shape))
-    a.dv = _attn_rows(chk, dv, "dv", tuple(v.shape))
-    a.workspace, a.workspace_bytes = _workspace(chk, workspace)
-    return chk, a
-
-
-def mla_attn_bwd_workspace_size(dout, q, k, v, out, lse, dq, dk, dv, *, scale, cap=0.0, slopes=None, spans=None,
-                                at=None) -> int:
-    chk, a = _attn_bwd_args(dout, q, k, v, out, lse, dq, dk, dv, scale, cap, slopes, spans, at, None)
-    return _size_on(chk.device, lib().mla_attn_bwd_workspace_size, ctypes.byref(a))
+    a.fwd = _sizes_only("mla_attn_bwd", q, k, v, scale, cap)
+    return _size_on(q.device, lib().mla_attn_bwd_workspace_size, ctypes.byref(a))
 
 
 def mla_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, scale, cap=0.0, slopes=None, spans=None, at=None,
@@ -981,5 +993,8 @@ def mla_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, scale, cap=0.0, slopes=
     """Backward of mla_attn_fwd from its out and lse: dout like out -> dq like q, dk like k, dv like v (heads that
     share a key head add up). Strides are free as in the forward: dq may be the token-major [T,H,D] that mla_qup_bwd
     reads. workspace: mla_attn_bwd_workspace_size() bytes."""
-    chk, a = _attn_bwd_args(dout, q, k, v, out, lse, dq, dk, dv, scale, cap, slopes, spans, at, workspace)
+    chk, fwd = _attn_args("mla_attn_bwd", q, k, v, out, lse, scale, cap, slopes, spans, at, None)
+    ws, ws_bytes = _workspace(chk, workspace)
+    a = mla_attn_bwd_args(fwd, _attn_rows(chk, dout, "dout", out.shape), _attn_rows(chk, dq, "dq", q.shape),
+                          _attn_rows(chk, dk, "dk", k.shape), _attn_rows(chk, dv, "dv", v.shape), ws, ws_bytes)
     _call(chk.where, chk.device, stream, lib().mla_attn_bwd, ctypes.byref(a))

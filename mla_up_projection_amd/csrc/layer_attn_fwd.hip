@@ -306,46 +306,63 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   }
 }
 
-// Parts of a row joined: a wave to a row, four rows to a workgroup.
+// Parts of a row joined: half a wave to a row, eight rows to a workgroup. A lane holds
+// the statistics of two parts and four columns.
 __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= (int64_t)p.B * p.H * p.Sq) return;
-  const int64_t bh = row / p.Sq;
+  const int lane = threadIdx.x & 63, l32 = lane & 31;
+  const int64_t rows_all = (int64_t)p.B * p.H * p.Sq, at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const bool live = at < rows_all;
+  const int64_t row = live ? at : rows_all - 1, bh = row / p.Sq;
   const int i = (int)(row - bh * p.Sq), b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
-  const int rows = p.plan.rows, tq = i / rows;
+  const int rows = p.plan.rows, tq = i / rows, n = p.plan.splits;
   const int64_t g = bh * p.plan.tiles_q + (p.plan.tiles_q - 1 - tq);
-  const int64_t slot0 = g * p.plan.splits * rows + i % rows;
+  const int64_t slot0 = g * n * rows + i % rows;
+  float2 ml[2];
   float m = -__builtin_inff();
-  for (int s = 0; s < p.plan.splits; ++s) m = fmaxf(m, p.part_ml[2 * (slot0 + (int64_t)s * rows)]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    ml[k] = make_float2(-__builtin_inff(), 0.0f);
+    const int s = l32 + 32 * k;
+    if (s < n) ml[k] = *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot0 + (int64_t)s * rows));
+    m = fmaxf(m, ml[k].x);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
   const float mu = m == -__builtin_inff() ? 0.0f : m;
-  float l = 0, o[2] = {0, 0};
-  for (int s = 0; s < p.plan.splits; ++s) {
-    const int64_t at = slot0 + (int64_t)s * rows;
-    const float w = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - mu);
-    l = __builtin_fmaf(p.part_ml[2 * at + 1], w, l);
+  float w[2], l = 0;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      if (lane + 64 * c < p.d_v) o[c] = __builtin_fmaf(p.part_o[at * p.d_v + lane + 64 * c], w, o[c]);
+  for (int k = 0; k < 2; ++k) {
+    w[k] = __builtin_amdgcn_exp2f(ml[k].x - mu);
+    l = __builtin_fmaf(ml[k].y, w[k], l);
   }
-  const bool none = l == 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) l += __shfl_xor(l, o);
+  const int c = 4 * l32;
+  const bool in = c < p.d_v;
+  float4 o = make_float4(0, 0, 0, 0);
+  const float* from = p.part_o + slot0 * p.d_v + c;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float ws = __shfl(s < 32 ? w[0] : w[1], (lane & 32) | (s & 31));
+    if (in) {
+      const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * rows * p.d_v);
+      o.x = __builtin_fmaf(v.x, ws, o.x), o.y = __builtin_fmaf(v.y, ws, o.y);
+      o.z = __builtin_fmaf(v.z, ws, o.z), o.w = __builtin_fmaf(v.w, ws, o.w);
+    }
+  }
+  const bool none = l == 0, fine = l < __builtin_inff();
   const float inv = none ? 0.0f : 1.0f / l;
-  const bool fine = l < __builtin_inff();
-  if (p.lse && fine && lane == 0) p.lse[row] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
-  bool odd = !fine;
+  o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+  if (live && p.lse && fine && l32 == 0) p.lse[row] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
+  const bool odd = !fine || max(max(abs_bits(o.x), abs_bits(o.y)), max(abs_bits(o.z), abs_bits(o.w))) >= 0x7F800000u;
+  const uint64_t bad = __builtin_amdgcn_ballot_w64(odd && live);
+  const uint32_t mine = (uint32_t)(bad >> (lane & 32));
+  if (live && in && !mine)
+    *reinterpret_cast<uint2*>(const_cast<uint16_t*>(row_of(p.out, b, h, i)) + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    o[c] *= inv;
-    odd |= abs_bits(o[c]) >= 0x7F800000u;
-  }
-  if (__builtin_amdgcn_ballot_w64(odd)) {
-    slow_forward(p, b, h, i, !fine, lane);
-    return;
-  }
-  uint16_t* out = const_cast<uint16_t*>(row_of(p.out, b, h, i));
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-    if (lane + 64 * c < p.d_v) out[lane + 64 * c] = (uint16_t)f32_to_bf16_bits(o[c]);
+  for (int k = 0; k < 2; ++k)
+    if ((uint32_t)(bad >> (32 * k)))
+      slow_forward(p, __shfl(b, 32 * k), __shfl(h, 32 * k), __shfl(i, 32 * k), !__shfl((int)fine, 32 * k), lane);
 }
 
 __global__ __launch_bounds__(256) void spans_kernel(SpanParams p) {
@@ -422,7 +439,7 @@ hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream) {
   else fwd<192, 128>(p, stream);
   if (p.plan.splits > 1) {
     const int64_t rows = (int64_t)p.B * p.H * p.Sq;
-    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p);
   }
   return hipGetLastError();
 }

@@ -119,7 +119,9 @@ __device__ __forceinline__ void int8_scale(uint32_t amax_bits, float& scale, flo
   }
 }
 
-template <int WPR, int CH>
+// AHEAD: gamma is loaded with the row instead of behind the wait for its sum, which
+// costs registers that many rows want for each other's loads.
+template <int WPR, int CH, bool AHEAD>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : THREADS) void rmsnorm_kernel(NormParams p) {
   constexpr int WAVES = WPR > 4 ? WPR : THREADS / 64;
   __shared__ float red[2][WAVES];
@@ -127,7 +129,12 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : THREADS) void rmsnorm_kernel(N
   const int64_t t = (int64_t)blockIdx.x * (WAVES / WPR) + wave / WPR;
   const bool row = t < p.T;
   const int chunks = p.K / 8, first = (wave % WPR) * 64 + lane;
-  F8 h[CH];
+  F8 h[CH], g[CH];
+  const auto gamma = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[c].v[k] = 1.0f;
+    if (p.gamma) g[c] = load8(p.gamma, 8 * (first + c * 64 * WPR), p.gamma_f32);
+  };
   float ss = 0;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -135,6 +142,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : THREADS) void rmsnorm_kernel(N
 #pragma unroll
     for (int k = 0; k < 8; ++k) h[c].v[k] = 0;
     if (row && at < chunks) {
+      if (AHEAD) gamma(c);
       h[c] = load8(p.x, t * p.ld_x + 8 * at, false);
       if (p.res) {
         const F8 r = load8(p.res, t * p.K + 8 * at, p.res_f32);
@@ -159,13 +167,10 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : THREADS) void rmsnorm_kernel(N
   for (int c = 0; c < CH; ++c) {
     const int at = first + c * 64 * WPR;
     if (row && at < chunks) {
-      F8 g;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g.v[k] = 1.0f;
-      if (p.gamma) g = load8(p.gamma, 8 * at, p.gamma_f32);
+      if (!AHEAD) gamma(c);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        h[c].v[k] = h[c].v[k] * rstd * g.v[k];
+        h[c].v[k] = h[c].v[k] * rstd * g[c].v[k];
         amax = max(amax, abs_bits(h[c].v[k]));
       }
       if (p.y) *reinterpret_cast<uint4*>(p.y + t * p.K + 8 * at) = to_bf16(h[c]);
@@ -231,42 +236,102 @@ __global__ __launch_bounds__(THREADS) void int8_quantize_kernel(const void* x, i
   }
 }
 
-// Each workgroup walks rows in strides of the grid and keeps the sums of
-// dgamma of its columns in registers; the partial sums are added afterwards in
-// a fixed order.
-template <int WAVES, int CH>
+// Eight elements as they are loaded.
+template <bool F32>
+struct Raw8 {
+  uint4 a[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const uint4* s = reinterpret_cast<const uint4*>(F32 ? static_cast<const void*>(static_cast<const float*>(p) + at)
+                                                        : static_cast<const void*>(static_cast<const uint16_t*>(p) + at));
+    a[0] = s[0];
+    if (F32) a[F32 ? 1 : 0] = s[1];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < (F32 ? 2 : 1); ++k) a[k] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ F8 get() const {
+    if (!F32) return from_bf16(a[0]);
+    F8 r;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 u = a[F32 ? k : 0];
+      r.v[4 * k] = __uint_as_float(u.x), r.v[4 * k + 1] = __uint_as_float(u.y);
+      r.v[4 * k + 2] = __uint_as_float(u.z), r.v[4 * k + 3] = __uint_as_float(u.w);
+    }
+    return r;
+  }
+};
+
+// Each workgroup walks rows in strides of the grid, with AHEAD the next row's loads
+// under way while it sums one up, and keeps the sums of dgamma of its columns in registers;
+// the partial sums are added afterwards in a fixed order.
+template <int WAVES, int CH, bool F32, bool AHEAD>
 __global__ __launch_bounds__(64 * WAVES) void rmsnorm_bwd_kernel(NormBwdParams p) {
   __shared__ float red[2][WAVES];
   const int wave = threadIdx.x >> 6;
   const int chunks = p.K / 8;
-  F8 gamma[CH], dg[CH];
+  struct Row {
+    Raw8<F32> h[CH], d[CH];
+    Raw8<false> y[CH];
+    float rstd;
+  };
+  F8 dg[CH];
+  Raw8<false> gb[CH];
+  Raw8<true> gf[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int at = (int)threadIdx.x + c * 64 * WAVES;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) gamma[c].v[k] = 1.0f, dg[c].v[k] = 0;
-    if (p.gamma && at < chunks) gamma[c] = load8(p.gamma, 8 * at, p.gamma_f32);
+    for (int k = 0; k < 8; ++k) dg[c].v[k] = 0;
+    gb[c].zero();
+    gf[c].zero();
+    if (AHEAD && p.gamma && at < chunks) {
+      if (p.gamma_f32) gf[c].load(p.gamma, 8 * at);
+      else gb[c].load(p.gamma, 8 * at);
+    }
   }
-  int turn = 0;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-    const float rstd = p.rstd[t];
-    F8 xh[CH], dy[CH];
-    float dot = 0;
+  const auto load = [&](Row& r, int64_t t) {
+    r.rstd = p.rstd[t];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int at = (int)threadIdx.x + c * 64 * WAVES;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) xh[c].v[k] = dy[c].v[k] = 0;
+      r.h[c].zero();
+      r.d[c].zero();
+      r.y[c].zero();
       if (at < chunks) {
-        xh[c] = load8(p.h, t * p.ld_h + 8 * at, p.h_f32);
-        dy[c] = load8(p.dy, t * p.K + 8 * at, false);
+        r.h[c].load(p.h, t * p.ld_h + 8 * at);
+        r.y[c].load(p.dy, t * p.K + 8 * at);
+        if (p.dh) r.d[c].load(p.dh, t * p.K + 8 * at);
       }
+    }
+  };
+  const auto gamma = [&](int c) {
+    F8 g;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g.v[k] = 1.0f;
+    const int at = (int)threadIdx.x + c * 64 * WAVES;
+    if (!AHEAD && p.gamma && at < chunks) g = load8(p.gamma, 8 * at, p.gamma_f32);
+    if (AHEAD && p.gamma) g = p.gamma_f32 ? gf[c].get() : gb[c].get();
+    return g;
+  };
+  int turn = 0;
+  Row now;
+  int64_t t = blockIdx.x;
+  if (AHEAD && t < p.T) load(now, t);
+  for (; t < p.T; t += gridDim.x, turn ^= 1) {
+    Row next;
+    if (!AHEAD) load(now, t);
+    else if (t + gridDim.x < p.T) load(next, t + gridDim.x);
+    float dot = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const F8 h = now.h[c].get(), y = now.y[c].get(), g = gamma(c);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        xh[c].v[k] *= rstd;
-        dg[c].v[k] = __builtin_fmaf(dy[c].v[k], xh[c].v[k], dg[c].v[k]);
-        dy[c].v[k] *= gamma[c].v[k];
-        dot = __builtin_fmaf(dy[c].v[k], xh[c].v[k], dot);
+        const float xh = h.v[k] * now.rstd;
+        dg[c].v[k] = __builtin_fmaf(y.v[k], xh, dg[c].v[k]);
+        dot = __builtin_fmaf(y.v[k] * g.v[k], xh, dot);
       }
     }
     dot = row_sum<WAVES>(dot, red[turn], wave) / (float)p.K;
@@ -275,18 +340,15 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_bwd_kernel(NormBwdParams p
       for (int c = 0; c < CH; ++c) {
         const int at = (int)threadIdx.x + c * 64 * WAVES;
         if (at < chunks) {
+          const F8 h = now.h[c].get(), y = now.y[c].get(), g = gamma(c), d = now.d[c].get();
           F8 o;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o.v[k] = (dy[c].v[k] - xh[c].v[k] * dot) * rstd;
-          if (p.dh) {
-            const F8 d = load8(p.dh, t * p.K + 8 * at, p.h_f32);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o.v[k] += d.v[k];
-          }
+          for (int k = 0; k < 8; ++k) o.v[k] = (y.v[k] * g.v[k] - h.v[k] * now.rstd * dot) * now.rstd + d.v[k];
           if (p.dx) *reinterpret_cast<uint4*>(p.dx + t * p.K + 8 * at) = to_bf16(o);
           if (p.dres) store8_f32(p.dres + t * p.K + 8 * at, o);
         }
       }
+    if (AHEAD) now = next;
   }
   if (p.dgamma)
 #pragma unroll
@@ -296,58 +358,68 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_bwd_kernel(NormBwdParams p
     }
 }
 
-// Column sums of the partial sums: eight columns to a workgroup's wave row, the
-// rows divided over its threads and joined in a fixed order.
+// Column sums of the partial sums: 32 columns to a workgroup, its 32 groups of eight
+// threads taking rows in turn, joined in a fixed order.
 __global__ __launch_bounds__(THREADS) void dgamma_kernel(const float* part, int groups, int K, float* dgamma) {
-  __shared__ float red[16][17];
-  const int col = threadIdx.x & 15, sub = threadIdx.x >> 4;
-  const int k = blockIdx.x * 16 + col;
-  float s = 0;
-  if (k < K)
-    for (int g = sub; g < groups; g += 16) s += part[(int64_t)g * K + k];
-  red[sub][col] = s;
+  __shared__ float red[32][33];
+  const int c4 = (threadIdx.x & 7) * 4, sub = threadIdx.x >> 3;
+  const int k = blockIdx.x * 32 + c4;
+  float4 s = make_float4(0, 0, 0, 0);
+  if (k < K) {  // (K is a multiple of 8)
+#pragma unroll 16
+    for (int g = sub; g < groups; g += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)g * K + k);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+  }
+  red[sub][c4] = s.x, red[sub][c4 + 1] = s.y, red[sub][c4 + 2] = s.z, red[sub][c4 + 3] = s.w;
   __syncthreads();
-  if (sub == 0 && k < K) {
-    s = 0;
+  if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < K) {
+    float v = 0;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) s += red[q][col];
-    dgamma[k] = s;
+    for (int q = 0; q < 32; ++q) v += red[q][threadIdx.x];
+    dgamma[blockIdx.x * 32 + threadIdx.x] = v;
   }
 }
 
-template <int WPR, int CH>
+template <int WPR, int CH, bool AHEAD>
 void norm(const NormParams& p, hipStream_t stream) {
   constexpr int rows = WPR > 4 ? 1 : THREADS / 64 / WPR;
-  hipLaunchKernelGGL((rmsnorm_kernel<WPR, CH>), dim3((unsigned)((p.T + rows - 1) / rows)),
+  hipLaunchKernelGGL((rmsnorm_kernel<WPR, CH, AHEAD>), dim3((unsigned)((p.T + rows - 1) / rows)),
                      dim3(WPR > 4 ? 64 * WPR : THREADS), 0, stream, p);
 }
-template <int WAVES, int CH>
+template <int WAVES, int CH, bool AHEAD = true>
 void norm_bwd(const NormBwdParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((rmsnorm_bwd_kernel<WAVES, CH>), dim3((unsigned)p.groups), dim3(64 * WAVES), 0, stream, p);
+  const dim3 grid((unsigned)p.groups), block(64 * WAVES);
+  if (p.h_f32) hipLaunchKernelGGL((rmsnorm_bwd_kernel<WAVES, CH, true, AHEAD>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((rmsnorm_bwd_kernel<WAVES, CH, false, AHEAD>), grid, block, 0, stream, p);
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm(const NormParams& p, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
-  if (p.K <= 512) norm<1, 1>(p, stream);
-  else if (p.K <= 2048) norm<1, 4>(p, stream);
-  else if (p.K <= 8192) norm<4, 4>(p, stream);
-  else norm<16, 4>(p, stream);
+  // few rows: as many waves to a row as it has elements for, since nothing but its
+  // latency counts
+  const bool few = p.T <= 256;
+  if (p.K <= 512) norm<1, 1, true>(p, stream);
+  else if (p.K <= 2048) few ? norm<4, 1, true>(p, stream) : norm<1, 4, false>(p, stream);
+  else if (p.K <= 8192) few ? norm<16, 1, true>(p, stream) : norm<4, 4, false>(p, stream);
+  else norm<16, 4, false>(p, stream);
   return hipGetLastError();
 }
 
 int rmsnorm_bwd_groups(int64_t T, int K) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(T, K <= 2048 ? 2048 : K <= 8192 ? 1024 : 256));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(T, K <= 512 ? 2048 : K <= 2048 ? 1024 : 512));
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdParams& p, hipStream_t stream) {
   if (p.K <= 512) norm_bwd<1, 1>(p, stream);
   else if (p.K <= 2048) norm_bwd<4, 1>(p, stream);
-  else if (p.K <= 8192) norm_bwd<4, 4>(p, stream);
-  else norm_bwd<16, 4>(p, stream);
+  else if (p.K <= 8192) norm_bwd<8, 2>(p, stream);
+  else norm_bwd<16, 4, false>(p, stream);
   if (p.dgamma)
-    hipLaunchKernelGGL(dgamma_kernel, dim3((unsigned)((p.K + 15) / 16)), dim3(THREADS), 0, stream, p.part, p.groups, p.K,
+    hipLaunchKernelGGL(dgamma_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(THREADS), 0, stream, p.part, p.groups, p.K,
                        p.dgamma);
   return hipGetLastError();
 }
