@@ -999,7 +999,11 @@ void qup_fwd_kernel(FwdParams p) {
       }
     }
     if constexpr (TL::I8) {
-      const int64_t t_lane = t0c + 32 * WBLK_T * wt + (lane & 31);
+      // what the epilogue derives from the lane is worked out in each tile: kept
+      // across them it spills, and each reload waits for the stages on their way
+      int el = lane;
+      asm volatile("" : "+v"(el));
+      const int64_t t_lane = t0c + 32 * WBLK_T * wt + (el & 31);
       f32x16_t q[WBLK_N][WBLK_T];
       float xs[WBLK_T];
 #pragma unroll
@@ -1009,14 +1013,14 @@ void qup_fwd_kernel(FwdParams p) {
         float ws[16];  // rows 8g + 4 half + 0..3 of the block
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int n = min(n0c + 32 * WBLK_N * wn + 32 * nb, p.N - 32) + 8 * g + 4 * half;
+          const int n = min(n0c + 32 * WBLK_N * wn + 32 * nb, p.N - 32) + 8 * g + 4 * (el >> 5);
 #pragma unroll
           for (int k = 0; k < 4; ++k) ws[4 * g + k] = p.w_row_scales[n + k];
         }
 #pragma unroll
         for (int tb = 0; tb < WBLK_T; ++tb) q[nb][tb] = i8_scaled(acc[nb][tb], xs[tb], ws);
       }
-      epilogue_tile<true>(p, tm, q, n0c + 32 * WBLK_N * wn, t_lane, lane, tab, 32 * WBLK_T * wt + (lane & 31));
+      epilogue_tile<true>(p, tm, q, n0c + 32 * WBLK_N * wn, t_lane, el, tab, 32 * WBLK_T * wt + (el & 31));
     } else if constexpr (EPI == EPI_PLAIN)
       plain_tile(p, static_cast<uint8_t*>(p.out) + (int64_t)split_c * p.split_stride, acc,
                  n0c + 32 * WBLK_N * wn, t0c + 32 * WBLK_T * wt + (lane & 31), lane);
