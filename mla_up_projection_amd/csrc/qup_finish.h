@@ -6,32 +6,56 @@
 
 namespace mla {
 
-// v: columns n .. n + 7 of token t. Four consecutive lanes hold 32 columns of one
-// head and come here together; `first` marks the one that stores their scale.
-// live: there are such a token and column.
+// What eight columns n .. n + 7 of token t need besides their sums. It can be loaded
+// ahead of them.
+struct Finish8 {
+  int64_t o;       // the columns' place in the output
+  int d0;          // and in their head
+  float cs[4], sn[4], bias[8];
+};
 template <class P>
-__device__ __forceinline__ void finish8(const P& p, const TokenMap& tm, int64_t t, int n, bool live, bool first,
-                                        float (&v)[8]) {
+__device__ __forceinline__ Finish8 finish8_begin(const P& p, const TokenMap& tm, int64_t t, int n, bool live) {
+  Finish8 f{};
   int pos = 0, bb = 0, ss = 0;
-  const int h = n / p.D, d0 = n - h * p.D;
+  const int h = n / p.D;
+  f.d0 = n - h * p.D;
   if (live) {
     token_coords(tm, t, pos, bb, ss);
     if (p.positions) pos = p.positions[t];
     if (p.bias)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += bf16_bits_to_f32(p.bias[n + k]);
+      for (int k = 0; k < 8; ++k) f.bias[k] = bf16_bits_to_f32(p.bias[n + k]);
 #pragma unroll
     for (int k = 0; k < 8; k += 2)
-      if (d0 + k >= p.d_nope) {
+      if (f.d0 + k >= p.d_nope) {
         const bool ok = pos >= 0 && pos < p.rope_rows;
-        const int64_t ti = (int64_t)(ok ? pos : 0) * p.rope_pairs + (d0 + k - p.d_nope) / 2;
-        const float cs = ok ? p.cos[ti] : __builtin_nanf(""), sn = ok ? p.sin[ti] : __builtin_nanf("");
-        const float a = v[k], b = v[k + 1];
+        const int64_t ti = (int64_t)(ok ? pos : 0) * p.rope_pairs + (f.d0 + k - p.d_nope) / 2;
+        f.cs[k / 2] = ok ? p.cos[ti] : __builtin_nanf("");
+        f.sn[k / 2] = ok ? p.sin[ti] : __builtin_nanf("");
+      }
+  }
+  f.o = (((int64_t)bb * p.H + h) * p.S + ss) * p.D + f.d0;
+  return f;
+}
+
+// v: the columns' sums. Four consecutive lanes hold 32 columns of one head and come
+// here together; `first` marks the one that stores their scale. live: there are such
+// a token and column.
+template <class P>
+__device__ __forceinline__ void finish8_end(const P& p, const Finish8& f, bool live, bool first, float (&v)[8]) {
+  if (live) {
+    if (p.bias)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += f.bias[k];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      if (f.d0 + k >= p.d_nope) {
+        const float cs = f.cs[k / 2], sn = f.sn[k / 2], a = v[k], b = v[k + 1];
         v[k] = a * cs - b * sn;
         v[k + 1] = a * sn + b * cs;
       }
   }
-  const int64_t o = (((int64_t)bb * p.H + h) * p.S + ss) * p.D + d0;
+  const int64_t o = f.o;
   if (!p.out_mx) {
     if (live)
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o) =
@@ -55,6 +79,12 @@ __device__ __forceinline__ void finish8(const P& p, const TokenMap& tm, int64_t 
       if (first) p.out_scales[o / 32] = (uint8_t)sc;
     }
   }
+}
+
+template <class P>
+__device__ __forceinline__ void finish8(const P& p, const TokenMap& tm, int64_t t, int n, bool live, bool first,
+                                        float (&v)[8]) {
+  finish8_end(p, finish8_begin(p, tm, t, n, live), live, first, v);
 }
 
 }  // namespace mla

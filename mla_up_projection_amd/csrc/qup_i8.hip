@@ -103,6 +103,114 @@ __global__ __launch_bounds__(64 * WAVES) void qup_i8_kernel(I8Params p) {
   }
 }
 
+// Tokens 16 MT, weight rows divided over the waves: 16 rows to a wave, 64 to a
+// workgroup, all of K. X comes by direct loads into LDS, half a kilobyte of every
+// row at a time for all four waves; the weights of the next 512 k are under way
+// meanwhile, 8 KB to a wave, with nothing to wait for in between. The form for so many
+// weight rows that 64 of them to a workgroup fill the chip.
+constexpr int SLAB = 512;
+template <int MT>
+__global__ __launch_bounds__(256) void qup_i8_rows_kernel(I8Params p) {
+  constexpr int XS = MT * 16 * SLAB, PITCH = 68;
+  static_assert(MT * 16 * PITCH * 4 <= 2 * XS, "the sums fit where X was");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * XS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, c4 = lane >> 4;
+  const int n0 = blockIdx.x * 64;
+  const int slabs = (p.K + SLAB - 1) / SLAB;
+  const int8_t* wrow = p.w + (int64_t)min(n0 + 16 * wave + l16, p.N - 1) * p.K + 32 * c4;
+  const uint32_t ring = lds_u32(lds);
+  // 16-byte piece q of row r lies at place q ^ (r & 15), so that the 16 rows of a
+  // fragment meet no bank twice. Rows behind T repeat the last, pieces behind K the
+  // row's first (they meet weights of 0).
+  const auto load_x = [&](int s, int slot) {
+#pragma unroll
+    for (int g = 0; g < MT * 2; ++g) {
+      const int r = 8 * g + 2 * wave + (lane >> 5);
+      int k = s * SLAB + 16 * ((lane & 31) ^ (r & 15));
+      if (k >= p.K) k = 0;
+      dma16(p.x, (uint32_t)min((int64_t)r, p.T - 1) * (uint32_t)p.K + (uint32_t)k,
+            __builtin_amdgcn_readfirstlane(ring + slot * XS + (8 * g + 2 * wave) * SLAB));
+    }
+  };
+  const auto load_w = [&](i32x4_t(&w)[4][2], int s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int k = s * SLAB + 128 * c;
+      w[c][0] = w[c][1] = i32x4_t{0, 0, 0, 0};
+      if (k + 32 * c4 < p.K) {
+        const i32x4_t* src = reinterpret_cast<const i32x4_t*>(wrow + k);
+        w[c][0] = src[0], w[c][1] = src[1];
+      }
+    }
+  };
+  i32x4_t acc[MT], w[4][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = i32x4_t{0, 0, 0, 0};
+  load_w(w, 0);
+  load_x(0, 0);
+  // the end's loads, which depend on each other, run under the weights' too
+  constexpr int ENDS = (MT * 16 * 8 + 255) / 256;
+  const TokenMap tm{p.fmt, p.B, p.S, p.cu, p.nseq};
+  Finish8 fin[ENDS];
+  float xs[ENDS], ws[ENDS][8];
+#pragma unroll
+  for (int e = 0; e < ENDS; ++e) {
+    const int i = threadIdx.x + 256 * e, t = i >> 3, n = n0 + 8 * (i & 7);
+    const bool live = t < p.T && t < MT * 16 && n < p.N;
+    fin[e] = finish8_begin(p, tm, t, n, live);
+    xs[e] = live ? p.xs[t] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ws[e][k] = live ? p.ws[n + k] : 0.0f;
+  }
+  for (int s = 0; s < slabs; ++s) {
+    vm_wait<0>();
+    barrier();
+    i32x4_t wn[4][2];
+    if (s + 1 < slabs) {
+      load_w(wn, s + 1);
+      load_x(s + 1, (s + 1) & 1);
+    }
+    const uint8_t* x = lds + (s & 1) * XS;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const i32x4_t v = *reinterpret_cast<const i32x4_t*>(x + (16 * m + l16) * SLAB + (((8 * c + 2 * c4 + j) ^ l16) << 4));
+          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, w[c][j], acc[m], 0, 0, 0);
+        }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) w[c][j] = wn[c][j];
+  }
+  __syncthreads();
+  // acc[m][i]: token 16 m + 4 c4 + i, weight row 16 wave + l16
+  int(*red)[PITCH] = reinterpret_cast<int(*)[PITCH]>(lds);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[16 * m + 4 * c4 + i][16 * wave + l16] = acc[m][i];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < ENDS; ++e) {
+    const int i = threadIdx.x + 256 * e, t = i >> 3;
+    if (t >= MT * 16) break;
+    const bool live = t < p.T && n0 + 8 * (i & 7) < p.N;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = (float)red[t][8 * (i & 7) + k] * xs[e] * ws[e][k];
+    finish8_end(p, fin[e], live, (i & 3) == 0, v);
+  }
+}
+
+template <int MT>
+void launch_rows(const I8Params& p, hipStream_t stream) {
+  hipLaunchKernelGGL((qup_i8_rows_kernel<MT>), dim3((unsigned)((p.N + 63) / 64)), dim3(256), 0, stream, p);
+}
+
 template <int MT, int NT, int WAVES>
 void launch_few(const I8Params& p, hipStream_t stream) {
   const int64_t blocks = (p.T + 16 * MT - 1) / (16 * MT);
@@ -144,7 +252,12 @@ hipError_t launch_qup_i8(const I8Params& p, hipStream_t stream) {
     f.k_splits = 1;
     return launch_qup_fwd_i8(f, stream);
   }
-  if (p.T <= 16) launch_few<1, 2, 4>(p, stream);
+  // 64 weight rows to a workgroup want 8192 of them: 52 tokens, K 1536, 128 heads of
+  // 192 (N 24576) take 14.9 us so and 22.0 with K divided over the waves, 32 tokens
+  // 11.5 and 13.7; but 52 tokens of 16 heads 11.0 and 8.8. One token takes 10.3 us
+  // either way (3.7 TB/s), K 4096 and N 12288 14.8 and 13.2.
+  if (p.T > 16 && p.N >= 64 * 128) p.T <= 32 ? launch_rows<2>(p, stream) : launch_rows<4>(p, stream);
+  else if (p.T <= 16) launch_few<1, 2, 4>(p, stream);
   else if (p.T <= 32) launch_few<2, 2, 4>(p, stream);
   else launch_few<4, 2, 4>(p, stream);
   return hipGetLastError();
