@@ -400,6 +400,10 @@ int attn_cus() {
   return n > 0 ? n : 256;
 }
 
+mla::AttnBwdPlan attn_bwd_plan(const mla_attn_args* f) {
+  return mla::plan_layer_attn_bwd(f->B, f->H, f->H_kv, f->Sq, f->Sk, f->d_k, f->d_v, attn_cus());
+}
+
 }  // namespace
 
 extern "C" {
@@ -431,7 +435,7 @@ mla_status mla_attn_fwd(const mla_attn_args* a, void* stream) {
 
 size_t mla_attn_bwd_workspace_size(const mla_attn_bwd_args* a) {
   if (a == nullptr || check_layer_attn(&a->fwd)) return 0;
-  return mla::plan_layer_attn_bwd(a->fwd.B, a->fwd.H, a->fwd.Sq).total;
+  return attn_bwd_plan(&a->fwd).total;
 }
 
 mla_status mla_attn_bwd(const mla_attn_bwd_args* a, void* stream) {
@@ -445,7 +449,7 @@ mla_status mla_attn_bwd(const mla_attn_bwd_args* a, void* stream) {
   if ((st = check_rows(dout, false)) || (st = check_rows(dq, true)) || (st = check_rows(dk, true)) ||
       (st = check_rows(dv, true)))
     return st;
-  const mla::AttnBwdPlan plan = mla::plan_layer_attn_bwd(f->B, f->H, f->Sq);
+  const mla::AttnBwdPlan plan = attn_bwd_plan(f);
   if ((st = check_ws(a->workspace, a->workspace_bytes, plan.total))) return st;
   LayerRanges r;
   r.input(f->lse, (size_t)f->B * f->H * f->Sq * 4);
@@ -464,6 +468,7 @@ mla_status mla_attn_bwd(const mla_attn_bwd_args* a, void* stream) {
   p.plan = plan;
   p.records = (float*)((uint8_t*)a->workspace + plan.records);
   p.tiles = (int32_t*)((uint8_t*)a->workspace + plan.tiles);
+  p.part = (float*)((uint8_t*)a->workspace + plan.part);
   return launched(mla::launch_layer_attn_bwd(p, (hipStream_t)stream));
 }
 

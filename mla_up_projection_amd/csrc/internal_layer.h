@@ -122,7 +122,8 @@ hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream);
 // ints: lse in powers of two, delta, lo, hi, and the rows' places (64 each).
 struct AttnBwdPlan {
   int tiles_q;            // of 64 query rows
-  size_t records, tiles, total;
+  int splits;             // parts that the query tiles of 128 keys are divided into
+  size_t records, tiles, part, total;
 };
 constexpr int ATTN_RECORD = 512;  // words of a record
 struct LayerAttnBwdParams {
@@ -130,9 +131,10 @@ struct LayerAttnBwdParams {
   AttnRows dout, dq, dk, dv;
   float* records;         // [B, H, tiles_q, ATTN_RECORD]
   int32_t* tiles;         // [B, tiles_q, 4]: smallest lo, largest hi, largest lo, smallest hi
+  float* part;            // [splits, B, H_kv, Sk, d_k + d_v]: sums for dk (without the scale) and dv
   AttnBwdPlan plan;
 };
-AttnBwdPlan plan_layer_attn_bwd(int B, int H, int Sq);
+AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k, int d_v, int cus);
 hipError_t launch_layer_attn_bwd(const LayerAttnBwdParams& p, hipStream_t stream);
 
 }  // namespace mla

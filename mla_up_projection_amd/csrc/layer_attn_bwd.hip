@@ -175,6 +175,56 @@ __device__ __forceinline__ void store_cols(uint16_t* out, const f32x16_t (&o)[NB
   }
 }
 
+template <int NB>
+__device__ __forceinline__ void store_sums(float* out, const f32x16_t (&o)[NB], int width, int half) {
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int d = 32 * n + 8 * k + 4 * half;
+      if (d < width) *reinterpret_cast<float4*>(out + d) = make_float4(o[n][4 * k], o[n][4 * k + 1], o[n][4 * k + 2], o[n][4 * k + 3]);
+    }
+}
+
+// The parts of dK and dV added in their order: a wave to a key row.
+__global__ __launch_bounds__(256) void attn_bwd_join_kernel(LayerAttnBwdParams p) {
+  const LayerAttnParams& f = p.f;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = (int64_t)f.B * f.H_kv * f.Sk, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int64_t bh = row / f.Sk;
+  const int j = (int)(row - bh * f.Sk), b = (int)(bh / f.H_kv), hk = (int)(bh - (int64_t)b * f.H_kv);
+  const int width = f.d_k + f.d_v;
+  float4 o[2];
+  uint32_t odd = 0;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int d = 4 * (lane + 64 * c);
+    o[c] = make_float4(0, 0, 0, 0);
+    if (d >= width) continue;
+    const float* from = p.part + row * width + d;
+#pragma unroll 8
+    for (int s = 0; s < p.plan.splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * rows * width);
+      o[c].x += v.x, o[c].y += v.y, o[c].z += v.z, o[c].w += v.w;
+    }
+    odd |= max(max(abs_bits(o[c].x), abs_bits(o[c].y)), max(abs_bits(o[c].z), abs_bits(o[c].w))) >= 0x7F800000u;
+  }
+  if (__builtin_amdgcn_ballot_w64(odd)) {
+    slow_dkdv(p, b, hk, j, lane);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int d = 4 * (lane + 64 * c);
+    if (d >= width) continue;
+    const bool k = d < f.d_k;
+    const float times = k ? f.scale : 1.0f;
+    uint16_t* to = const_cast<uint16_t*>(k ? row_of(p.dk, b, hk, j) + d : row_of(p.dv, b, hk, j) + d - f.d_k);
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[c].x * times, o[c].y * times), pack_bf16x2(o[c].z * times, o[c].w * times));
+  }
+}
+
 // P out of products, and with a cap its derivative. Element r of a block: row 8 (r /
 // 4) + 4 half + r % 4 of the streamed tile's 32, column the lane's own.
 template <bool EXTRA>
@@ -203,8 +253,9 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5;
   const int tiles_k = (f.Sk + 127) / 128;
-  const int u = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k));
-  if (u < 0) return;
+  const int us = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k * p.plan.splits));
+  if (us < 0) return;
+  const int u = us / p.plan.splits, split = us - u * p.plan.splits;
   const int bh = u / tiles_k, k0 = (u - bh * tiles_k) * 128;
   const int b = bh / f.H_kv, hk = bh - b * f.H_kv;
   const int j = k0 + 32 * wave + (lane & 31);  // this lane's key
@@ -221,12 +272,15 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
 
   // Query tiles that see any of the keys, and whether all their rows see all of
   // them, looked at 64 tiles at a time: a load in each step would wait for the
-  // tile that is on its way.
-  int h = hk * f.group, word = -1;
+  // tile that is on its way. Of several parts each takes every splits-th.
+  int h = hk * f.group, word = -1, skip = split;
   uint64_t left = 0, whole = 0;
   bool all_next = false;
   const auto next = [&]() {
-    while (!left) {
+    for (;;) {
+      const int n = __builtin_popcountll(left);
+      if (n > skip) break;
+      skip -= n;
       if (++word * 64 >= p.plan.tiles_q) {
         word = 0;
         if (++h >= (hk + 1) * f.group) return -1;
@@ -241,8 +295,10 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
       left = __builtin_amdgcn_ballot_w64(some);
       whole = __builtin_amdgcn_ballot_w64(all);
     }
+    for (; skip; --skip) left &= left - 1;
     const int r = __builtin_ctzll(left);
     left &= left - 1;
+    skip = p.plan.splits - 1;
     all_next = (whole >> r) & 1;
     return word * 64 + r;
   };
@@ -378,6 +434,13 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
     }
   }
   const bool live = j < f.Sk;
+  if (p.plan.splits > 1) {
+    if (!live) return;
+    float* row = p.part + (((int64_t)split * f.B * f.H_kv + bh) * f.Sk + j) * (f.d_k + f.d_v);
+    store_sums(row, dk, f.d_k, half);
+    store_sums(row + f.d_k, dv, f.d_v, half);
+    return;
+  }
   const uint32_t odd = not_finite(dk, f.d_k, half) | not_finite(dv, f.d_v, half);
   store_cols(const_cast<uint16_t*>(row_of(p.dk, b, hk, min(j, f.Sk - 1))), dk, f.d_k, half, live && !odd, f.scale);
   store_cols(const_cast<uint16_t*>(row_of(p.dv, b, hk, min(j, f.Sk - 1))), dv, f.d_v, half, live && !odd, 1.0f);
@@ -537,9 +600,13 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
 template <int DK, int DV, bool EXTRA>
 void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
   const LayerAttnParams& f = p.f;
-  const int64_t keys = (int64_t)f.B * f.H_kv * ((f.Sk + 127) / 128), rows = (int64_t)f.B * f.H * ((f.Sq + 127) / 128);
+  const int64_t keys = (int64_t)f.B * f.H_kv * ((f.Sk + 127) / 128) * p.plan.splits, rows = (int64_t)f.B * f.H * ((f.Sq + 127) / 128);
   if (keys)
     hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, EXTRA>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(256), 0, stream, p);
+  if (keys && p.plan.splits > 1) {
+    const int64_t n = (int64_t)f.B * f.H_kv * f.Sk;
+    hipLaunchKernelGGL(attn_bwd_join_kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream, p);
+  }
   if (rows)
     hipLaunchKernelGGL((attn_dq_kernel<DK, DV, EXTRA>), dim3((unsigned)((rows + 7) / 8 * 8)), dim3(256), 0, stream, p);
 }
@@ -550,12 +617,19 @@ void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
 
 }  // namespace
 
-AttnBwdPlan plan_layer_attn_bwd(int B, int H, int Sq) {
+AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k, int d_v, int cus) {
   AttnBwdPlan pl{};
   pl.tiles_q = (Sq + TT - 1) / TT;
   pl.records = 0;
   pl.tiles = (size_t)B * H * pl.tiles_q * ATTN_RECORD * 4;
-  pl.total = pl.tiles + (size_t)B * pl.tiles_q * 16;
+  pl.part = (pl.tiles + (size_t)B * pl.tiles_q * 16 + 255) / 256 * 256;
+  // Few keys, or few key heads of many: the query tiles of 128 keys go to several
+  // workgroups, up to one to a compute unit, if each has two tiles left. More than
+  // eight parts cost more to write and add than they save.
+  const int64_t groups = (int64_t)B * H_kv * ((Sk + 127) / 128), steps = (int64_t)(H / H_kv) * pl.tiles_q;
+  pl.splits = groups ? (int)std::max<int64_t>(1, std::min<int64_t>({cus / groups, steps / 2, 8})) : 1;
+  pl.total = pl.part;
+  if (pl.splits > 1) pl.total += (size_t)pl.splits * B * H_kv * Sk * (d_k + d_v) * 4;
   return pl;
 }
 
