@@ -107,6 +107,14 @@ __device__ __forceinline__ const uint16_t* uniform(const uint16_t* p) {
   return reinterpret_cast<const uint16_t*>((uint64_t)hi << 32 | lo);
 }
 
+// 4 bytes per lane: lane i writes LDS bytes [lds_addr + 4 i, + 4).
+__device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :
+               : "s"(lds_addr), "v"(voff), "s"(sbase)
+               : "memory", "m0");
+}
+
 // Rows row0 .. row0 + R - 1 of `width` columns into a tile of W columns by direct
 // loads of eight rows by 64 columns; WAVES waves share them, PIECES each. Rows from
 // `rows` on repeat the last one and columns from `width` on the row's first: what

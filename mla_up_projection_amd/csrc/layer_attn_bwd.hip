@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void attn_bwd_prep_kernel(LayerAttnBwdParams p
     }
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o);
-    if ((lane & 15) == 0) rec[TT + r] = s;
+    if ((lane & 15) == 0) rec[TT + r] = -s;
   }
   if (wave == 0) {
     const int i = tq * TT + lane;
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void attn_bwd_prep_kernel(LayerAttnBwdParams p
       const float l = f.lse[(int64_t)bh * f.Sq + i];
       l2 = l == -__builtin_inff() ? __builtin_inff() : l * LOG2E;
     }
-    rec[lane] = l2;
+    rec[lane] = p.plain ? -l2 / score_form(f, h).scale2 : l2;
     rec[2 * TT + lane] = __int_as_float(sp.lo);
     rec[3 * TT + lane] = __int_as_float(sp.hi);
     rec[4 * TT + lane] = __int_as_float(f.slopes && i < f.Sq ? row_place(f, b, i) : 0);
@@ -80,9 +80,9 @@ __device__ __forceinline__ Weights pair_weights(const LayerAttnBwdParams& p, con
   float slope;
   const float s = score_of(f, dot_rows(row_of(p.f.q, b, h, i), row_of(p.f.k, b, hk, j), p.f.d_k),
                            __float_as_int(rec[4 * TT + i % TT]), j, slope);
-  const float w = __builtin_amdgcn_exp2f(s - rec[i % TT]);
+  const float w = __builtin_amdgcn_exp2f(p.plain ? s + rec[i % TT] * f.scale2 : s - rec[i % TT]);
   const float dp = dot_rows(row_of(p.dout, b, h, i), row_of(p.f.v, b, hk, j), p.f.d_v);
-  return Weights{w, w * (dp - rec[TT + i % TT]) * slope};
+  return Weights{w, w * (dp + rec[TT + i % TT]) * slope};
 }
 __device__ __forceinline__ const float* record(const LayerAttnBwdParams& p, int b, int h, int tq) {
   return p.records + (((int64_t)b * p.f.H + h) * p.plan.tiles_q + tq) * ATTN_RECORD;
@@ -115,7 +115,7 @@ __device__ __forceinline__ void slow_dq(const LayerAttnBwdParams& p, int b, int 
   store_row(p.dq, b, h, i, o, p.f.d_k, p.f.scale, lane);
 }
 
-__device__ __forceinline__ void slow_dkdv(const LayerAttnBwdParams& p, int b, int hk, int j, int lane) {
+__device__ __forceinline__ void slow_dkdv(const LayerAttnBwdParams& p, int b, int hk, int j, bool want_k, bool want_v, int lane) {
   float ok[3] = {0, 0, 0}, ov[3] = {0, 0, 0};
   for (int h = hk * p.f.group; h < (hk + 1) * p.f.group; ++h) {
     const ScoreForm f = score_form(p.f, h);
@@ -140,8 +140,8 @@ __device__ __forceinline__ void slow_dkdv(const LayerAttnBwdParams& p, int b, in
       }
     }
   }
-  store_row(p.dk, b, hk, j, ok, p.f.d_k, p.f.scale, lane);
-  store_row(p.dv, b, hk, j, ov, p.f.d_v, 1.0f, lane);
+  if (want_k) store_row(p.dk, b, hk, j, ok, p.f.d_k, p.f.scale, lane);
+  if (want_v) store_row(p.dv, b, hk, j, ov, p.f.d_v, 1.0f, lane);
 }
 
 // Columns of a lane's row out of the transposed sums, as bf16. Returns whether one
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(LayerAttnBwdParams p
     odd |= max(max(abs_bits(o[c].x), abs_bits(o[c].y)), max(abs_bits(o[c].z), abs_bits(o[c].w))) >= 0x7F800000u;
   }
   if (__builtin_amdgcn_ballot_w64(odd)) {
-    slow_dkdv(p, b, hk, j, lane);
+    slow_dkdv(p, b, hk, j, true, true, lane);
     return;
   }
 #pragma unroll
@@ -245,30 +245,38 @@ __device__ __forceinline__ void probability(const ScoreForm& sf, f32x16_t& s, f3
   s[r] = __builtin_amdgcn_exp2f(x);
 }
 
+// LDS of the kernel below: three slots of a tile of 64 queries (Q, dO, the record),
+// and two sets of operands that waves hand to each other.
 template <int DK, int DV, bool EXTRA>
-__global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p) {
-  constexpr int QB = TT * 2 * DK, OB = TT * 2 * DV, RB = 2048, SB = QB + OB + RB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SB];
+struct Kv {
+  static constexpr int QB = TT * 2 * DK, OB = TT * 2 * DV, RB = EXTRA ? 1280 : 1024, SB = QB + OB + RB;
+  static constexpr int HAND = 3 * SB, HAND_SET = 8 * 2048, LDS = HAND + 2 * HAND_SET;
+  static_assert(SB % 128 == 0 && LDS <= 160 * 1024, "a compute unit's LDS");
+};
+
+// dK and dV of 128 keys: eight waves, two to 32 keys, so that each SIMD has two to
+// choose from. Of a tile of 64 queries, the first of two waves makes S, P, dP and dS
+// for 32 and the second for the others; then the first adds all 64 to dV and the
+// second to dK. For that they hand P and dS to each other, as operands, through LDS,
+// a tile later: the products with a tile's P and dS run next to the next tile's
+// scores, and one barrier to a tile is enough. S starts from -lse / scale and dP from
+// -delta, which saves registers and subtractions.
+template <int DK, int DV, bool EXTRA, int ROLE>
+__device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* lds, int b, int hk, int bh, int k0, int split,
+                                          int wave, int lane) {
+  using L = Kv<DK, DV, EXTRA>;
   const LayerAttnParams& f = p.f;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5;
-  const int tiles_k = (f.Sk + 127) / 128;
-  const int us = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k * p.plan.splits));
-  if (us < 0) return;
-  const int u = us / p.plan.splits, split = us - u * p.plan.splits;
-  const int bh = u / tiles_k, k0 = (u - bh * tiles_k) * 128;
-  const int b = bh / f.H_kv, hk = bh - b * f.H_kv;
-  const int j = k0 + 32 * wave + (lane & 31);  // this lane's key
+  const int j = k0 + 32 * (wave & 3) + (lane & 31);  // this lane's key
   bf16x8_t kf[DK / 16], vf[DV / 16];
   load_row_frags<DK>(row_of(f.k, b, hk, min(j, f.Sk - 1)), f.d_k, half, kf);
   load_row_frags<DV>(row_of(f.v, b, hk, min(j, f.Sk - 1)), f.d_v, half, vf);
   const uint32_t rb = row_base(lane), cb = col_base(lane);
   const uint32_t ring = lds_u32(lds);
-  f32x16_t dk[DK / 32], dv[DV / 32];
+  constexpr int NB = (ROLE ? DK : DV) / 32;
+  f32x16_t acc[NB];  // dK^T or dV^T
 #pragma unroll
-  for (int n = 0; n < DK / 32; ++n) dk[n] = zero16();
-#pragma unroll
-  for (int n = 0; n < DV / 32; ++n) dv[n] = zero16();
+  for (int n = 0; n < NB; ++n) acc[n] = zero16();
 
   // Query tiles that see any of the keys, and whether all their rows see all of
   // them, looked at 64 tiles at a time: a load in each step would wait for the
@@ -302,154 +310,191 @@ __global__ __launch_bounds__(256, 1) void attn_dkdv_kernel(LayerAttnBwdParams p)
     all_next = (whole >> r) & 1;
     return word * 64 + r;
   };
-  TileLoads<TT, DK, 4> ql(f.d_k, (uint32_t)(f.q.ss * 2), wave, lane);
-  TileLoads<TT, DV, 4> ol(f.d_v, (uint32_t)(p.dout.ss * 2), wave, lane);
-  const float* rec_from = nullptr;
-  const auto begin = [&](int tq, int head) {
+  TileLoads<TT, DK, 8> ql(f.d_k, (uint32_t)(f.q.ss * 2), wave, lane);
+  TileLoads<TT, DV, 8> ol(f.d_v, (uint32_t)(p.dout.ss * 2), wave, lane);
+  const auto load = [&](int tq, int head, uint32_t at) {
     ql.begin(row_of(f.q, b, head, 0), tq * TT, f.Sq);
     ol.begin(row_of(p.dout, b, head, 0), tq * TT, f.Sq);
-    rec_from = record(p, b, head, tq);
+    ql.all(at);
+    ol.all(at + L::QB);
+    const uint16_t* rec = uniform(reinterpret_cast<const uint16_t*>(record(p, b, head, tq)));
+    if (wave == 0) dma16(rec, lane * 16, __builtin_amdgcn_readfirstlane(at + L::QB + L::OB));
+    if (EXTRA && wave == 1) dma4(rec, 1024 + lane * 4, __builtin_amdgcn_readfirstlane(at + L::QB + L::OB + 1024));
   };
-  const auto load_record = [&](uint32_t at) {
-    if (wave < (EXTRA ? 2 : 1))
-      dma16(uniform(reinterpret_cast<const uint16_t*>(rec_from)), wave * 1024 + lane * 16,
-            __builtin_amdgcn_readfirstlane(at + QB + OB + wave * 1024));
+  const auto hand = [&](int set, int w, int i) {  // operand i of wave w's two
+    return reinterpret_cast<u32x4_t*>(lds + L::HAND + set * L::HAND_SET + w * 2048 + i * 1024 + lane * 16);
   };
-  int tq = next(), slot = 0;
+  int tq = next();
   arrived(kf);
   arrived(vf);
   vm_wait<0>();
-  if (tq >= 0) {
-    begin(tq, h);
-    ql.all(ring);
-    ol.all(ring + QB);
-    load_record(ring);
-  }
+  if (tq >= 0) load(tq, h, ring);
   ScoreForm sf = score_form(f, min(h, f.H - 1));
-  while (tq >= 0) {
+  bool before = false;  // a tile's P and dS wait for their products
+  int now = 0, set = 0;
+  bf16x8_t mine[2];
+  while (tq >= 0 || before) {
+    const bool here = tq >= 0, all = all_next;
     const ScoreForm form = sf;
-    const bool all = all_next;
-    const int head = h;
-    tq = next();
-    if (EXTRA && tq >= 0 && h != head) sf = score_form(f, h);
     vm_wait<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was handed over is written
     barrier();
-    const bool more = tq >= 0;
-    const uint32_t fill = ring + (slot ^ 1) * SB;
-    if (more) begin(tq, h);
-    const RowAddr rows = row_addr(rb + (ring + slot * SB));
-    const ColAddr cols = col_addr(cb + (ring + slot * SB));
-    const uint8_t* rec = lds + slot * SB + QB + OB;
-    slot ^= 1;
-    // Four phases for 32 queries: the products for S, dP, dV and dK. Each reads the
-    // next one's operands while its own matrix instructions run.
-    bf16x8_t qr[DK / 16];
+    const int then = now == 0 ? 2 : now - 1, soon = now == 2 ? 0 : now + 1;
+    int tq_next = -1;
+    if (here) {
+      const int head = h;
+      tq_next = next();
+      if (EXTRA && tq_next >= 0 && h != head) sf = score_form(f, h);
+      if (tq_next >= 0) load(tq_next, h, ring + soon * L::SB);
+    }
+    f32x16_t s, dp, slope;
+    bf16x8_t w[2];
+    constexpr int NS = DK / 16, NP = DV / 16, AHEAD = 4;
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    if (here) {
+      const RowAddr rows = row_addr(rb + (ring + now * L::SB));
+      const uint8_t* rec = lds + now * L::SB + L::QB + L::OB + 4 * (32 * ROLE + 4 * half);  // rows 8 g + 4 half + 0..3
+      bf16x8_t op[AHEAD];
+      const auto read = [&](int x) {
+        if (x < NS) op[x % AHEAD] = row_frag<TT>(rows, 0, x, ROLE);
+        else if (x < NS + NP) op[x % AHEAD] = row_frag<TT>(rows, L::QB, x - NS, ROLE);
+      };
+      if (EXTRA) s = zero16();
+      else {
 #pragma unroll
-    for (int c = 0; c < DK / 16; ++c) qr[c] = row_frag<TT>(rows, 0, c, 0);
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(rec + 32 * g);
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
-      typedef int i32x4 __attribute__((ext_vector_type(4)));
-      f32x16_t s, dp;
-      bf16x8_t dr[DV / 16], dc[DV / 32][2], qc[DK / 32][2];
-      f32x4_t lse2[4], delta[4];
-      i32x4 at[4];
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int c = 0; c < DV / 16; ++c) dr[c] = row_frag<TT>(rows, QB, c, qb);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int row = 32 * qb + 8 * g + 4 * half;
-        lse2[g] = *reinterpret_cast<const f32x4_t*>(rec + 4 * row);
-        delta[g] = *reinterpret_cast<const f32x4_t*>(rec + 4 * (TT + row));
-        if (EXTRA) at[g] = *reinterpret_cast<const i32x4*>(rec + 4 * (4 * TT + row));
-      }
-#pragma unroll
-      for (int c = 0; c < DK / 16; ++c) {
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qr[c], kf[c], c ? s : zero16(), 0, 0, 0);
-        if (qb == 0) {  // the next tile's loads, one behind each
-          __builtin_amdgcn_sched_barrier(0);
-          constexpr int PQ = decltype(ql)::PIECES, PO = decltype(ol)::PIECES;
-          static_assert(PQ + PO <= DK / 16, "a load between two matrix instructions");
-          if (more) {
-            if (c < PQ) ql.piece(c, fill);
-            else if (c < PQ + PO) ol.piece(c - PQ, fill + QB);
-            if (c == 0) load_record(fill);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+          for (int r = 0; r < 4; ++r) s[4 * g + r] = v[r];
         }
       }
-      if (qb == 1) interleave<DK / 16, 2, 0>();
+#pragma unroll
+      for (int x = 0; x < AHEAD; ++x) read(x);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int x = 0; x < NS; ++x) {
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], kf[x], s, 0, 0, 0);
+        read(x + AHEAD);
+      }
+      interleave<NS, 1, 0>();
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = 0; n < DV / 32; ++n) dc[n][c] = col_frag<TT>(cols, QB, n, 2 * qb + c);
+      for (int g = 0; g < 4; ++g) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(rec + 4 * TT + 32 * g);
 #pragma unroll
-      for (int c = 0; c < DV / 16; ++c) dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(dr[c], vf[c], c ? dp : zero16(), 0, 0, 0);
-      f32x16_t slope;
+        for (int r = 0; r < 4; ++r) dp[4 * g + r] = v[r];
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        probability<EXTRA>(form, s, slope, r, EXTRA ? at[r / 4][r % 4] - j : 0, lse2[r / 4][r % 4]);
-      interleave<DV / 16, 2, 6>();
+      for (int x = NS; x < NS + NP; ++x) {
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], vf[x - NS], dp, 0, 0, 0);
+        read(x + AHEAD);
+      }
+      if (EXTRA) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t lse2 = *reinterpret_cast<const f32x4_t*>(rec + 32 * g);
+          const i32x4 at = *reinterpret_cast<const i32x4*>(rec + 16 * TT + 32 * g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) probability<true>(form, s, slope, 4 * g + r, at[r] - j, lse2[r]);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r] * form.scale2);
+        interleave<NP - AHEAD, 1, 4>();
+        interleave<AHEAD, 0, 4>();
+      }
       __builtin_amdgcn_sched_barrier(0);
       if (!all) {
         // (dS is 0 with P, unless dP is not finite, which the results then show)
         rare();
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int row = 32 * qb + 8 * g + 4 * half;
-          const i32x4 lo = *reinterpret_cast<const i32x4*>(rec + 4 * (2 * TT + row));
-          const i32x4 hi = *reinterpret_cast<const i32x4*>(rec + 4 * (3 * TT + row));
+          const i32x4 lo = *reinterpret_cast<const i32x4*>(rec + 8 * TT + 32 * g);
+          const i32x4 hi = *reinterpret_cast<const i32x4*>(rec + 12 * TT + 32 * g);
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[4 * g + r] = j >= lo[r] && j < hi[r] ? s[4 * g + r] : 0.0f;
         }
       }
-      const bf16x8_t w[2] = {pack_frag(s, 0), pack_frag(s, 1)};
-      __builtin_amdgcn_sched_barrier(0);
+      // P goes to the first of the two waves, dS to the second
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int i = 0; i < 2; ++i) {
+        w[i] = pack_frag(s, i);
+        if (ROLE) *hand(set, wave, i) = __builtin_bit_cast(u32x4_t, w[i]);
+      }
 #pragma unroll
-        for (int n = 0; n < DK / 32; ++n) qc[n][c] = col_frag<TT>(cols, 0, n, 2 * qb + c);
+      for (int r = 0; r < 16; ++r) dp[r] *= EXTRA ? s[r] * slope[r] : s[r];
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int n = 0; n < DV / 32; ++n) dv[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(dc[n][c], w[c], dv[n], 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta[r / 4][r % 4]);
-      if (EXTRA)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
-      const bf16x8_t d[2] = {pack_frag(dp, 0), pack_frag(dp, 1)};
-      interleave<DV / 16, 3, 6>();
-      __builtin_amdgcn_sched_barrier(0);
-      if (qb == 0)
-#pragma unroll
-        for (int c = 0; c < DK / 16; ++c) qr[c] = row_frag<TT>(rows, 0, c, 1);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int n = 0; n < DK / 32; ++n) dk[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qc[n][c], d[c], dk[n], 0, 0, 0);
-      interleave<DK / 16, 1, 0>();
+      for (int i = 0; i < 2; ++i) {
+        const bf16x8_t d = pack_frag(dp, i);
+        if (ROLE) w[i] = d;
+        else *hand(set, wave, i) = __builtin_bit_cast(u32x4_t, d);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
+    // The tile before: all 64 of its queries, half of them from the other wave.
+    if (before) {
+      const ColAddr cols = col_addr(cb + (ring + then * L::SB));
+      constexpr int N = 4 * NB;
+      bf16x8_t op[AHEAD], theirs[2];
+      const auto read = [&](int y) {
+        if (y < N) op[y % AHEAD] = col_frag<TT>(cols, ROLE ? 0 : L::QB, y % NB, y / NB);
+      };
+#pragma unroll
+      for (int i = 0; i < 2; ++i) theirs[i] = __builtin_bit_cast(bf16x8_t, *hand(set ^ 1, wave ^ 4, i));
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y) read(y);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int y = 0; y < N; ++y) {
+        const int c = y / NB, n = y % NB;
+        acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[y % AHEAD], (c >> 1) == ROLE ? mine[c & 1] : theirs[c & 1], acc[n], 0, 0, 0);
+        read(y + AHEAD);
+      }
+      interleave<N - AHEAD, 2, 0>();
+      interleave<AHEAD, 0, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mine[i] = w[i];
+    before = here;
+    tq = tq_next;
+    now = soon;
+    set ^= 1;
   }
   const bool live = j < f.Sk;
+  const int width = ROLE ? f.d_k : f.d_v;
   if (p.plan.splits > 1) {
     if (!live) return;
     float* row = p.part + (((int64_t)split * f.B * f.H_kv + bh) * f.Sk + j) * (f.d_k + f.d_v);
-    store_sums(row, dk, f.d_k, half);
-    store_sums(row + f.d_k, dv, f.d_v, half);
+    store_sums(row + (ROLE ? 0 : f.d_k), acc, width, half);
     return;
   }
-  const uint32_t odd = not_finite(dk, f.d_k, half) | not_finite(dv, f.d_v, half);
-  store_cols(const_cast<uint16_t*>(row_of(p.dk, b, hk, min(j, f.Sk - 1))), dk, f.d_k, half, live && !odd, f.scale);
-  store_cols(const_cast<uint16_t*>(row_of(p.dv, b, hk, min(j, f.Sk - 1))), dv, f.d_v, half, live && !odd, 1.0f);
+  const uint32_t odd = not_finite(acc, width, half);
+  store_cols(const_cast<uint16_t*>(row_of(ROLE ? p.dk : p.dv, b, hk, min(j, f.Sk - 1))), acc, width, half, live && !odd,
+             ROLE ? f.scale : 1.0f);
   uint64_t bad = __builtin_amdgcn_ballot_w64(live && odd) & 0xFFFFFFFFull;
   while (bad) {
     const int r = __builtin_ctzll(bad);
     bad &= bad - 1;
-    slow_dkdv(p, b, hk, k0 + 32 * wave + r, lane);
+    slow_dkdv(p, b, hk, k0 + 32 * (wave & 3) + r, ROLE, !ROLE, lane);
   }
+}
+
+template <int DK, int DV, bool EXTRA>
+__global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Kv<DK, DV, EXTRA>::LDS];
+  const LayerAttnParams& f = p.f;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_k = (f.Sk + 127) / 128;
+  const int us = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k * p.plan.splits));
+  if (us < 0) return;
+  const int u = us / p.plan.splits, split = us - u * p.plan.splits;
+  const int bh = u / tiles_k, k0 = (u - bh * tiles_k) * 128;
+  const int b = bh / f.H_kv, hk = bh - b * f.H_kv;
+  // (both ways meet the same barriers)
+  if (wave < 4) dkdv_wave<DK, DV, EXTRA, 0>(p, lds, b, hk, bh, k0, split, wave, lane);
+  else dkdv_wave<DK, DV, EXTRA, 1>(p, lds, b, hk, bh, k0, split, wave, lane);
 }
 
 template <int DK, int DV, bool EXTRA>
@@ -486,7 +531,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   const ScoreForm sf = score_form(f, h);
   const int ic = min(i, f.Sq - 1);
   const float* rec = record(p, b, h, ic / TT);
-  float lse2 = rec[ic % TT], delta = rec[TT + ic % TT];
+  float lse2 = EXTRA ? rec[ic % TT] : -rec[ic % TT] * sf.scale2, delta = -rec[TT + ic % TT];
   int place = EXTRA ? __float_as_int(rec[4 * TT + ic % TT]) : 0;
   bf16x8_t q[DK / 16], d[DV / 16];
   load_row_frags<DK>(row_of(f.q, b, h, ic), f.d_k, half, q);
@@ -602,7 +647,7 @@ void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
   const LayerAttnParams& f = p.f;
   const int64_t keys = (int64_t)f.B * f.H_kv * ((f.Sk + 127) / 128) * p.plan.splits, rows = (int64_t)f.B * f.H * ((f.Sq + 127) / 128);
   if (keys)
-    hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, EXTRA>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, EXTRA>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(512), 0, stream, p);
   if (keys && p.plan.splits > 1) {
     const int64_t n = (int64_t)f.B * f.H_kv * f.Sk;
     hipLaunchKernelGGL(attn_bwd_join_kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream, p);
@@ -612,7 +657,7 @@ void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
 }
 template <int DK, int DV>
 void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
-  p.f.cap > 0 || p.f.slopes ? bwd<DK, DV, true>(p, stream) : bwd<DK, DV, false>(p, stream);
+  p.plain ? bwd<DK, DV, false>(p, stream) : bwd<DK, DV, true>(p, stream);
 }
 
 }  // namespace
@@ -633,7 +678,9 @@ AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k,
   return pl;
 }
 
-hipError_t launch_layer_attn_bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
+hipError_t launch_layer_attn_bwd(const LayerAttnBwdParams& p_in, hipStream_t stream) {
+  LayerAttnBwdParams p = p_in;
+  p.plain = !(p.f.cap > 0) && !p.f.slopes && p.f.scale > 0;
   const int64_t blocks = (int64_t)p.f.B * p.f.H * p.plan.tiles_q;
   if (blocks) hipLaunchKernelGGL(attn_bwd_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
   if (p.f.d_k <= 64 && p.f.d_v <= 64) bwd<64, 64>(p, stream);
