@@ -119,8 +119,8 @@ AttnPlanFwd plan_layer_attn(int B, int H, int Sq, int Sk, int d_v, int cus);
 hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream);
 
 // What the backward needs of 64 query rows of a head, in one record of floats and
-// ints: lse in powers of two (plain scores: minus it, in units of the products),
-// minus delta, lo, hi, and the rows' places (64 each).
+// ints: minus lse in powers of two (without a cap in units of the products), minus
+// delta, lo, hi, and the rows' places (64 each).
 struct AttnBwdPlan {
   int tiles_q;            // of 64 query rows
   int splits;             // parts that the query tiles of 128 keys are divided into
@@ -133,7 +133,7 @@ struct LayerAttnBwdParams {
   float* records;         // [B, H, tiles_q, ATTN_RECORD]
   int32_t* tiles;         // [B, tiles_q, 4]: smallest lo, largest hi, largest lo, smallest hi
   float* part;            // [splits, B, H_kv, Sk, d_k + d_v]: sums for dk (without the scale) and dv
-  int plain;              // set by the launcher: scores are products times a positive scale
+  int units;              // set by the launcher: the records hold lse in units of the products
   AttnBwdPlan plan;
 };
 AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k, int d_v, int cus);

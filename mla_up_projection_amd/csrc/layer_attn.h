@@ -186,6 +186,14 @@ __device__ __forceinline__ void arrived(int& x) { asm volatile("" : "+v"(x)); }
 // ---------------------------------------------------------------------------
 // Scores. t = q . k scale; the scores are kept in powers of two (times log2 e).
 // ---------------------------------------------------------------------------
+// How a kernel forms them:
+//   FORM_PLAIN: the product times a positive scale,
+//   FORM_FAR  : the same, less a slope times the distance,
+//   FORM_ANY  : whatever else there is (a cap, a scale that is not positive).
+enum { FORM_PLAIN = 0, FORM_FAR = 1, FORM_ANY = 2 };
+inline int form_of(const LayerAttnParams& p) {
+  return p.cap > 0 || !(p.scale > 0) ? FORM_ANY : p.slopes ? FORM_FAR : FORM_PLAIN;
+}
 struct ScoreForm {
   float scale2;       // scale log2 e, or 2 scale log2 e / cap where there is a cap
   float cap2;         // cap log2 e; 0: none

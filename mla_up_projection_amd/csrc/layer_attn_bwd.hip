@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void attn_bwd_prep_kernel(LayerAttnBwdParams p
       const float l = f.lse[(int64_t)bh * f.Sq + i];
       l2 = l == -__builtin_inff() ? __builtin_inff() : l * LOG2E;
     }
-    rec[lane] = p.plain ? -l2 / score_form(f, h).scale2 : l2;
+    rec[lane] = p.units ? -l2 / score_form(f, h).scale2 : -l2;
     rec[2 * TT + lane] = __int_as_float(sp.lo);
     rec[3 * TT + lane] = __int_as_float(sp.hi);
     rec[4 * TT + lane] = __int_as_float(f.slopes && i < f.Sq ? row_place(f, b, i) : 0);
@@ -80,7 +80,7 @@ __device__ __forceinline__ Weights pair_weights(const LayerAttnBwdParams& p, con
   float slope;
   const float s = score_of(f, dot_rows(row_of(p.f.q, b, h, i), row_of(p.f.k, b, hk, j), p.f.d_k),
                            __float_as_int(rec[4 * TT + i % TT]), j, slope);
-  const float w = __builtin_amdgcn_exp2f(p.plain ? s + rec[i % TT] * f.scale2 : s - rec[i % TT]);
+  const float w = __builtin_amdgcn_exp2f(p.units ? __builtin_fmaf(rec[i % TT], f.scale2, s) : s + rec[i % TT]);
   const float dp = dot_rows(row_of(p.dout, b, h, i), row_of(p.f.v, b, hk, j), p.f.d_v);
   return Weights{w, w * (dp + rec[TT + i % TT]) * slope};
 }
@@ -225,31 +225,29 @@ __global__ __launch_bounds__(256) void attn_bwd_join_kernel(LayerAttnBwdParams p
   }
 }
 
-// P out of products, and with a cap its derivative. Element r of a block: row 8 (r /
-// 4) + 4 half + r % 4 of the streamed tile's 32, column the lane's own.
-template <bool EXTRA>
-__device__ __forceinline__ void probability(const ScoreForm& sf, f32x16_t& s, f32x16_t& slope, int r, int away, float lse2) {
-  float x;
-  if (EXTRA) {
-    x = s[r] * sf.scale2;
-    slope[r] = 1.0f;
+// P out of product s, and with a cap its derivative; minus the row's lse is `less`, or
+// within s (then `less` is 0).
+template <int FORM>
+__device__ __forceinline__ float probability(const ScoreForm& sf, float s, float far, float less, float& slope) {
+  float x = __builtin_fmaf(s, sf.scale2, FORM == FORM_ANY ? 0.0f : less);
+  if (FORM == FORM_ANY) {
+    slope = 1.0f;
     if (sf.cap2 > 0) {
       const float t = tanh_of(x);
-      slope[r] = 1.0f - t * t;
+      slope = 1.0f - t * t;
       x = sf.cap2 * t;
     }
-    x = x - sf.slope2 * fabsf((float)away) - lse2;
-  } else {
-    x = __builtin_fmaf(s[r], sf.scale2, -lse2);
+    x += less;
   }
-  s[r] = __builtin_amdgcn_exp2f(x);
+  if (FORM != FORM_PLAIN) x = __builtin_fmaf(-sf.slope2, fabsf(far), x);
+  return __builtin_amdgcn_exp2f(x);
 }
 
 // LDS of the kernel below: three slots of a tile of 64 queries (Q, dO, the record),
 // and two sets of operands that waves hand to each other.
-template <int DK, int DV, bool EXTRA>
+template <int DK, int DV, int FORM>
 struct Kv {
-  static constexpr int QB = TT * 2 * DK, OB = TT * 2 * DV, RB = EXTRA ? 1280 : 1024, SB = QB + OB + RB;
+  static constexpr int QB = TT * 2 * DK, OB = TT * 2 * DV, RB = FORM == FORM_PLAIN ? 1024 : 1280, SB = QB + OB + RB;
   static constexpr int HAND = 3 * SB, HAND_SET = 8 * 2048, LDS = HAND + 2 * HAND_SET;
   static_assert(SB % 128 == 0 && LDS <= 160 * 1024, "a compute unit's LDS");
 };
@@ -261,10 +259,10 @@ struct Kv {
 // a tile later: the products with a tile's P and dS run next to the next tile's
 // scores, and one barrier to a tile is enough. S starts from -lse / scale and dP from
 // -delta, which saves registers and subtractions.
-template <int DK, int DV, bool EXTRA, int ROLE>
+template <int DK, int DV, int FORM, int ROLE>
 __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* lds, int b, int hk, int bh, int k0, int split,
                                           int wave, int lane) {
-  using L = Kv<DK, DV, EXTRA>;
+  using L = Kv<DK, DV, FORM>;
   const LayerAttnParams& f = p.f;
   const int half = lane >> 5;
   const int j = k0 + 32 * (wave & 3) + (lane & 31);  // this lane's key
@@ -319,7 +317,7 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
     ol.all(at + L::QB);
     const uint16_t* rec = uniform(reinterpret_cast<const uint16_t*>(record(p, b, head, tq)));
     if (wave == 0) dma16(rec, lane * 16, __builtin_amdgcn_readfirstlane(at + L::QB + L::OB));
-    if (EXTRA && wave == 1) dma4(rec, 1024 + lane * 4, __builtin_amdgcn_readfirstlane(at + L::QB + L::OB + 1024));
+    if (FORM != FORM_PLAIN && wave == 1) dma4(rec, 1024 + lane * 4, __builtin_amdgcn_readfirstlane(at + L::QB + L::OB + 1024));
   };
   const auto hand = [&](int set, int w, int i) {  // operand i of wave w's two
     return reinterpret_cast<u32x4_t*>(lds + L::HAND + set * L::HAND_SET + w * 2048 + i * 1024 + lane * 16);
@@ -344,7 +342,7 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
     if (here) {
       const int head = h;
       tq_next = next();
-      if (EXTRA && tq_next >= 0 && h != head) sf = score_form(f, h);
+      if (FORM != FORM_PLAIN && tq_next >= 0 && h != head) sf = score_form(f, h);
       if (tq_next >= 0) load(tq_next, h, ring + soon * L::SB);
     }
     f32x16_t s, dp, slope;
@@ -359,7 +357,7 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
         if (x < NS) op[x % AHEAD] = row_frag<TT>(rows, 0, x, ROLE);
         else if (x < NS + NP) op[x % AHEAD] = row_frag<TT>(rows, L::QB, x - NS, ROLE);
       };
-      if (EXTRA) s = zero16();
+      if (FORM == FORM_ANY) s = zero16();
       else {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -390,19 +388,25 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
         dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(op[x % AHEAD], vf[x - NS], dp, 0, 0, 0);
         read(x + AHEAD);
       }
-      if (EXTRA) {
+      if (FORM == FORM_PLAIN) {
+        float unused;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4_t lse2 = *reinterpret_cast<const f32x4_t*>(rec + 32 * g);
-          const i32x4 at = *reinterpret_cast<const i32x4*>(rec + 16 * TT + 32 * g);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) probability<true>(form, s, slope, 4 * g + r, at[r] - j, lse2[r]);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r] * form.scale2);
+        for (int r = 0; r < 16; ++r) s[r] = probability<FORM>(form, s[r], 0, 0, unused);
         interleave<NP - AHEAD, 1, 4>();
         interleave<AHEAD, 0, 4>();
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const i32x4 at = *reinterpret_cast<const i32x4*>(rec + 16 * TT + 32 * g);
+          f32x4_t less = {0, 0, 0, 0};
+          if (FORM == FORM_ANY) less = *reinterpret_cast<const f32x4_t*>(rec + 32 * g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float c = 1.0f;
+            s[4 * g + r] = probability<FORM>(form, s[4 * g + r], (float)(at[r] - j), less[r], c);
+            if (FORM == FORM_ANY) slope[4 * g + r] = c;
+          }
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
       if (!all) {
@@ -423,7 +427,7 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
         if (ROLE) *hand(set, wave, i) = __builtin_bit_cast(u32x4_t, w[i]);
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] *= EXTRA ? s[r] * slope[r] : s[r];
+      for (int r = 0; r < 16; ++r) dp[r] *= FORM == FORM_ANY ? s[r] * slope[r] : s[r];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const bf16x8_t d = pack_frag(dp, i);
@@ -481,9 +485,9 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
   }
 }
 
-template <int DK, int DV, bool EXTRA>
+template <int DK, int DV, int FORM>
 __global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Kv<DK, DV, EXTRA>::LDS];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Kv<DK, DV, FORM>::LDS];
   const LayerAttnParams& f = p.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_k = (f.Sk + 127) / 128;
@@ -493,11 +497,11 @@ __global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p)
   const int bh = u / tiles_k, k0 = (u - bh * tiles_k) * 128;
   const int b = bh / f.H_kv, hk = bh - b * f.H_kv;
   // (both ways meet the same barriers)
-  if (wave < 4) dkdv_wave<DK, DV, EXTRA, 0>(p, lds, b, hk, bh, k0, split, wave, lane);
-  else dkdv_wave<DK, DV, EXTRA, 1>(p, lds, b, hk, bh, k0, split, wave, lane);
+  if (wave < 4) dkdv_wave<DK, DV, FORM, 0>(p, lds, b, hk, bh, k0, split, wave, lane);
+  else dkdv_wave<DK, DV, FORM, 1>(p, lds, b, hk, bh, k0, split, wave, lane);
 }
 
-template <int DK, int DV, bool EXTRA>
+template <int DK, int DV, int FORM>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   constexpr int KB = TT * 2 * DK, VB = TT * 2 * DV, SB = KB + VB;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SB];
@@ -531,8 +535,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   const ScoreForm sf = score_form(f, h);
   const int ic = min(i, f.Sq - 1);
   const float* rec = record(p, b, h, ic / TT);
-  float lse2 = EXTRA ? rec[ic % TT] : -rec[ic % TT] * sf.scale2, delta = -rec[TT + ic % TT];
-  int place = EXTRA ? __float_as_int(rec[4 * TT + ic % TT]) : 0;
+  float less = FORM == FORM_ANY ? rec[ic % TT] : rec[ic % TT] * sf.scale2, delta = rec[TT + ic % TT];  // (both minus)
+  int place = FORM != FORM_PLAIN ? __float_as_int(rec[4 * TT + ic % TT]) : 0;
   bf16x8_t q[DK / 16], d[DV / 16];
   load_row_frags<DK>(row_of(f.q, b, h, ic), f.d_k, half, q);
   load_row_frags<DV>(row_of(p.dout, b, h, ic), f.d_v, half, d);
@@ -546,7 +550,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   for (int n = 0; n < DK / 32; ++n) dq[n] = zero16();
   arrived(q);
   arrived(d);
-  arrived(lse2);
+  arrived(less);
   arrived(delta);
   arrived(place);
   vm_wait<0>();
@@ -596,6 +600,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
       interleave<NS, 1, 0>();
       __builtin_amdgcn_sched_barrier(0);
       const int j0 = t * TT + 32 * k + 4 * half;
+      const float far = FORM != FORM_PLAIN ? (float)(place - j0) : 0.0f;
 #pragma unroll
       for (int c = 0; c < NP; ++c) {
         const int x = k * N + NS + c;
@@ -603,13 +608,17 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
         read(x + AHEAD);
       }
 #pragma unroll
-      for (int r = 0; r < 16; ++r) probability<EXTRA>(sf, s, slope, r, place - (j0 + 8 * (r / 4) + r % 4), lse2);
+      for (int r = 0; r < 16; ++r) {
+        float c = 1.0f;
+        s[r] = probability<FORM>(sf, s[r], far - (float)(8 * (r / 4) + r % 4), less, c);
+        if (FORM == FORM_ANY) slope[r] = c;
+      }
       interleave<NP - AHEAD, 1, 4>();
       interleave<AHEAD, 2, 4>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] - delta);
-      if (EXTRA)
+      for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] + delta);
+      if (FORM == FORM_ANY)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
       if (!all) {
@@ -642,22 +651,26 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   }
 }
 
-template <int DK, int DV, bool EXTRA>
+template <int DK, int DV, int FORM>
 void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
   const LayerAttnParams& f = p.f;
   const int64_t keys = (int64_t)f.B * f.H_kv * ((f.Sk + 127) / 128) * p.plan.splits, rows = (int64_t)f.B * f.H * ((f.Sq + 127) / 128);
   if (keys)
-    hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, EXTRA>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, FORM>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(512), 0, stream, p);
   if (keys && p.plan.splits > 1) {
     const int64_t n = (int64_t)f.B * f.H_kv * f.Sk;
     hipLaunchKernelGGL(attn_bwd_join_kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream, p);
   }
   if (rows)
-    hipLaunchKernelGGL((attn_dq_kernel<DK, DV, EXTRA>), dim3((unsigned)((rows + 7) / 8 * 8)), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((attn_dq_kernel<DK, DV, FORM>), dim3((unsigned)((rows + 7) / 8 * 8)), dim3(256), 0, stream, p);
 }
 template <int DK, int DV>
 void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
-  p.plain ? bwd<DK, DV, false>(p, stream) : bwd<DK, DV, true>(p, stream);
+  switch (form_of(p.f)) {
+    case FORM_PLAIN: bwd<DK, DV, FORM_PLAIN>(p, stream); break;
+    case FORM_FAR: bwd<DK, DV, FORM_FAR>(p, stream); break;
+    default: bwd<DK, DV, FORM_ANY>(p, stream);
+  }
 }
 
 }  // namespace
@@ -680,7 +693,7 @@ AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k,
 
 hipError_t launch_layer_attn_bwd(const LayerAttnBwdParams& p_in, hipStream_t stream) {
   LayerAttnBwdParams p = p_in;
-  p.plain = !(p.f.cap > 0) && !p.f.slopes && p.f.scale > 0;
+  p.units = form_of(p.f) != FORM_ANY;
   const int64_t blocks = (int64_t)p.f.B * p.f.H * p.plan.tiles_q;
   if (blocks) hipLaunchKernelGGL(attn_bwd_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, p);
   if (p.f.d_k <= 64 && p.f.d_v <= 64) bwd<64, 64>(p, stream);

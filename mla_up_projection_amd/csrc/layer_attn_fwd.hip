@@ -62,10 +62,7 @@ struct Fwd {
   static constexpr int NJ = DK / 16, NV = DV / 32;
 };
 
-// EXTRA: scores have a cap, depend on distance or fall as the product rises; else
-// they are the products times a positive scale, which the exponent's one fused
-// multiply-add brings in.
-template <int DK, int DV, int WAVES, bool EXTRA>
+template <int DK, int DV, int WAVES, int FORM>
 __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kernel(LayerAttnParams p) {
   using F = Fwd<DK, DV>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * F::SB];
@@ -109,7 +106,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   }
 
   const ScoreForm sf = score_form(p, h);
-  int place = EXTRA && p.slopes && i < p.Sq ? row_place(p, b, i) : 0;
+  int place = FORM != FORM_PLAIN && p.slopes && i < p.Sq ? row_place(p, b, i) : 0;
   arrived(place);
   bf16x8_t q[F::NJ];
   load_row_frags<DK>(row_of(p.q, b, h, min(i, p.Sq - 1)), p.d_k, half, q);
@@ -180,14 +177,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     __builtin_amdgcn_sched_barrier(0);
     // element r of block k: key t TK + 32 k + 8 (r / 4) + 4 half + r % 4
     const int j0 = t * TK + 4 * half;
-    if (EXTRA) {
+    if (FORM != FORM_PLAIN) {
+      const float far = (float)(place - j0);  // (past 2^24 keys away the distance is rounded)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
+          const float d = fabsf(far - (float)(32 * k + 8 * (r / 4) + r % 4));
           float x = s[k][r] * sf.scale2;
-          if (p.cap > 0) x = sf.cap2 * tanh_of(x);
-          s[k][r] = x - sf.slope2 * fabsf((float)(place - (j0 + 32 * k + 8 * (r / 4) + r % 4)));
+          if (FORM == FORM_ANY && p.cap > 0) x = sf.cap2 * tanh_of(x);
+          s[k][r] = __builtin_fmaf(-sf.slope2, d, x);
         }
     }
     if (t * TK < wlo_all || (t + 1) * TK > whi_all) {
@@ -207,7 +206,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
       const u32x2_t x = swap_halves(__float_as_uint(mt), __float_as_uint(mt));
       mt = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
     }
-    const float sc = EXTRA ? 1.0f : sf.scale2;
+    // (plain scores are still products: the exponent's fused multiply-add scales them)
+    const float sc = FORM == FORM_PLAIN ? sf.scale2 : 1.0f;
     mt *= sc;
     // The sums are rescaled only where the maximum rises by more than 2^8: weights
     // up to that lose nothing in bf16 and fp32.
@@ -359,7 +359,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
   const uint32_t mine = (uint32_t)(bad >> (lane & 32));
   if (live && in && !mine)
     *reinterpret_cast<uint2*>(const_cast<uint16_t*>(row_of(p.out, b, h, i)) + c) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-#pragma unroll
   for (int k = 0; k < 2; ++k)
     if ((uint32_t)(bad >> (32 * k)))
       slow_forward(p, __shfl(b, 32 * k), __shfl(h, 32 * k), __shfl(i, 32 * k), !__shfl((int)fine, 32 * k), lane);
@@ -402,8 +401,11 @@ template <int DK, int DV, int WAVES>
 void fwd(const LayerAttnParams& p, hipStream_t stream) {
   const int64_t units = p.plan.groups * p.plan.splits;
   const dim3 grid((unsigned)((units + 7) / 8 * 8)), block(64 * WAVES);
-  if (p.cap > 0 || p.slopes || !(p.scale > 0)) hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, true>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, false>), grid, block, 0, stream, p);
+  switch (form_of(p)) {
+    case FORM_PLAIN: hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, FORM_PLAIN>), grid, block, 0, stream, p); break;
+    case FORM_FAR: hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, FORM_FAR>), grid, block, 0, stream, p); break;
+    default: hipLaunchKernelGGL((attn_fwd_kernel<DK, DV, WAVES, FORM_ANY>), grid, block, 0, stream, p);
+  }
 }
 template <int DK, int DV>
 void fwd(const LayerAttnParams& p, hipStream_t stream) {
