@@ -600,7 +600,7 @@ typedef struct {
 } mla_rmsnorm_args;
 
 /* Errors: MLA_EINVAL (also where neither y nor codes nor h nor rstd is asked
- * for), MLA_EALIAS, MLA_EDEVICE. */
+ * for), MLA_EALIAS, MLA_EUNSUPPORTED (2^22 rows and more), MLA_EDEVICE. */
 MLA_API mla_status mla_rmsnorm_fwd(const mla_rmsnorm_args* args, void* stream);
 
 /* Its backward. With xhat = h rstd and g = gamma dy:
@@ -635,7 +635,7 @@ MLA_API mla_status mla_rmsnorm_bwd(const mla_rmsnorm_bwd_args* args, void* strea
 /* Quantize the rows of a matrix to int8 with one scale each, by the rule of
  * mla_rmsnorm_fwd: the weights of mla_qup_fwd_i8 (a scale for each output
  * channel), or its activations.
- *   x      : as mxfp8_quantize. rows: 0 .. 2^24; cols: a multiple of 8, > 0.
+ *   x      : as mxfp8_quantize. rows: 0 .. 2^24 - 1; cols: a multiple of 8, > 0.
  *   codes  : device int8[rows*cols], 8-byte aligned. scales: device float[rows].
  * Errors: MLA_EINVAL, MLA_EALIAS, MLA_EDEVICE. */
 MLA_API mla_status int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,

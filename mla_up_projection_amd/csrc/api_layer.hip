@@ -60,6 +60,7 @@ mla_status mla_rmsnorm_fwd(const mla_rmsnorm_args* a, void* stream) {
   if (a->ld_x < a->K || a->ld_x % 8 || a->ld_x > ((int64_t)1 << 40)) return MLA_EINVAL;
   if (!(a->eps >= 0) || !isfinite(a->eps)) return MLA_EINVAL;
   if (a->T == 0) return MLA_OK;
+  if (a->T >= (1 << 22)) return MLA_EUNSUPPORTED;  // (a grid's work-items stay below 2^32)
   if (!a->y && !a->codes && !a->h && !a->rstd) return MLA_EINVAL;
   if ((a->res || a->h) && !float_type(a->res_dtype)) return MLA_EINVAL;
   if (a->gamma && !float_type(a->gamma_dtype)) return MLA_EINVAL;
@@ -155,7 +156,7 @@ mla_status mla_rmsnorm_bwd(const mla_rmsnorm_bwd_args* a, void* stream) {
 mla_status int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* codes,
                          float* scales, void* stream) {
   if (!float_type(x_dtype)) return MLA_EINVAL;
-  if (rows < 0 || rows > ((int64_t)1 << 24) || cols <= 0 || cols % 8 || ld < cols || ld > ((int64_t)1 << 40)) return MLA_EINVAL;
+  if (rows < 0 || rows >= ((int64_t)1 << 24) || cols <= 0 || cols % 8 || ld < cols || ld > ((int64_t)1 << 40)) return MLA_EINVAL;
   if (rows == 0) return MLA_OK;
   if (rows > ((int64_t)1 << 36) / cols) return MLA_EINVAL;
   const size_t es = float_size(x_dtype);

@@ -189,10 +189,11 @@ __device__ __forceinline__ void arrived(int& x) { asm volatile("" : "+v"(x)); }
 // How a kernel forms them:
 //   FORM_PLAIN: the product times a positive scale,
 //   FORM_FAR  : the same, less a slope times the distance,
-//   FORM_ANY  : whatever else there is (a cap, a scale that is not positive).
+//   FORM_ANY  : whatever else there is (a cap, a scale that is not positive, or so
+//               small that lse in units of the products would leave fp32's range).
 enum { FORM_PLAIN = 0, FORM_FAR = 1, FORM_ANY = 2 };
 inline int form_of(const LayerAttnParams& p) {
-  return p.cap > 0 || !(p.scale > 0) ? FORM_ANY : p.slopes ? FORM_FAR : FORM_PLAIN;
+  return p.cap > 0 || !(p.scale > 0x1p-60f) ? FORM_ANY : p.slopes ? FORM_FAR : FORM_PLAIN;
 }
 struct ScoreForm {
   float scale2;       // scale log2 e, or 2 scale log2 e / cap where there is a cap

@@ -29,12 +29,15 @@ __device__ __forceinline__ void slow_forward(const LayerAttnParams& p, int b, in
     if (j < sp.hi) s = score_of(f, dot_rows(q, row_of(p.k, b, hk, j), p.d_k), at, j, g);
     const float mt = la_wave_max(s);
     const float mn = fmaxf(m, mt), mu = mn == -__builtin_inff() ? 0.0f : mn;
-    const float a = __builtin_amdgcn_exp2f(m - mu);
     float w = __builtin_amdgcn_exp2f(s - mu);  // (NaN scores make NaN here)
+    // o is the mean so far, so that it stays in the values' range
+    const float kept = l * __builtin_amdgcn_exp2f(m - mu);
     m = mn;
-    l = l * a + la_wave_sum(w);
-    o[0] *= a;
-    o[1] *= a;
+    l = kept + la_wave_sum(w);
+    const float inv = l > 0 ? 1.0f / l : l;
+    w *= inv;
+    o[0] *= kept * inv;
+    o[1] *= kept * inv;
     const int n = min(64, sp.hi - j0);
     for (int r = 0; r < n; ++r) {
       const float wr = __shfl(w, r);
@@ -51,7 +54,7 @@ __device__ __forceinline__ void slow_forward(const LayerAttnParams& p, int b, in
   uint16_t* out = const_cast<uint16_t*>(row_of(p.out, b, h, i));
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    if (lane + 64 * c < p.d_v) out[lane + 64 * c] = (uint16_t)f32_to_bf16_bits(none ? 0.0f : o[c] / l);
+    if (lane + 64 * c < p.d_v) out[lane + 64 * c] = (uint16_t)f32_to_bf16_bits(none ? 0.0f : o[c]);
   if (p.lse && want_lse && lane == 0)
     p.lse[((int64_t)b * p.H + h) * p.Sq + i] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
 }
@@ -341,7 +344,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
   const bool in = c < p.d_v;
   float4 o = make_float4(0, 0, 0, 0);
   const float* from = p.part_o + slot0 * p.d_v + c;
-#pragma unroll 4
   for (int s = 0; s < n; ++s) {
     const float ws = __shfl(s < 32 ? w[0] : w[1], (lane & 32) | (s & 31));
     if (in) {

@@ -68,7 +68,7 @@ def norm(**over):
     (dict(gamma_dtype=3), EINVAL), (dict(res=None), EINVAL), (dict(q_dtype=0), EINVAL), (dict(scales=None), EINVAL),
     (dict(codes=None), EINVAL), (dict(h=None, rstd=None, y=None, codes=None, scales=None), EINVAL), (dict(codes=addr(7, 4)), EINVAL),
     (dict(q_dtype=3, scales=addr(8, 2)), EINVAL), (dict(y=addr(1)), EALIAS), (dict(h=addr(2)), EALIAS), (dict(y=addr(6), h=addr(6, 16)), EALIAS),
-    (dict(rstd=addr(3)), EALIAS), (dict(T=0, x=None), OK),
+    (dict(rstd=addr(3)), EALIAS), (dict(T=0, x=None), OK), (dict(T=1 << 22), EUNSUP),
 ])
 def test_norm(L, over, status):
     assert L.mla_rmsnorm_fwd(ctypes.byref(norm(**over)), None) == status
@@ -99,7 +99,7 @@ def test_norm_workspace(L):
 @pytest.mark.parametrize("args, status", [
     ((addr(1), 2, 5, 64, 64, addr(2), addr(3)), EINVAL), ((addr(1), 0, -1, 64, 64, addr(2), addr(3)), EINVAL),
     ((addr(1), 0, 5, 60, 64, addr(2), addr(3)), EINVAL), ((addr(1), 0, 5, 64, 56, addr(2), addr(3)), EINVAL),
-    ((addr(1), 0, (1 << 24) + 1, 64, 64, addr(2), addr(3)), EINVAL), ((None, 0, 5, 64, 64, addr(2), addr(3)), EINVAL),
+    ((addr(1), 0, 1 << 24, 64, 64, addr(2), addr(3)), EINVAL), ((None, 0, 5, 64, 64, addr(2), addr(3)), EINVAL),
     ((addr(1), 0, 5, 64, 68, addr(2), addr(3)), EINVAL), ((addr(1), 0, 5, 64, 64, addr(2, 4), addr(3)), EINVAL),
     ((addr(1), 0, 5, 64, 64, addr(1), addr(3)), EALIAS), ((addr(1), 0, 5, 64, 64, addr(2), addr(2)), EALIAS),
     ((None, 0, 0, 64, 64, None, None), OK),

@@ -96,7 +96,7 @@ def test_sequence_bounds_outside_the_rows_are_cut():
 
 
 # ------------------------------------------------------------------ values
-WIDTHS = [(192, 128), (128, 128), (64, 64), (96, 64), (8, 8), (40, 24), (72, 128), (136, 120)]
+WIDTHS = [(192, 128), (128, 128), (64, 64), (96, 64), (8, 8), (40, 24), (72, 128), (136, 120), (24, 96), (192, 8)]
 
 
 @pytest.mark.parametrize("dk, dv", WIDTHS)
@@ -174,6 +174,56 @@ def test_large_scores_and_a_maximum_that_rises_late():
     q, k, v, do = make(4, 1, 2, 2, 130, 700, 64, 64)
     k = (k.float() * torch.linspace(0.1, 30, 700, device=DEV)[None, None, :, None]).to(BF)
     check(q, k, v, torch.ones(1, 130, 700, dtype=torch.bool, device=DEV), scale=1.0, dout=do)
+
+
+@pytest.mark.parametrize("H, hk, S", [(2, 1, 4500), (4, 1, 4200), (1, 1, 8300)])
+def test_many_tiles(H, hk, S):
+    """More than 64 tiles of 64 queries, so that the list of those that see a key has several words, for every head."""
+    cu = [0, 5, 1000, 4100, S - 30]
+    q, k, v, do = make(S, 1, H, hk, S, S, 64, 64)
+    s, _ = spans_of(1, S, S, cu_q=cu)
+    check(q, k, v, ref.span_mask(s, S), scale=0.15, spans=s, dout=do)
+
+
+@pytest.mark.parametrize("Sq", [3, 150])
+def test_keys_that_batch_entries_share(Sq):
+    """Keys and values of one entry seen by all of the batch (stride 0)."""
+    q, k, v, _ = make(Sq, 3, 4, 2, Sq, 333, 128, 128)
+    k, v = k[:1].expand(3, -1, -1, -1), v[:1].expand(3, -1, -1, -1)
+    assert k.stride(0) == 0
+    check(q, k, v, torch.ones(3, Sq, 333, dtype=torch.bool, device=DEV), scale=0.1)
+
+
+def test_rows_past_32_bits_of_offset():
+    """Batch entries 2^31 elements apart, in bytes past 2^32."""
+    B, H, S, d = 2, 1, 70, 64
+    far = (1 << 31) + 64
+    g = gen(21)
+    t = {n: torch.as_strided(torch.empty(far + H * S * d, dtype=BF, device=DEV), (B, H, S, d), (far, S * d, d, 1))
+         for n in ("q", "k", "v", "do")}
+    for x in t.values():
+        x.copy_(rand(g, B, H, S, d))
+    s, _ = spans_of(B, S, S)
+    check(t["q"], t["k"], t["v"], ref.span_mask(s, S), scale=0.1, spans=s, dout=t["do"])
+
+
+@pytest.mark.parametrize("Sq, Sk", [(5, 900), (150, 300)])
+def test_values_at_the_end_of_the_range(Sq, Sk):
+    """A mean of values up to 2^127 is finite, also where their sum is not."""
+    q, k, v, _ = make(31, 1, 2, 2, Sq, Sk, 64, 64)
+    v = torch.where(v.float() > 0, 2.0 ** 127, 2.0 ** 126).to(BF)
+    k = (k.float() * torch.linspace(0.2, 8, Sk, device=DEV)[None, None, :, None]).to(BF)
+    s = torch.ones(1, Sq, Sk, dtype=torch.bool, device=DEV)
+    out, _ = forward(q, k, v, scale=1.0)
+    o, _, p, _ = ref.attention(q, k, v, s, 1.0)
+    ref.within(out, o, ref.attention_bound(q, v, o, p), "out")
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e-6])
+def test_scales_near_nothing(scale):
+    q, k, v, do = make(32, 1, 2, 2, 100, 100, 64, 64)
+    s, _ = spans_of(1, 100, 100)
+    check(q, k, v, ref.span_mask(s, 100), scale=scale, spans=s, dout=do)
 
 
 # ------------------------------------------------------------------ what is not seen

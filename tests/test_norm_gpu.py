@@ -144,3 +144,29 @@ def test_int8_quantize(rows, cols, dtype):
     s = x.to(F64).abs().amax(1) / 127
     ref.within(scales, s, s * 2.0 ** -23, "scales")
     ref.within(codes, x.to(F64) / s[:, None], torch.tensor(0.5 + 1e-4, device=DEV, dtype=F64), "codes")
+
+
+def test_rows_past_32_bits_of_offset():
+    T, K = 530000, 8192  # 2^32 elements and more
+    x, y = (torch.empty(T, K, dtype=BF, device=DEV) for _ in range(2))
+    g = gen(3)
+    at = [0, 1, T - 2, T - 1]
+    x[at] = rand(g, len(at), K)
+    m.mla_rmsnorm_fwd(x, None, eps=1e-6, y=y)
+    want = ref.norm(x[at], None, 1e-6)[2]
+    ref.within(y[at], want, want.abs() * (ref.BF16 + SUM) + 1e-30, "y")
+
+
+@pytest.mark.parametrize("T", [255, 256, 257, 300])
+@pytest.mark.parametrize("K", [544, 2048, 2080])
+def test_both_divisions_of_rows_agree(T, K):
+    """Few rows are divided over more waves than many: codes and scales as they are for each row alone."""
+    g = gen(T + K)
+    x, gamma = rand(g, T, K), rand(g, K)
+    codes, scales = torch.empty(T, K, dtype=torch.uint8, device=DEV), torch.empty(T, K // 32, dtype=torch.uint8, device=DEV)
+    y, one = torch.empty_like(x), torch.empty(1, K, dtype=BF, device=DEV)
+    m.mla_rmsnorm_fwd(x, gamma, y=y, codes=codes, scales=scales)
+    m.mla_rmsnorm_fwd(x[T - 1:], gamma, y=one)
+    want = ref.norm(x[T - 1:], gamma, 1e-6)[2]
+    for got in (y[T - 1:], one):
+        ref.within(got, want, want.abs() * (ref.BF16 + SUM) + 1e-30, "y")
