@@ -760,53 +760,84 @@ def mla_tree_attention(q, pool, out, seqs, cu_q, *, stream=None, **kw):
 # ----------------------------------------------------- around the projection --
 _I8 = torch.int8
 _FLOATS = (_BF16, _FP32)
+_BF16S = (_BF16,)
 
 
 def _dtype_of(t) -> int:
     return DTYPE_FP32 if t is not None and t.dtype == _FP32 else DTYPE_BF16
 
 
+class _Fast(_Dev):
+    """_Dev whose first tensor has named the device: `index` is that of the GPU."""
+
+    def __init__(self, where, t):
+        self.where, self.device, self.index = where, t.device, t.get_device()
+
+
+def _first(where, t, name, dtypes) -> _Fast:
+    """The checks of a call whose first tensor is t (of any strides)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device.type != DEVICE_TYPE:
+        _Dev(where)(t[:0] if isinstance(t, torch.Tensor) and t.dim() else t, name, dtypes)
+    return _Fast(where, t)
+
+
 def _opt(chk, t, name, dtype, numel):
     """Device address of a tensor that may be missing; _Dev's checks, and its words where one fails."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == numel and t.device == chk.device
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.get_device() == chk.index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
     return chk(t, name, (dtype,), numel=numel)
+
+
+def _launch(chk, stream, fn, args):
+    """fn(args, stream): the given stream, or the device's current one, with the device current while the call lasts."""
+    index = chk.index
+    if index < 0 or index != torch._C._cuda_getDevice():
+        return _call(chk.where, chk.device, stream, fn, ctypes.byref(args))
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = fn(ctypes.byref(args), raw)
+    if status:
+        raise MlaError(status, chk.where)
 
 
 def _float(chk, t, name, numel):
     """The same for a bf16 or fp32 tensor, and its type."""
     if t is None:
         return None, DTYPE_BF16
-    if isinstance(t, torch.Tensor) and t.dtype is _FP32:
-        return _opt(chk, t, name, _FP32, numel), DTYPE_FP32
-    return (_opt(chk, t, name, _BF16, numel) if isinstance(t, torch.Tensor) and t.dtype is _BF16
-            else chk(t, name, _FLOATS, numel=numel)), DTYPE_BF16
+    dtype = getattr(t, "dtype", None)
+    if dtype is not _BF16 and dtype is not _FP32:
+        chk(t, name, _FLOATS)  # raises
+    return _opt(chk, t, name, dtype, numel), DTYPE_FP32 if dtype is _FP32 else DTYPE_BF16
 
 
-def _row_view(chk, t, name, dtypes):
-    """Address and row stride of a 2-D tensor whose rows are dense."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (t.stride(1) != 1 and t.numel() and t.shape[1] > 1):
-        raise ValueError(f"{chk.where}: {name} must be 2-D with contiguous rows")
+def _row_view(where, t, name, dtypes):
+    """The checks of a call whose first tensor is 2-D with dense rows, its address and row stride."""
+    chk = _first(where, t, name, dtypes)
+    if t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be 2-D with contiguous rows")
     rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols:
-        raise ValueError(f"{chk.where}: the rows of {name} overlap")
-    if t.dtype not in dtypes or t.device.type != DEVICE_TYPE or (chk.device is not None and t.device != chk.device):
-        chk(t[:0], name, dtypes)
-    chk.device = t.device
-    return t.data_ptr(), ld
+    ld, step = t.stride()
+    if step != 1 and cols > 1 and rows:
+        raise ValueError(f"{where}: {name} must be 2-D with contiguous rows")
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"{where}: the rows of {name} overlap")
+    return chk, t.data_ptr(), ld, rows, cols
 
 
 def mla_rmsnorm_fwd(x, gamma, *, eps=1e-6, res=None, h=None, y=None, codes=None, scales=None, rstd=None, stream=None):
     """RMS norm of x bf16 [T,K] (row stride may exceed K), to which res bf16/fp32 [T,K] is added first. Outputs, each
     optional: h [T,K] like res (the sum), y bf16 [T,K], rstd fp32 [T], and 8-bit codes of y: uint8 [T,K] with scales
     uint8 [T,K/32] (MXFP8), or int8 [T,K] with scales fp32 [T]. gamma bf16/fp32 [K] or None (ones)."""
-    chk = _Dev("mla_rmsnorm_fwd")
-    px, ld = _row_view(chk, x, "x", (_BF16,))
-    T, K = x.shape
+    chk, px, ld, T, K = _row_view("mla_rmsnorm_fwd", x, "x", _BF16S)
     n = T * K
     pr, res_dtype = _float(chk, res, "res", n)
     pg, gamma_dtype = _float(chk, gamma, "gamma", K)
@@ -822,7 +853,7 @@ def mla_rmsnorm_fwd(x, gamma, *, eps=1e-6, res=None, h=None, y=None, codes=None,
     a = mla_rmsnorm_args(px, ld, pr, res_dtype, pg, gamma_dtype, eps, T, K,
                          _opt(chk, h, "h", _FP32 if res_dtype == DTYPE_FP32 else _BF16, n),
                          _opt(chk, rstd, "rstd", _FP32, T), _opt(chk, y, "y", _BF16, n), q_dtype, pc, ps)
-    _call(chk.where, chk.device, stream, lib().mla_rmsnorm_fwd, ctypes.byref(a))
+    _launch(chk, stream, lib().mla_rmsnorm_fwd, a)
 
 
 def mla_rmsnorm_bwd_workspace_size(T, K) -> int:
@@ -834,9 +865,7 @@ def mla_rmsnorm_bwd(dy, h, rstd, gamma, *, dh=None, dx=None, dres=None, dgamma=N
     exceed K); rstd fp32 [T]; dh [T,K] like h, the gradient that reaches h on other ways, or None. Outputs, each
     optional: the gradient of x and res as dx bf16 [T,K] and dres fp32 [T,K], and dgamma fp32 [K], which needs a
     workspace of mla_rmsnorm_bwd_workspace_size(T, K) bytes."""
-    chk = _Dev("mla_rmsnorm_bwd")
-    ph, ld = _row_view(chk, h, "h", _FLOATS)
-    T, K = h.shape
+    chk, ph, ld, T, K = _row_view("mla_rmsnorm_bwd", h, "h", _FLOATS)
     n = T * K
     pg, gamma_dtype = _float(chk, gamma, "gamma", K)
     ws, ws_bytes = _workspace(chk, workspace)
@@ -845,14 +874,12 @@ def mla_rmsnorm_bwd(dy, h, rstd, gamma, *, dh=None, dx=None, dres=None, dgamma=N
     a = mla_rmsnorm_bwd_args(_opt(chk, dy, "dy", _BF16, n), ph, _dtype_of(h), ld, _opt(chk, rstd, "rstd", _FP32, T), pg,
                              gamma_dtype, _opt(chk, dh, "dh", h.dtype, n), T, K, _opt(chk, dx, "dx", _BF16, n),
                              _opt(chk, dres, "dres", _FP32, n), _opt(chk, dgamma, "dgamma", _FP32, K), ws, ws_bytes)
-    _call(chk.where, chk.device, stream, lib().mla_rmsnorm_bwd, ctypes.byref(a))
+    _launch(chk, stream, lib().mla_rmsnorm_bwd, a)
 
 
 def int8_quantize(x, codes, scales, stream=None):
     """x [rows, cols] bf16/fp32 (row stride may exceed cols) -> codes int8 [rows, cols], scales fp32 [rows]."""
-    chk = _Dev("int8_quantize")
-    px, ld = _row_view(chk, x, "x", _FLOATS)
-    rows, cols = x.shape
+    chk, px, ld, rows, cols = _row_view("int8_quantize", x, "x", _FLOATS)
     pc, ps = _opt(chk, codes, "codes", _I8, rows * cols), _opt(chk, scales, "scales", _FP32, rows)
     _call(chk.where, chk.device, stream, lib().int8_quantize, px, _dtype_of(x), rows, cols, ld, pc, ps)
 
@@ -862,14 +889,11 @@ def mla_qup_fwd_i8(x, x_scales, w, w_scales, out, *, H, d_nope, d_rope, cos=None
     """Forward in 8-bit integers: x int8 [T,K] with x_scales fp32 [T] (mla_rmsnorm_fwd, int8_quantize), w int8 [N,K]
     with w_scales fp32 [N] (int8_quantize); out and out_scales as mla_qup_fwd's. positions int32 [T]: each token's
     position, in place of the format's."""
-    chk = _Dev("mla_qup_fwd_i8")
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("mla_qup_fwd_i8: x must be [T, K]")
+    chk = _first("mla_qup_fwd_i8", x, "x", (_I8,))
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("mla_qup_fwd_i8: x must be [T, K] and contiguous")
     T, K = x.shape
     N = H * (d_nope + d_rope)
-    if x.dtype is not _I8 or x.device.type != DEVICE_TYPE or not x.is_contiguous():
-        chk(x, "x", (_I8,))
-    chk.device = x.device
     px = x.data_ptr()
     tk = mla_tokens(FMT_BSHD, B, S if S is not None else (T // B if B else 0), T) if fmt == FMT_BSHD else \
         _tokens(chk, T, fmt, B, S, cu_seqlens, max_seqlen)
@@ -886,7 +910,7 @@ def mla_qup_fwd_i8(x, x_scales, w, w_scales, out, *, H, d_nope, d_rope, cos=None
                         tk, _opt(chk, positions, "positions", _I32, T), rope, DTYPE_MXFP8 if mx else DTYPE_BF16,
                         _opt(chk, out, "out", _U8 if mx else _BF16, T * N),
                         _opt(chk, out_scales, "out_scales", _U8, T * N // 32))
-    _call(chk.where, chk.device, stream, lib().mla_qup_fwd_i8, ctypes.byref(a))
+    _launch(chk, stream, lib().mla_qup_fwd_i8, a)
 
 
 def mla_attn_spans(spans, at=None, *, Sk, cu_q=None, cu_k=None, len_q=None, len_k=None, prefix=None, causal=True,
@@ -895,13 +919,10 @@ def mla_attn_spans(spans, at=None, *, Sk, cu_q=None, cu_k=None, len_q=None, len_
     at int32 [B,Sq] or None. Packed documents: cu_q int32 [n+1] (and cu_k, None: the same); else one sequence per batch
     entry with len_q / len_k int32 [B] (None: all rows). prefix int32 [n or B]: keys that all rows of a sequence see.
     window: how far back a row sees (0: all the way)."""
-    chk = _Dev("mla_attn_spans")
-    if not isinstance(spans, torch.Tensor) or spans.dim() != 3 or spans.shape[2] != 2:
-        raise ValueError("mla_attn_spans: spans must be [B, Sq, 2]")
+    chk = _first("mla_attn_spans", spans, "spans", (_I32,))
+    if spans.dim() != 3 or spans.shape[2] != 2 or not spans.is_contiguous():
+        raise ValueError("mla_attn_spans: spans must be [B, Sq, 2] and contiguous")
     B, Sq = spans.shape[:2]
-    if spans.dtype is not _I32 or spans.device.type != DEVICE_TYPE or not spans.is_contiguous():
-        chk(spans, "spans", (_I32,))
-    chk.device = spans.device
     n, nseq, pq = B, 0, None
     if cu_q is not None:
         pq = chk(cu_q, "cu_q", (_I32,), min_numel=2)
@@ -912,14 +933,14 @@ def mla_attn_spans(spans, at=None, *, Sk, cu_q=None, cu_k=None, len_q=None, len_
                             _opt(chk, cu_k, "cu_k", _I32, n + 1), nseq, _opt(chk, len_q, "len_q", _I32, n),
                             _opt(chk, len_k, "len_k", _I32, n), _opt(chk, prefix, "prefix", _I32, n),
                             1 if causal else 0, window)
-    _call(chk.where, chk.device, stream, lib().mla_attn_spans, ctypes.byref(a))
+    _launch(chk, stream, lib().mla_attn_spans, a)
 
 
 def _attn_rows(chk, t, name, shape):
     """A bf16 [B, H, S, d] view whose rows are dense; other strides are free."""
     if not isinstance(t, torch.Tensor) or t.shape != shape:
         raise ValueError(f"{chk.where}: {name} must be {list(shape)}")
-    if t.dtype is not _BF16 or t.device != chk.device:
+    if t.dtype is not _BF16 or t.get_device() != chk.index:
         chk(t[:0], name, (_BF16,))
     b, h, s, d = t.stride()
     if d != 1 and shape[3] > 1 and t.numel():
@@ -937,11 +958,8 @@ def _attn_sizes(where, q, k, v):
 
 
 def _attn_args(where, q, k, v, out, lse, scale, cap, slopes, spans, at, workspace):
-    chk = _Dev(where)
+    chk = _first(where, q, "q", _BF16S)
     sizes = B, H, H_kv, Sq, Sk, d_k, d_v = _attn_sizes(where, q, k, v)
-    if q.device.type != DEVICE_TYPE:
-        chk(q[:0], "q", (_BF16,))
-    chk.device = q.device
     ws, ws_bytes = _workspace(chk, workspace)
     a = mla_attn_args(_attn_rows(chk, q, "q", (B, H, Sq, d_k)), _attn_rows(chk, k, "k", (B, H_kv, Sk, d_k)),
                       _attn_rows(chk, v, "v", (B, H_kv, Sk, d_v)), _attn_rows(chk, out, "out", (B, H, Sq, d_v)),
@@ -978,7 +996,7 @@ def mla_attn_fwd(q, k, v, out, *, scale, lse=None, cap=0.0, slopes=None, spans=N
     cap: scores go through cap tanh(./cap); slopes fp32 [H]: minus slope times distance; spans and at from
     mla_attn_spans (None: every key). workspace: mla_attn_fwd_workspace_size() bytes (None if that is 0)."""
     chk, a = _attn_args("mla_attn_fwd", q, k, v, out, lse, scale, cap, slopes, spans, at, workspace)
-    _call(chk.where, chk.device, stream, lib().mla_attn_fwd, ctypes.byref(a))
+    _launch(chk, stream, lib().mla_attn_fwd, a)
 
 
 def mla_attn_bwd_workspace_size(dout, q, k, v, out=None, lse=None, dq=None, dk=None, dv=None, *, scale, cap=0.0, **_) -> int:
@@ -997,4 +1015,4 @@ def mla_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, *, scale, cap=0.0, slopes=
     ws, ws_bytes = _workspace(chk, workspace)
     a = mla_attn_bwd_args(fwd, _attn_rows(chk, dout, "dout", out.shape), _attn_rows(chk, dq, "dq", q.shape),
                           _attn_rows(chk, dk, "dk", k.shape), _attn_rows(chk, dv, "dv", v.shape), ws, ws_bytes)
-    _call(chk.where, chk.device, stream, lib().mla_attn_bwd, ctypes.byref(a))
+    _launch(chk, stream, lib().mla_attn_bwd, a)
