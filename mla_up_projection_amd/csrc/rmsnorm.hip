@@ -399,12 +399,13 @@ void norm_bwd(const NormBwdParams& p, hipStream_t stream) {
 
 hipError_t launch_rmsnorm(const NormParams& p, hipStream_t stream) {
   if (p.T == 0) return hipSuccess;
-  // few rows: as many waves to a row as it has elements for, since nothing but its
-  // latency counts
-  const bool few = p.T <= 256;
+  // Few rows: as many waves to a row as it has elements for, since its latency is what
+  // counts (1024 rows of 1536: 4.3 us, with a wave to a row 5.2; 300 of 7168: 5.9 and,
+  // with eight waves, 6.0). Many rows: more of each in a wave, whose loads are under
+  // way together (8192 of 1536: 13.6 us and 16.2; 4096 of 4096: 23.6 and 29.3).
   if (p.K <= 512) norm<1, 1, true>(p, stream);
-  else if (p.K <= 2048) few ? norm<4, 1, true>(p, stream) : norm<1, 4, false>(p, stream);
-  else if (p.K <= 8192) few ? norm<16, 1, true>(p, stream) : norm<4, 4, false>(p, stream);
+  else if (p.K <= 2048) p.T <= 2048 ? norm<4, 1, true>(p, stream) : norm<1, 4, false>(p, stream);
+  else if (p.K <= 8192) p.T <= 512 ? norm<16, 1, true>(p, stream) : norm<8, 2, false>(p, stream);
   else norm<16, 4, false>(p, stream);
   return hipGetLastError();
 }

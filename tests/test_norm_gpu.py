@@ -157,8 +157,8 @@ def test_rows_past_32_bits_of_offset():
     ref.within(y[at], want, want.abs() * (ref.BF16 + SUM) + 1e-30, "y")
 
 
-@pytest.mark.parametrize("T", [255, 256, 257, 300])
-@pytest.mark.parametrize("K", [544, 2048, 2080])
+@pytest.mark.parametrize("T", [512, 513, 2048, 2049])
+@pytest.mark.parametrize("K", [544, 2048, 2080, 7168])
 def test_both_divisions_of_rows_agree(T, K):
     """Few rows are divided over more waves than many: codes and scales as they are for each row alone."""
     g = gen(T + K)
