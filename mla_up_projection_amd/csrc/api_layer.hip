@@ -469,6 +469,7 @@ mla_status mla_attn_bwd(const mla_attn_bwd_args* a, void* stream) {
   p.plan = plan;
   p.records = (float*)((uint8_t*)a->workspace + plan.records);
   p.tiles = (int32_t*)((uint8_t*)a->workspace + plan.tiles);
+  p.live = (int32_t*)((uint8_t*)a->workspace + plan.live);
   p.part = (float*)((uint8_t*)a->workspace + plan.part);
   return launched(mla::launch_layer_attn_bwd(p, (hipStream_t)stream));
 }

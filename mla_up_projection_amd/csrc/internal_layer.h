@@ -124,7 +124,7 @@ hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream);
 struct AttnBwdPlan {
   int tiles_q;            // of 64 query rows
   int splits;             // parts that the query tiles of 128 keys are divided into
-  size_t records, tiles, part, total;
+  size_t records, tiles, live, part, total;
 };
 constexpr int ATTN_RECORD = 512;  // words of a record
 struct LayerAttnBwdParams {
@@ -132,6 +132,7 @@ struct LayerAttnBwdParams {
   AttnRows dout, dq, dk, dv;
   float* records;         // [B, H, tiles_q, ATTN_RECORD]
   int32_t* tiles;         // [B, tiles_q, 4]: smallest lo, largest hi, largest lo, smallest hi
+  int32_t* live;          // [B, tiles_q]: first row that sees something, and behind the last << 8
   float* part;            // [splits, B, H_kv, Sk, d_k + d_v]: sums for dk (without the scale) and dv
   int units;              // set by the launcher: the records hold lse in units of the products
   AttnBwdPlan plan;

@@ -116,9 +116,10 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 }
 
 // Rows row0 .. row0 + R - 1 of `width` columns into a tile of W columns by direct
-// loads of eight rows by 64 columns; WAVES waves share them, PIECES each. Rows from
-// `rows` on repeat the last one and columns from `width` on the row's first: what
-// they hold meets zeros or is masked. The pieces are issued one at a time, between
+// loads of eight rows by 64 columns; WAVES waves share them, PIECES each. Only rows
+// `first` .. `end` - 1 are read: others of the tile repeat the nearest of those, so that
+// what lies in rows that nobody here sees, NaN for instance, does not meet a weight
+// of 0. Columns from `width` on repeat the row's first; they meet zeros. The pieces are issued one at a time, between
 // matrix instructions.
 template <int R, int W, int WAVES>
 struct TileLoads {
@@ -128,7 +129,7 @@ struct TileLoads {
   uint32_t col[KINDS][W / 64];  // bytes into the row
   const uint16_t* from;
   uint32_t stride;
-  int last, wave, r0;
+  int low, high, wave, r0;
 
   __device__ __forceinline__ TileLoads(int width, uint32_t stride_bytes, int w, int lane) : stride(stride_bytes), wave(w), r0(lane >> 3) {
 #pragma unroll
@@ -140,13 +141,14 @@ struct TileLoads {
       }
   }
   // base: the first row of the batch entry and head
-  __device__ __forceinline__ void begin(const uint16_t* base, int row0, int rows) {
+  __device__ __forceinline__ void begin(const uint16_t* base, int row0, int first, int end) {
     from = uniform(base + (int64_t)row0 * (stride >> 1));
-    last = rows - 1 - row0;
+    low = max(first - row0, 0);
+    high = end - 1 - row0;
   }
   __device__ __forceinline__ void piece(int i, uint32_t tile) const {
     const int j = i * WAVES + wave, b = i * WAVES / (R / 8), r8 = (j % (R / 8)) * 8;
-    const uint32_t row = (uint32_t)min(r0 + r8, last);
+    const uint32_t row = (uint32_t)min(max(r0 + r8, low), high);
     dma16(from, __umul24(row, stride) + col[WAVES == 1 ? i & 1 : 0][b], __builtin_amdgcn_readfirstlane(tile + j * 1024));
   }
   __device__ __forceinline__ void all(uint32_t tile) const {

@@ -30,7 +30,8 @@ __global__ __launch_bounds__(256) void attn_bwd_prep_kernel(LayerAttnBwdParams p
   for (int k = 0; k < 4; ++k) {
     const int r = 16 * wave + 4 * k + (lane >> 4), i = tq * TT + r;
     float s = 0;
-    if (i < f.Sq && c < f.d_v) {
+    const Span sp = row_span(f, b, i);
+    if (sp.lo < sp.hi && c < f.d_v) {  // (0 for a row that sees nothing, whatever is in it)
       const u32x4_t x = *reinterpret_cast<const u32x4_t*>(row_of(p.dout, b, h, i) + c);
       const u32x4_t y = *reinterpret_cast<const u32x4_t*>(row_of(f.out, b, h, i) + c);
 #pragma unroll
@@ -65,7 +66,12 @@ __global__ __launch_bounds__(256) void attn_bwd_prep_kernel(LayerAttnBwdParams p
         lo_all = max(lo_all, __shfl_xor(lo_all, o));
         hi_all = min(hi_all, __shfl_xor(hi_all, o));
       }
-      if (lane == 0) *reinterpret_cast<int4*>(p.tiles + 4 * ((int64_t)b * p.plan.tiles_q + tq)) = make_int4(lo, hi, lo_all, hi_all);
+      const uint64_t live = __builtin_amdgcn_ballot_w64(sp.lo < sp.hi);
+      if (lane == 0) {
+        const int64_t at = (int64_t)b * p.plan.tiles_q + tq;
+        *reinterpret_cast<int4*>(p.tiles + 4 * at) = make_int4(lo, hi, lo_all, hi_all);
+        p.live[at] = live ? __builtin_ctzll(live) | (64 - __builtin_clzll(live)) << 8 : 0;
+      }
     }
   }
 }
@@ -280,8 +286,8 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
   // them, looked at 64 tiles at a time: a load in each step would wait for the
   // tile that is on its way. Of several parts each takes every splits-th.
   int h = hk * f.group, word = -1, skip = split;
-  uint64_t left = 0, whole = 0;
-  bool all_next = false;
+  uint64_t left = 0, whole = 0, holes = 0;
+  bool all_next = false, hole_next = false;
   const auto next = [&]() {
     for (;;) {
       const int n = __builtin_popcountll(left);
@@ -292,12 +298,14 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
         if (++h >= (hk + 1) * f.group) return -1;
       }
       const int tq = word * 64 + lane;
-      bool some = false, all = false;
+      bool some = false, all = false, hole = false;
       if (tq < p.plan.tiles_q) {
         const int4 x = *reinterpret_cast<const int4*>(p.tiles + 4 * ((int64_t)b * p.plan.tiles_q + tq));
         some = x.x < k0 + 128 && x.y > k0;
         all = x.z <= k0 && x.w >= k0 + 128;
+        hole = x.w == 0;  // a row sees nothing
       }
+      holes = __builtin_amdgcn_ballot_w64(hole);
       left = __builtin_amdgcn_ballot_w64(some);
       whole = __builtin_amdgcn_ballot_w64(all);
     }
@@ -306,13 +314,20 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
     left &= left - 1;
     skip = p.plan.splits - 1;
     all_next = (whole >> r) & 1;
+    hole_next = (holes >> r) & 1;
     return word * 64 + r;
   };
   TileLoads<TT, DK, 8> ql(f.d_k, (uint32_t)(f.q.ss * 2), wave, lane);
   TileLoads<TT, DV, 8> ol(f.d_v, (uint32_t)(p.dout.ss * 2), wave, lane);
   const auto load = [&](int tq, int head, uint32_t at) {
-    ql.begin(row_of(f.q, b, head, 0), tq * TT, f.Sq);
-    ol.begin(row_of(p.dout, b, head, 0), tq * TT, f.Sq);
+    int first = tq * TT, end = first + TT;
+    if (hole_next) {  // padding in front of or behind the rows that see something (or no rows at all)
+      const int live = __builtin_amdgcn_readfirstlane(p.live[(int64_t)b * p.plan.tiles_q + tq]);
+      end = first + (live >> 8);
+      first += live & 255;
+    }
+    ql.begin(row_of(f.q, b, head, 0), tq * TT, first, end);
+    ol.begin(row_of(p.dout, b, head, 0), tq * TT, first, end);
     ql.all(at);
     ol.all(at + L::QB);
     const uint16_t* rec = uniform(reinterpret_cast<const uint16_t*>(record(p, b, head, tq)));
@@ -555,8 +570,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   arrived(place);
   vm_wait<0>();
   if (first < last) {
-    kl.begin(kb, first * TT, f.Sk);
-    vl.begin(vb, first * TT, f.Sk);
+    kl.begin(kb, first * TT, lo, hi);
+    vl.begin(vb, first * TT, lo, hi);
     kl.all(ring);
     vl.all(ring + KB);
   }
@@ -567,8 +582,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
     barrier();
     const bool more = t + 1 < last;
     if (more) {
-      kl.begin(kb, (t + 1) * TT, f.Sk);
-      vl.begin(vb, (t + 1) * TT, f.Sk);
+      kl.begin(kb, (t + 1) * TT, lo, hi);
+      vl.begin(vb, (t + 1) * TT, lo, hi);
       kl.all(fill);
       vl.all(fill + KB);
     }
@@ -680,7 +695,8 @@ AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k,
   pl.tiles_q = (Sq + TT - 1) / TT;
   pl.records = 0;
   pl.tiles = (size_t)B * H * pl.tiles_q * ATTN_RECORD * 4;
-  pl.part = (pl.tiles + (size_t)B * pl.tiles_q * 16 + 255) / 256 * 256;
+  pl.live = pl.tiles + (size_t)B * pl.tiles_q * 16;
+  pl.part = (pl.live + (size_t)B * pl.tiles_q * 4 + 255) / 256 * 256;
   // Few keys, or few key heads of many: the query tiles of 128 keys go to several
   // workgroups, up to one to a compute unit, if each has two tiles left. More than
   // eight parts cost more to write and add than they save.

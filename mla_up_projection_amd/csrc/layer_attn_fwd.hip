@@ -126,8 +126,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   arrived(q);
   vm_wait<0>();
   if (first < last) {
-    kl.begin(kb, first * TK, p.Sk);
-    vl.begin(vb, first * TK, p.Sk);
+    kl.begin(kb, first * TK, lo, hi);
+    vl.begin(vb, first * TK, lo, hi);
     kl.all(ring);
     vl.all(ring + F::KB);
   }
@@ -138,8 +138,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     barrier();
     const bool more = t + 1 < last;
     if (more) {
-      kl.begin(kb, (t + 1) * TK, p.Sk);
-      vl.begin(vb, (t + 1) * TK, p.Sk);
+      kl.begin(kb, (t + 1) * TK, lo, hi);
+      vl.begin(vb, (t + 1) * TK, lo, hi);
     }
     const RowAddr kt = row_addr(rb + (ring + slot * F::SB));
     const ColAddr vt = col_addr(cb + (ring + slot * F::SB));

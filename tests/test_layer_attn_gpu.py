@@ -126,6 +126,18 @@ def test_caps_and_distances(cap, slope, scale, dk, dv):
     check(q, k, v, ref.span_mask(s, Sk), scale=scale, cap=cap, slopes=slopes, spans=s, at=at, dout=do)
 
 
+@pytest.mark.parametrize("Sq, Sk", [(1, 700), (40, 90), (200, 200)])
+def test_distances_without_places(Sq, Sk):
+    """Without `at` the queries are the last of the keys; without spans they see all of them; lse need not be asked for."""
+    q, k, v, do = make(Sq, 2, 4, 4, Sq, Sk, 64, 64)
+    slopes = torch.tensor([0.5, 0.1, 0.01, 0.0], device=DEV)
+    out, _ = check(q, k, v, torch.ones(2, Sq, Sk, dtype=torch.bool, device=DEV), scale=0.2, slopes=slopes, dout=do)
+    alone = torch.empty_like(out)
+    ws = torch.empty(m.mla_attn_fwd_workspace_size(q, k, v, scale=0.2) or 1, dtype=torch.uint8, device=DEV)
+    m.mla_attn_fwd(q, k, v, alone, scale=0.2, slopes=slopes, workspace=ws)
+    assert torch.equal(alone, out)
+
+
 @pytest.mark.parametrize("H, hk", [(8, 8), (8, 2), (6, 1)])
 def test_packed_documents(H, hk):
     cu = [0, 1, 64, 64, 200, 333, 460]  # rows 460 .. 499 are padding
@@ -247,6 +259,32 @@ def test_rows_that_are_not_seen_have_no_influence(bad, Sq):
     for name, a, b in zip(("dq", "dk", "dv"), backward(do2, q2, k2, v2, out, lse, scale=0.1, spans=s), grads):
         assert torch.isfinite(a).all(), name
         ref.within(a, b.to(F64), b.to(F64).abs() * 4 * ref.BF16 + 0.02 * b.float().abs().max(), name)
+
+
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_holes_between_rows(cap):
+    """Rows that see nothing in front of, between and behind others, all with NaN: gradients of the others are finite
+    and what they are without them."""
+    Sq, Sk = 260, 300
+    q, k, v, do = make(17, 1, 4, 2, Sq, Sk, 64, 64)
+    s, _ = spans_of(1, Sq, Sk, causal=False)
+    s[:, :, 0], s[:, :, 1] = 30, 250
+    for a, b in ((0, 5), (64, 70), (100, 101), (120, 192), (255, 260)):
+        s[:, a:b] = 7
+    sees = ref.span_mask(s, Sk)
+    kw = dict(scale=0.1, cap=cap, spans=s)
+    check(q, k, v, sees, dout=do, **kw)
+    out, lse = forward(q, k, v, **kw)
+    want = backward(do, q, k, v, out, lse, **kw)
+    dead = ~sees[0].any(1)
+    q[:, :, dead], do[:, :, dead] = float("nan"), float("inf")
+    k[:, :, :30], k[:, :, 250:], v[:, :, :30], v[:, :, 250:] = float("nan"), float("nan"), float("inf"), float("nan")
+    again, lse2 = forward(q, k, v, **kw)
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+    for name, a, b in zip(("dq", "dk", "dv"), backward(do, q, k, v, again, lse2, **kw), want):
+        assert torch.isfinite(a).all(), name
+        ref.within(a, b.to(F64), b.to(F64).abs() * 4 * ref.BF16 + 0.02 * b.float().abs().max(), name)
+    assert (want[1][:, :, :30] == 0).all() and (want[1][:, :, 250:] == 0).all()
 
 
 def test_a_value_that_some_see():

@@ -48,6 +48,7 @@ def want(x, w, xs, ws, b, cos, sin, H, dn, dr, pos):
 
 
 SHAPES = [(1, 64, 1, 128, 64), (1, 1536, 16, 128, 64), (16, 192, 3, 64, 64), (17, 320, 5, 0, 64), (33, 1536, 8, 128, 64),
+          (17, 64, 43, 128, 64), (33, 576, 64, 64, 64), (64, 1088, 257, 0, 32), (32, 512, 129, 64, 0), (50, 1536, 128, 128, 64),
           (64, 128, 2, 32, 0), (65, 64, 1, 128, 64), (130, 192, 3, 16, 16), (300, 1536, 5, 128, 64), (129, 128, 7, 0, 64)]
 
 
@@ -65,7 +66,8 @@ def test_bf16_output(T, K, H, dn, dr, bias):
     ref.within(out[0].transpose(0, 1), q, q.abs() * ref.BF16 + size * 2.0 ** -21 + 1e-30, "out")
 
 
-@pytest.mark.parametrize("T, K, H, dn, dr", [(1, 64, 1, 128, 64), (17, 320, 5, 0, 64), (130, 192, 3, 16, 16), (300, 1536, 5, 128, 64)])
+@pytest.mark.parametrize("T, K, H, dn, dr", [(1, 64, 1, 128, 64), (17, 320, 5, 0, 64), (33, 576, 64, 64, 64), (64, 1088, 257, 0, 32),
+                                            (130, 192, 3, 16, 16), (300, 1536, 5, 128, 64)])
 def test_mxfp8_output(T, K, H, dn, dr):
     a = case(T, K, H, dn, dr, T)
     pos = torch.arange(T, device=DEV, dtype=torch.int32)
@@ -85,8 +87,9 @@ def test_mxfp8_output(T, K, H, dn, dr):
 
 
 @pytest.mark.parametrize("fmt, T", [("bshd", 60), ("sbhd", 60), ("thd", 60), ("bshd", 210), ("sbhd", 210), ("thd", 210)])
-def test_token_formats(fmt, T):
-    H, dn, dr, K = 3, 128, 64, 256
+@pytest.mark.parametrize("H", [3, 45])
+def test_token_formats(fmt, T, H):
+    dn, dr, K = 128, 64, 256
     a = case(T, K, H, dn, dr, 11)
     x, w, xs, ws, b, cos, sin = a
     kw = dict(H=H, d_nope=dn, d_rope=dr, cos=cos, sin=sin)
