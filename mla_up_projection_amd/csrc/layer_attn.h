@@ -234,6 +234,10 @@ __device__ __forceinline__ const uint16_t* row_of(const AttnRows& r, int b, int 
 
 // Workgroup g of a grid of n units, rounded up to a multiple of 8, on the chip's
 // eight dies: consecutive units share a die, and with it that die's L2. -1: none.
+// Batch entries come inside heads in the order of units, so that every die has its
+// part of a long sequence among short ones (eight sequences of 256 to 2048 tokens, 16
+// heads: forward 133 us and backward 494; with heads inside, 217 and 741; equal
+// lengths: 222 and 777, 229 and 774).
 __device__ __forceinline__ int die_order(uint32_t g, uint32_t n) {
   const uint32_t per = (n + 7) / 8, u = (g & 7) * per + (g >> 3);
   return u < n ? (int)u : -1;

@@ -509,8 +509,8 @@ __global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p)
   const int us = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k * p.plan.splits));
   if (us < 0) return;
   const int u = us / p.plan.splits, split = us - u * p.plan.splits;
-  const int bh = u / tiles_k, k0 = (u - bh * tiles_k) * 128;
-  const int b = bh / f.H_kv, hk = bh - b * f.H_kv;
+  const int hb = u / tiles_k, k0 = (u - hb * tiles_k) * 128;
+  const int hk = hb / f.B, b = hb - hk * f.B, bh = b * f.H_kv + hk;
   // (both ways meet the same barriers)
   if (wave < 4) dkdv_wave<DK, DV, FORM, 0>(p, lds, b, hk, bh, k0, split, wave, lane);
   else dkdv_wave<DK, DV, FORM, 1>(p, lds, b, hk, bh, k0, split, wave, lane);
@@ -526,8 +526,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   const int tiles = (f.Sq + 127) / 128;
   const int u = die_order(blockIdx.x, (uint32_t)(f.B * f.H * tiles));
   if (u < 0) return;
-  const int bh = u / tiles, t0 = tiles - 1 - (u - bh * tiles);  // the last rows first
-  const int b = bh / f.H, h = bh - b * f.H, hk = h / f.group;
+  const int hb = u / tiles, t0 = tiles - 1 - (u - hb * tiles);  // the last rows first
+  const int h = hb / f.B, b = hb - h * f.B, hk = h / f.group;
   const int i = t0 * 128 + 32 * wave + (lane & 31);
   const Span sp = row_span(f, b, i);
   int lo = INT32_MAX, hi = 0;

@@ -75,8 +75,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
   if (u < 0) return;
   const int split = u % p.plan.splits, g = u / p.plan.splits;
   // the last query tiles, whose rows see the most under a causal mask, go first
-  const int bh = g / p.plan.tiles_q, tq = p.plan.tiles_q - 1 - (g - bh * p.plan.tiles_q);
-  const int b = bh / p.H, h = bh - b * p.H, hk = h / p.group;
+  const int hb = g / p.plan.tiles_q, tq = p.plan.tiles_q - 1 - (g - hb * p.plan.tiles_q);
+  const int h = hb / p.B, b = hb - h * p.B, hk = h / p.group;
   const int i = tq * (32 * WAVES) + 32 * wave + (lane & 31);  // this lane's query
   const Span sp = row_span(p, b, i);
 
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
     }
   }
   if (p.lse && live && fine && half == 0)
-    p.lse[(int64_t)bh * p.Sq + i] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
+    p.lse[((int64_t)b * p.H + h) * p.Sq + i] = none ? -__builtin_inff() : (m + __builtin_log2f(l)) * LN2;
   uint64_t bad = __builtin_amdgcn_ballot_w64(live && odd) & 0xFFFFFFFFull;
   while (bad) {
     const int r = __builtin_ctzll(bad);
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
   const int64_t row = live ? at : rows_all - 1, bh = row / p.Sq;
   const int i = (int)(row - bh * p.Sq), b = (int)(bh / p.H), h = (int)(bh - (int64_t)b * p.H);
   const int rows = p.plan.rows, tq = i / rows, n = p.plan.splits;
-  const int64_t g = bh * p.plan.tiles_q + (p.plan.tiles_q - 1 - tq);
+  const int64_t g = ((int64_t)h * p.B + b) * p.plan.tiles_q + (p.plan.tiles_q - 1 - tq);
   const int64_t slot0 = g * n * rows + i % rows;
   float2 ml[2];
   float m = -__builtin_inff();
