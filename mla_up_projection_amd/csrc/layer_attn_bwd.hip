@@ -10,6 +10,7 @@
 // As in the forward the matrix unit's results, transposed by the choice of its
 // operands, are the operands of the next products as they lie.
 #include <algorithm>
+#include <cmath>
 
 #include "layer_attn.h"
 
@@ -698,10 +699,13 @@ AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k,
   pl.live = pl.tiles + (size_t)B * pl.tiles_q * 16;
   pl.part = (pl.live + (size_t)B * pl.tiles_q * 4 + 255) / 256 * 256;
   // Few keys, or few key heads of many: the query tiles of 128 keys go to several
-  // workgroups, up to one to a compute unit, if each has two tiles left. More than
-  // eight parts cost more to write and add than they save.
+  // workgroups, up to one to a compute unit. A tile takes as long as the parts of some
+  // 34 such groups of keys take to be written and added, so that with s parts the time
+  // is as steps / s + groups s / 34, least at the root below. (Two of 400 tokens, 16
+  // heads: one part 53 us in all, two 63. 512 tokens, ten heads of one key head: 51 with
+  // 26 parts, 57 with eight.)
   const int64_t groups = (int64_t)B * H_kv * ((Sk + 127) / 128), steps = (int64_t)(H / H_kv) * pl.tiles_q;
-  pl.splits = groups ? (int)std::max<int64_t>(1, std::min<int64_t>({cus / groups, steps / 2, 8})) : 1;
+  pl.splits = groups ? (int)std::max<int64_t>(1, std::min<int64_t>({cus / groups, (int64_t)std::sqrt(34.0 * steps / groups), steps})) : 1;
   pl.total = pl.part;
   if (pl.splits > 1) pl.total += (size_t)pl.splits * B * H_kv * Sk * (d_k + d_v) * 4;
   return pl;

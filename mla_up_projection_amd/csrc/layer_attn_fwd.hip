@@ -14,7 +14,8 @@
 namespace mla {
 namespace {
 
-constexpr int TK = 64;  // keys of a tile
+constexpr int TK = 64;         // keys of a tile
+constexpr int MAX_PARTS = 32;  // of a row's keys: the join has a lane to each
 
 // Output row (b, h, i), and its lse where that is wanted, the slow way.
 __device__ __forceinline__ void slow_forward(const LayerAttnParams& p, int b, int h, int i, bool want_lse, int lane) {
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
 }
 
 // Parts of a row joined: half a wave to a row, eight rows to a workgroup. A lane holds
-// the statistics of two parts and four columns.
+// the statistics of one part and four columns.
 __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
   const int lane = threadIdx.x & 63, l32 = lane & 31;
   const int64_t rows_all = (int64_t)p.B * p.H * p.Sq, at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -320,24 +321,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
   const int rows = p.plan.rows, tq = i / rows, n = p.plan.splits;
   const int64_t g = ((int64_t)h * p.B + b) * p.plan.tiles_q + (p.plan.tiles_q - 1 - tq);
   const int64_t slot0 = g * n * rows + i % rows;
-  float2 ml[2];
-  float m = -__builtin_inff();
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    ml[k] = make_float2(-__builtin_inff(), 0.0f);
-    const int s = l32 + 32 * k;
-    if (s < n) ml[k] = *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot0 + (int64_t)s * rows));
-    m = fmaxf(m, ml[k].x);
-  }
+  const float2 ml = l32 < n ? *reinterpret_cast<const float2*>(p.part_ml + 2 * (slot0 + (int64_t)l32 * rows))
+                            : make_float2(-__builtin_inff(), 0.0f);
+  float m = ml.x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-  const float mu = m == -__builtin_inff() ? 0.0f : m;
-  float w[2], l = 0;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    w[k] = __builtin_amdgcn_exp2f(ml[k].x - mu);
-    l = __builtin_fmaf(ml[k].y, w[k], l);
-  }
+  const float w = __builtin_amdgcn_exp2f(ml.x - (m == -__builtin_inff() ? 0.0f : m));
+  float l = ml.y * w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) l += __shfl_xor(l, o);
   const int c = 4 * l32;
@@ -345,7 +335,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(LayerAttnParams p) {
   float4 o = make_float4(0, 0, 0, 0);
   const float* from = p.part_o + slot0 * p.d_v + c;
   for (int s = 0; s < n; ++s) {
-    const float ws = __shfl(s < 32 ? w[0] : w[1], (lane & 32) | (s & 31));
+    const float ws = __shfl(w, (lane & 32) | s);
     if (in) {
       const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)s * rows * p.d_v);
       o.x = __builtin_fmaf(v.x, ws, o.x), o.y = __builtin_fmaf(v.y, ws, o.y);
@@ -422,10 +412,26 @@ AttnPlanFwd plan_layer_attn(int B, int H, int Sq, int Sk, int d_v, int cus) {
   pl.tiles_q = (Sq + pl.rows - 1) / pl.rows;
   pl.groups = (int64_t)B * H * pl.tiles_q;
   pl.splits = 1;
-  if (pl.groups > 0) {
-    // two workgroups to a compute unit, four tiles of keys to a part at least
-    const int64_t want = (2 * (int64_t)cus + pl.groups - 1) / pl.groups;
-    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({want, (Sk + 4 * TK - 1) / (4 * TK), 64}));
+  const int64_t steps = (Sk + TK - 1) / TK;
+  if (pl.groups > 0 && pl.rows == 32) {
+    // Few query rows wait for keys and values, and their parts are small: two workgroups
+    // to a compute unit, three tiles of keys to a part at least (one row of 16 heads over
+    // 700 keys: 15.9 us, with four tiles 17.5; over 5000: 26.5, with two tiles 28.9). More
+    // than 32 parts take longer to join than they save (eight heads, 16000 keys: 34.6 us,
+    // with 63 parts 40.7).
+    pl.splits = (int)std::max<int64_t>(1, std::min<int64_t>({(2 * (int64_t)cus + pl.groups - 1) / pl.groups, (steps + 2) / 3, MAX_PARTS}));
+  } else if (pl.groups > 0) {
+    // Of up to two workgroups to a compute unit the number of parts that takes the
+    // least by this estimate: 1.5 us to a tile, 2.1 where two share a unit; for more
+    // than one part 5 us and 0.025 for each that is written and read. (16 heads, 2048
+    // rows: one part 49 us, two 61; 400 rows of two sequences: 16 and 24; six heads, 2000
+    // rows: four parts 34, six 37.)
+    double least = 0;
+    for (int s = 1; s <= MAX_PARTS && s <= steps && (s == 1 || pl.groups * s <= 2 * (int64_t)cus); ++s) {
+      const int64_t n = pl.groups * s;
+      const double t = (double)((steps + s - 1) / s) * (n <= cus ? 1.5 : 2.1) + (s > 1 ? 5 + 0.025 * (double)n : 0);
+      if (s == 1 || t < least) least = t, pl.splits = s;
+    }
   }
   if (pl.splits > 1) {
     const size_t rows = (size_t)pl.groups * pl.splits * pl.rows;

@@ -107,7 +107,7 @@ def test_causal(dk, dv, Sq, Sk):
     check(q, k, v, ref.span_mask(s, Sk), scale=1 / math.sqrt(dk), spans=s, dout=do)
 
 
-@pytest.mark.parametrize("Sq, Sk", [(1, 64), (1, 517), (1, 5000), (2, 1777), (32, 700), (64, 300), (65, 900), (127, 128), (128, 64),
+@pytest.mark.parametrize("Sq, Sk", [(1, 64), (1, 517), (1, 5000), (1, 6500), (300, 2300), (2, 1777), (32, 700), (64, 300), (65, 900), (127, 128), (128, 64),
                                     (129, 65), (200, 63), (257, 511)])
 @pytest.mark.parametrize("dk, dv", [(192, 128), (64, 64)])
 def test_all_keys(Sq, Sk, dk, dv):
@@ -188,7 +188,7 @@ def test_large_scores_and_a_maximum_that_rises_late():
     check(q, k, v, torch.ones(1, 130, 700, dtype=torch.bool, device=DEV), scale=1.0, dout=do)
 
 
-@pytest.mark.parametrize("H, hk, S", [(2, 1, 4500), (4, 1, 4200), (1, 1, 8300)])
+@pytest.mark.parametrize("H, hk, S", [(2, 1, 4500), (4, 1, 4200), (1, 1, 8300), (16, 1, 130), (24, 1, 60)])
 def test_many_tiles(H, hk, S):
     """More than 64 tiles of 64 queries, so that the list of those that see a key has several words, for every head."""
     cu = [0, 5, 1000, 4100, S - 30]
