@@ -124,6 +124,7 @@ hipError_t launch_layer_attn(const LayerAttnParams& p, hipStream_t stream);
 struct AttnBwdPlan {
   int tiles_q;            // of 64 query rows
   int splits;             // parts that the query tiles of 128 keys are divided into
+  bool both;              // dK, dV and dQ in one launch
   size_t records, tiles, live, part, total;
 };
 constexpr int ATTN_RECORD = 512;  // words of a record

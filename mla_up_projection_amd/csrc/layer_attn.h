@@ -119,25 +119,29 @@ __device__ __forceinline__ void dma4(const void* sbase, uint32_t voff, uint32_t 
 // loads of eight rows by 64 columns; WAVES waves share them, PIECES each. Only rows
 // `first` .. `end` - 1 are read: others of the tile repeat the nearest of those, so that
 // what lies in rows that nobody here sees, NaN for instance, does not meet a weight
-// of 0. Columns from `width` on repeat the row's first; they meet zeros. The pieces are issued one at a time, between
-// matrix instructions.
-template <int R, int W, int WAVES>
+// of 0. Columns from `width` on repeat the row's first; they meet zeros. The pieces are
+// issued one at a time, between matrix instructions. LEAN: a piece's place in its row is
+// worked out at the piece, for kernels whose registers are full (in the forward, whose
+// are not, that costs 2 %).
+template <int R, int W, int WAVES, bool LEAN = false>
 struct TileLoads {
   static constexpr int PIECES = R / 8 * (W / 64) / WAVES;
   static constexpr int KINDS = WAVES == 1 ? 2 : 1;  // (places alternate between groups of eight rows)
   static_assert(R % 16 == 0 && (R / 8) % WAVES == 0 && (WAVES == 1 || WAVES % 2 == 0), "every wave loads as much");
-  uint32_t col[KINDS][W / 64];  // bytes into the row
+  static constexpr int KEPT = LEAN ? 1 : W / 64;
+  uint32_t col[KINDS][KEPT];  // bytes into the row (LEAN: of the first 64 columns)
   const uint16_t* from;
-  uint32_t stride;
+  uint32_t stride, width2;
   int low, high, wave, r0;
 
-  __device__ __forceinline__ TileLoads(int width, uint32_t stride_bytes, int w, int lane) : stride(stride_bytes), wave(w), r0(lane >> 3) {
+  __device__ __forceinline__ TileLoads(int width, uint32_t stride_bytes, int w, int lane)
+      : stride(stride_bytes), width2(2 * width), wave(w), r0(lane >> 3) {
 #pragma unroll
     for (int k = 0; k < KINDS; ++k)
 #pragma unroll
-      for (int b = 0; b < W / 64; ++b) {
+      for (int b = 0; b < KEPT; ++b) {
         const int c = 64 * b + 8 * ((lane & 7) ^ tile_swz(r0 + 8 * (WAVES == 1 ? k : w & 1)));
-        col[k][b] = c < width ? 2 * c : 0;
+        col[k][b] = LEAN || c < width ? 2 * c : 0;
       }
   }
   // base: the first row of the batch entry and head
@@ -145,11 +149,21 @@ struct TileLoads {
     from = uniform(base + (int64_t)row0 * (stride >> 1));
     low = max(first - row0, 0);
     high = end - 1 - row0;
+    if (LEAN) {  // (nor is what pieces add kept in registers over a loop)
+      asm volatile("" : "+v"(r0));
+#pragma unroll
+      for (int k = 0; k < KINDS; ++k) asm volatile("" : "+v"(col[k][0]));
+    }
   }
   __device__ __forceinline__ void piece(int i, uint32_t tile) const {
     const int j = i * WAVES + wave, b = i * WAVES / (R / 8), r8 = (j % (R / 8)) * 8;
     const uint32_t row = (uint32_t)min(max(r0 + r8, low), high);
-    dma16(from, __umul24(row, stride) + col[WAVES == 1 ? i & 1 : 0][b], __builtin_amdgcn_readfirstlane(tile + j * 1024));
+    uint32_t c = col[WAVES == 1 ? i & 1 : 0][LEAN ? 0 : b];
+    if (LEAN) {
+      c += 128 * b;
+      c = c < width2 ? c : 0;
+    }
+    dma16(from, __umul24(row, stride) + c, __builtin_amdgcn_readfirstlane(tile + j * 1024));
   }
   __device__ __forceinline__ void all(uint32_t tile) const {
 #pragma unroll

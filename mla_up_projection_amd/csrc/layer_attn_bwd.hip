@@ -2,13 +2,18 @@
 // forward's statistics and delta = rowsum(dout out):
 //   dV = P^T dO,  dS = P (dO V^T - delta) c',  dK = scale dS^T Q,  dQ = scale dS K.
 //
-// Two kernels, so that every sum stays in registers and no atomics are needed: one
+// Two parts, so that every sum stays in registers and no atomics are needed: one
 // owns 128 keys and goes through the queries that see them (dK and dV; heads that
 // share the keys one after the other), one owns 128 queries and goes through their
-// keys (dQ). Both make S and dP again, at 32 + 32 matrix products of the 26 that one
-// pass with atomics would take, but with results that do not depend on timing.
-// As in the forward the matrix unit's results, transposed by the choice of its
-// operands, are the operands of the next products as they lie.
+// keys (dQ). Both make S and dP, which costs 7 products of a pair where one pass with
+// atomics would take 5, but results do not depend on timing. As in the forward the
+// matrix unit's results, transposed by the choice of its operands, are the operands of
+// the next products as they lie.
+//
+// Bound by the matrix units at the clock that their power leaves: 4096 causal tokens,
+// 128 heads of 192 + 128: 1.48 ms for dK and dV (930 TFLOP/s of the products done),
+// 0.96 for dQ (1150), 0.05 for the rows' statistics; on zeros, which take less power,
+// all together 13 % less.
 #include <algorithm>
 #include <cmath>
 
@@ -318,8 +323,8 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
     hole_next = (holes >> r) & 1;
     return word * 64 + r;
   };
-  TileLoads<TT, DK, 8> ql(f.d_k, (uint32_t)(f.q.ss * 2), wave, lane);
-  TileLoads<TT, DV, 8> ol(f.d_v, (uint32_t)(p.dout.ss * 2), wave, lane);
+  TileLoads<TT, DK, 8, (DK > 128)> ql(f.d_k, (uint32_t)(f.q.ss * 2), wave, lane);
+  TileLoads<TT, DV, 8, (DK > 128)> ol(f.d_v, (uint32_t)(p.dout.ss * 2), wave, lane);
   const auto load = [&](int tq, int head, uint32_t at) {
     int first = tq * TT, end = first + TT;
     if (hole_next) {  // padding in front of or behind the rows that see something (or no rows at all)
@@ -502,12 +507,11 @@ __device__ __forceinline__ void dkdv_wave(const LayerAttnBwdParams& p, uint8_t* 
 }
 
 template <int DK, int DV, int FORM>
-__global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Kv<DK, DV, FORM>::LDS];
+__device__ __forceinline__ void dkdv(const LayerAttnBwdParams& p, uint8_t* lds, uint32_t block) {
   const LayerAttnParams& f = p.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_k = (f.Sk + 127) / 128;
-  const int us = die_order(blockIdx.x, (uint32_t)(f.B * f.H_kv * tiles_k * p.plan.splits));
+  const int us = die_order(block, (uint32_t)(f.B * f.H_kv * tiles_k * p.plan.splits));
   if (us < 0) return;
   const int u = us / p.plan.splits, split = us - u * p.plan.splits;
   const int hb = u / tiles_k, k0 = (u - hb * tiles_k) * 128;
@@ -517,15 +521,19 @@ __global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p)
   else dkdv_wave<DK, DV, FORM, 1>(p, lds, b, hk, bh, k0, split, wave, lane);
 }
 
+// LDS of the part below: two slots of a tile of 64 keys.
+template <int DK, int DV>
+constexpr int DQ_LDS = 2 * TT * 2 * (DK + DV);
+
+// dQ of 128 queries, by four waves.
 template <int DK, int DV, int FORM>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
+__device__ __forceinline__ void dq_rows(const LayerAttnBwdParams& p, uint8_t* lds, uint32_t block) {
   constexpr int KB = TT * 2 * DK, VB = TT * 2 * DV, SB = KB + VB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SB];
   const LayerAttnParams& f = p.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5;
   const int tiles = (f.Sq + 127) / 128;
-  const int u = die_order(blockIdx.x, (uint32_t)(f.B * f.H * tiles));
+  const int u = die_order(block, (uint32_t)(f.B * f.H * tiles));
   if (u < 0) return;
   const int hb = u / tiles, t0 = tiles - 1 - (u - hb * tiles);  // the last rows first
   const int h = hb / f.B, b = hb - h * f.B, hk = h / f.group;
@@ -559,8 +567,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
   const uint32_t rb = row_base(lane), cb = col_base(lane);
   const uint32_t ring = lds_u32(lds);
   const uint16_t *kb = row_of(f.k, b, hk, 0), *vb = row_of(f.v, b, hk, 0);
-  TileLoads<TT, DK, 4> kl(f.d_k, (uint32_t)(f.k.ss * 2), wave, lane);
-  TileLoads<TT, DV, 4> vl(f.d_v, (uint32_t)(f.v.ss * 2), wave, lane);
+  TileLoads<TT, DK, 4, (DK > 128)> kl(f.d_k, (uint32_t)(f.k.ss * 2), wave, lane);
+  TileLoads<TT, DV, 4, (DK > 128)> vl(f.d_v, (uint32_t)(f.v.ss * 2), wave, lane);
   f32x16_t dq[DK / 32];
 #pragma unroll
   for (int n = 0; n < DK / 32; ++n) dq[n] = zero16();
@@ -592,8 +600,10 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
     const ColAddr cols = col_addr(cb + (ring + slot * SB));
     const bool all = t * TT >= wlo_all && (t + 1) * TT <= whi_all;
     // The operands of a block of 32 keys are one stream: K by rows for S, V by rows
-    // for dP, K by columns for dQ, read AHEAD matrix instructions before their use.
-    constexpr int NS = DK / 16, NP = DV / 16, NQ = DK / 16, N = NS + NP + NQ, AHEAD = 4;
+    // for dP, K by columns for dQ, read AHEAD matrix instructions before their use (at
+    // 192 columns less: registers that spill in this loop make it wait for its loads;
+    // 4096 causal tokens, 128 heads, backward: 2.48 ms, with four ahead 2.59).
+    constexpr int NS = DK / 16, NP = DV / 16, NQ = DK / 16, N = NS + NP + NQ, AHEAD = DK <= 128 ? 4 : FORM == FORM_ANY ? 2 : 3;
     bf16x8_t op[AHEAD];
     const auto read = [&](int x) {
       const int k = x / N, y = x % N;
@@ -606,7 +616,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      f32x16_t s, dp, slope;
+      f32x16_t s, dp;
 #pragma unroll
       for (int c = 0; c < NS; ++c) {
         const int x = k * N + c;
@@ -627,16 +637,13 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
       for (int r = 0; r < 16; ++r) {
         float c = 1.0f;
         s[r] = probability<FORM>(sf, s[r], far - (float)(8 * (r / 4) + r % 4), less, c);
-        if (FORM == FORM_ANY) slope[r] = c;
+        if (FORM == FORM_ANY) s[r] *= c;
       }
       interleave<NP - AHEAD, 1, 4>();
       interleave<AHEAD, 2, 4>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int r = 0; r < 16; ++r) dp[r] = s[r] * (dp[r] + delta);
-      if (FORM == FORM_ANY)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) dp[r] *= slope[r];
       if (!all) {
         rare();
 #pragma unroll
@@ -668,17 +675,36 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
 }
 
 template <int DK, int DV, int FORM>
+__global__ __launch_bounds__(512, 2) void attn_dkdv_kernel(LayerAttnBwdParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Kv<DK, DV, FORM>::LDS];
+  dkdv<DK, DV, FORM>(p, lds, blockIdx.x);
+}
+template <int DK, int DV, int FORM>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(LayerAttnBwdParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[DQ_LDS<DK, DV>];
+  dq_rows<DK, DV, FORM>(p, lds, blockIdx.x);
+}
+// Both at once, where they leave compute units to each other.
+template <int DK, int DV, int FORM>
+__global__ __launch_bounds__(512, 2) void attn_bwd_kernel(LayerAttnBwdParams p, uint32_t first) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Kv<DK, DV, FORM>::LDS];
+  static_assert(DQ_LDS<DK, DV> <= Kv<DK, DV, FORM>::LDS, "room for either");
+  if (blockIdx.x < first) dkdv<DK, DV, FORM>(p, lds, blockIdx.x);
+  else if (threadIdx.x < 256) dq_rows<DK, DV, FORM>(p, lds, blockIdx.x - first);  // (the other waves end here)
+}
+
+template <int DK, int DV, int FORM>
 void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
   const LayerAttnParams& f = p.f;
   const int64_t keys = (int64_t)f.B * f.H_kv * ((f.Sk + 127) / 128) * p.plan.splits, rows = (int64_t)f.B * f.H * ((f.Sq + 127) / 128);
-  if (keys)
-    hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, FORM>), dim3((unsigned)((keys + 7) / 8 * 8)), dim3(512), 0, stream, p);
-  if (keys && p.plan.splits > 1) {
+  const unsigned keys8 = (unsigned)((keys + 7) / 8 * 8), rows8 = (unsigned)((rows + 7) / 8 * 8);
+  if (p.plan.both) hipLaunchKernelGGL((attn_bwd_kernel<DK, DV, FORM>), dim3(keys8 + rows8), dim3(512), 0, stream, p, keys8);
+  else if (keys) hipLaunchKernelGGL((attn_dkdv_kernel<DK, DV, FORM>), dim3(keys8), dim3(512), 0, stream, p);
+  if (p.plan.splits > 1) {
     const int64_t n = (int64_t)f.B * f.H_kv * f.Sk;
     hipLaunchKernelGGL(attn_bwd_join_kernel, dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream, p);
   }
-  if (rows)
-    hipLaunchKernelGGL((attn_dq_kernel<DK, DV, FORM>), dim3((unsigned)((rows + 7) / 8 * 8)), dim3(256), 0, stream, p);
+  if (rows && !p.plan.both) hipLaunchKernelGGL((attn_dq_kernel<DK, DV, FORM>), dim3(rows8), dim3(256), 0, stream, p);
 }
 template <int DK, int DV>
 void bwd(const LayerAttnBwdParams& p, hipStream_t stream) {
@@ -704,8 +730,20 @@ AttnBwdPlan plan_layer_attn_bwd(int B, int H, int H_kv, int Sq, int Sk, int d_k,
   // is as steps / s + groups s / 34, least at the root below. (Two of 400 tokens, 16
   // heads: one part 53 us in all, two 63. 512 tokens, ten heads of one key head: 51 with
   // 26 parts, 57 with eight.)
+  // dK, dV and dQ are made at once where the compute units have room for the workgroups
+  // of both, or for one of each (these then balance what a mask leaves uneven: 8
+  // heads of 4096 causal tokens 184 us in all, in turn 264).
   const int64_t groups = (int64_t)B * H_kv * ((Sk + 127) / 128), steps = (int64_t)(H / H_kv) * pl.tiles_q;
-  pl.splits = groups ? (int)std::max<int64_t>(1, std::min<int64_t>({cus / groups, (int64_t)std::sqrt(34.0 * steps / groups), steps})) : 1;
+  const int64_t rows = (int64_t)B * H * ((Sq + 127) / 128);
+  pl.splits = 1;
+  if (groups > 0) {
+    const auto parts = [&](int64_t units) {
+      return (int)std::max<int64_t>(1, std::min<int64_t>({units / groups, (int64_t)std::sqrt(34.0 * steps / groups), steps}));
+    };
+    pl.splits = parts(cus);
+    pl.both = rows > 0 && (groups + rows <= cus || (pl.splits == 1 && groups <= cus && rows <= cus));
+    if (pl.both) pl.splits = parts(cus - rows);
+  }
   pl.total = pl.part;
   if (pl.splits > 1) pl.total += (size_t)pl.splits * B * H_kv * Sk * (d_k + d_v) * 4;
   return pl;

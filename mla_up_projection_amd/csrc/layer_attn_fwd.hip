@@ -7,6 +7,13 @@
 // wave; P^T, rounded to bf16, is the operand of O^T += V^T P^T as it lies. K and V
 // stream through a ring of two 64-key tiles by direct loads, a tile ahead. Q stays
 // in registers.
+//
+// Many rows: bound by the matrix units at the clock that their power leaves (4096
+// causal tokens, 128 heads of 192 + 128: 0.72 ms, 960 TFLOP/s; on zeros, which take
+// less power, 0.60). One wave of two to a SIMD does the softmax while the other's
+// products run; products of the next 32 keys next to the softmax within a wave took
+// the same time. One token: bound by reading K and V (1777 of them, 128 heads: 31 us,
+// 4.7 TB/s, and 4 for the join).
 #include <algorithm>
 
 #include "layer_attn.h"

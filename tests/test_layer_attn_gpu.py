@@ -126,6 +126,18 @@ def test_caps_and_distances(cap, slope, scale, dk, dv):
     check(q, k, v, ref.span_mask(s, Sk), scale=scale, cap=cap, slopes=slopes, spans=s, at=at, dout=do)
 
 
+@pytest.mark.parametrize("cap, slope", [(0.0, False), (0.0, True), (20.0, True)])
+@pytest.mark.parametrize("dk, dv", [(192, 128), (128, 128), (64, 64)])
+@pytest.mark.parametrize("B, H, hk, S", [(3, 88, 88, 130), (1, 64, 2, 600), (1, 40, 40, 600)])
+def test_more_rows_than_compute_units(B, H, hk, S, dk, dv, cap, slope):
+    """More tiles of 128 queries than the chip has compute units, with as many key tiles and with few; as many as it has
+    of each together. The backward's kernels run in turn or at once, with one part or several."""
+    q, k, v, do = make(S + dk, B, H, hk, S, S, dk, dv)
+    slopes = torch.rand(H, device=DEV, generator=gen(5)) if slope else None
+    s, at = spans_of(B, S, S, slope, len_q=[S, 77, 1][:B], len_k=[S, 77, 1][:B])
+    check(q, k, v, ref.span_mask(s, S), scale=0.09, cap=cap, slopes=slopes, spans=s, at=at, dout=do)
+
+
 @pytest.mark.parametrize("Sq, Sk", [(1, 700), (40, 90), (200, 200)])
 def test_distances_without_places(Sq, Sk):
     """Without `at` the queries are the last of the keys; without spans they see all of them; lse need not be asked for."""
@@ -190,7 +202,8 @@ def test_large_scores_and_a_maximum_that_rises_late():
 
 @pytest.mark.parametrize("H, hk, S", [(2, 1, 4500), (4, 1, 4200), (1, 1, 8300), (16, 1, 130), (24, 1, 60)])
 def test_many_tiles(H, hk, S):
-    """More than 64 tiles of 64 queries, so that the list of those that see a key has several words, for every head."""
+    """More than 64 tiles of 64 queries, so that the list of those that see a key has several words, for every head; or
+    few rows and many heads to a key head, whose tiles go to many workgroups."""
     cu = [0, 5, 1000, 4100, S - 30]
     q, k, v, do = make(S, 1, H, hk, S, S, 64, 64)
     s, _ = spans_of(1, S, S, cu_q=cu)
