@@ -227,6 +227,17 @@ __device__ __forceinline__ ScoreForm score_form(const LayerAttnParams& p, int h)
 __device__ __forceinline__ float tanh_of(float x2) {
   return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x2));
 }
+// The same of arguments below SMALL_TANH (x below 0.28): five terms of its series
+// x (1 - x^2 / 3 + 2 x^4 / 15 - 17 x^6 / 315 + 62 x^8 / 2835); the sixth is 2^-25 of the sum.
+constexpr float SMALL_TANH = 0.8f;
+__device__ __forceinline__ float tanh_small(float x2) {
+  constexpr float u = 0.34657359f, w = u * u;  // (ln 2 / 2)
+  const float z = x2 * x2;
+  float s = __builtin_fmaf(z, 62.0f / 2835 * w * w * w * w, -17.0f / 315 * w * w * w);
+  s = __builtin_fmaf(z, s, 2.0f / 15 * w * w);
+  s = __builtin_fmaf(z, s, -w / 3);
+  return u * x2 * __builtin_fmaf(z, s, 1.0f);
+}
 
 struct Span {
   int lo, hi;

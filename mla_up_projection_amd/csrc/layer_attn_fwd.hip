@@ -193,11 +193,33 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 4 ? 2 : 1) void attn_fwd_kerne
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
+        for (int r = 0; r < 16; ++r) s[k][r] *= sf.scale2;
+      if (FORM == FORM_ANY && p.cap > 0) {
+        float most = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(s[k][r]));
+        // Scores far below the cap take the series, whose error is relative to them: that
+        // of 1 - 2 / (1 + e) is 2^-23 of the cap.
+        if (__builtin_amdgcn_ballot_w64(!(most < SMALL_TANH)) == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[k][r] = sf.cap2 * tanh_small(s[k][r]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[k][r] = sf.cap2 * tanh_of(s[k][r]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
         for (int r = 0; r < 16; ++r) {
           const float d = fabsf(far - (float)(32 * k + 8 * (r / 4) + r % 4));
-          float x = s[k][r] * sf.scale2;
-          if (FORM == FORM_ANY && p.cap > 0) x = sf.cap2 * tanh_of(x);
-          s[k][r] = __builtin_fmaf(-sf.slope2, d, x);
+          s[k][r] = __builtin_fmaf(-sf.slope2, d, s[k][r]);
         }
     }
     if (t * TK < wlo_all || (t + 1) * TK > whi_all) {
