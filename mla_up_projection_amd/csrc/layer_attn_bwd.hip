@@ -12,8 +12,8 @@
 //
 // Bound by the matrix units at the clock that their power leaves: 4096 causal tokens,
 // 128 heads of 192 + 128: 1.48 ms for dK and dV (930 TFLOP/s of the products done),
-// 0.96 for dQ (1150), 0.05 for the rows' statistics; on zeros, which take less power,
-// all together 13 % less.
+// 1.0 for dQ (1100), 0.05 for the rows' statistics; on zeros, which take less power,
+// all together 12 % less.
 #include <algorithm>
 #include <cmath>
 

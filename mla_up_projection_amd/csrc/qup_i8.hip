@@ -1,7 +1,8 @@
 // Query up-projection in 8-bit integers for gfx950: Q[t, n] = xs[t] ws[n]
 // sum_k X[t, k] W[n, k] (+ bias), RoPE, bf16 or MXFP8 in BHSD. Sums are exact in
-// 32 bits. Many tokens go to the tiled kernel of the fused forward; the one here
-// is for few, where reading W once (K N bytes) is what bounds it.
+// 32 bits. Many tokens go to the tiled kernel of the fused forward; the two here
+// are for few, where reading W once (K N bytes) is what bounds it: K 1536, N 24576
+// is 38 MB, for one token 10.3 us (3.7 TB/s), for 52 tokens 15.9.
 //
 // A lane holds 32 consecutive k of one weight row in two 16-byte loads, so a
 // wave reads whole 128-byte lines. The MFMA's k slots are a sum's terms and
