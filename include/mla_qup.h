@@ -635,7 +635,8 @@ MLA_API mla_status mla_rmsnorm_bwd(const mla_rmsnorm_bwd_args* args, void* strea
 /* Quantize the rows of a matrix to int8 with one scale each, by the rule of
  * mla_rmsnorm_fwd: the weights of mla_qup_fwd_i8 (a scale for each output
  * channel), or its activations.
- *   x      : as mxfp8_quantize. rows: 0 .. 2^24 - 1; cols: a multiple of 8, > 0.
+ *   x      : as mxfp8_quantize. rows: 0 .. 2^24 - 1; cols: a multiple of 8, > 0;
+ *            rows * cols <= 2^36.
  *   codes  : device int8[rows*cols], 8-byte aligned. scales: device float[rows].
  * Errors: MLA_EINVAL, MLA_EALIAS, MLA_EDEVICE. */
 MLA_API mla_status int8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld,
@@ -739,7 +740,7 @@ typedef struct {
 MLA_API size_t mla_attn_fwd_workspace_size(const mla_attn_args* args);
 
 /* Errors: MLA_EINVAL, MLA_EALIAS, MLA_EWORKSPACE, MLA_EUNSUPPORTED (wider rows,
- * or 2^22 and more tiles of query rows), MLA_EDEVICE. */
+ * or 2^22 and more tiles of 32 rows, of B H Sq or B H Sk), MLA_EDEVICE. */
 MLA_API mla_status mla_attn_fwd(const mla_attn_args* args, void* stream);
 
 /* Its backward, from the forward's out and lse:

@@ -274,6 +274,18 @@ def test_rows_that_are_not_seen_have_no_influence(bad, Sq):
         ref.within(a, b.to(F64), b.to(F64).abs() * 4 * ref.BF16 + 0.02 * b.float().abs().max(), name)
 
 
+@pytest.mark.parametrize("cap", [0.0, 20.0, 50.0, 1e4])
+def test_one_key_far_below_the_cap(cap):
+    """Its lse is the score. Eight exact products are added (8 2^-23 of their magnitudes); scale, series and cap are at
+    most 16 roundings relative to the score."""
+    q, k, v, _ = make(int(cap), 2, 3, 3, 70, 1, 8, 8)
+    _, lse = forward(q, k, v, scale=0.1, cap=cap)
+    prod = q.to(F64) * k.to(F64)
+    s = prod.sum(-1) * 0.1
+    s = cap * torch.tanh(s / cap) if cap else s
+    ref.within(lse, s, 8 * 2.0 ** -23 * 0.1 * prod.abs().sum(-1) + 2.0 ** -20 * s.abs(), "lse")
+
+
 @pytest.mark.parametrize("cap", [0.0, 20.0])
 def test_holes_between_rows(cap):
     """Rows that see nothing in front of, between and behind others, all with NaN: gradients of the others are finite

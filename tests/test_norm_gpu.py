@@ -126,6 +126,24 @@ def test_backward(T, K, kind):
     assert torch.equal(again, dg)
 
 
+@pytest.mark.parametrize("hd", [BF, F32])
+@pytest.mark.parametrize("T, K", [(5, 96), (700, 1536), (3, 8224)])
+def test_backward_gives_each_output_alone(T, K, hd):
+    g = gen(T)
+    h, gamma, dy, dh = rand(g, T, K, dtype=hd), rand(g, K), rand(g, T, K), rand(g, T, K, dtype=hd)
+    rstd = ref.norm(h, gamma, 1e-6)[1].to(F32)
+    ws = torch.empty(m.mla_rmsnorm_bwd_workspace_size(T, K), dtype=torch.uint8, device=DEV)
+    new = dict(dx=lambda: torch.full((T, K), 9.0, dtype=BF, device=DEV), dres=lambda: torch.full((T, K), 9.0, device=DEV),
+               dgamma=lambda: torch.full((K,), 9.0, device=DEV))
+    all_of = {n: f() for n, f in new.items()}
+    m.mla_rmsnorm_bwd(dy, h, rstd, gamma, dh=dh, workspace=ws, **all_of)
+    assert torch.equal(all_of["dres"].to(BF), all_of["dx"])
+    for n, f in new.items():
+        one = f()
+        m.mla_rmsnorm_bwd(dy, h, rstd, gamma, dh=dh, workspace=ws if n == "dgamma" else None, **{n: one})
+        assert torch.equal(one, all_of[n]), n
+
+
 def test_no_rows():
     e = torch.empty(0, 64, dtype=BF, device=DEV)
     m.mla_rmsnorm_fwd(e, None, y=torch.empty_like(e))
